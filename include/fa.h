@@ -67,6 +67,9 @@ extern "C" {
 #define FA_ERR_BOUNDS (-8)         /* bounds-checked build only: a kernel computed a tile, mask
                                       or row index outside its array and stopped before using it
                                       (reported by fa_device_status) */
+#define FA_ERR_PAGE (-9)           /* a paged cache's device-side tables hold a row range, length,
+                                      position or page number outside its bounds (reported by
+                                      fa_device_status) */
 
 /*
  * Forward pass.
@@ -235,6 +238,100 @@ int fa_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* lse,
                size_t workspace_bytes, void* stream);
 
 /*
+ * Paged key/value cache: appending to it, and attention over it (serving; the
+ * pages name paged key/value gathers, cs2680 Lecture 9 sec. 9.8, and define
+ * none).
+ *
+ * Layout.  k_pages, v_pages: [num_pages][Hkv][page_size][d] bf16, a page being
+ * one [H][N][d] block of the library's layout; page_size a power of two from
+ * 16 to 256.  page_table: [B][max_pages] int32, the pages of sequence b in
+ * order.  New tokens are packed rows [T][heads][d] bf16, row t at t * stride
+ * elements (stride a multiple of 8 and at least heads * d; heads contiguous),
+ * so q, k and v may be slices of one projection's output.  cu_q: [B + 1] int32,
+ * ascending: sequence b's new tokens are rows cu_q[b] .. cu_q[b+1] - 1 (none:
+ * equal entries); rows outside every sequence are padding, which no call
+ * writes.  seq_lens: [B] int32, each sequence's keys with its new tokens
+ * included; row t of sequence b is position
+ *     pos(t) = seq_lens[b] - (cu_q[b+1] - t).
+ * Both calls take the same tables: append, then attend.
+ *
+ * The tables are device memory, read by the kernels only, so a call can be
+ * captured into a graph and replayed with other lengths and pages.  Their
+ * values are checked on the device: an entry outside its bounds (a row range
+ * not ascending in [0, T], a length above max_pages * page_size, a position
+ * outside the cache or the rotation table, a page number outside
+ * [0, num_pages)) records FA_ERR_PAGE in the status word; nothing is read or
+ * written through it, and the results of that sequence are unspecified.
+ * Table entries past a sequence's last page are not read.
+ */
+
+/*
+ * Appends T packed rows of keys and values to the cache, rotating the first
+ * rope_dim channels of every new key (and query) by its position:
+ *   k, v    : [T][Hkv][d], read; written to slot pos % page_size of page
+ *             page_table[b][pos / page_size] (v unrotated).
+ *   q, q_out: [T][Hq][d]; both or neither NULL.  q_out receives the rotated
+ *             queries; it may be q itself (with the same stride).
+ *   rope    : [rope_len][rope_dim] fp32, row pos: rope_dim / 2 cosines, then
+ *             as many sines; NULL with rope_dim = 0 (no rotation).  rope_dim
+ *             a multiple of 16, at most d.  Channel pairs are (i, i +
+ *             rope_dim / 2), or (2i, 2i + 1) with interleaved = 1; the pair
+ *             (x, y) becomes (x c - y s, x s + y c), in fp32, rounded to bf16
+ *             once.
+ * Two rows that write the same slot of the same page race (the cache's owner
+ * gives each position one page).  Errors: FA_ERR_ARG, FA_ERR_UNSUPPORTED_D,
+ * FA_ERR_ALIGN (16 bytes for q, k, v, q_out, the pages and rope; 4 for the
+ * tables), FA_ERR_DEVICE, FA_ERR_LAUNCH.
+ */
+int fa_kv_append(const void* q, const void* k, const void* v, void* q_out, void* k_pages,
+                 void* v_pages, const int* page_table, const int* seq_lens, const int* cu_q,
+                 const float* rope, int T, int B, int Hq, int Hkv, int d, long long q_stride,
+                 long long k_stride, long long v_stride, long long q_out_stride, int num_pages,
+                 int page_size, int max_pages, int rope_dim, int rope_len, int interleaved,
+                 void* stream);
+
+/*
+ * Attention of T packed query rows over the cache.
+ *   q   : [T][Hq][d] (row stride q_stride); o : [T][Hq][d] contiguous, written;
+ *         lse : [T][Hq] fp32, written.  Hq is a multiple of Hkv, at most 128
+ *         query heads per key/value head (head h reads key/value head
+ *         h / (Hq / Hkv)).
+ *   causal = 1: row t sees its sequence's keys j <= pos(t); 0: all of them.
+ *         A row without keys gets O = 0 and lse = -inf.
+ *   max_q : the most new tokens of a sequence, as far as the caller knows: it
+ *         decides how query rows are packed into tiles, and any value >= 1
+ *         gives right results.
+ *   workspace: device buffer of fa_fwd_paged_workspace_size(...) bytes,
+ *         256-byte aligned (may be NULL where that is 0).  Two calls in flight
+ *         at once need two workspaces.
+ * Keys in slots past a sequence's length are never used, whatever they hold.
+ */
+size_t fa_fwd_paged_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_q,
+                                   int prefix_len);
+int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+                 const int* page_table, const int* seq_lens, const int* cu_q, int T, int B, int Hq,
+                 int Hkv, int d, long long q_stride, int num_pages, int page_size, int max_pages,
+                 int max_q, int causal, float scale, void* workspace, size_t workspace_bytes,
+                 void* stream);
+
+/*
+ * fa_fwd_paged for a batch whose sequences all begin with the same prefix_len
+ * keys (a positive multiple of page_size, at most max_pages pages), held once
+ * in the pages prefix_pages[0 .. prefix_len / page_size): their attention is
+ * computed once for the query rows of the whole batch and merged with each
+ * sequence's own by logsumexp.  seq_lens and positions count the prefix; the first prefix_len /
+ * page_size entries of each page_table row stand for the prefix and are not
+ * read.  Other arguments, results and errors as fa_fwd_paged, with the
+ * workspace size for the same prefix_len.
+ */
+int fa_fwd_paged_prefix(const void* q, const void* k_pages, const void* v_pages, void* o,
+                        float* lse, const int* page_table, const int* seq_lens, const int* cu_q,
+                        const int* prefix_pages, int prefix_len, int T, int B, int Hq, int Hkv,
+                        int d, long long q_stride, int num_pages, int page_size, int max_pages,
+                        int max_q, int causal, float scale, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
  * Size of the scratch array fa_bwd_noalloc uses: 32 MiB of static device
  * data on every GPU that loads the library, held until the process exits.
  */
@@ -267,11 +364,13 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  * Synchronises `stream`, then returns and clears the status word of the
  * current device: FA_OK, FA_ERR_TIMEOUT if a kernel gave up on a pipeline
  * wait since the last call, FA_ERR_BOUNDS if a kernel of the bounds-checked
- * build caught an out-of-range index, or FA_ERR_LAUNCH if the stream holds a
+ * build caught an out-of-range index, FA_ERR_PAGE if a paged-cache kernel met
+ * a table entry outside its bounds, or FA_ERR_LAUNCH if the stream holds a
  * CUDA error.  The first error recorded wins.  If `site` is not NULL it
  * receives the identifier of the wait or check that raised it (0 if none):
  * 101-199 a wait of the forward kernel, 201-299 one of the backward main
- * kernel, 1101-1199 a bounds check of the forward kernels, 1201-1299 one of
+ * kernel, 301-304 the paged cache's tables (row ranges, lengths, positions,
+ * page numbers), 1101-1199 a bounds check of the forward kernels, 1201-1299 one of
  * the backward kernels, FA_SITE_SELFTEST and FA_SITE_SELFTEST_BOUNDS the self
  * tests'.
  */

@@ -457,6 +457,137 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* o, const v
   return launch_bwd(tq, tk, tv, tdo, p, d, static_cast<cudaStream_t>(stream), phase_mask);
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Shape checks shared by the paged-cache calls; *page_shift = log2(page_size).
+int paged_shape(int T, int B, int Hq, int Hkv, int d, int num_pages, int page_size, int max_pages,
+                int* page_shift) {
+  if (T < 1 || B < 1 || Hq < 1 || Hkv < 1 || num_pages < 1 || max_pages < 1) return FA_ERR_ARG;
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0) return FA_ERR_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED_D;
+  // Row and page coordinates, and positions, are 32-bit.
+  if (B == 0x7fffffff || (long long)T * Hq > 0x7fffffffLL || (long long)T * Hkv > 0x7fffffffLL)
+    return FA_ERR_ARG;
+  if ((long long)num_pages * Hkv > 0x7fffffffLL) return FA_ERR_ARG;
+  if ((long long)max_pages * page_size > (1LL << 30)) return FA_ERR_ARG;
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  *page_shift = s;
+  return FA_OK;
+}
+
+bool row_stride_ok(long long stride, int heads, int d) {
+  return stride >= (long long)heads * d && stride % 8 == 0 && stride < (1LL << 38);
+}
+
+int kv_append_impl(const void* q, const void* k, const void* v, void* q_out, void* k_pages,
+                   void* v_pages, const int* page_table, const int* seq_lens, const int* cu_q,
+                   const float* rope, int T, int B, int Hq, int Hkv, int d, long long q_stride,
+                   long long k_stride, long long v_stride, long long q_out_stride, int num_pages,
+                   int page_size, int max_pages, int rope_dim, int rope_len, int interleaved,
+                   void* stream) {
+  if (!k || !v || !k_pages || !v_pages || !page_table || !seq_lens || !cu_q) return FA_ERR_ARG;
+  if ((q == nullptr) != (q_out == nullptr)) return FA_ERR_ARG;
+  if (interleaved != 0 && interleaved != 1) return FA_ERR_ARG;
+  KvAppendParams p;
+  int rc = paged_shape(T, B, q ? Hq : 1, Hkv, d, num_pages, page_size, max_pages, &p.page_shift);
+  if (rc != FA_OK) return rc;
+  if (rope_dim < 0 || rope_dim > d || rope_dim % 16 != 0) return FA_ERR_ARG;
+  if ((rope_dim > 0) != (rope != nullptr) || (rope_dim > 0 && rope_len < 1)) return FA_ERR_ARG;
+  if (!row_stride_ok(k_stride, Hkv, d) || !row_stride_ok(v_stride, Hkv, d)) return FA_ERR_ARG;
+  if (q && (!row_stride_ok(q_stride, Hq, d) || !row_stride_ok(q_out_stride, Hq, d)))
+    return FA_ERR_ARG;
+  if (q == q_out && q && q_stride != q_out_stride) return FA_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
+      !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(rope) || !aligned4(page_table) ||
+      !aligned4(seq_lens) || !aligned4(cu_q))
+    return FA_ERR_ALIGN;
+  DeviceState* ds;
+  if ((rc = device_state(&ds)) != FA_OK) return rc;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.k_pages = static_cast<__nv_bfloat16*>(k_pages);
+  p.v_pages = static_cast<__nv_bfloat16*>(v_pages);
+  p.page_table = page_table;
+  p.seq_lens = seq_lens;
+  p.cu_q = cu_q;
+  p.rope = rope;
+  p.status = ds->status;
+  p.T = T;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out_stride = q_out_stride;
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  p.rope_dim = rope_dim;
+  p.rope_len = rope_len;
+  p.interleaved = interleaved;
+  return launch_kv_append(p, d, static_cast<cudaStream_t>(stream));
+}
+
+// Attention over the paged cache; prefix_pages null and prefix_len 0 without
+// a shared prefix.
+int fwd_paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+                   const int* page_table, const int* seq_lens, const int* cu_q,
+                   const int* prefix_pages, int prefix_len, int T, int B, int Hq, int Hkv, int d,
+                   long long q_stride, int num_pages, int page_size, int max_pages, int max_q,
+                   int causal, float scale, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  if (!q || !k_pages || !v_pages || !o || !lse || !page_table || !seq_lens || !cu_q)
+    return FA_ERR_ARG;
+  if (causal != 0 && causal != 1) return FA_ERR_ARG;
+  if (!std::isfinite(scale) || max_q < 1) return FA_ERR_ARG;
+  PagedParams p;
+  int rc = paged_shape(T, B, Hq, Hkv, d, num_pages, page_size, max_pages, &p.page_shift);
+  if (rc != FA_OK) return rc;
+  if (Hq % Hkv != 0 || Hq / Hkv > 128) return FA_ERR_ARG;
+  if (!row_stride_ok(q_stride, Hq, d)) return FA_ERR_ARG;
+  if (prefix_pages &&
+      (prefix_len < page_size || prefix_len % page_size != 0 || prefix_len / page_size > max_pages))
+    return FA_ERR_ARG;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) ||
+      !aligned16(lse) || !aligned4(page_table) || !aligned4(seq_lens) || !aligned4(cu_q) ||
+      !aligned4(prefix_pages))
+    return FA_ERR_ALIGN;
+  const size_t need = fa_fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len);
+  if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+                   workspace_bytes < need))
+    return FA_ERR_WORKSPACE;
+  DeviceState* ds;
+  if ((rc = device_state(&ds)) != FA_OK) return rc;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
+  p.v_pages = static_cast<const __nv_bfloat16*>(v_pages);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.page_table = page_table;
+  p.seq_lens = seq_lens;
+  p.cu_q = cu_q;
+  p.prefix_pages = prefix_pages;
+  p.status = ds->status;
+  p.T = T;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.q_stride = q_stride;
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  p.prefix_len = prefix_len;
+  p.max_q = max_q;
+  p.causal = causal;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  return launch_fwd_paged(p, d, static_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 }  // namespace fa
@@ -478,6 +609,7 @@ const char* fa_status_string(int status) {
     case FA_ERR_LAUNCH: return "CUDA launch error";
     case FA_ERR_TIMEOUT: return "a kernel pipeline wait timed out";
     case FA_ERR_BOUNDS: return "a kernel computed an out-of-range index (bounds-checked build)";
+    case FA_ERR_PAGE: return "a paged cache's row range, length, position or page number is out of bounds";
     default: return "unknown status";
   }
 }
@@ -602,6 +734,45 @@ int fa_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* lse,
   if (rc != FA_OK) return rc;
   return fwd_fp8_quantized_impl(o, lse, B, H, N, d, causal, scale, hadamard, workspace,
                                 workspace_bytes, stream);
+}
+
+int fa_kv_append(const void* q, const void* k, const void* v, void* q_out, void* k_pages,
+                 void* v_pages, const int* page_table, const int* seq_lens, const int* cu_q,
+                 const float* rope, int T, int B, int Hq, int Hkv, int d, long long q_stride,
+                 long long k_stride, long long v_stride, long long q_out_stride, int num_pages,
+                 int page_size, int max_pages, int rope_dim, int rope_len, int interleaved,
+                 void* stream) {
+  return kv_append_impl(q, k, v, q_out, k_pages, v_pages, page_table, seq_lens, cu_q, rope, T, B,
+                        Hq, Hkv, d, q_stride, k_stride, v_stride, q_out_stride, num_pages,
+                        page_size, max_pages, rope_dim, rope_len, interleaved, stream);
+}
+
+size_t fa_fwd_paged_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_q,
+                                   int prefix_len) {
+  (void)T, (void)B, (void)Hq, (void)Hkv, (void)d, (void)max_q, (void)prefix_len;
+  return 0;
+}
+
+int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+                 const int* page_table, const int* seq_lens, const int* cu_q, int T, int B, int Hq,
+                 int Hkv, int d, long long q_stride, int num_pages, int page_size, int max_pages,
+                 int max_q, int causal, float scale, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+  return fwd_paged_impl(q, k_pages, v_pages, o, lse, page_table, seq_lens, cu_q, nullptr, 0, T, B,
+                        Hq, Hkv, d, q_stride, num_pages, page_size, max_pages, max_q, causal,
+                        scale, workspace, workspace_bytes, stream);
+}
+
+int fa_fwd_paged_prefix(const void* q, const void* k_pages, const void* v_pages, void* o,
+                        float* lse, const int* page_table, const int* seq_lens, const int* cu_q,
+                        const int* prefix_pages, int prefix_len, int T, int B, int Hq, int Hkv,
+                        int d, long long q_stride, int num_pages, int page_size, int max_pages,
+                        int max_q, int causal, float scale, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  if (!prefix_pages) return FA_ERR_ARG;
+  return fwd_paged_impl(q, k_pages, v_pages, o, lse, page_table, seq_lens, cu_q, prefix_pages,
+                        prefix_len, T, B, Hq, Hkv, d, q_stride, num_pages, page_size, max_pages,
+                        max_q, causal, scale, workspace, workspace_bytes, stream);
 }
 
 int fa_device_status(void* stream, int* site) {

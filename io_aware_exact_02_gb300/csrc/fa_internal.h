@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -210,6 +211,48 @@ inline Fp8Workspace fp8_workspace_layout(long long BH, int N, int d) {
 // multiplied by the 128 x 128 Sylvester Hadamard matrix.
 int launch_fp8_quantize(const void* q, const void* k, const void* v, int BH, int N, int hadamard,
                         char* ws, const Fp8Workspace& layout, cudaStream_t stream);
+
+// The paged key/value cache (fa_kv_append, fa_fwd_paged): packed rows
+// [T][heads][d], pages [num_pages][Hkv][page_size][d].
+struct KvAppendParams {
+  const __nv_bfloat16* q;  // null: no queries
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  __nv_bfloat16* q_out;
+  __nv_bfloat16* k_pages;
+  __nv_bfloat16* v_pages;
+  const int* page_table;  // [B][max_pages]
+  const int* seq_lens;    // [B], new tokens included
+  const int* cu_q;        // [B + 1]
+  const float* rope;      // [rope_len][rope_dim]: cosines, then sines (rope_dim / 2 each)
+  int* status;
+  int T, B, Hq, Hkv;
+  long long q_stride, k_stride, v_stride, q_out_stride;  // elements between rows
+  int num_pages, page_size, page_shift, max_pages;
+  int rope_dim, rope_len, interleaved;
+};
+int launch_kv_append(const KvAppendParams& p, int d, cudaStream_t stream);
+
+struct PagedParams {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k_pages;
+  const __nv_bfloat16* v_pages;
+  __nv_bfloat16* o;  // [T][Hq][d]
+  float* lse;        // [T][Hq]
+  const int* page_table;
+  const int* seq_lens;
+  const int* cu_q;
+  const int* prefix_pages;  // null: no shared prefix
+  int* status;
+  int T, B, Hq, Hkv, G;
+  long long q_stride;
+  int num_pages, page_size, page_shift, max_pages;
+  int prefix_len;
+  int max_q;
+  int causal;
+  float scale_log2;
+};
+int launch_fwd_paged(const PagedParams& p, int d, cudaStream_t stream);
 
 // A rank-3 tensor map over a [BH][rows][inner] array of bytes: box
 // (128, 128, 1), 128-byte swizzle, zero fill outside.

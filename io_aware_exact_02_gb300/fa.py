@@ -34,12 +34,14 @@ FA_ERR_DEVICE = -5
 FA_ERR_LAUNCH = -6
 FA_ERR_TIMEOUT = -7
 FA_ERR_BOUNDS = -8
+FA_ERR_PAGE = -9
 
 # Size of the static scratch array fa_bwd_noalloc uses (FA_NOALLOC_SCRATCH_BYTES).
 FA_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 # Every symbol include/fa.h declares, with (restype, argtypes).
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll = ctypes.c_longlong
 _ip = ctypes.POINTER(ctypes.c_int)
 SIGNATURES = {
     "fa_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp]),
@@ -62,6 +64,10 @@ SIGNATURES = {
     "fa_fp8_quantize": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _sz, _vp]),
     "fa_fwd_fp8_quantized": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _f, _i, _vp, _sz, _vp]),
     "fa_fwd_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _i, _vp, _sz, _vp]),
+    "fa_kv_append": (_i, [_vp] * 10 + [_i] * 5 + [_ll] * 4 + [_i] * 6 + [_vp]),
+    "fa_fwd_paged_workspace_size": (_sz, [_i] * 7),
+    "fa_fwd_paged": (_i, [_vp] * 8 + [_i] * 5 + [_ll] + [_i] * 5 + [_f, _vp, _sz, _vp]),
+    "fa_fwd_paged_prefix": (_i, [_vp] * 9 + [_i] * 6 + [_ll] + [_i] * 5 + [_f, _vp, _sz, _vp]),
     "fa_device_status": (_i, [_vp, _ip]),
     "fa_selftest_timeout": (_i, [_i, _vp]),
     "fa_checks_enabled": (_i, []),
@@ -408,6 +414,150 @@ def fwd_fp8(q, k, v, causal: bool = False, scale: float | None = None, hadamard:
                                nbytes, _stream_of(q))
     _check("fa_fwd_fp8", rc)
     return out, lse
+
+
+def rope_table(length: int, rope_dim: int, base: float = 10000.0, device="cuda"):
+    """The rotation table kv_append reads: (length, rope_dim) fp32, row p the
+    cosines then the sines of the angles p * base**(-2i / rope_dim), computed
+    in fp64.  Any other table of that layout serves as well."""
+    half = rope_dim // 2
+    freq = float(base) ** (-torch.arange(half, dtype=torch.float64, device=device) / half)
+    angle = torch.arange(length, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).to(torch.float32)
+
+
+def _check_rows(name, t, T, H, d):
+    """Packed rows (T, H, d) bf16, heads contiguous; returns the row stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != torch.bfloat16:
+        raise ValueError("%s must be torch.bfloat16" % name)
+    if tuple(t.shape) != (T, H, d):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (T, H, d)))
+    stride = t.stride()
+    if stride[2] != 1 or (H > 1 and stride[1] != d):
+        raise ValueError("%s must have contiguous heads" % name)
+    return stride[0] if T > 1 else max(stride[0], H * d)
+
+
+def _check_cache(k_pages, v_pages, page_table, seq_lens, cu_q):
+    """The cache and its tables; returns (num_pages, Hkv, page_size, d, B, max_pages)."""
+    shape = tuple(k_pages.shape)
+    if len(shape) != 4:
+        raise ValueError("k_pages must have shape (num_pages, Hkv, page_size, d)")
+    _check_qkv("k_pages", k_pages, shape)
+    _check_qkv("v_pages", v_pages, shape)
+    B = seq_lens.shape[0]
+    if page_table.dim() != 2:
+        raise ValueError("page_table must have shape (B, max_pages)")
+    _check_qkv("page_table", page_table, (B, page_table.shape[1]), torch.int32)
+    _check_qkv("seq_lens", seq_lens, (B,), torch.int32)
+    _check_qkv("cu_q", cu_q, (B + 1,), torch.int32)
+    return shape + (B, page_table.shape[1])
+
+
+def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_q, q=None, q_out=None, rope=None,
+              interleaved: bool = False):
+    """Append packed rows k, v (T, Hkv, d) to the paged cache, rotating keys
+    (and q, if given) by the table ``rope`` (see rope_table; None: no
+    rotation).  Sequence b's rows are cu_q[b] .. cu_q[b+1]-1 and end at
+    position seq_lens[b]-1.  Returns the rotated queries (``q_out``,
+    allocated if not given; it may be ``q``), or None without q."""
+    num_pages, Hkv, page_size, d, B, max_pages = _check_cache(k_pages, v_pages, page_table,
+                                                              seq_lens, cu_q)
+    T = k.shape[0]
+    ks, vs = _check_rows("k", k, T, Hkv, d), _check_rows("v", v, T, Hkv, d)
+    Hq, qs, qos = 0, 0, 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must have shape (T, Hq, d)")
+        Hq = q.shape[1]
+        qs = _check_rows("q", q, T, Hq, d)
+        if q_out is None:  # rows of no sequence are not written
+            q_out = torch.zeros((T, Hq, d), dtype=q.dtype, device=q.device)
+        qos = _check_rows("q_out", q_out, T, Hq, d)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    rope_len = rope_dim = 0
+    if rope is not None:
+        if rope.dim() != 2:
+            raise ValueError("rope must have shape (length, rope_dim)")
+        rope_len, rope_dim = rope.shape
+        _check_qkv("rope", rope, (rope_len, rope_dim), torch.float32)
+    with _on_device(k, v=v, q=q, q_out=q_out, k_pages=k_pages, v_pages=v_pages,
+                    page_table=page_table, seq_lens=seq_lens, cu_q=cu_q, rope=rope):
+        rc = load().fa_kv_append(
+            None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            None if q is None else q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+            page_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(),
+            None if rope is None else rope.data_ptr(), T, B, Hq, Hkv, d, qs, ks, vs, qos,
+            num_pages, page_size, max_pages, rope_dim, rope_len, int(bool(interleaved)),
+            _stream_of(k))
+    _check("fa_kv_append", rc)
+    return q_out
+
+
+def fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len=0) -> int:
+    return int(load().fa_fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len))
+
+
+def _fwd_paged(fn, q, k_pages, v_pages, page_table, seq_lens, cu_q, prefix_pages, max_q, causal,
+               scale, out, lse, workspace):
+    num_pages, Hkv, page_size, d, B, max_pages = _check_cache(k_pages, v_pages, page_table,
+                                                              seq_lens, cu_q)
+    if q.dim() != 3:
+        raise ValueError("q must have shape (T, Hq, d)")
+    T, Hq, _ = q.shape
+    qs = _check_rows("q", q, T, Hq, d)
+    scale = default_scale(d) if scale is None else float(scale)
+    max_q = T if max_q is None else int(max_q)
+    if out is None:  # rows of no sequence are not written
+        out = torch.zeros((T, Hq, d), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.full((T, Hq), -math.inf, dtype=torch.float32, device=q.device)
+    _check_qkv("out", out, (T, Hq, d))
+    _check_qkv("lse", lse, (T, Hq), torch.float32)
+    prefix_len = 0
+    if prefix_pages is not None:
+        _check_qkv("prefix_pages", prefix_pages, (prefix_pages.numel(),), torch.int32)
+        prefix_len = prefix_pages.numel() * page_size
+    need = fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws_ptr = workspace.data_ptr() if workspace is not None else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    prefix = () if prefix_pages is None else (prefix_pages.data_ptr(), prefix_len)
+    with _on_device(q, k_pages=k_pages, v_pages=v_pages, page_table=page_table,
+                    seq_lens=seq_lens, cu_q=cu_q, prefix_pages=prefix_pages, out=out, lse=lse,
+                    workspace=workspace):
+        rc = getattr(load(), fn)(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
+            page_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), *prefix, T, B, Hq, Hkv,
+            d, qs, num_pages, page_size, max_pages, max_q, int(bool(causal)),
+            ctypes.c_float(scale), ws_ptr, ws_bytes, _stream_of(q))
+    _check(fn, rc)
+    return out, lse
+
+
+def fwd_paged(q, k_pages, v_pages, page_table, seq_lens, cu_q, max_q=None, causal: bool = True,
+              scale: float | None = None, out=None, lse=None, workspace=None):
+    """Attention of packed query rows q (T, Hq, d) over the paged cache: the
+    rows of sequence b are its last cu_q[b+1] - cu_q[b] positions of
+    seq_lens[b].  ``max_q``: the most rows of a sequence (None: T), which
+    decides the kernel and never the result.  Returns (o, lse), (T, Hq, d)
+    and (T, Hq)."""
+    return _fwd_paged("fa_fwd_paged", q, k_pages, v_pages, page_table, seq_lens, cu_q, None,
+                      max_q, causal, scale, out, lse, workspace)
+
+
+def fwd_paged_prefix(q, k_pages, v_pages, page_table, seq_lens, cu_q, prefix_pages, max_q=None,
+                     causal: bool = True, scale: float | None = None, out=None, lse=None,
+                     workspace=None):
+    """fwd_paged for a batch whose sequences all begin with the keys of
+    ``prefix_pages`` (int32, in order), whose attention is computed once for
+    all rows.  Lengths and positions count the prefix.  Returns (o, lse)."""
+    return _fwd_paged("fa_fwd_paged_prefix", q, k_pages, v_pages, page_table, seq_lens, cu_q,
+                      prefix_pages, max_q, causal, scale, out, lse, workspace)
 
 
 def device_status(stream=None):
