@@ -208,6 +208,21 @@ int make_tmap_bhnd_rows(const void* base, int BH, int N, int d, int box_rows, CU
   return r == CUDA_SUCCESS ? FA_OK : FA_ERR_ARG;
 }
 
+int make_tmap_rows(const void* base, int heads, int T, long long stride, int d, int box_heads,
+                   int box_rows, CUtensorMap* out) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  int rc = get_encode(&enc);
+  if (rc != FA_OK) return rc;
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)T};
+  cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                   strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_ARG;
+}
+
 // The self test's kernel: one thread waits on a barrier nothing arrives on
 // until the limit passes, then records the timeout like any kernel wait.
 __global__ void fa_selftest_timeout_kernel(int* status, unsigned long long limit_ns) {
@@ -585,6 +600,8 @@ int fwd_paged_impl(const void* q, const void* k_pages, const void* v_pages, void
   p.max_q = max_q;
   p.causal = causal;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.ctas = ds->sm_count < kPagedMaxCtas ? ds->sm_count : kPagedMaxCtas;
+  p.workspace = static_cast<char*>(workspace);
   return launch_fwd_paged(p, d, static_cast<cudaStream_t>(stream));
 }
 
@@ -749,8 +766,10 @@ int fa_kv_append(const void* q, const void* k, const void* v, void* q_out, void*
 
 size_t fa_fwd_paged_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_q,
                                    int prefix_len) {
-  (void)T, (void)B, (void)Hq, (void)Hkv, (void)d, (void)max_q, (void)prefix_len;
-  return 0;
+  int shift;
+  if (paged_shape(T, B, Hq, Hkv, d, 1, 16, 1, &shift) != FA_OK) return 0;
+  if (Hq % Hkv != 0 || Hq / Hkv > 128 || max_q < 1 || prefix_len < 0) return 0;
+  return paged_workspace_layout(T, Hq, d, paged_form(T, Hq / Hkv, max_q, prefix_len)).total;
 }
 
 int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,

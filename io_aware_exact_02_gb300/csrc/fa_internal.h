@@ -233,6 +233,13 @@ struct KvAppendParams {
 };
 int launch_kv_append(const KvAppendParams& p, int d, cudaStream_t stream);
 
+// CTAs that share a call's work at most (one per SM; GB300 has 152), which
+// sizes the workspace without a device.
+constexpr int kPagedMaxCtas = 160;
+// Most query rows of a unit in the decode kernel and rows of a unit in the
+// prompt kernel (two 128-row Q tiles).
+constexpr int kPagedDecodeRows = 64;
+
 struct PagedParams {
   const __nv_bfloat16* q;
   const __nv_bfloat16* k_pages;
@@ -251,8 +258,58 @@ struct PagedParams {
   int max_q;
   int causal;
   float scale_log2;
+  int ctas;         // persistent CTAs
+  char* workspace;  // PagedWorkspace
 };
+
+// How a call runs: the rows of a unit in the attention of the sequences'
+// own keys and, with share, of the shared prefix (rows of the whole batch).
+struct PagedForm {
+  int rows;         // 16, 32, 64: the decode kernel; 256: the prompt kernel
+  int share;        // the prefix is attended once for the batch
+  int prefix_rows;
+};
+inline int paged_unit_rows(long long rows) {
+  return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= kPagedDecodeRows ? 64 : kPairRows));
+}
+inline PagedForm paged_form(int T, int G, int max_q, int prefix_len) {
+  PagedForm f;
+  f.rows = paged_unit_rows((long long)(max_q < T ? max_q : T) * G);
+  f.share = prefix_len > 0 ? 1 : 0;
+  f.prefix_rows = paged_unit_rows((long long)T * G);
+  return f;
+}
+
+// Byte offsets of the paged forward's workspace, 256-byte aligned: the split
+// records of the CTAs, their partial results (two slots each: fp32 O rows,
+// then the rows' logsumexp), and with a shared prefix its results, fp32
+// [T][Hq][d] and [T][Hq].
+struct PagedWorkspace {
+  size_t rec, slot_o, slot_lse, pre_o, pre_lse, total;
+};
+constexpr size_t kPagedRecBytes = 64;
+inline PagedWorkspace paged_workspace_layout(int T, int Hq, int d, const PagedForm& f) {
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  const int rows = f.share && f.prefix_rows > f.rows ? f.prefix_rows : f.rows;
+  const size_t slots = (size_t)kPagedMaxCtas * 2 * (size_t)rows;
+  PagedWorkspace w;
+  w.rec = 0;
+  w.slot_o = up(kPagedMaxCtas * kPagedRecBytes);
+  w.slot_lse = w.slot_o + up(slots * (size_t)d * sizeof(float));
+  w.pre_o = w.slot_lse + up(slots * sizeof(float));
+  const size_t pre = f.share ? (size_t)T * (size_t)Hq : 0;
+  w.pre_lse = w.pre_o + up(pre * (size_t)d * sizeof(float));
+  w.total = w.pre_lse + up(pre * sizeof(float));
+  return w;
+}
+
 int launch_fwd_paged(const PagedParams& p, int d, cudaStream_t stream);
+
+// A rank-3 tensor map over packed rows [T][heads][d] bf16 with `stride`
+// elements between rows: dims (d, heads, T), box (64, box_heads, box_rows),
+// 128-byte swizzle, zero fill outside.
+int make_tmap_rows(const void* base, int heads, int T, long long stride, int d, int box_heads,
+                   int box_rows, CUtensorMap* out);
 
 // A rank-3 tensor map over a [BH][rows][inner] array of bytes: box
 // (128, 128, 1), 128-byte swizzle, zero fill outside.

@@ -18,6 +18,16 @@ enum : int {
   kSitePagedPosition,    // a new token's position outside the table (or the rope table)
   kSitePagedPage         // a page number outside [0, num_pages)
 };
+// Wait sites of the paged kernels.
+enum : int {
+  kSitePgQFull = 311, kSitePgQEmpty, kSitePgKvFull, kSitePgKvEmpty, kSitePgSFull, kSitePgPFull,
+  kSitePgPHalf, kSitePgPvDone, kSitePgOFull, kSitePgOEmpty, kSitePgItemFull, kSitePgItemEmpty
+};
+// Bounds checks of the checked build.
+enum : int {
+  kChkPgItem = 1301,  // a unit's rows or head
+  kChkPgRow           // an output row
+};
 
 struct PagedRow {
   int b;    // the row's sequence, -1: none (padding, or bad tables)
@@ -57,6 +67,353 @@ __device__ __forceinline__ PagedRow paged_row(const int* cu_q, const int* seq_le
   r.b = lo;
   r.pos = seq_lens[lo] - (t1 - t);
   return r;
+}
+
+// ------------------------------------------------------------------ the plan
+//
+// The work of a call is a list of units: (sequence, key/value head, a run of
+// query tokens) in that order, a unit's rows being its tokens' G query heads.
+// A unit costs its number of 128-key tiles (one at least), and the list's
+// tiles are dealt to the CTAs in equal contiguous ranges, whatever the
+// lengths: a CTA's first and last unit may be shared with its neighbours, and
+// each of the parts leaves its normalised fp32 O and logsumexp in a slot of
+// the workspace (slot 0 of a CTA: its first segment, slot 1: its last) that
+// the merge kernel joins in list order; so the result does not depend on
+// timing.  Every CTA derives its range from the tables itself: no launch
+// needs the lengths on the host.
+
+// The phase of a call a kernel runs.
+struct PagedPhase {
+  int whole_batch;     // 1: the shared prefix, attended by the rows of the whole batch
+  int key0;            // the first key attended (prefix_len after a shared prefix)
+  int unit_tokens;     // query tokens of a unit
+  int tile_tokens;     // query tokens of a Q tile (decode: the unit's)
+  int slot_rows;       // rows of a slot: 16 .. 64, or 256
+  char* rec;           // PagedRec per CTA
+  float* slot_o;       // [CTA][2][slot_rows][d]
+  float* slot_lse;     // [CTA][2][slot_rows], log2 units
+  const float* pre_o;  // results to merge in ([T][Hq][d], [T][Hq], log2 units), or null
+  const float* pre_lse;
+  float* out_o;        // fp32 results instead of o and lse, or null
+  float* out_lse;
+};
+
+// What the merge kernel needs to know of a CTA's first unit.
+struct PagedRec {
+  long long total;       // tiles in the list
+  long long unit_start;  // the unit's first tile in the list
+  long long unit_end;
+  int split;             // the unit began in an earlier CTA
+  int tok0, ntok, h;
+};
+static_assert(sizeof(PagedRec) <= kPagedRecBytes, "record size");
+
+struct PagedSeq {
+  int t0, n, len;  // first row, new tokens, keys
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, const PagedPhase& ph, int b) {
+  PagedSeq s;
+  if (ph.whole_batch) {
+    s.t0 = 0;
+    s.n = p.T;
+    s.len = p.prefix_len;
+    return s;
+  }
+  const int t0 = p.cu_q[b], t1 = p.cu_q[b + 1];
+  s.t0 = t0;
+  s.n = t1 - t0;
+  s.len = p.seq_lens[b];
+  int abort_flag = 0;
+  if (t0 < 0 || t1 < t0 || t1 > p.T) {
+    report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedRows);
+    s.t0 = s.n = 0;
+  }
+  if (s.n > 0 && (s.len < 0 || s.len > (p.max_pages << p.page_shift))) {
+    report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedLength);
+    s.len = s.len < 0 ? 0 : p.max_pages << p.page_shift;
+  }
+  return s;
+}
+
+// Keys [key0, unit_hi) concern the i-th unit of a sequence's head.
+__device__ __forceinline__ int paged_unit_hi(const PagedParams& p, const PagedPhase& ph,
+                                             const PagedSeq& s, int i) {
+  if (ph.whole_batch || !p.causal) return s.len;
+  const int e = min((i + 1) * ph.unit_tokens, s.n);
+  return max(s.len - s.n + e, 0);
+}
+__device__ __forceinline__ int paged_unit_tiles(const PagedParams& p, const PagedPhase& ph,
+                                                const PagedSeq& s, int i) {
+  const int x = paged_unit_hi(p, ph, s, i) - ph.key0;
+  return x <= 0 ? 0 : (x + kTile - 1) / kTile;
+}
+__device__ __forceinline__ int paged_units(const PagedPhase& ph, const PagedSeq& s) {
+  return (s.n + ph.unit_tokens - 1) / ph.unit_tokens;
+}
+// Tiles of one head of a sequence.
+__device__ __forceinline__ long long paged_head_cost(const PagedParams& p, const PagedPhase& ph,
+                                                     const PagedSeq& s) {
+  const int R = paged_units(ph, s);
+  if (R == 0) return 0;
+  if (!p.causal || ph.whole_batch) return (long long)R * max(1, paged_unit_tiles(p, ph, s, 0));
+  long long c = 0;
+  for (int i = 0; i < R; ++i) c += max(1, paged_unit_tiles(p, ph, s, i));
+  return c;
+}
+
+// CTA c's range of the list is [paged_lo(c), paged_lo(c + 1)); with fewer
+// tiles than CTAs the first `total` CTAs take one each.
+__host__ __device__ inline long long paged_active(long long total, int ctas) {
+  return total < ctas ? total : ctas;
+}
+__host__ __device__ inline long long paged_lo(long long total, long long active, long long c) {
+  return c >= active ? total : total * c / active;
+}
+// The CTA whose range holds tile x of the list.
+__host__ __device__ inline long long paged_owner(long long total, long long active, long long x) {
+  return ((x + 1) * active + total - 1) / total - 1;
+}
+
+// One segment of a unit, as the producer hands it to the other roles.
+struct PagedItem {
+  int end;        // 1: no more items
+  int nj;         // key tiles (0: the unit has no keys)
+  int b, h;
+  int tok0, ntok; // the unit's rows: packed rows tok0 .. tok0 + ntok - 1
+  int key;        // the segment's first key
+  int k_hi;       // the unit's keys end here
+  int pos0;       // row tok0's position (whole_batch: unused)
+  int len;
+  int slot;       // -1: the whole unit, written straight to the output; else 0 or 1
+  int first;      // the segment begins the unit (and merges pre_o in)
+};
+
+struct PagedScan {
+  long long warp_sum[32];
+  long long total, found_excl;
+  int found_b;
+};
+
+// A CTA's walk along its range of the list.
+struct PagedWalk {
+  long long g, hi, total;
+  int b, h, i, tile, units;
+  PagedSeq s;
+  bool first;
+};
+
+// All threads of the CTA: the list's length and the sequence that holds the
+// CTA's first tile.
+__device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhase& ph,
+                                           PagedScan& sc, PagedWalk& w) {
+  const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31, nw = nt >> 5;
+  const int B = ph.whole_batch ? 1 : p.B;
+  auto cost = [&](int b) -> long long {
+    if (b >= B) return 0;
+    const PagedSeq s = paged_seq(p, ph, b);
+    return paged_head_cost(p, ph, s) * p.Hkv;
+  };
+  const long long mine = cost(tid);
+  long long sum = mine;
+  for (int b = tid + nt; b < B; b += nt) sum += cost(b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) sc.warp_sum[warp] = sum;
+  __syncthreads();
+  long long total = 0;
+  for (int i = 0; i < nw; ++i) total += sc.warp_sum[i];
+  const long long active = paged_active(total, gridDim.x);
+  const long long lo = paged_lo(total, active, blockIdx.x);
+  w.total = total;
+  w.g = lo;
+  w.hi = paged_lo(total, active, (long long)blockIdx.x + 1);
+  w.first = true;
+  if (w.g >= w.hi) return;  // idle CTA; uniform in the CTA
+  long long run = 0;
+  for (int b0 = 0; b0 < B; b0 += nt) {
+    const long long c = b0 == 0 ? mine : cost(b0 + tid);
+    long long inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    __syncthreads();  // warp_sum was read
+    if (lane == 31) sc.warp_sum[warp] = inc;
+    __syncthreads();
+    long long before = run, chunk = 0;
+    for (int i = 0; i < nw; ++i) {
+      if (i < warp) before += sc.warp_sum[i];
+      chunk += sc.warp_sum[i];
+    }
+    const long long excl = before + inc - c;
+    if (c > 0 && excl <= lo && lo < excl + c) {
+      sc.found_b = b0 + tid;
+      sc.found_excl = excl;
+    }
+    run += chunk;
+    if (lo < run) break;
+  }
+  __syncthreads();
+  w.b = sc.found_b;
+  w.s = paged_seq(p, ph, w.b);
+  w.units = paged_units(ph, w.s);
+  long long off = lo - sc.found_excl;
+  const long long head = paged_head_cost(p, ph, w.s);
+  w.h = (int)(off / head);
+  off -= w.h * head;
+  w.i = 0;
+  if (!p.causal || ph.whole_batch) {  // units of equal cost
+    const int c = max(1, paged_unit_tiles(p, ph, w.s, 0));
+    w.i = (int)(off / c);
+    off -= (long long)w.i * c;
+  } else {
+    for (;; ++w.i) {
+      const int c = max(1, paged_unit_tiles(p, ph, w.s, w.i));
+      if (off < c) break;
+      off -= c;
+    }
+  }
+  w.tile = (int)off;
+}
+
+// The walk's next segment.
+__device__ __forceinline__ PagedItem paged_next(const PagedParams& p, const PagedPhase& ph,
+                                                PagedWalk& w) {
+  PagedItem it;
+  it.end = w.g >= w.hi ? 1 : 0;
+  if (it.end) return it;
+  const int tiles = paged_unit_tiles(p, ph, w.s, w.i), cost = max(1, tiles);
+  const int take = (int)min((long long)(cost - w.tile), w.hi - w.g);
+  it.nj = tiles == 0 ? 0 : take;
+  it.b = w.b;
+  it.h = w.h;
+  it.tok0 = w.s.t0 + w.i * ph.unit_tokens;
+  it.ntok = min(ph.unit_tokens, w.s.n - w.i * ph.unit_tokens);
+  it.key = ph.key0 + w.tile * kTile;
+  it.k_hi = paged_unit_hi(p, ph, w.s, w.i);
+  it.pos0 = w.s.len - w.s.n + w.i * ph.unit_tokens;
+  it.len = w.s.len;
+  it.slot = take == cost ? -1 : (w.first ? 0 : 1);
+  it.first = w.tile == 0;
+  if (w.first && lane_id() == 0) {
+    PagedRec r;
+    r.total = w.total;
+    r.unit_start = w.g - w.tile;
+    r.unit_end = r.unit_start + cost;
+    r.split = w.tile > 0;
+    r.tok0 = it.tok0;
+    r.ntok = it.ntok;
+    r.h = it.h;
+    *reinterpret_cast<PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes) = r;
+  }
+  w.first = false;
+  w.g += take;
+  w.tile += take;
+  if (w.tile == cost && w.g < w.hi) {
+    w.tile = 0;
+    if (++w.i == w.units) {
+      w.i = 0;
+      if (++w.h == p.Hkv) {
+        w.h = 0;
+        do {  // the range's end bounds the walk: a later sequence has tiles
+          ++w.b;
+          w.s = paged_seq(p, ph, w.b);
+        } while (w.s.n == 0 && w.b + 1 < p.B);
+        w.units = paged_units(ph, w.s);
+      }
+    }
+  }
+  return it;
+}
+
+// Keys row t of the batch sees of the shared prefix.
+__device__ __forceinline__ int paged_prefix_limit(const PagedParams& p, int t) {
+  if (t >= p.T) return 0;
+  // The largest b with cu_q[b] <= t, b = t first: one token per sequence.
+  int lo = -1, hi = p.B;  // cu_q[lo] <= t < cu_q[hi], as far as known
+  if (t < p.B && p.cu_q[t] <= t) {
+    lo = t;
+    if (p.cu_q[t + 1] > t) hi = t + 1;
+  }
+  if (lo < 0 && p.cu_q[0] > t) return 0;
+  if (p.cu_q[p.B] <= t) return 0;  // a padding row
+  if (lo < 0) lo = 0;
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if (p.cu_q[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  const int len = p.seq_lens[lo];
+  const int lim = p.causal ? len - (p.cu_q[lo + 1] - t) + 1 : len;
+  return max(0, min(lim, p.prefix_len));
+}
+
+// The page numbers of a segment, 32 at a time in the lanes of the producer
+// warp, the next 32 in flight while these are used.
+struct PagedPages {
+  const int* list;  // page numbers from the sequence's first page on
+  int n;            // pages of the unit's keys end here
+  int prefix_n;     // pages below it come from the prefix's list
+  const int* prefix;
+  int base, cur, next;
+};
+__device__ __forceinline__ int paged_page_at(const PagedParams& p, const PagedPages& g, int i) {
+  if (i >= g.n) return -1;  // past the unit's keys: read as zeros
+  const int id = i < g.prefix_n ? g.prefix[i] : g.list[i];
+  if (id < 0 || id >= p.num_pages) {
+    int abort_flag = 0;
+    report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
+    return -1;
+  }
+  return id;
+}
+__device__ __forceinline__ void paged_pages_begin(const PagedParams& p, const PagedPhase& ph,
+                                                  const PagedItem& it, PagedPages& g) {
+  g.list = p.page_table + (long long)it.b * p.max_pages;
+  g.prefix = p.prefix_pages;
+  g.prefix_n = p.prefix_len >> p.page_shift;
+  g.n = (it.k_hi + p.page_size - 1) >> p.page_shift;
+  g.base = it.key >> p.page_shift;
+  g.cur = paged_page_at(p, g, g.base + (int)lane_id());
+  g.next = paged_page_at(p, g, g.base + 32 + (int)lane_id());
+}
+// The page number of page i (uniform or not; all lanes call it), i at most
+// 31 past the last call's.
+__device__ __forceinline__ void paged_pages_advance(const PagedParams& p, PagedPages& g, int last) {
+  if (last >= g.base + 32) {
+    g.base += 32;
+    g.cur = g.next;
+    g.next = paged_page_at(p, g, g.base + 32 + (int)lane_id());
+  }
+}
+
+// The producer warp's loads of one 128-key tile of K or V: one box per page
+// (at most 128 rows) and 64 channels, a lane each.
+template <int D>
+__device__ __forceinline__ void paged_load_tile(const PagedParams& p, const CUtensorMap* map,
+                                                PagedPages& g, int h, int key, uint8_t* dst,
+                                                uint64_t* bar) {
+  const int lane = (int)lane_id();
+  const int rows = min(p.page_size, kTile);
+  const int per = kTile / rows;  // pages of the tile
+  const int first = key >> p.page_shift;
+  paged_pages_advance(p, g, first + per - 1);
+  if (lane == 0) mbar_arrive_expect_tx(bar, kTile * D * 2);
+  const int sub = lane & (per - 1), half = lane / per;
+  // A tile's pages may straddle the 32 at hand and the next ones only if
+  // its first page does: runs of `per` pages (a power of two) start at
+  // multiples of `per` past the segment's first.
+  const int id = __shfl_sync(0xffffffffu, g.cur, (first + sub - g.base) & 31);
+  __syncwarp();
+  if (half < D / 64) {
+    const int z = id < 0 ? p.num_pages * p.Hkv : id * p.Hkv + h;
+    tma_load_3d(dst + half * (kTile * 128) + sub * rows * 128, map, bar, half * 64,
+                key & (p.page_size - 1) & ~(rows - 1), z);
+  }
 }
 
 }  // namespace fa
