@@ -17,11 +17,16 @@
 // each thread keeping the sum of its own keys' probabilities until the unit
 // ends.  P goes to shared memory as the B operand of the second product.
 //
-// Warps: 0-3 compute (and write results), 4 producer (TMA: a lane per page
-// box), 5 issues the products.  K and V stream through one ring of 32 KB (d =
-// 128) tiles in the order K0 V0 K1 V1 ..., across units; S and P have two
-// buffers and O one per unit parity, so that the next tile's (and the next
-// unit's) S is there before this one's P is done.
+// Two compute warpgroups take the units in turn, so that one's ending (sums,
+// weights, O out of tensor memory, stores: about 2,500 cycles) runs beside the
+// other's tiles; with N = 64 each has half of the columns of every unit
+// instead, as a thread's registers hold no more.
+//
+// Warps: 0-3 and 4-7 compute (and write results), 8 producer (TMA: a lane per
+// page box), 9 issues the products, each as soon as its operands are there.
+// K and V stream through one ring of 32 KB (d = 128) tiles in the order K0 V0
+// K1 V1 ..., across units; four S buffers let S run ahead of P V, into the
+// next units.
 #include "fa_internal.h"
 #include "fa_paged.cuh"
 #include "fa_paged_launch.h"
@@ -33,37 +38,52 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kItemRing = 4;
-constexpr int kDecodeThreads = 192;
-constexpr int kCompute = 128;  // threads of the compute warps
+constexpr int kDecodeThreads = 320;
+constexpr int kCompute = 256;  // threads of the compute warps
+constexpr int kSBufs = 4;      // S buffers, shared out among the groups
+// A row's reference maximum before it has seen a key: finite, so that the
+// exponent of a masked score is -inf and not NaN.
+constexpr float kNoRef = -3.0e38f;
 
 template <int D, int N>
 struct DecodeCfg {
   static constexpr int kTileBytes = kTile * D * 2;
   // As many ring slots as the 227 KB allow beside Q and P.
   static constexpr int kStages =
-      D == 128 ? (N == 16 ? 6 : (N == 32 ? 5 : 4)) : (N == 64 ? 10 : 12);
-  static constexpr uint32_t kTmemCols = 4 * N;  // S twice, O twice
+      D == 128 ? (N == 16 ? 6 : (N == 32 ? 5 : 4)) : (N == 16 ? 12 : 10);
+  // The warpgroups split a unit's columns (else they take units in turn).
+  static constexpr bool kHalves = N == 64;
+  static constexpr int kCols = kHalves ? N / 2 : N;  // columns of a thread
+  static constexpr uint32_t kTmemCols = 8 * N;  // 4 S buffers, 2 O (a power of two)
   static __device__ __forceinline__ uint32_t col_s(int i) { return (uint32_t)i * N; }
-  static __device__ __forceinline__ uint32_t col_o(int i) { return (uint32_t)(2 + i) * N; }
+  // O of the units of parity i.
+  static __device__ __forceinline__ uint32_t col_o(int i) { return (uint32_t)(kSBufs + i) * N; }
+  // The threads that work on a unit together, and their named barrier.
+  static constexpr int kGroups = kHalves ? 1 : 2;
+  static constexpr int kGroup = kCompute / kGroups;
+  // A group's n-th tile uses its S buffer n % kSPer and its P buffer n % 2.
+  static constexpr int kSPer = kSBufs / kGroups, kPBufs = 2 * kGroups;
+  static __device__ __forceinline__ int barrier(int wg) { return kHalves ? 1 : 2 + wg; }
 };
 
 template <int D, int N>
 struct alignas(1024) DecodeSmem {
   uint8_t kv[DecodeCfg<D, N>::kStages][DecodeCfg<D, N>::kTileBytes];
-  uint8_t q[2][N * D * 2];    // [d / 64][N rows][128 B], 128B-swizzled
-  uint8_t pt[2][N * kTile * 2];  // P: [2 blocks of 64 keys][N rows][128 B], swizzled
+  uint8_t q[2][N * D * 2];       // [d / 64][N rows][128 B], 128B-swizzled
+  uint8_t pt[DecodeCfg<D, N>::kPBufs][N * kTile * 2];  // P: [2 blocks of 64 keys][N rows][128 B], swizzled
+  float4 top[2][N];              // column maxima of a warpgroup's four warps
+  float sum[2][4][N];            // column sums of a warpgroup's four warps
+  float ref[2][N];               // reference maxima of the unit
+  float f_own[2][N], f_pre[2][N];  // weights of O and of pre_o
+  int lim[2][N];                 // keys row n sees end here
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[DecodeCfg<D, N>::kStages], kv_empty[DecodeCfg<D, N>::kStages];
-  uint64_t s_full[2], p_full[2], pv_done[2];
-  uint64_t o_full[2], o_empty[2];
+  uint64_t s_full[kSBufs], p_full[DecodeCfg<D, N>::kPBufs], pv_done[DecodeCfg<D, N>::kPBufs];
+  uint64_t o_full[2];
   uint64_t item_full[kItemRing], item_empty[kItemRing];
   uint64_t drain;
   PagedItem item[kItemRing];
   PagedScan scan;
-  int lim[N];            // keys row n sees end here
-  float top[4][N];       // per compute warp: a tile's column maxima
-  float sum[4][N];       // and the unit's column sums
-  float f_own[N], f_pre[N], lse2[N];
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -77,58 +97,83 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
-// A vote of the 128 compute threads: true for all when true for any.  Also a
-// barrier among them.  Every compute thread reaches every vote, failed waits
-// or not: a failure is carried into the next vote.
-__device__ __forceinline__ bool compute_any(bool x) {
+// A vote of `threads` compute threads on named barrier `id`: true for all
+// when true for any.  Also a barrier among them.  Every thread of the group
+// reaches every vote, failed waits or not: a failure is carried into the next
+// vote.
+__device__ __forceinline__ bool vote_any(int id, int threads, bool x) {
   int r;
   asm volatile(
       "{\n\t.reg .pred P, Q;\n\t"
       "setp.ne.b32 P, %1, 0;\n\t"
-      "barrier.cta.red.or.pred Q, 1, 128, P;\n\t"
+      "barrier.cta.red.or.pred Q, %2, %3, P;\n\t"
       "selp.b32 %0, 1, 0, Q;\n\t}"
       : "=r"(r)
-      : "r"((int)x)
+      : "r"((int)x), "r"(id), "r"(threads)
       : "memory");
   return r != 0;
 }
 
 template <int N>
 __device__ __forceinline__ void load_cols(uint32_t addr, float (&x)[N]) {
-  if constexpr (N == 16) {
+  if constexpr (N == 8) {
+    uint32_t r[8];
+    tmem_ld8(addr, r);
+    tmem_wait_ld8(r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r[i]);
+  } else if constexpr (N == 16) {
     uint32_t r[16];
     tmem_ld16(addr, r);
     tmem_wait_ld16(r);
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
   } else {
+    static_assert(N == 32, "columns");
+    uint32_t r[32];
+    tmem_ld32(addr, r);
+    tmem_wait_ld(r);
 #pragma unroll
-    for (int c = 0; c < N / 32; ++c) {
-      uint32_t r[32];
-      tmem_ld32(addr + c * 32, r);
-      tmem_wait_ld(r);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[c * 32 + i] = __uint_as_float(r[i]);
-    }
+    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
   }
 }
 template <int N>
 __device__ __forceinline__ void store_cols(uint32_t addr, const float (&x)[N]) {
-  if constexpr (N == 16) {
-    uint32_t r[16];
+  uint32_t r[N];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(x[i]);
+  for (int i = 0; i < N; ++i) r[i] = __float_as_uint(x[i]);
+  if constexpr (N == 16)
     tmem_st16(addr, r);
-  } else {
+  else
+    tmem_st32(addr, r);
+  tmem_wait_st();
+}
+
+// Reduces each of N columns (16 or 32) over the warp's 32 lanes, halving the
+// columns a lane holds at every step (N shuffles in all, not 5 N).  Returns
+// the reduction of column col_of_lane<N>().
+template <int N>
+__device__ __forceinline__ int col_of_lane() {
+  return (int)lane_id() >> (N == 16 ? 1 : 0);
+}
+template <int N, class Op>
+__device__ __forceinline__ float reduce_cols(const float (&x)[N], Op op) {
+  float y[N];
 #pragma unroll
-    for (int c = 0; c < N / 32; ++c) {
-      uint32_t r[32];
+  for (int i = 0; i < N; ++i) y[i] = x[i];
+  const int lane = (int)lane_id();
+  int bit = 16;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(x[c * 32 + i]);
-      tmem_st32(addr + c * 32, r);
+  for (int h = N / 2; h >= 1; h >>= 1, bit >>= 1) {
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float keep = up ? y[i + h] : y[i], send = up ? y[i] : y[i + h];
+      y[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, bit));
     }
   }
-  tmem_wait_st();
+  if constexpr (N == 16) y[0] = op(y[0], __shfl_xor_sync(0xffffffffu, y[0], 1));
+  return y[0];
 }
 
 template <int D, int N>
@@ -138,31 +183,33 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                            const __grid_constant__ CUtensorMap tv, const PagedParams p,
                            const PagedPhase ph) {
   using Cfg = DecodeCfg<D, N>;
-  constexpr int S = Cfg::kStages;
+  constexpr int S = Cfg::kStages, NC = Cfg::kCols;
+  constexpr bool kHalves = Cfg::kHalves;
   extern __shared__ uint8_t smem_raw[];
   DecodeSmem<D, N>& sm = *reinterpret_cast<DecodeSmem<D, N>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abortf = &sm.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5;
-  constexpr int kWarpLoad = 4, kWarpMma = 5;
+  constexpr int kWarpLoad = 8, kWarpMma = 9;
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&sm.kv_full[s], 1);
       mbar_init(&sm.kv_empty[s], 1);
     }
+    for (int i = 0; i < kSBufs; ++i) mbar_init(&sm.s_full[i], 1);
+    for (int i = 0; i < Cfg::kPBufs; ++i) {
+      mbar_init(&sm.p_full[i], Cfg::kGroup);
+      mbar_init(&sm.pv_done[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 1);
       mbar_init(&sm.q_empty[i], 1);
-      mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], kCompute);
-      mbar_init(&sm.pv_done[i], 1);
       mbar_init(&sm.o_full[i], 1);
-      mbar_init(&sm.o_empty[i], kCompute);
     }
     for (int i = 0; i < kItemRing; ++i) {
       mbar_init(&sm.item_full[i], 1);
-      mbar_init(&sm.item_empty[i], 1 + 4);  // the issuing thread, four compute warps
+      mbar_init(&sm.item_empty[i], 1 + Cfg::kGroup / 32);  // the issuing thread, the group's warps
     }
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -186,29 +233,24 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  launch_dependents();
   wait_prior_grid();
   PagedWalk walk;
   paged_plan(p, ph, sm.scan, walk);
 
-  auto take_item = [&](int m, bool& ok) -> PagedItem {
-    const int slot = m % kItemRing;
-    PagedItem it;
-    it.end = 1;
-    if (ok) ok = mbar_wait(&sm.item_full[slot], (m / kItemRing) & 1, p.status, abortf, kSitePgItemFull);
-    if (ok) it = sm.item[slot];
-    return it;
-  };
-
   if (warp == kWarpLoad) {
     // ------------------------------------------------------------ producer
     const int lane = (int)lane_id();
-    int c = 0, n_q = 0;
+    int g = 0, n_q = 0;  // tiles and units loaded
     bool ok = true;
     if (walk.g >= walk.hi && lane == 0) {
       PagedRec r = {};
       r.total = walk.total;
       *reinterpret_cast<PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes) = r;
     }
+    const PagedBox box = paged_box<D>(p, lane);
+    // The warpgroups that take units in turn each find an end of the list.
+    int ends = kHalves ? 1 : 2;
     for (int m = 0; ok; ++m) {
       const int is = m % kItemRing;
       if (m >= kItemRing)
@@ -220,7 +262,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         sm.item[is] = it;
         mbar_arrive(&sm.item_full[is]);
       }
-      if (it.end) break;
+      if (it.end) {
+        if (--ends == 0) break;
+        continue;
+      }
       if (it.nj == 0) continue;
       PagedPages pages;
       paged_pages_begin(p, ph, it, pages);
@@ -235,23 +280,23 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           tma_load_3d(sm.q[qb] + h * (N * 128), &tq, &sm.q_full[qb], h * 64, it.h * p.G, it.tok0);
       }
       ++n_q;
-      for (int j = 0; j < it.nj && ok; ++j) {
-        for (int w = 0; w < 2; ++w) {
-          const int slot = c % S, use = c / S;
-          if (use > 0)
-            ok = mbar_wait(&sm.kv_empty[slot], (use - 1) & 1, p.status, abortf, kSitePgKvEmpty);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          paged_load_tile<D>(p, w == 0 ? &tk : &tv, pages, it.h, it.key + j * kTile, sm.kv[slot],
-                             &sm.kv_full[slot]);
-          ++c;
-        }
+      for (int j = 0; j < it.nj; ++j, ++g) {
+        // K into one slot of the ring, V into the next, once both are free.
+        const int ck = 2 * g, sk = ck % S, sv = (ck + 1) % S;
+        if (ck >= S)
+          ok = mbar_wait(&sm.kv_empty[sk], (ck / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
+        if (ok && ck + 1 >= S)
+          ok = mbar_wait(&sm.kv_empty[sv], ((ck + 1) / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        paged_load_pair<D>(p, box, &tk, &tv, pages, it.h, it.key + j * kTile, sm.kv[sk],
+                           &sm.kv_full[sk], sm.kv[sv], &sm.kv_full[sv]);
       }
     }
     if (!ok && lane == 0) {
       // Let the copies already issued land before the CTA exits.
       for (int i = n_q - 1; i >= 0 && i >= n_q - 2; --i) drain_wait(&sm.q_full[i & 1], (i >> 1) & 1);
-      for (int cc = c - 1; cc >= 0 && cc >= c - S; --cc)
+      for (int cc = 2 * g - 1; cc >= 0 && cc >= 2 * g - S; --cc)
         drain_wait(&sm.kv_full[cc % S], (cc / S) & 1);
     }
     __syncwarp();
@@ -260,103 +305,106 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     if (lane_id() == 0) {
       const uint32_t id_s = idesc_bf16(128, N, false, false);
       const uint32_t id_o = idesc_bf16(128, N, true, false);
-      bool ok = true;
-      int m = 0;                 // items read
-      int gs = 0, gp = 0;        // S and P V products issued, over all units
-      bool have = false, end = false;  // a unit whose S products are not all issued
-      int s_nj = 0, s_j = 0, s_n = -1; // that unit: tiles, tiles issued, its number
-      int p_nj = 0, p_j = 0, p_n = 0;  // the unit of the next P V product
-      // The next unit with keys, waiting for its record or only if it is there.
-      auto fetch = [&](bool wait) {
-        while (ok && !have && !end) {
-          const int slot = m % kItemRing;
-          if (!wait && !mbar_try_wait(smem_u32(&sm.item_full[slot]), (m / kItemRing) & 1)) return;
-          const PagedItem it = take_item(m, ok);
-          if (!ok) return;
-          mbar_arrive(&sm.item_empty[slot]);
-          ++m;
-          if (it.end) {
-            end = true;
-          } else if (it.nj > 0) {
+      int m = 0;                        // items read
+      int gs = 0, gp = 0;               // S and P V products issued, over all units
+      int ns[2] = {0, 0}, np[2] = {0, 0};  // and by group
+      bool have = false, end = false;   // have: a unit whose S products are not all issued
+      int s_nj = 0, s_j = 0, s_n = -1;  // that unit: tiles, tiles issued, its number
+      int s_m = 0, s_u = 0;             // its item's, its group
+      int p_nj = 0, p_j = 0, p_n = -1;  // the unit of the next P V product
+      int ob = 0, p_u = 0;              // its O, its group
+      int of_unit[8];                   // tiles and item parity of the units begun, by number % 8
+      uint32_t idle = 0;
+      unsigned long long t0 = 0;
+      for (;;) {
+        bool did = false;
+        // The next unit with keys.
+        if (!have && !end && mbar_test_wait(&sm.item_full[m % kItemRing], (m / kItemRing) & 1)) {
+          const PagedItem& it = sm.item[m % kItemRing];
+          end = it.end != 0;
+          if (!end && it.nj > 0) {
             have = true;
             s_nj = it.nj;
             s_j = 0;
+            s_m = m;
+            s_u = kHalves ? 0 : m & 1;
             ++s_n;
           }
+          mbar_arrive(&sm.item_empty[m % kItemRing]);
+          ++m;
+          did = true;
         }
-      };
-      auto issue_s = [&] {
-        const int qb = s_n & 1;
-        if (s_j == 0)
-          ok = mbar_wait(&sm.q_full[qb], (s_n >> 1) & 1, p.status, abortf, kSitePgQFull);
-        const int c = 2 * gs, slot = c % S;
-        if (ok) ok = mbar_wait(&sm.kv_full[slot], (c / S) & 1, p.status, abortf, kSitePgKvFull);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t kd = desc_here(sdesc_sw128(smem_u32(sm.kv[slot]), 16, 1024));
-        const uint64_t qd = desc_here(sdesc_sw128(smem_u32(sm.q[qb]), 16, 1024));
+        // S of the next tile: its K (and Q) has arrived and its buffer's last
+        // S has been read (that tile's P V is issued).
+        if (have && (s_u ? ns[1] - np[1] : ns[0] - np[0]) < Cfg::kSPer && mbar_test_wait(&sm.kv_full[(2 * gs) % S], ((2 * gs) / S) & 1) &&
+            (s_j > 0 || mbar_test_wait(&sm.q_full[s_n & 1], (s_n >> 1) & 1))) {
+          const int slot = (2 * gs) % S, qb = s_n & 1;
+          const int sb = s_u * Cfg::kSPer + (s_u ? ns[1]++ : ns[0]++) % Cfg::kSPer;
+          tc_fence_after();
+          const uint64_t kd = desc_here(sdesc_sw128(smem_u32(sm.kv[slot]), 16, 1024));
+          const uint64_t qd = desc_here(sdesc_sw128(smem_u32(sm.q[qb]), 16, 1024));
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + Cfg::col_s(gs & 1), desc_plus(kd, (kk >> 2) * (kTile * 128) + (kk & 3) * 32),
-                 desc_plus(qd, (kk >> 2) * (N * 128) + (kk & 3) * 32), id_s, kk > 0);
-        tc_commit(&sm.s_full[gs & 1]);
-        tc_commit(&sm.kv_empty[slot]);
-        ++gs;
-        if (++s_j == s_nj) {
-          tc_commit(&sm.q_empty[qb]);
-          have = false;
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + Cfg::col_s(sb), desc_plus(kd, (kk >> 2) * (kTile * 128) + (kk & 3) * 32),
+                   desc_plus(qd, (kk >> 2) * (N * 128) + (kk & 3) * 32), id_s, kk > 0);
+          tc_commit(&sm.s_full[sb]);
+          tc_commit(&sm.kv_empty[slot]);
+          if (s_j == 0) of_unit[s_n & 7] = 2 * s_nj + (s_m & 1);
+          ++gs;
+          if (++s_j == s_nj) {
+            tc_commit(&sm.q_empty[qb]);
+            have = false;
+          }
+          did = true;
         }
-      };
-      auto issue_pv = [&] {
-        const int ob = p_n & 1, pb = gp & 1;
-        const int c = 2 * gp + 1, slot = c % S;
-        ok = mbar_wait(&sm.p_full[pb], (gp >> 1) & 1, p.status, abortf, kSitePgPFull);
-        if (ok) ok = mbar_wait(&sm.kv_full[slot], (c / S) & 1, p.status, abortf, kSitePgKvFull);
-        if (ok && p_j == 0 && p_n >= 2)
-          ok = mbar_wait(&sm.o_empty[ob], ((p_n >> 1) - 1) & 1, p.status, abortf, kSitePgOEmpty);
-        if (!ok) return;
-        tc_fence_after();
-        // V^T: the tile's 64-channel blocks along M.  At d = 64 there is one
-        // block; the product's upper 64 rows repeat the tile 8 keys on and
-        // are never read.
-        const uint64_t vd =
-            desc_here(sdesc_sw128(smem_u32(sm.kv[slot]), D == 128 ? kTile * 128 : 1024, 1024));
-        const uint64_t pd = desc_here(sdesc_sw128(smem_u32(sm.pt[pb]), 16, 1024));
+        // P V of the oldest tile whose S is issued.
+        if (gp < gs) {
+          if (p_j == p_nj) {
+            ++p_n;
+            p_nj = of_unit[p_n & 7] >> 1;
+            ob = of_unit[p_n & 7] & 1;
+            p_u = kHalves ? 0 : ob;
+            p_j = 0;
+          }
+          // The unit's first product overwrites its O.  The group that wrote
+          // this P has by then read the O of the unit before in that place.
+          const int n = p_u ? np[1] : np[0], pb = 2 * p_u + (n & 1), c = 2 * gp + 1, slot = c % S;
+          if (mbar_test_wait(&sm.p_full[pb], (n >> 1) & 1) &&
+              mbar_test_wait(&sm.kv_full[slot], (c / S) & 1)) {
+            tc_fence_after();
+            // V^T: the tile's 64-channel blocks along M.  At d = 64 there is
+            // one block; the product's upper 64 rows repeat the tile 8 keys on
+            // and are never read.
+            const uint64_t vd =
+                desc_here(sdesc_sw128(smem_u32(sm.kv[slot]), D == 128 ? kTile * 128 : 1024, 1024));
+            const uint64_t pd = desc_here(sdesc_sw128(smem_u32(sm.pt[pb]), 16, 1024));
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_ss(tmem + Cfg::col_o(ob), desc_plus(vd, kk * 2048),
-                 desc_plus(pd, (kk >> 2) * (N * 128) + (kk & 3) * 32), id_o,
-                 (p_j > 0 || kk > 0) ? 1u : 0u);
-        tc_commit(&sm.pv_done[pb]);
-        tc_commit(&sm.kv_empty[slot]);
-        ++gp;
-        if (++p_j == p_nj) tc_commit(&sm.o_full[ob]);
-      };
-      // S runs one tile ahead of P V, into the next unit where it is known.
-      int q_nj[2] = {0, 0};  // tiles of the units by parity of their number
-      while (ok) {
-        if (gs == gp) fetch(true);
-        if (!ok) break;
-        if (gs == gp) {
-          if (!have) break;  // the list's end
-          q_nj[s_n & 1] = s_nj;
-          issue_s();
-          if (!ok) break;
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_ss(tmem + Cfg::col_o(ob), desc_plus(vd, kk * 2048),
+                     desc_plus(pd, (kk >> 2) * (N * 128) + (kk & 3) * 32), id_o,
+                     (p_j > 0 || kk > 0) ? 1u : 0u);
+            tc_commit(&sm.pv_done[pb]);
+            tc_commit(&sm.kv_empty[slot]);
+            ++gp;
+            p_u ? ++np[1] : ++np[0];
+            if (++p_j == p_nj) tc_commit(&sm.o_full[ob]);
+            did = true;
+          }
+        } else if (end && !have) {
+          break;
         }
-        if (gs == gp + 1) {
-          if (!have) fetch(false);
-          if (ok && have) {
-            q_nj[s_n & 1] = s_nj;
-            issue_s();
+        // Nothing was ready: give up after the time limit, or with the CTA.
+        if (did) {
+          idle = 0;
+        } else if ((++idle & 255u) == 0) {
+          if (*abortf) break;
+          const unsigned long long now = globaltimer_ns();
+          if (idle == 256) t0 = now;
+          if (now - t0 > kWaitTimeoutNs) {
+            report_timeout(p.status, abortf, kSitePgPFull);
+            break;
           }
         }
-        if (!ok) break;
-        if (p_j == p_nj) {  // the next unit's first product (its S is issued)
-          if (gp > 0) ++p_n;
-          p_nj = q_nj[p_n & 1];
-          p_j = 0;
-        }
-        issue_pv();
       }
       // Every product issued so far must finish before TMEM is released.
       tc_commit(&sm.drain);
@@ -365,120 +413,128 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ compute
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    const int lane = tid & 31;
-    const float ninf = __int_as_float(0xff800000);
-    const float c2 = p.scale_log2;
+    const int wg = warp >> 2, key_t = tid & 127, lane = tid & 31;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const float c2 = p.scale_log2, ninf = __int_as_float(0xff800000);
+    const int col0 = kHalves ? wg * NC : 0;  // this thread's columns of a unit
+    const int buf = kHalves ? 0 : wg;        // its group's copy of the shared arrays
+    const int bar = Cfg::barrier(wg);
+    const int row = kHalves ? tid : key_t;   // its row of a unit, if below N
     // This thread's place in a row of P: its key's 16-byte chunk (swizzled
     // with the row) and byte in it.
-    uint8_t* const pt0 = sm.pt[0] + (tid >> 6) * (N * 128) + (tid & 7) * 2;
-    const int pchunk = (tid & 63) >> 3;
+    uint8_t* const pt0 = sm.pt[2 * buf] + (key_t >> 6) * (N * 128) + col0 * 128 + (key_t & 7) * 2;
+    const int pchunk = (key_t & 63) >> 3;
+    // Row n of a unit is query head n % G of its token n / G.
+    const int row_tok = row / p.G, row_head = row % p.G;
+    const int tok_c = col0 / p.G, head_c = col0 % p.G;
     bool fail = false;
-    int g = 0, n_item = 0;
-    for (int m = 0;; ++m) {
-      bool ok = !fail;
-      const PagedItem it = take_item(m, ok);
-      fail = !ok;
+    int n_t = 0;             // tiles the group has had
+    int n_done[2] = {0, 0};  // units with keys, by the parity of their item
+    for (int m = kHalves ? 0 : wg;; m += Cfg::kGroups) {
+      PagedItem it;
+      it.end = 1;
+      it.nj = it.ntok = 0;
+      fail = !mbar_wait(&sm.item_full[m % kItemRing], (m / kItemRing) & 1, p.status, abortf,
+                        kSitePgItemFull);
+      if (!fail) it = sm.item[m % kItemRing];
       __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&sm.item_empty[m % kItemRing]);
+      if (!fail && lane == 0) mbar_arrive(&sm.item_empty[m % kItemRing]);
       const int rows = it.end ? 0 : it.ntok * p.G;
       if (!bound_ok(it.end || (it.tok0 >= 0 && it.tok0 + it.ntok <= p.T && rows <= N && it.h < p.Hkv),
                     p.status, abortf, kChkPgItem))
         fail = true;
-      // Keys of the unit's rows: row n is query head n % G of token n / G.
-      if (!fail && !it.end && tid < N) {
+      // Keys of the unit's rows (0 for the columns past them).
+      if (!fail && !it.end && row < N) {
         int lim = 0;
-        if (tid < rows) {
-          const int tok = tid / p.G;
+        if (row < rows) {
           if (ph.whole_batch)
-            lim = paged_prefix_limit(p, it.tok0 + tok);
+            lim = paged_prefix_limit(p, it.tok0 + row_tok);
           else
-            lim = p.causal ? max(0, min(it.pos0 + tok + 1, it.len)) : it.len;
+            lim = p.causal ? max(0, min(it.pos0 + row_tok + 1, it.len)) : it.len;
         }
-        sm.lim[tid] = lim;  // 0 for the columns past the unit's rows
+        sm.lim[buf][row] = lim;
       }
-      if (compute_any(fail)) break;
+      if (vote_any(bar, Cfg::kGroup, fail)) break;
       if (it.end) break;
-      int min_lim = 0x7fffffff;
-      for (int n = 0; n < rows; ++n) min_lim = min(min_lim, sm.lim[n]);
-      float mref[N], l[N];
+      // Tiles that end at or before min_lim need no masking.
+      int min_lim = p.causal ? it.pos0 + 1 : it.len;
+      if (ph.whole_batch) {
+        min_lim = 0x7fffffff;
+        for (int n = 0; n < rows; ++n) min_lim = min(min_lim, sm.lim[buf][n]);
+      }
+      float ref[NC], l[NC];
 #pragma unroll
-      for (int n = 0; n < N; ++n) mref[n] = ninf, l[n] = 0.f;
-      const uint32_t colO = tmem + lane_base + Cfg::col_o(n_item & 1);
-      bool stop = false;
-      for (int j = 0; j < it.nj; ++j, ++g) {
-        const int key = it.key + j * kTile + tid;
-        const int b = g & 1;
+      for (int n = 0; n < NC; ++n) ref[n] = kNoRef, l[n] = 0.f;
+      const uint32_t colO = tmem + lane_base + Cfg::col_o(m & 1) + col0;
+      for (int j = 0; j < it.nj; ++j, ++n_t) {
+        const int sb = buf * Cfg::kSPer + n_t % Cfg::kSPer;  // buffers of S, of P
+        const int pb = 2 * buf + (n_t & 1);
+        const int key = it.key + j * kTile + key_t;
         if (!fail)
-          fail = !mbar_wait(&sm.s_full[b], (g >> 1) & 1, p.status, abortf, kSitePgSFull);
+          fail = !mbar_wait(&sm.s_full[sb], (n_t / Cfg::kSPer) & 1, p.status, abortf, kSitePgSFull);
         fail = __any_sync(0xffffffffu, fail);  // keep the warp's TMEM accesses converged
-        float t[N];
+        float s[NC];
+#pragma unroll
+        for (int n = 0; n < NC; ++n) s[n] = 0.f;
         if (!fail) {
           tc_fence_after();
-          load_cols<N>(tmem + lane_base + Cfg::col_s(b), t);
+          load_cols<NC>(tmem + lane_base + Cfg::col_s(sb) + col0, s);
           tc_fence_before();
-        } else {
-#pragma unroll
-          for (int n = 0; n < N; ++n) t[n] = ninf;
         }
+        // Exponents before the reference is subtracted; masked: -inf.
+        const bool masked = it.key + (j + 1) * kTile > min_lim;
 #pragma unroll
-        for (int n = 0; n < N; ++n) t[n] *= c2;
-        if (it.key + (j + 1) * kTile > min_lim) {
+        for (int n = 0; n < NC; ++n) s[n] *= c2;
+        if (masked) {
 #pragma unroll
-          for (int n = 0; n < N; ++n)
-            if (key >= sm.lim[n]) t[n] = ninf;
+          for (int n = 0; n < NC; ++n)
+            if (key >= sm.lim[buf][col0 + n]) s[n] = ninf;
         }
-        bool grow = false;
+        float over = s[0] - ref[0];
 #pragma unroll
-        for (int n = 0; n < N; ++n) grow |= t[n] > mref[n] + kRescaleSlack;
-        if (compute_any(grow || fail)) {
+        for (int n = 1; n < NC; ++n) over = fmaxf(over, s[n] - ref[n]);
+        if (vote_any(bar, Cfg::kGroup, over > kRescaleSlack || fail)) {
           // Some score outgrew the reference: move every row's to its maximum.
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            float x = t[n];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-            if (lane == 0) sm.top[warp][n] = x;
-          }
-          if (compute_any(fail)) {
-            stop = true;
+          const float x = reduce_cols<NC>(s, [](float a, float b) { return fmaxf(a, b); });
+          if (NC == 32 || (lane & 1) == 0)
+            reinterpret_cast<float*>(&sm.top[buf][col0 + col_of_lane<NC>()])[warp & 3] = x;
+          if (vote_any(bar, Cfg::kGroup, fail)) {
+            fail = true;
             break;
           }
-          float alpha[N];
+          float alpha[NC];
 #pragma unroll
-          for (int n = 0; n < N; ++n) {
-            const float top = fmaxf(fmaxf(fmaxf(sm.top[0][n], sm.top[1][n]),
-                                          fmaxf(sm.top[2][n], sm.top[3][n])),
-                                    mref[n]);
-            alpha[n] = top == ninf ? 1.f : ex2_approx(mref[n] - top);
-            mref[n] = top;
+          for (int n = 0; n < NC; ++n) {
+            const float4 q = sm.top[buf][col0 + n];
+            const float top = fmaxf(fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w)), ref[n]);
+            alpha[n] = ex2_approx(ref[n] - top);
+            ref[n] = top;
             l[n] *= alpha[n];
           }
           if (j > 0) {
             // O holds the unit's earlier tiles once their products are done.
-            if (!mbar_wait(&sm.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, p.status, abortf,
-                           kSitePgPvDone))
-              fail = true;
+            fail = !mbar_wait(&sm.pv_done[pb ^ 1], ((n_t - 1) >> 1) & 1, p.status, abortf,
+                              kSitePgPvDone);
             fail = __any_sync(0xffffffffu, fail);
             if (!fail) {
               tc_fence_after();
-              float o[N];
-              load_cols<N>(colO, o);
+              float o[NC];
+              load_cols<NC>(colO, o);
 #pragma unroll
-              for (int n = 0; n < N; ++n) o[n] *= alpha[n];
-              store_cols<N>(colO, o);
+              for (int n = 0; n < NC; ++n) o[n] *= alpha[n];
+              store_cols<NC>(colO, o);
               tc_fence_before();
             }
           }
         }
         // P's buffer is free once the product before last has read it.
-        if (!fail && g >= 2)
-          fail = !mbar_wait(&sm.pv_done[b], ((g >> 1) - 1) & 1, p.status, abortf, kSitePgPvDone);
+        if (!fail && n_t >= 2)
+          fail = !mbar_wait(&sm.pv_done[pb], ((n_t >> 1) - 1) & 1, p.status, abortf, kSitePgPvDone);
         if (!fail) {
-          uint8_t* const pt = pt0 + b * (N * kTile * 2);
+          uint8_t* const pt = pt0 + (n_t & 1) * (N * kTile * 2);
 #pragma unroll
-          for (int n = 0; n < N; ++n) {
-            const float x = ex2_approx(t[n] - (mref[n] == ninf ? 0.f : mref[n]));
+          for (int n = 0; n < NC; ++n) {
+            const float x = ex2_approx(s[n] - ref[n]);
             l[n] += x;
             *reinterpret_cast<__nv_bfloat16*>(pt + n * 128 + ((pchunk ^ (n & 7)) << 4)) =
                 __float2bfloat16(x);
@@ -486,93 +542,93 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           if (it.key + (j + 1) * kTile > it.k_hi && key >= it.k_hi) {
             // Slots past the unit's keys may hold anything, and 0 * NaN is
             // NaN: their value rows become zero.
-            const int c = 2 * g + 1, slot = c % S;
+            const int c = 2 * (it.tile0 + j) + 1, slot = c % S;
             fail = !mbar_wait(&sm.kv_full[slot], (c / S) & 1, p.status, abortf, kSitePgKvFull);
             if (!fail) {
 #pragma unroll
               for (int h = 0; h < D / 64; ++h)
                 for (int i = 0; i < 8; ++i)
-                  *reinterpret_cast<uint4*>(sm.kv[slot] + h * (kTile * 128) + tid * 128 + i * 16) =
+                  *reinterpret_cast<uint4*>(sm.kv[slot] + h * (kTile * 128) + key_t * 128 + i * 16) =
                       make_uint4(0u, 0u, 0u, 0u);
             }
           }
           fence_proxy_async_smem();
-          mbar_arrive(&sm.p_full[b]);
+          mbar_arrive(&sm.p_full[pb]);
         }
       }
-      if (stop) break;
       // ------------------------------------------------------ the unit's result
+      {
+        const float x = reduce_cols<NC>(l, [](float a, float b) { return a + b; });
+        if (NC == 32 || (lane & 1) == 0) sm.sum[buf][warp & 3][col0 + col_of_lane<NC>()] = x;
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        float x = l[n];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0) sm.sum[warp][n] = x;
-        if (tid == n) sm.lse2[n] = mref[n];
+        for (int n = 0; n < NC; ++n)
+          if (key_t == n) sm.ref[buf][col0 + n] = ref[n];
       }
-      if (compute_any(fail)) break;
+      if (vote_any(bar, Cfg::kGroup, fail)) break;
       const bool merge = it.first && ph.pre_o != nullptr;
-      if (tid < N) {
-        const float sum = (sm.sum[0][tid] + sm.sum[1][tid]) + (sm.sum[2][tid] + sm.sum[3][tid]);
-        float lse2 = sum > 0.f ? sm.lse2[tid] + __log2f(sum) : (sum == 0.f ? ninf : sum);
+      if (row < N) {
+        const float sum = (sm.sum[buf][0][row] + sm.sum[buf][1][row]) +
+                          (sm.sum[buf][2][row] + sm.sum[buf][3][row]);
+        float lse2 = sum == 0.f ? ninf : sm.ref[buf][row] + __log2f(sum);
         float own = sum == 0.f ? 0.f : 1.f / sum, pre = 0.f;
-        if (tid < rows) {
-          const int tok = it.tok0 + tid / p.G, head = it.h * p.G + tid % p.G;
-          const long long row = (long long)tok * p.Hq + head;
+        if (row < rows) {
+          const long long at = (long long)(it.tok0 + row_tok) * p.Hq + it.h * p.G + row_head;
           if (merge) {
-            const float other = ph.pre_lse[row], top = fmaxf(lse2, other);
-            if (top != ninf) {
-              const float wa = exp2f(lse2 - top), wb = exp2f(other - top), s = wa + wb;
-              own *= wa / s;
-              pre = wb / s;
-              lse2 = top + log2f(s);
+            const float other = ph.pre_lse[at], big = fmaxf(lse2, other);
+            if (big != ninf) {
+              const float wa = exp2f(lse2 - big), wb = exp2f(other - big), both = wa + wb;
+              own *= wa / both;
+              pre = wb / both;
+              lse2 = big + log2f(both);
             }
           }
           if (it.slot >= 0)
-            ph.slot_lse[((long long)blockIdx.x * 2 + it.slot) * ph.slot_rows + tid] = lse2;
+            ph.slot_lse[((long long)blockIdx.x * 2 + it.slot) * ph.slot_rows + row] = lse2;
           else if (ph.out_lse)
-            ph.out_lse[row] = lse2;
+            ph.out_lse[at] = lse2;
           else
-            p.lse[row] = lse2 == ninf ? ninf : lse2 * kLn2;
+            p.lse[at] = lse2 == ninf ? ninf : lse2 * kLn2;
         }
-        sm.f_own[tid] = own;
-        sm.f_pre[tid] = pre;
+        sm.f_own[buf][row] = own;
+        sm.f_pre[buf][row] = pre;
       }
       if (it.nj > 0)
-        fail = !mbar_wait(&sm.o_full[n_item & 1], (n_item >> 1) & 1, p.status, abortf, kSitePgOFull);
-      fail = compute_any(fail);
-      if (fail) break;
-      float o[N];
+        fail = !mbar_wait(&sm.o_full[m & 1], n_done[m & 1] & 1, p.status, abortf, kSitePgOFull);
+      if (vote_any(bar, Cfg::kGroup, fail)) break;
+      // A thread has one channel of every row of its columns.
+      float o[NC];
+#pragma unroll
+      for (int n = 0; n < NC; ++n) o[n] = 0.f;
       if (it.nj > 0) {
         tc_fence_after();
-        load_cols<N>(colO, o);
+        load_cols<NC>(colO, o);
         tc_fence_before();
-        mbar_arrive(&sm.o_empty[n_item & 1]);
-        ++n_item;
-      } else {
-#pragma unroll
-        for (int n = 0; n < N; ++n) o[n] = 0.f;
+        ++n_done[m & 1];
       }
-      if (tid < D) {
-        int tok = it.tok0, gh = 0;
+      if (key_t < D) {
+        int gh = head_c;
+        long long at =
+            ((long long)(it.tok0 + tok_c) * p.Hq + it.h * p.G + head_c) * D + key_t;
+        float* slot = ph.slot_o +
+                      (((long long)blockIdx.x * 2 + it.slot) * ph.slot_rows + col0) * D + key_t;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          if (n < rows) {
-            const long long at = ((long long)tok * p.Hq + it.h * p.G + gh) * D + tid;
-            const float w = sm.f_own[n];
-            float x = w == 0.f ? 0.f : o[n] * w;
+        for (int n = 0; n < NC; ++n) {
+          if (col0 + n < rows) {
+            const float f = sm.f_own[buf][col0 + n];
+            float x = f == 0.f ? 0.f : f * o[n];
             if (merge) {
-              const float wp = sm.f_pre[n];
-              if (wp != 0.f) x += wp * ph.pre_o[at];
+              const float fp = sm.f_pre[buf][col0 + n];
+              if (fp != 0.f) x += fp * ph.pre_o[at];
             }
             if (it.slot >= 0)
-              ph.slot_o[(((long long)blockIdx.x * 2 + it.slot) * ph.slot_rows + n) * D + tid] = x;
+              slot[n * D] = x;
             else if (ph.out_o)
               ph.out_o[at] = x;
             else
               p.o[at] = __float2bfloat16(x);
           }
-          if (++gh == p.G) gh = 0, ++tok;
+          at += D;
+          if (++gh == p.G) gh = 0, at += (long long)(p.Hq - p.G) * D;
         }
       }
     }
@@ -586,112 +642,119 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   }
 }
 
-// Joins the parts of the units that were shared between CTAs.  A block looks
-// at one boundary between CTAs and kRows rows of the unit across it; it has
-// work if the boundary is the first inside its unit.  kWarps warps share a
-// row's parts (few rows and many parts when decoding, the reverse for
-// prompts); the parts are added in list order within a warp and the warps'
-// sums in order, so the result does not depend on timing.
-template <int D, int kWarps>
-__global__ void __launch_bounds__(256) fa_paged_merge_kernel(const PagedParams p,
-                                                             const PagedPhase ph) {
+// Joins the parts of the units that were shared between CTAs.  The blocks of
+// a column of the grid look at one boundary between CTAs; they have work if it
+// is the first inside its unit.  The column's warps are spread over the
+// unit's rows, several to a row when the rows are few (decoding, where a unit
+// may have a part in every CTA); parts are added in list order within a warp
+// and the warps' sums in order, so the result does not depend on timing.
+constexpr int kMergeWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const PagedParams p,
+                                                                          const PagedPhase ph) {
+  launch_dependents();
   wait_prior_grid();
-  constexpr int kPer = D / 32, kRows = 8 / kWarps;
-  __shared__ float part_o[8][D], part_l[8];
+  constexpr int kPer = D / 32;
+  __shared__ float part_o[kMergeWarps][D], part_l[kMergeWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const PagedRec rec = *reinterpret_cast<const PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes);
   if (!rec.split) return;
   const long long active = paged_active(rec.total, p.ctas);
   const long long before = paged_lo(rec.total, active, (long long)blockIdx.x - 1);
   if (before > rec.unit_start) return;  // an earlier boundary has the unit
-  const int row = blockIdx.y * kRows + warp / kWarps;
-  // Row of the unit -> token and head: Q tiles of tile_tokens tokens, 128 (or
-  // slot_rows) rows apart.
-  const int in_tile = row % kTile;
-  const int tok = (row / kTile) * ph.tile_tokens + in_tile / p.G;
-  const bool valid = in_tile < ph.tile_tokens * p.G && tok < rec.ntok;
-  if (kRows == 1 && !valid) return;
   const float ninf = __int_as_float(0xff800000);
+  const int rows = rec.ntok * p.G;
+  int share = 1;  // warps to a row
+  while (share < kMergeWarps && 2 * share * rows <= (int)gridDim.y * kMergeWarps) share *= 2;
+  const int per_block = kMergeWarps / share, sub = warp % share;
   const int c0 = (int)blockIdx.x - 1;  // the unit's first CTA, in its last segment's slot
   const int c1 = (int)paged_owner(rec.total, active, rec.unit_end - 1);
   const int n = c1 - c0 + 1;
-  auto slot_of = [&](int i) -> long long {
-    const int slot = i == 0 && before < rec.unit_start ? 1 : 0;
-    return ((long long)(c0 + i) * 2 + slot) * ph.slot_rows + row;
-  };
-  float m = ninf;
-  if (valid)
+  const int slot0 = before < rec.unit_start ? 1 : 0;
+  for (int r0 = (int)blockIdx.y * per_block; r0 < rows; r0 += (int)gridDim.y * per_block) {
+    const int r = r0 + warp / share;
+    const bool valid = r < rows;
+    // Row r -> token and head, and its place in a slot: Q tiles of
+    // tile_tokens tokens, 128 rows apart.
+    const int tok = valid ? r / p.G : 0, head = valid ? r % p.G : 0;
+    const int row = (tok / ph.tile_tokens) * kTile + (tok % ph.tile_tokens) * p.G + head;
+    auto slot_of = [&](int i) -> long long {
+      return ((long long)(c0 + i) * 2 + (i == 0 ? slot0 : 0)) * ph.slot_rows + row;
+    };
+    float m = ninf;
     for (int i = lane; i < n; i += 32) m = fmaxf(m, ph.slot_lse[slot_of(i)]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float acc[kPer], sum = 0.f;
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float acc[kPer], sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-  if (valid && m != ninf) {
-    constexpr int kBatch = 4;
-    for (int i0 = warp % kWarps; i0 < n; i0 += kBatch * kWarps) {
-      float v[kBatch][kPer], w[kBatch];
+    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+    if (m != ninf) {
+      constexpr int kBatch = 4;
+      for (int i0 = sub; i0 < n; i0 += kBatch * share) {
+        float v[kBatch][kPer], w[kBatch];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int i = i0 + b * kWarps;
-        w[b] = 0.f;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) v[b][e] = 0.f;
-        if (i < n) {
-          const long long s = slot_of(i);
-          w[b] = ph.slot_lse[s];
-          const float* src = ph.slot_o + s * D + lane * kPer;
-          if constexpr (kPer == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(src);
-            v[b][0] = x.x, v[b][1] = x.y, v[b][kPer - 2] = x.z, v[b][kPer - 1] = x.w;
-          } else {
-            const float2 x = *reinterpret_cast<const float2*>(src);
-            v[b][0] = x.x, v[b][1] = x.y;
-          }
-        } else {
+        for (int b = 0; b < kBatch; ++b) {
+          const int i = i0 + b * share;
           w[b] = ninf;
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) v[b][e] = 0.f;
+          if (i < n) {
+            const long long s = slot_of(i);
+            w[b] = ph.slot_lse[s];
+            const float* src = ph.slot_o + s * D + lane * kPer;
+            if constexpr (kPer == 4) {
+              const float4 x = *reinterpret_cast<const float4*>(src);
+              v[b][0] = x.x, v[b][1] = x.y, v[b][kPer - 2] = x.z, v[b][kPer - 1] = x.w;
+            } else {
+              const float2 x = *reinterpret_cast<const float2*>(src);
+              v[b][0] = x.x, v[b][1] = x.y;
+            }
+          }
         }
-      }
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const float e = exp2f(w[b] - m);
-        sum += e;
-        if (e != 0.f) {
+        for (int b = 0; b < kBatch; ++b) {
+          const float e = exp2f(w[b] - m);
+          sum += e;
+          if (e != 0.f) {
 #pragma unroll
-          for (int x = 0; x < kPer; ++x) acc[x] += e * v[b][x];
+            for (int x = 0; x < kPer; ++x) acc[x] += e * v[b][x];
+          }
         }
       }
     }
-  }
-  if constexpr (kWarps > 1) {
+    if (share > 1) {  // the same for the whole block
+      __syncthreads();  // the last rows' parts were read
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) part_o[warp][lane * kPer + e] = acc[e];
-    if (lane == 0) part_l[warp] = sum;
-    __syncthreads();
-    if (warp % kWarps != 0) return;
-    for (int w = 1; w < kWarps; ++w) {
-      sum += part_l[warp + w];
+      for (int e = 0; e < kPer; ++e) part_o[warp][lane * kPer + e] = acc[e];
+      if (lane == 0) part_l[warp] = sum;
+      __syncthreads();
+      if (sub == 0) {
+        for (int w = 1; w < share; ++w) {
+          sum += part_l[warp + w];
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] += part_o[warp + w][lane * kPer + e];
+          for (int e = 0; e < kPer; ++e) acc[e] += part_o[warp + w][lane * kPer + e];
+        }
+      }
     }
-  }
-  if (!valid) return;
-  const float inv = m == ninf ? 0.f : 1.f / sum;
-  const long long out = (long long)(rec.tok0 + tok) * p.Hq + rec.h * p.G + in_tile % p.G;
-  const float lse2 = m == ninf ? ninf : m + log2f(sum);
-  int no_abort = 0;
-  if (!bound_ok(rec.tok0 + tok < p.T && rec.h < p.Hkv, p.status, &no_abort, kChkPgRow)) return;
-  if (ph.out_o) {
-    float* dst = ph.out_o + out * D + lane * kPer;
+    if (!valid || sub != 0) continue;
+    const float inv = m == ninf ? 0.f : 1.f / sum;
+    const long long out = (long long)(rec.tok0 + tok) * p.Hq + rec.h * p.G + head;
+    const float lse2 = m == ninf ? ninf : m + log2f(sum);
+    int no_abort = 0;
+    if (!bound_ok(rec.tok0 + tok < p.T && rec.h < p.Hkv, p.status, &no_abort, kChkPgRow)) continue;
+    if (ph.out_o) {
+      float* dst = ph.out_o + out * D + lane * kPer;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) dst[e] = acc[e] * inv;
-    if (lane == 0) ph.out_lse[out] = lse2;
-  } else {
-    __nv_bfloat16* dst = p.o + out * D + lane * kPer;
+      for (int e = 0; e < kPer; ++e) dst[e] = acc[e] * inv;
+      if (lane == 0) ph.out_lse[out] = lse2;
+    } else {
+      __nv_bfloat16* dst = p.o + out * D + lane * kPer;
 #pragma unroll
-    for (int e = 0; e < kPer; e += 2)
-      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0) p.lse[out] = m == ninf ? ninf : lse2 * kLn2;
+      for (int e = 0; e < kPer; e += 2)
+        *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+      if (lane == 0) p.lse[out] = m == ninf ? ninf : lse2 * kLn2;
+    }
   }
 }
 
@@ -716,17 +779,10 @@ int launch_decode(const PagedMaps& t, const PagedParams& p, const PagedPhase& ph
 template <int D>
 int launch_merge(const PagedParams& p, const PagedPhase& ph, const cudaLaunchConfig_t& base) {
   cudaLaunchConfig_t c = base;
-  c.blockDim = dim3(256, 1, 1);
+  c.blockDim = dim3(32 * kMergeWarps, 1, 1);
   c.dynamicSmemBytes = 0;
-  cudaError_t e;
-  if (ph.slot_rows <= kPagedDecodeRows) {
-    c.gridDim = dim3((unsigned)p.ctas, (unsigned)ph.slot_rows, 1);
-    e = cudaLaunchKernelEx(&c, fa_paged_merge_kernel<D, 8>, p, ph);
-  } else {
-    c.gridDim = dim3((unsigned)p.ctas, (unsigned)ph.slot_rows / 8, 1);
-    e = cudaLaunchKernelEx(&c, fa_paged_merge_kernel<D, 1>, p, ph);
-  }
-  if (e != cudaSuccess) {
+  c.gridDim = dim3((unsigned)p.ctas, ph.slot_rows <= kPagedDecodeRows ? 4 : 16, 1);
+  if (cudaLaunchKernelEx(&c, fa_paged_merge_kernel<D>, p, ph) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
   }

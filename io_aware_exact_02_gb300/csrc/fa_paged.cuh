@@ -187,6 +187,7 @@ struct PagedItem {
   int len;
   int slot;       // -1: the whole unit, written straight to the output; else 0 or 1
   int first;      // the segment begins the unit (and merges pre_o in)
+  int tile0;      // key tiles of the CTA's segments before this one
 };
 
 struct PagedScan {
@@ -198,7 +199,7 @@ struct PagedScan {
 // A CTA's walk along its range of the list.
 struct PagedWalk {
   long long g, hi, total;
-  int b, h, i, tile, units;
+  int b, h, i, tile, units, tiles;
   PagedSeq s;
   bool first;
 };
@@ -229,6 +230,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhas
   w.g = lo;
   w.hi = paged_lo(total, active, (long long)blockIdx.x + 1);
   w.first = true;
+  w.tiles = 0;
   if (w.g >= w.hi) return;  // idle CTA; uniform in the CTA
   long long run = 0;
   for (int b0 = 0; b0 < B; b0 += nt) {
@@ -297,6 +299,8 @@ __device__ __forceinline__ PagedItem paged_next(const PagedParams& p, const Page
   it.len = w.s.len;
   it.slot = take == cost ? -1 : (w.first ? 0 : 1);
   it.first = w.tile == 0;
+  it.tile0 = w.tiles;
+  w.tiles += it.nj;
   if (w.first && lane_id() == 0) {
     PagedRec r;
     r.total = w.total;
@@ -391,29 +395,50 @@ __device__ __forceinline__ void paged_pages_advance(const PagedParams& p, PagedP
   }
 }
 
-// The producer warp's loads of one 128-key tile of K or V: one box per page
-// (at most 128 rows) and 64 channels, a lane each.
+// The producer warp's loads of a 128-key tile of K and of V: one box per page
+// (at most 128 rows) and 64 channels of each, a lane to a box; 32 lanes are
+// enough (pages of 16 keys, d = 128).
+struct PagedBox {
+  int kind;         // 0: a box of K, 1: of V, 2: none
+  int sub;          // the box's page among the tile's
+  int x;            // its first channel
+  int dst;          // its place in the tile, bytes
+  int in_page;      // bits of the key that give the box's first row in a page
+  int last;         // pages of the tile - 1
+};
 template <int D>
-__device__ __forceinline__ void paged_load_tile(const PagedParams& p, const CUtensorMap* map,
-                                                PagedPages& g, int h, int key, uint8_t* dst,
-                                                uint64_t* bar) {
-  const int lane = (int)lane_id();
-  const int rows = min(p.page_size, kTile);
-  const int per = kTile / rows;  // pages of the tile
+__device__ __forceinline__ PagedBox paged_box(const PagedParams& p, int lane) {
+  const int rows = min(p.page_size, kTile), per = kTile / rows;
+  PagedBox b;
+  b.sub = lane % per;
+  const int half = lane / per % (D / 64);
+  b.kind = min(lane / (per * (D / 64)), 2);
+  b.x = half * 64;
+  b.dst = half * (kTile * 128) + b.sub * rows * 128;
+  b.in_page = (p.page_size - 1) & ~(rows - 1);
+  b.last = per - 1;
+  return b;
+}
+template <int D>
+__device__ __forceinline__ void paged_load_pair(const PagedParams& p, const PagedBox& box,
+                                                const CUtensorMap* tk, const CUtensorMap* tv,
+                                                PagedPages& g, int h, int key, uint8_t* dst_k,
+                                                uint64_t* bar_k, uint8_t* dst_v,
+                                                uint64_t* bar_v) {
   const int first = key >> p.page_shift;
-  paged_pages_advance(p, g, first + per - 1);
-  if (lane == 0) mbar_arrive_expect_tx(bar, kTile * D * 2);
-  const int sub = lane & (per - 1), half = lane / per;
-  // A tile's pages may straddle the 32 at hand and the next ones only if
-  // its first page does: runs of `per` pages (a power of two) start at
-  // multiples of `per` past the segment's first.
-  const int id = __shfl_sync(0xffffffffu, g.cur, (first + sub - g.base) & 31);
-  __syncwarp();
-  if (half < D / 64) {
-    const int z = id < 0 ? p.num_pages * p.Hkv : id * p.Hkv + h;
-    tma_load_3d(dst + half * (kTile * 128) + sub * rows * 128, map, bar, half * 64,
-                key & (p.page_size - 1) & ~(rows - 1), z);
+  // A tile's pages lie among the 32 at hand or among the next ones: runs of
+  // box.last + 1 pages (a power of two) from the segment's first page on.
+  paged_pages_advance(p, g, first + box.last);
+  if (lane_id() == 0) {
+    mbar_arrive_expect_tx(bar_k, kTile * D * 2);
+    mbar_arrive_expect_tx(bar_v, kTile * D * 2);
   }
+  const int id = __shfl_sync(0xffffffffu, g.cur, (first + box.sub - g.base) & 31);
+  const int z = id < 0 ? p.num_pages * p.Hkv : id * p.Hkv + h;  // past the map: zeros
+  __syncwarp();
+  if (box.kind < 2)
+    tma_load_3d((box.kind ? dst_v : dst_k) + box.dst, box.kind ? tv : tk,
+                box.kind ? bar_v : bar_k, box.x, key & box.in_page, z);
 }
 
 }  // namespace fa

@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  launch_dependents();
   wait_prior_grid();
   PagedWalk walk;
   paged_plan(p, ph, sm.scan, walk);
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       r.total = walk.total;
       *reinterpret_cast<PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes) = r;
     }
+    const PagedBox box = paged_box<D>(p, lane);
     for (int m = 0; ok; ++m) {
       const int is = m % kItemRing;
       if (m >= kItemRing)
@@ -178,17 +180,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         it.tok0 + t * ph.tile_tokens);
       }
       ++n_q;
-      for (int j = 0; j < nmax && ok; ++j) {
-        for (int w = 0; w < 2; ++w) {
-          const int slot = c % S, use = c / S;
-          if (use > 0)
-            ok = mbar_wait(&sm.kv_empty[slot], (use - 1) & 1, p.status, abortf, kSitePgKvEmpty);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          paged_load_tile<D>(p, w == 0 ? &tk : &tv, pages, it.h, it.key + j * kTile, sm.kv[slot],
-                             &sm.kv_full[slot]);
-          ++c;
-        }
+      for (int j = 0; j < nmax; ++j, c += 2) {
+        // K into one slot of the ring, V into the next, once both are free.
+        const int sk = c % S, sv = (c + 1) % S;
+        if (c >= S)
+          ok = mbar_wait(&sm.kv_empty[sk], (c / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
+        if (ok && c + 1 >= S)
+          ok = mbar_wait(&sm.kv_empty[sv], ((c + 1) / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        paged_load_pair<D>(p, box, &tk, &tv, pages, it.h, it.key + j * kTile, sm.kv[sk],
+                           &sm.kv_full[sk], sm.kv[sv], &sm.kv_full[sv]);
       }
     }
     if (!ok && lane == 0) {

@@ -426,34 +426,70 @@ def rope_table(length: int, rope_dim: int, base: float = 10000.0, device="cuda")
     return torch.cat([angle.cos(), angle.sin()], 1).to(torch.float32)
 
 
-def _check_rows(name, t, T, H, d):
-    """Packed rows (T, H, d) bf16, heads contiguous; returns the row stride."""
+# The paged-cache calls serve single tokens, where the call itself is what a
+# step costs: their checks look at each tensor once, and only a failed one
+# finds out what is wrong with it.
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+
+
+def _refuse(name, t, shape, dtype, device):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dtype != torch.bfloat16:
-        raise ValueError("%s must be torch.bfloat16" % name)
-    if tuple(t.shape) != (T, H, d):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (T, H, d)))
-    stride = t.stride()
-    if stride[2] != 1 or (H > 1 and stride[1] != d):
+    if t.get_device() != device:
+        raise ValueError("%s is on %s, expected cuda:%d (one call's tensors must share a device)"
+                         % (name, t.device, device))
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s" % (name, dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _checked(name, t, shape, dtype, device):
+    """The data pointer of a contiguous tensor of that shape, type and device."""
+    if (not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not dtype
+            or t.shape != shape or not t.is_contiguous()):
+        _refuse(name, t, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _checked_rows(name, t, T, H, d, device):
+    """Data pointer and row stride of packed rows (T, H, d) bf16 whose heads
+    are contiguous."""
+    if (not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not _BF16
+            or t.shape != (T, H, d)):
+        _refuse(name, t, (T, H, d), _BF16, device)
+    row, head, one = t.stride()
+    if (one != 1 and d > 1) or (head != d and H > 1):
         raise ValueError("%s must have contiguous heads" % name)
-    return stride[0] if T > 1 else max(stride[0], H * d)
+    return t.data_ptr(), row if T > 1 else max(row, H * d)
 
 
-def _check_cache(k_pages, v_pages, page_table, seq_lens, cu_q):
-    """The cache and its tables; returns (num_pages, Hkv, page_size, d, B, max_pages)."""
-    shape = tuple(k_pages.shape)
-    if len(shape) != 4:
+def _checked_cache(k_pages, v_pages, page_table, seq_lens, cu_q, device):
+    """Data pointers and sizes of the cache and its tables."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
         raise ValueError("k_pages must have shape (num_pages, Hkv, page_size, d)")
-    _check_qkv("k_pages", k_pages, shape)
-    _check_qkv("v_pages", v_pages, shape)
-    B = seq_lens.shape[0]
-    if page_table.dim() != 2:
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must have shape (B, max_pages)")
-    _check_qkv("page_table", page_table, (B, page_table.shape[1]), torch.int32)
-    _check_qkv("seq_lens", seq_lens, (B,), torch.int32)
-    _check_qkv("cu_q", cu_q, (B + 1,), torch.int32)
-    return shape + (B, page_table.shape[1])
+    shape, (B, width) = k_pages.shape, page_table.shape
+    return (_checked("k_pages", k_pages, shape, _BF16, device),
+            _checked("v_pages", v_pages, shape, _BF16, device),
+            _checked("page_table", page_table, (B, width), _I32, device),
+            _checked("seq_lens", seq_lens, (B,), _I32, device),
+            _checked("cu_q", cu_q, (B + 1,), _I32, device)), shape, B, width
+
+
+def _call_on(device, fn, *args):
+    """The library call with `device` current, on its current stream."""
+    f = getattr(load(), fn)
+    stream = torch._C._cuda_getCurrentRawStream(device)
+    if torch.cuda.current_device() == device:
+        rc = f(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, stream)
+    if rc != FA_OK:
+        _check(fn, rc)
 
 
 def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_q, q=None, q_out=None, rope=None,
@@ -463,37 +499,35 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_q, q=None, q_out=
     rotation).  Sequence b's rows are cu_q[b] .. cu_q[b+1]-1 and end at
     position seq_lens[b]-1.  Returns the rotated queries (``q_out``,
     allocated if not given; it may be ``q``), or None without q."""
-    num_pages, Hkv, page_size, d, B, max_pages = _check_cache(k_pages, v_pages, page_table,
-                                                              seq_lens, cu_q)
+    if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 3:
+        raise ValueError("k must be a CUDA tensor of shape (T, Hkv, d)")
+    dev = k.get_device()
+    (kp, vp, table, lens, cu), (num_pages, Hkv, page_size, d), B, width = _checked_cache(
+        k_pages, v_pages, page_table, seq_lens, cu_q, dev)
     T = k.shape[0]
-    ks, vs = _check_rows("k", k, T, Hkv, d), _check_rows("v", v, T, Hkv, d)
-    Hq, qs, qos = 0, 0, 0
+    k_ptr, ks = _checked_rows("k", k, T, Hkv, d, dev)
+    v_ptr, vs = _checked_rows("v", v, T, Hkv, d, dev)
+    q_ptr = q_out_ptr = None
+    Hq = qs = qos = rope_len = rope_dim = 0
     if q is not None:
-        if q.dim() != 3:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q must have shape (T, Hq, d)")
         Hq = q.shape[1]
-        qs = _check_rows("q", q, T, Hq, d)
+        q_ptr, qs = _checked_rows("q", q, T, Hq, d, dev)
         if q_out is None:  # rows of no sequence are not written
-            q_out = torch.zeros((T, Hq, d), dtype=q.dtype, device=q.device)
-        qos = _check_rows("q_out", q_out, T, Hq, d)
+            q_out = torch.zeros((T, Hq, d), dtype=_BF16, device=q.device)
+        q_out_ptr, qos = _checked_rows("q_out", q_out, T, Hq, d, dev)
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    rope_len = rope_dim = 0
+    rope_ptr = None
     if rope is not None:
-        if rope.dim() != 2:
+        if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
             raise ValueError("rope must have shape (length, rope_dim)")
         rope_len, rope_dim = rope.shape
-        _check_qkv("rope", rope, (rope_len, rope_dim), torch.float32)
-    with _on_device(k, v=v, q=q, q_out=q_out, k_pages=k_pages, v_pages=v_pages,
-                    page_table=page_table, seq_lens=seq_lens, cu_q=cu_q, rope=rope):
-        rc = load().fa_kv_append(
-            None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            None if q is None else q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-            page_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(),
-            None if rope is None else rope.data_ptr(), T, B, Hq, Hkv, d, qs, ks, vs, qos,
-            num_pages, page_size, max_pages, rope_dim, rope_len, int(bool(interleaved)),
-            _stream_of(k))
-    _check("fa_kv_append", rc)
+        rope_ptr = _checked("rope", rope, (rope_len, rope_dim), _F32, dev)
+    _call_on(dev, "fa_kv_append", q_ptr, k_ptr, v_ptr, q_out_ptr, kp, vp, table, lens, cu,
+             rope_ptr, T, B, Hq, Hkv, d, qs, ks, vs, qos, num_pages, page_size, width, rope_dim,
+             rope_len, 1 if interleaved else 0)
     return q_out
 
 
@@ -503,39 +537,36 @@ def fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len=0) -> int:
 
 def _fwd_paged(fn, q, k_pages, v_pages, page_table, seq_lens, cu_q, prefix_pages, max_q, causal,
                scale, out, lse, workspace):
-    num_pages, Hkv, page_size, d, B, max_pages = _check_cache(k_pages, v_pages, page_table,
-                                                              seq_lens, cu_q)
-    if q.dim() != 3:
-        raise ValueError("q must have shape (T, Hq, d)")
+    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+        raise ValueError("q must be a CUDA tensor of shape (T, Hq, d)")
+    dev = q.get_device()
+    (kp, vp, table, lens, cu), (num_pages, Hkv, page_size, d), B, width = _checked_cache(
+        k_pages, v_pages, page_table, seq_lens, cu_q, dev)
     T, Hq, _ = q.shape
-    qs = _check_rows("q", q, T, Hq, d)
+    q_ptr, qs = _checked_rows("q", q, T, Hq, d, dev)
     scale = default_scale(d) if scale is None else float(scale)
     max_q = T if max_q is None else int(max_q)
     if out is None:  # rows of no sequence are not written
-        out = torch.zeros((T, Hq, d), dtype=torch.bfloat16, device=q.device)
+        out = torch.zeros((T, Hq, d), dtype=_BF16, device=q.device)
     if lse is None:
-        lse = torch.full((T, Hq), -math.inf, dtype=torch.float32, device=q.device)
-    _check_qkv("out", out, (T, Hq, d))
-    _check_qkv("lse", lse, (T, Hq), torch.float32)
-    prefix_len = 0
+        lse = torch.full((T, Hq), -math.inf, dtype=_F32, device=q.device)
+    o_ptr = _checked("out", out, (T, Hq, d), _BF16, dev)
+    lse_ptr = _checked("lse", lse, (T, Hq), _F32, dev)
+    prefix, prefix_len = (), 0
     if prefix_pages is not None:
-        _check_qkv("prefix_pages", prefix_pages, (prefix_pages.numel(),), torch.int32)
-        prefix_len = prefix_pages.numel() * page_size
-    need = fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws_ptr = workspace.data_ptr() if workspace is not None else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    prefix = () if prefix_pages is None else (prefix_pages.data_ptr(), prefix_len)
-    with _on_device(q, k_pages=k_pages, v_pages=v_pages, page_table=page_table,
-                    seq_lens=seq_lens, cu_q=cu_q, prefix_pages=prefix_pages, out=out, lse=lse,
-                    workspace=workspace):
-        rc = getattr(load(), fn)(
-            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
-            page_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), *prefix, T, B, Hq, Hkv,
-            d, qs, num_pages, page_size, max_pages, max_q, int(bool(causal)),
-            ctypes.c_float(scale), ws_ptr, ws_bytes, _stream_of(q))
-    _check(fn, rc)
+        if not isinstance(prefix_pages, torch.Tensor) or prefix_pages.dim() != 1:
+            raise ValueError("prefix_pages must have shape (pages,)")
+        n = prefix_pages.shape[0]
+        prefix_len = n * page_size
+        prefix = (_checked("prefix_pages", prefix_pages, (n,), _I32, dev), prefix_len)
+    if workspace is None:
+        workspace = torch.empty(max(1, fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len)),
+                                dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev:
+        _refuse("workspace", workspace, workspace.shape, workspace.dtype, dev)
+    _call_on(dev, fn, q_ptr, kp, vp, o_ptr, lse_ptr, table, lens, cu, *prefix, T, B, Hq, Hkv, d,
+             qs, num_pages, page_size, width, max_q, 1 if causal else 0, scale,
+             workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out, lse
 
 
