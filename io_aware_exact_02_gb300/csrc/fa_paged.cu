@@ -22,8 +22,9 @@
 // other's tiles; with N = 64 each has half of the columns of every unit
 // instead, as a thread's registers hold no more.
 //
-// Warps: 0-3 and 4-7 compute (and write results), 8 producer (TMA: a lane per
-// page box), 9 issues the products, each as soon as its operands are there.
+// Warps: 0-3 and 4-7 compute (and write results), 8 and 10 load K and V (TMA: a
+// lane per page box), 9 issues the products, each as soon as its operands are
+// there, 11 is idle.
 // K and V stream through one ring of 32 KB (d = 128) tiles in the order K0 V0
 // K1 V1 ..., across units; four S buffers let S run ahead of P V, into the
 // next units.
@@ -37,8 +38,8 @@ namespace fa {
 namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kItemRing = 4;
-constexpr int kDecodeThreads = 320;
+constexpr int kItemRing = 8;  // even: an item's slot belongs to one warpgroup
+constexpr int kDecodeThreads = 384;
 constexpr int kCompute = 256;  // threads of the compute warps
 constexpr int kSBufs = 4;      // S buffers, shared out among the groups
 // A row's reference maximum before it has seen a key: finite, so that the
@@ -87,15 +88,6 @@ struct alignas(1024) DecodeSmem {
   uint32_t tmem_base;
   int abort_flag;
 };
-
-// Wait without the abort shortcut: used while winding down.
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
-  const uint32_t a = smem_u32(bar);
-  const unsigned long long t0 = globaltimer_ns();
-  while (!mbar_try_wait(a, parity)) {
-    if (globaltimer_ns() - t0 > 100000000ull) return;  // 100 ms
-  }
-}
 
 // A vote of `threads` compute threads on named barrier `id`: true for all
 // when true for any.  Also a barrier among them.  Every thread of the group
@@ -190,7 +182,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abortf = &sm.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5;
-  constexpr int kWarpLoad = 8, kWarpMma = 9;
+  constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpLoadV = 10;
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -209,7 +201,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     }
     for (int i = 0; i < kItemRing; ++i) {
       mbar_init(&sm.item_full[i], 1);
-      mbar_init(&sm.item_empty[i], 1 + Cfg::kGroup / 32);  // the issuing thread, the group's warps
+      // Read by the issuing thread, the V warp and the group's warps.
+      mbar_init(&sm.item_empty[i], 2 + Cfg::kGroup / 32);
     }
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -239,67 +232,27 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   paged_plan(p, ph, sm.scan, walk);
 
   if (warp == kWarpLoad) {
-    // ------------------------------------------------------------ producer
-    const int lane = (int)lane_id();
-    int g = 0, n_q = 0;  // tiles and units loaded
-    bool ok = true;
-    if (walk.g >= walk.hi && lane == 0) {
-      PagedRec r = {};
-      r.total = walk.total;
-      *reinterpret_cast<PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes) = r;
-    }
-    const PagedBox box = paged_box<D>(p, lane);
-    // The warpgroups that take units in turn each find an end of the list.
-    int ends = kHalves ? 1 : 2;
-    for (int m = 0; ok; ++m) {
-      const int is = m % kItemRing;
-      if (m >= kItemRing)
-        ok = mbar_wait(&sm.item_empty[is], (m / kItemRing - 1) & 1, p.status, abortf, kSitePgItemEmpty);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const PagedItem it = paged_next(p, ph, walk);
-      if (lane == 0) {
-        sm.item[is] = it;
-        mbar_arrive(&sm.item_full[is]);
-      }
-      if (it.end) {
-        if (--ends == 0) break;
-        continue;
-      }
-      if (it.nj == 0) continue;
-      PagedPages pages;
-      paged_pages_begin(p, ph, it, pages);
+    // ------------------------------------------------------------ Q and K
+    int n_q = 0;  // units loaded
+    paged_produce_k<D, S, kItemRing>(p, ph, sm, &tk, walk, Cfg::kGroups, [&](const PagedItem& it) {
       const int qb = n_q & 1;
-      if (n_q >= 2)
-        ok = mbar_wait(&sm.q_empty[qb], ((n_q >> 1) - 1) & 1, p.status, abortf, kSitePgQEmpty);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (lane == 0) {
+      if (n_q >= 2 && !mbar_wait(&sm.q_empty[qb], ((n_q >> 1) - 1) & 1, p.status, abortf,
+                                 kSitePgQEmpty))
+        return false;
+      if (lane_id() == 0) {
         mbar_arrive_expect_tx(&sm.q_full[qb], ph.tile_tokens * p.G * D * 2);
         for (int h = 0; h < D / 64; ++h)
           tma_load_3d(sm.q[qb] + h * (N * 128), &tq, &sm.q_full[qb], h * 64, it.h * p.G, it.tok0);
       }
       ++n_q;
-      for (int j = 0; j < it.nj; ++j, ++g) {
-        // K into one slot of the ring, V into the next, once both are free.
-        const int ck = 2 * g, sk = ck % S, sv = (ck + 1) % S;
-        if (ck >= S)
-          ok = mbar_wait(&sm.kv_empty[sk], (ck / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
-        if (ok && ck + 1 >= S)
-          ok = mbar_wait(&sm.kv_empty[sv], ((ck + 1) / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        paged_load_pair<D>(p, box, &tk, &tv, pages, it.h, it.key + j * kTile, sm.kv[sk],
-                           &sm.kv_full[sk], sm.kv[sv], &sm.kv_full[sv]);
-      }
-    }
-    if (!ok && lane == 0) {
-      // Let the copies already issued land before the CTA exits.
+      return true;
+    });
+    if (*abortf && lane_id() == 0)
       for (int i = n_q - 1; i >= 0 && i >= n_q - 2; --i) drain_wait(&sm.q_full[i & 1], (i >> 1) & 1);
-      for (int cc = 2 * g - 1; cc >= 0 && cc >= 2 * g - S; --cc)
-        drain_wait(&sm.kv_full[cc % S], (cc / S) & 1);
-    }
     __syncwarp();
+  } else if (warp == kWarpLoadV) {
+    // ------------------------------------------------------------ V
+    paged_produce_v<D, S, kItemRing>(p, sm, &tv);
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ products
     if (lane_id() == 0) {
@@ -411,7 +364,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       drain_wait(&sm.drain, 0);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ compute
     const int wg = warp >> 2, key_t = tid & 127, lane = tid & 31;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -426,7 +379,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     const int pchunk = (key_t & 63) >> 3;
     // Row n of a unit is query head n % G of its token n / G.
     const int row_tok = row / p.G, row_head = row % p.G;
-    const int tok_c = col0 / p.G, head_c = col0 % p.G;
     bool fail = false;
     int n_t = 0;             // tiles the group has had
     int n_done[2] = {0, 0};  // units with keys, by the parity of their item
@@ -595,42 +547,54 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       if (it.nj > 0)
         fail = !mbar_wait(&sm.o_full[m & 1], n_done[m & 1] & 1, p.status, abortf, kSitePgOFull);
       if (vote_any(bar, Cfg::kGroup, fail)) break;
-      // A thread has one channel of every row of its columns.
-      float o[NC];
-#pragma unroll
-      for (int n = 0; n < NC; ++n) o[n] = 0.f;
+      // O leaves through shared memory, in the group's P buffers (free: the
+      // unit's products are done), and is stored eight channels to a thread.
+      float* const stage = reinterpret_cast<float*>(sm.pt[2 * buf]);  // [N][D]
       if (it.nj > 0) {
         tc_fence_after();
+        float o[NC];
         load_cols<NC>(colO, o);
         tc_fence_before();
         ++n_done[m & 1];
-      }
-      if (key_t < D) {
-        int gh = head_c;
-        long long at =
-            ((long long)(it.tok0 + tok_c) * p.Hq + it.h * p.G + head_c) * D + key_t;
-        float* slot = ph.slot_o +
-                      (((long long)blockIdx.x * 2 + it.slot) * ph.slot_rows + col0) * D + key_t;
+        if (key_t < D) {
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-          if (col0 + n < rows) {
-            const float f = sm.f_own[buf][col0 + n];
-            float x = f == 0.f ? 0.f : f * o[n];
-            if (merge) {
-              const float fp = sm.f_pre[buf][col0 + n];
-              if (fp != 0.f) x += fp * ph.pre_o[at];
-            }
-            if (it.slot >= 0)
-              slot[n * D] = x;
-            else if (ph.out_o)
-              ph.out_o[at] = x;
-            else
-              p.o[at] = __float2bfloat16(x);
-          }
-          at += D;
-          if (++gh == p.G) gh = 0, at += (long long)(p.Hq - p.G) * D;
+          for (int n = 0; n < NC; ++n) stage[(col0 + n) * D + key_t] = o[n];
         }
       }
+      vote_any(bar, Cfg::kGroup, false);
+      for (int i = kHalves ? tid : key_t; i < rows * (D / 8); i += Cfg::kGroup) {
+        const int n = i / (D / 8), ch = i % (D / 8) * 8, tok = n / p.G;
+        const long long at =
+            ((long long)(it.tok0 + tok) * p.Hq + it.h * p.G + (n - tok * p.G)) * D + ch;
+        const float f = sm.f_own[buf][n];
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (f != 0.f) {
+          x = *reinterpret_cast<const float4*>(stage + n * D + ch);
+          y = *reinterpret_cast<const float4*>(stage + n * D + ch + 4);
+          x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+          y.x *= f, y.y *= f, y.z *= f, y.w *= f;
+        }
+        const float fp = sm.f_pre[buf][n];
+        if (fp != 0.f) {  // only where results are merged in
+          const float4 u = *reinterpret_cast<const float4*>(ph.pre_o + at);
+          const float4 v = *reinterpret_cast<const float4*>(ph.pre_o + at + 4);
+          x.x += fp * u.x, x.y += fp * u.y, x.z += fp * u.z, x.w += fp * u.w;
+          y.x += fp * v.x, y.y += fp * v.y, y.z += fp * v.z, y.w += fp * v.w;
+        }
+        if (it.slot >= 0 || ph.out_o) {
+          float* dst = it.slot >= 0
+                           ? ph.slot_o +
+                                 (((long long)blockIdx.x * 2 + it.slot) * ph.slot_rows + n) * D + ch
+                           : ph.out_o + at;
+          reinterpret_cast<float4*>(dst)[0] = x;
+          reinterpret_cast<float4*>(dst)[1] = y;
+        } else {
+          *reinterpret_cast<uint4*>(p.o + at) =
+              make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y),
+                         pack_bf16x2(y.z, y.w));
+        }
+      }
+      // (The next unit's first vote comes before P is written again.)
     }
   }
 
@@ -660,8 +624,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const PagedRec rec = *reinterpret_cast<const PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes);
   if (!rec.split) return;
-  const long long active = paged_active(rec.total, p.ctas);
-  const long long before = paged_lo(rec.total, active, (long long)blockIdx.x - 1);
+  const PagedShare parts(rec.total, p.ctas);
+  const long long before = parts.lo((int)blockIdx.x - 1);
   if (before > rec.unit_start) return;  // an earlier boundary has the unit
   const float ninf = __int_as_float(0xff800000);
   const int rows = rec.ntok * p.G;
@@ -669,7 +633,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
   while (share < kMergeWarps && 2 * share * rows <= (int)gridDim.y * kMergeWarps) share *= 2;
   const int per_block = kMergeWarps / share, sub = warp % share;
   const int c0 = (int)blockIdx.x - 1;  // the unit's first CTA, in its last segment's slot
-  const int c1 = (int)paged_owner(rec.total, active, rec.unit_end - 1);
+  const int c1 = parts.owner(rec.unit_end - 1);
   const int n = c1 - c0 + 1;
   const int slot0 = before < rec.unit_start ? 1 : 0;
   for (int r0 = (int)blockIdx.y * per_block; r0 < rows; r0 += (int)gridDim.y * per_block) {

@@ -82,6 +82,15 @@ __device__ __forceinline__ PagedRow paged_row(const int* cu_q, const int* seq_le
 // timing.  Every CTA derives its range from the tables itself: no launch
 // needs the lengths on the host.
 
+// Wait without the abort shortcut: used while winding down.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  const uint32_t a = smem_u32(bar);
+  const unsigned long long t0 = globaltimer_ns();
+  while (!mbar_try_wait(a, parity)) {
+    if (globaltimer_ns() - t0 > 100000000ull) return;  // 100 ms
+  }
+}
+
 // The phase of a call a kernel runs.
 struct PagedPhase {
   int whole_batch;     // 1: the shared prefix, attended by the rows of the whole batch
@@ -162,18 +171,32 @@ __device__ __forceinline__ long long paged_head_cost(const PagedParams& p, const
   return c;
 }
 
-// CTA c's range of the list is [paged_lo(c), paged_lo(c + 1)); with fewer
-// tiles than CTAs the first `total` CTAs take one each.
-__host__ __device__ inline long long paged_active(long long total, int ctas) {
-  return total < ctas ? total : ctas;
+// a / b of nonnegative numbers; nearly always both fit 32 bits, whose division
+// is several times shorter.
+__device__ __forceinline__ long long paged_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+  return a / b;
 }
-__host__ __device__ inline long long paged_lo(long long total, long long active, long long c) {
-  return c >= active ? total : total * c / active;
-}
-// The CTA whose range holds tile x of the list.
-__host__ __device__ inline long long paged_owner(long long total, long long active, long long x) {
-  return ((x + 1) * active + total - 1) / total - 1;
-}
+
+// CTA c's range of the list is [lo(c), lo(c + 1)): equal ranges, the first
+// `more` of them one tile longer; with fewer tiles than CTAs the first ones
+// take one each.
+struct PagedShare {
+  long long total, each;
+  int more;
+  __device__ __forceinline__ PagedShare(long long t, int ctas) : total(t) {
+    each = paged_div(t, ctas);
+    more = (int)(t - each * ctas);
+  }
+  __device__ __forceinline__ long long lo(int c) const {
+    return each * c + (c < more ? c : more);
+  }
+  // The CTA whose range holds tile x of the list.
+  __device__ __forceinline__ int owner(long long x) const {
+    const long long head = (each + 1) * more;
+    return x < head ? (int)paged_div(x, each + 1) : more + (int)paged_div(x - head, each);
+  }
+};
 
 // One segment of a unit, as the producer hands it to the other roles.
 struct PagedItem {
@@ -224,11 +247,11 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhas
   __syncthreads();
   long long total = 0;
   for (int i = 0; i < nw; ++i) total += sc.warp_sum[i];
-  const long long active = paged_active(total, gridDim.x);
-  const long long lo = paged_lo(total, active, blockIdx.x);
+  const PagedShare share(total, gridDim.x);
+  const long long lo = share.lo(blockIdx.x);
   w.total = total;
   w.g = lo;
-  w.hi = paged_lo(total, active, (long long)blockIdx.x + 1);
+  w.hi = share.lo(blockIdx.x + 1);
   w.first = true;
   w.tiles = 0;
   if (w.g >= w.hi) return;  // idle CTA; uniform in the CTA
@@ -263,12 +286,12 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhas
   w.units = paged_units(ph, w.s);
   long long off = lo - sc.found_excl;
   const long long head = paged_head_cost(p, ph, w.s);
-  w.h = (int)(off / head);
+  w.h = (int)paged_div(off, head);
   off -= w.h * head;
   w.i = 0;
   if (!p.causal || ph.whole_batch) {  // units of equal cost
     const int c = max(1, paged_unit_tiles(p, ph, w.s, 0));
-    w.i = (int)(off / c);
+    w.i = (int)paged_div(off, c);
     off -= (long long)w.i * c;
   } else {
     for (;; ++w.i) {
@@ -356,89 +379,202 @@ __device__ __forceinline__ int paged_prefix_limit(const PagedParams& p, int t) {
   return max(0, min(lim, p.prefix_len));
 }
 
-// The page numbers of a segment, 32 at a time in the lanes of the producer
-// warp, the next 32 in flight while these are used.
+// The page numbers of a segment, 32 at a time in the lanes of a producer warp,
+// the next 32 in flight while these are used.
 struct PagedPages {
-  const int* list;  // page numbers from the sequence's first page on
+  const int* list;  // the sequence's page numbers
   int n;            // pages of the unit's keys end here
-  int prefix_n;     // pages below it come from the prefix's list
-  const int* prefix;
   int base, cur, next;
 };
 __device__ __forceinline__ int paged_page_at(const PagedParams& p, const PagedPages& g, int i) {
   if (i >= g.n) return -1;  // past the unit's keys: read as zeros
-  const int id = i < g.prefix_n ? g.prefix[i] : g.list[i];
-  if (id < 0 || id >= p.num_pages) {
-    int abort_flag = 0;
-    report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
-    return -1;
-  }
-  return id;
+  return i < (p.prefix_len >> p.page_shift) ? p.prefix_pages[i] : g.list[i];
 }
-__device__ __forceinline__ void paged_pages_begin(const PagedParams& p, const PagedPhase& ph,
-                                                  const PagedItem& it, PagedPages& g) {
+__device__ __forceinline__ void paged_pages_begin(const PagedParams& p, const PagedItem& it,
+                                                  PagedPages& g) {
   g.list = p.page_table + (long long)it.b * p.max_pages;
-  g.prefix = p.prefix_pages;
-  g.prefix_n = p.prefix_len >> p.page_shift;
-  g.n = (it.k_hi + p.page_size - 1) >> p.page_shift;
+  g.n = it.nj == 0 ? 0 : (it.k_hi + p.page_size - 1) >> p.page_shift;
   g.base = it.key >> p.page_shift;
   g.cur = paged_page_at(p, g, g.base + (int)lane_id());
   g.next = paged_page_at(p, g, g.base + 32 + (int)lane_id());
 }
-// The page number of page i (uniform or not; all lanes call it), i at most
-// 31 past the last call's.
-__device__ __forceinline__ void paged_pages_advance(const PagedParams& p, PagedPages& g, int last) {
-  if (last >= g.base + 32) {
+
+// A producer warp's loads of one 128-key tile of K (or V): one box per page
+// (at most 128 rows) and 64 channels, a lane to a box.  A box takes the warp
+// about 70 cycles to issue, 16 of them (pages of 16 keys, d = 128) half of the
+// time in which a tile arrives: K and V have a warp each.
+struct PagedBox {
+  bool on;       // the lane has a box
+  int sub;       // its page among the tile's
+  int x;         // its first channel
+  int dst;       // its place in the tile, bytes
+  int in_page;   // bits of the key that give its first row in the page
+};
+template <int D>
+__device__ __forceinline__ PagedBox paged_box(const PagedParams& p) {
+  const int lane = (int)lane_id(), rows = min(p.page_size, kTile), per = kTile / rows;
+  const int half = lane / per;
+  PagedBox b;
+  b.on = half < D / 64;
+  b.sub = lane % per;
+  b.x = half * 64;
+  b.dst = half * (kTile * 128) + b.sub * rows * 128;
+  b.in_page = (p.page_size - 1) & ~(rows - 1);
+  return b;
+}
+template <int D>
+__device__ __forceinline__ void paged_load_tile(const PagedParams& p, const PagedBox& box,
+                                                const CUtensorMap* map, PagedPages& g, int h,
+                                                int key, uint8_t* dst, uint64_t* bar) {
+  const int first = key >> p.page_shift;
+  // A tile's pages are a power of two in number, and runs of them start with
+  // the segment's first page: they never straddle the 32 at hand.
+  if (first >= g.base + 32) {
     g.base += 32;
     g.cur = g.next;
     g.next = paged_page_at(p, g, g.base + 32 + (int)lane_id());
   }
+  int id = __shfl_sync(0xffffffffu, g.cur, (first + box.sub - g.base) & 31);
+  if (lane_id() == 0) mbar_arrive_expect_tx(bar, kTile * D * 2);
+  __syncwarp();
+  if (box.on) {
+    if (id < 0 || id >= p.num_pages) {
+      // Past the unit's keys, or no page: read as zeros, from past the map.
+      int abort_flag = 0;
+      if (first + box.sub < g.n) report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
+      id = p.num_pages;
+    }
+    tma_load_3d(dst + box.dst, map, bar, box.x, key & box.in_page,
+                id * p.Hkv + (id == p.num_pages ? 0 : h));
+  }
 }
 
-// The producer warp's loads of a 128-key tile of K and of V: one box per page
-// (at most 128 rows) and 64 channels of each, a lane to a box; 32 lanes are
-// enough (pages of 16 keys, d = 128).
-struct PagedBox {
-  int kind;         // 0: a box of K, 1: of V, 2: none
-  int sub;          // the box's page among the tile's
-  int x;            // its first channel
-  int dst;          // its place in the tile, bytes
-  int in_page;      // bits of the key that give the box's first row in a page
-  int last;         // pages of the tile - 1
-};
-template <int D>
-__device__ __forceinline__ PagedBox paged_box(const PagedParams& p, int lane) {
-  const int rows = min(p.page_size, kTile), per = kTile / rows;
-  PagedBox b;
-  b.sub = lane % per;
-  const int half = lane / per % (D / 64);
-  b.kind = min(lane / (per * (D / 64)), 2);
-  b.x = half * 64;
-  b.dst = half * (kTile * 128) + b.sub * rows * 128;
-  b.in_page = (p.page_size - 1) & ~(rows - 1);
-  b.last = per - 1;
-  return b;
-}
-template <int D>
-__device__ __forceinline__ void paged_load_pair(const PagedParams& p, const PagedBox& box,
-                                                const CUtensorMap* tk, const CUtensorMap* tv,
-                                                PagedPages& g, int h, int key, uint8_t* dst_k,
-                                                uint64_t* bar_k, uint8_t* dst_v,
-                                                uint64_t* bar_v) {
-  const int first = key >> p.page_shift;
-  // A tile's pages lie among the 32 at hand or among the next ones: runs of
-  // box.last + 1 pages (a power of two) from the segment's first page on.
-  paged_pages_advance(p, g, first + box.last);
-  if (lane_id() == 0) {
-    mbar_arrive_expect_tx(bar_k, kTile * D * 2);
-    mbar_arrive_expect_tx(bar_v, kTile * D * 2);
+// The two producer warps of a paged kernel.  The K warp walks the CTA's range
+// of the list, publishes the segments in the item ring (kRing slots), each as
+// soon as the one before has its first tile on the way, loads Q (load_q) and
+// K; the V warp follows the ring.  K and V tiles take the slots of the K/V
+// ring (S of them, tile_bytes each) in turn.  `ends` records end the list.
+template <int D, int S, int kRing, class Smem, class LoadQ>
+__device__ __forceinline__ void paged_produce_k(const PagedParams& p, const PagedPhase& ph,
+                                                Smem& sm, const CUtensorMap* tk, PagedWalk& walk,
+                                                int ends, LoadQ&& load_q) {
+  volatile int* abortf = &sm.abort_flag;
+  const int lane = (int)lane_id();
+  const PagedBox box = paged_box<D>(p);
+  bool ok = true;
+  int c = 0;  // ring uses
+  if (walk.g >= walk.hi && lane == 0) {
+    PagedRec r = {};
+    r.total = walk.total;
+    *reinterpret_cast<PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes) = r;
   }
-  const int id = __shfl_sync(0xffffffffu, g.cur, (first + box.sub - g.base) & 31);
-  const int z = id < 0 ? p.num_pages * p.Hkv : id * p.Hkv + h;  // past the map: zeros
+  auto publish = [&](int m, const PagedItem& it) {
+    const int is = m % kRing;
+    if (m >= kRing)
+      ok = mbar_wait(&sm.item_empty[is], (m / kRing - 1) & 1, p.status, abortf, kSitePgItemEmpty);
+    ok = __all_sync(0xffffffffu, ok);
+    if (ok && lane == 0) {
+      sm.item[is] = it;
+      mbar_arrive(&sm.item_full[is]);
+    }
+  };
+  PagedItem it = paged_next(p, ph, walk);
+  publish(0, it);
+  PagedPages pages;
+  if (!it.end) paged_pages_begin(p, it, pages);
+  for (int m = 0; ok && !it.end; ++m) {
+    PagedItem after;
+    PagedPages after_pages;
+    auto look_ahead = [&] {
+      after = paged_next(p, ph, walk);
+      publish(m + 1, after);
+      if (!after.end) paged_pages_begin(p, after, after_pages);
+    };
+    if (it.nj == 0) {
+      look_ahead();
+    } else {
+      ok = load_q(it);
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    for (int j = 0; j < it.nj && ok; ++j, c += 2) {
+      const int slot = c % S;
+      if (c >= S)
+        ok = mbar_wait(&sm.kv_empty[slot], (c / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      paged_load_tile<D>(p, box, tk, pages, it.h, it.key + j * kTile, sm.kv[slot],
+                         &sm.kv_full[slot]);
+      if (j == 0) look_ahead();
+    }
+    it = after;
+    pages = after_pages;
+    if (ok && it.end)
+      for (int e = 1; e < ends && ok; ++e) publish(m + 1 + e, it);
+  }
+  // A CTA without work has published one end so far.
+  if (ok && walk.tiles == 0 && walk.first)
+    for (int e = 1; e < ends && ok; ++e) publish(e, it);
+  if (!ok && lane == 0) {
+    // Let the copies already issued land before the CTA exits.
+    for (int cc = c - 2; cc >= 0 && cc > c - 2 - S; cc -= 2)
+      drain_wait(&sm.kv_full[cc % S], (cc / S) & 1);
+  }
   __syncwarp();
-  if (box.kind < 2)
-    tma_load_3d((box.kind ? dst_v : dst_k) + box.dst, box.kind ? tv : tk,
-                box.kind ? bar_v : bar_k, box.x, key & box.in_page, z);
+}
+
+template <int D, int S, int kRing, class Smem>
+__device__ __forceinline__ void paged_produce_v(const PagedParams& p, Smem& sm,
+                                                const CUtensorMap* tv) {
+  volatile int* abortf = &sm.abort_flag;
+  const int lane = (int)lane_id();
+  const PagedBox box = paged_box<D>(p);
+  bool ok = true;
+  int c = 1;
+  // Item m, and its page numbers, if it has been published (or: waited for).
+  auto take = [&](int m, bool wait, PagedItem& it, PagedPages& pages) -> bool {
+    const int is = m % kRing;
+    bool there = mbar_test_wait(&sm.item_full[is], (m / kRing) & 1);
+    if (!there && wait) {
+      ok = mbar_wait(&sm.item_full[is], (m / kRing) & 1, p.status, abortf, kSitePgItemFull);
+      there = ok;
+    }
+    there = __all_sync(0xffffffffu, there);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!there) return false;
+    it = sm.item[is];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.item_empty[is]);
+    if (!it.end) paged_pages_begin(p, it, pages);
+    return true;
+  };
+  PagedItem it;
+  PagedPages pages;
+  it.end = 1;
+  take(0, true, it, pages);
+  for (int m = 0; ok && !it.end; ++m) {
+    PagedItem after;
+    PagedPages after_pages;
+    bool have = false;
+    after.end = 1;
+    for (int j = 0; j < it.nj && ok; ++j, c += 2) {
+      const int slot = c % S;
+      if (c >= S)
+        ok = mbar_wait(&sm.kv_empty[slot], (c / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      paged_load_tile<D>(p, box, tv, pages, it.h, it.key + j * kTile, sm.kv[slot],
+                         &sm.kv_full[slot]);
+      if (!have) have = take(m + 1, false, after, after_pages);
+    }
+    if (ok && !have) take(m + 1, true, after, after_pages);
+    it = after;
+    pages = after_pages;
+  }
+  if (!ok && lane == 0) {
+    for (int cc = c - 2; cc >= 0 && cc > c - 2 - S; cc -= 2)
+      drain_wait(&sm.kv_full[cc % S], (cc / S) & 1);
+  }
+  __syncwarp();
 }
 
 }  // namespace fa

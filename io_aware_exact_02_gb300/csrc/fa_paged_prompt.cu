@@ -10,9 +10,9 @@
 // tensor core: while one exponentiates, the other tile's products run.  The
 // softmax step is the dense forward's (fa_softmax.cuh).
 //
-// Warps: 0-3 and 4-7 softmax (and results) of Q tiles 0 and 1, 8 producer
-// (TMA: a lane per page box), 9 issues the products.  Tensor memory: S / P of
-// the tiles at columns 0 and 128, O at 256 and 256 + d.
+// Warps: 0-3 and 4-7 softmax (and results) of Q tiles 0 and 1, 8 and 10 load K
+// and V (TMA: a lane per page box), 9 issues the products, 11 is idle.  Tensor
+// memory: S / P of the tiles at columns 0 and 128, O at 256 and 256 + d.
 #include "fa_internal.h"
 #include "fa_paged.cuh"
 #include "fa_paged_launch.h"
@@ -24,7 +24,7 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kItemRing = 4;
-constexpr int kPromptThreads = 320;
+constexpr int kPromptThreads = 384;
 
 template <int D>
 struct PromptCfg {
@@ -49,14 +49,6 @@ struct alignas(1024) PromptSmem {
   uint32_t tmem_base;
   int abort_flag;
 };
-
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
-  const uint32_t a = smem_u32(bar);
-  const unsigned long long t0 = globaltimer_ns();
-  while (!mbar_try_wait(a, parity)) {
-    if (globaltimer_ns() - t0 > 100000000ull) return;  // 100 ms
-  }
-}
 
 // Key tiles of the segment that Q tile t's rows see (0: it has no rows, or
 // they see none).
@@ -83,7 +75,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abortf = &sm.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5;
-  constexpr int kWarpLoad = 8, kWarpMma = 9;
+  constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpLoadV = 10;
 
   if (tid == 0) {
     mbar_init(&sm.q_full, 1);
@@ -101,7 +93,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     }
     for (int i = 0; i < kItemRing; ++i) {
       mbar_init(&sm.item_full[i], 1);
-      mbar_init(&sm.item_empty[i], 1 + 8);  // the issuing thread, eight softmax warps
+      // Read by the issuing thread, the V warp and the eight softmax warps.
+      mbar_init(&sm.item_empty[i], 2 + 8);
     }
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -142,37 +135,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   };
 
   if (warp == kWarpLoad) {
-    // ------------------------------------------------------------ producer
-    const int lane = (int)lane_id();
-    int c = 0, n_q = 0;
-    bool ok = true;
-    if (walk.g >= walk.hi && lane == 0) {
-      PagedRec r = {};
-      r.total = walk.total;
-      *reinterpret_cast<PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes) = r;
-    }
-    const PagedBox box = paged_box<D>(p, lane);
-    for (int m = 0; ok; ++m) {
-      const int is = m % kItemRing;
-      if (m >= kItemRing)
-        ok = mbar_wait(&sm.item_empty[is], (m / kItemRing - 1) & 1, p.status, abortf, kSitePgItemEmpty);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const PagedItem it = paged_next(p, ph, walk);
-      if (lane == 0) {
-        sm.item[is] = it;
-        mbar_arrive(&sm.item_full[is]);
-      }
-      if (it.end) break;
-      const int nmax = max(it.end ? 0 : tile_steps(p, ph, it, 0), tile_steps(p, ph, it, 1));
-      if (nmax == 0) continue;
-      PagedPages pages;
-      paged_pages_begin(p, ph, it, pages);
-      if (n_q > 0)
-        ok = mbar_wait(&sm.q_empty, (n_q - 1) & 1, p.status, abortf, kSitePgQEmpty);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (lane == 0) {
+    // ------------------------------------------------------------ Q and K
+    int n_q = 0;  // units loaded
+    paged_produce_k<D, S, kItemRing>(p, ph, sm, &tk, walk, 1, [&](const PagedItem& it) {
+      if (n_q > 0 &&
+          !mbar_wait(&sm.q_empty, (n_q - 1) & 1, p.status, abortf, kSitePgQEmpty))
+        return false;
+      if (lane_id() == 0) {
         mbar_arrive_expect_tx(&sm.q_full, 2 * ph.tile_tokens * p.G * D * 2);
         for (int t = 0; t < 2; ++t)
           for (int h = 0; h < D / 64; ++h)
@@ -180,26 +149,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         it.tok0 + t * ph.tile_tokens);
       }
       ++n_q;
-      for (int j = 0; j < nmax; ++j, c += 2) {
-        // K into one slot of the ring, V into the next, once both are free.
-        const int sk = c % S, sv = (c + 1) % S;
-        if (c >= S)
-          ok = mbar_wait(&sm.kv_empty[sk], (c / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
-        if (ok && c + 1 >= S)
-          ok = mbar_wait(&sm.kv_empty[sv], ((c + 1) / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        paged_load_pair<D>(p, box, &tk, &tv, pages, it.h, it.key + j * kTile, sm.kv[sk],
-                           &sm.kv_full[sk], sm.kv[sv], &sm.kv_full[sv]);
-      }
-    }
-    if (!ok && lane == 0) {
-      // Let the copies already issued land before the CTA exits.
-      if (n_q > 0) drain_wait(&sm.q_full, (n_q - 1) & 1);
-      for (int cc = c - 1; cc >= 0 && cc >= c - S; --cc)
-        drain_wait(&sm.kv_full[cc % S], (cc / S) & 1);
-    }
+      return true;
+    });
+    if (*abortf && lane_id() == 0 && n_q > 0) drain_wait(&sm.q_full, (n_q - 1) & 1);
     __syncwarp();
+  } else if (warp == kWarpLoadV) {
+    // ------------------------------------------------------------ V
+    paged_produce_v<D, S, kItemRing>(p, sm, &tv);
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ products
     if (lane_id() == 0) {
@@ -299,7 +255,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       drain_wait(&sm.drain, 0);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ softmax
     const int t = warp >> 2;  // Q tile
     const int r = tid & 127;  // row of the tile
