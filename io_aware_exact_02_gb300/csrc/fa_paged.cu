@@ -85,6 +85,7 @@ struct alignas(1024) DecodeSmem {
   uint64_t drain;
   PagedItem item[kItemRing];
   PagedScan scan;
+  int of_unit[8];                // the issuing thread's: tiles and item parity of its units
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -154,9 +155,9 @@ __device__ __forceinline__ float reduce_cols(const float (&x)[N], Op op) {
 #pragma unroll
   for (int i = 0; i < N; ++i) y[i] = x[i];
   const int lane = (int)lane_id();
-  int bit = 16;
 #pragma unroll
-  for (int h = N / 2; h >= 1; h >>= 1, bit >>= 1) {
+  for (int h = N / 2; h >= 1; h /= 2) {
+    const int bit = h * (32 / N);
     const bool up = (lane & bit) != 0;
 #pragma unroll
     for (int i = 0; i < h; ++i) {
@@ -266,7 +267,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       int s_m = 0, s_u = 0;             // its item's, its group
       int p_nj = 0, p_j = 0, p_n = -1;  // the unit of the next P V product
       int ob = 0, p_u = 0;              // its O, its group
-      int of_unit[8];                   // tiles and item parity of the units begun, by number % 8
       uint32_t idle = 0;
       unsigned long long t0 = 0;
       for (;;) {
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                    desc_plus(qd, (kk >> 2) * (N * 128) + (kk & 3) * 32), id_s, kk > 0);
           tc_commit(&sm.s_full[sb]);
           tc_commit(&sm.kv_empty[slot]);
-          if (s_j == 0) of_unit[s_n & 7] = 2 * s_nj + (s_m & 1);
+          if (s_j == 0) sm.of_unit[s_n & 7] = 2 * s_nj + (s_m & 1);
           ++gs;
           if (++s_j == s_nj) {
             tc_commit(&sm.q_empty[qb]);
@@ -314,8 +314,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         if (gp < gs) {
           if (p_j == p_nj) {
             ++p_n;
-            p_nj = of_unit[p_n & 7] >> 1;
-            ob = of_unit[p_n & 7] & 1;
+            p_nj = sm.of_unit[p_n & 7] >> 1;
+            ob = sm.of_unit[p_n & 7] & 1;
             p_u = kHalves ? 0 : ob;
             p_j = 0;
           }
@@ -415,6 +415,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         for (int n = 0; n < rows; ++n) min_lim = min(min_lim, sm.lim[buf][n]);
       }
       float ref[NC], l[NC];
+      float my_ref = kNoRef;  // thread n < NC: ref[n], for the unit's end
 #pragma unroll
       for (int n = 0; n < NC; ++n) ref[n] = kNoRef, l[n] = 0.f;
       const uint32_t colO = tmem + lane_base + Cfg::col_o(m & 1) + col0;
@@ -453,6 +454,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           if (vote_any(bar, Cfg::kGroup, fail)) {
             fail = true;
             break;
+          }
+          if (key_t < NC) {
+            const float4 q = sm.top[buf][col0 + key_t];
+            my_ref = fmaxf(fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w)), my_ref);
           }
           float alpha[NC];
 #pragma unroll
@@ -512,9 +517,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       {
         const float x = reduce_cols<NC>(l, [](float a, float b) { return a + b; });
         if (NC == 32 || (lane & 1) == 0) sm.sum[buf][warp & 3][col0 + col_of_lane<NC>()] = x;
-#pragma unroll
-        for (int n = 0; n < NC; ++n)
-          if (key_t == n) sm.ref[buf][col0 + n] = ref[n];
+        if (key_t < NC) sm.ref[buf][col0 + key_t] = my_ref;
       }
       if (vote_any(bar, Cfg::kGroup, fail)) break;
       const bool merge = it.first && ph.pre_o != nullptr;

@@ -213,12 +213,6 @@ struct PagedItem {
   int tile0;      // key tiles of the CTA's segments before this one
 };
 
-struct PagedScan {
-  long long warp_sum[32];
-  long long total, found_excl;
-  int found_b;
-};
-
 // A CTA's walk along its range of the list.
 struct PagedWalk {
   long long g, hi, total;
@@ -227,67 +221,92 @@ struct PagedWalk {
   bool first;
 };
 
+struct PagedScan {
+  long long warp_sum[32];
+  long long excl, head;  // of the sequence that holds the CTA's first tile
+  PagedSeq s;
+  int b;
+};
+
 // All threads of the CTA: the list's length and the sequence that holds the
-// CTA's first tile.
+// CTA's first tile, by one scan of the sequences' costs where a thread has a
+// sequence at most, else by a sum and a second pass.
 __device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhase& ph,
                                            PagedScan& sc, PagedWalk& w) {
   const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31, nw = nt >> 5;
   const int B = ph.whole_batch ? 1 : p.B;
-  auto cost = [&](int b) -> long long {
-    if (b >= B) return 0;
-    const PagedSeq s = paged_seq(p, ph, b);
-    return paged_head_cost(p, ph, s) * p.Hkv;
-  };
-  const long long mine = cost(tid);
-  long long sum = mine;
-  for (int b = tid + nt; b < B; b += nt) sum += cost(b);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) sc.warp_sum[warp] = sum;
-  __syncthreads();
-  long long total = 0;
-  for (int i = 0; i < nw; ++i) total += sc.warp_sum[i];
-  const PagedShare share(total, gridDim.x);
-  const long long lo = share.lo(blockIdx.x);
-  w.total = total;
-  w.g = lo;
-  w.hi = share.lo(blockIdx.x + 1);
-  w.first = true;
-  w.tiles = 0;
-  if (w.g >= w.hi) return;  // idle CTA; uniform in the CTA
-  long long run = 0;
-  for (int b0 = 0; b0 < B; b0 += nt) {
-    const long long c = b0 == 0 ? mine : cost(b0 + tid);
-    long long inc = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
+  PagedSeq s;
+  long long head = 0, cost = 0;
+  auto look = [&](int b) {
+    cost = 0;
+    if (b < B) {
+      s = paged_seq(p, ph, b);
+      head = paged_head_cost(p, ph, s);
+      cost = head * p.Hkv;
     }
-    __syncthreads();  // warp_sum was read
-    if (lane == 31) sc.warp_sum[warp] = inc;
+  };
+  // The sum of the costs of the warps before this one's and of all.
+  auto sums = [&](long long of_warp, long long& before, long long& all) {
+    if (lane == 31) sc.warp_sum[warp] = of_warp;
     __syncthreads();
-    long long before = run, chunk = 0;
+    before = all = 0;
     for (int i = 0; i < nw; ++i) {
       if (i < warp) before += sc.warp_sum[i];
-      chunk += sc.warp_sum[i];
+      all += sc.warp_sum[i];
     }
-    const long long excl = before + inc - c;
-    if (c > 0 && excl <= lo && lo < excl + c) {
-      sc.found_b = b0 + tid;
-      sc.found_excl = excl;
+  };
+  auto scan = [&](long long x) {  // inclusive, over the warp
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
-    run += chunk;
-    if (lo < run) break;
+    return x;
+  };
+  long long total = 0, before, all, inc = 0;
+  if (B > nt) {
+    for (int b = tid; b < B; b += nt) {
+      look(b);
+      inc += cost;
+    }
+    sums(scan(inc), before, total);
+    __syncthreads();
   }
-  __syncthreads();
-  w.b = sc.found_b;
-  w.s = paged_seq(p, ph, w.b);
+  long long run = 0;
+  for (int b0 = 0; b0 < B; b0 += nt) {
+    look(b0 + tid);
+    inc = scan(cost);
+    sums(inc, before, all);
+    if (B <= nt) total = all;
+    const PagedShare share(total, gridDim.x);
+    w.total = total;
+    w.g = share.lo(blockIdx.x);
+    w.hi = share.lo(blockIdx.x + 1);
+    const long long excl = run + before + inc - cost;
+    if (cost > 0 && excl <= w.g && w.g < excl + cost) {
+      sc.b = b0 + tid;
+      sc.excl = excl;
+      sc.head = head;
+      sc.s = s;
+    }
+    run += all;
+    __syncthreads();
+    if (w.g < run) break;  // found
+  }
+}
+
+// The K warp's start of the walk.
+__device__ __forceinline__ void paged_walk_begin(const PagedParams& p, const PagedPhase& ph,
+                                                 const PagedScan& sc, PagedWalk& w) {
+  w.first = true;
+  w.tiles = 0;
+  if (w.g >= w.hi) return;  // idle CTA
+  w.b = sc.b;
+  w.s = sc.s;
   w.units = paged_units(ph, w.s);
-  long long off = lo - sc.found_excl;
-  const long long head = paged_head_cost(p, ph, w.s);
-  w.h = (int)paged_div(off, head);
-  off -= w.h * head;
+  long long off = w.g - sc.excl;
+  w.h = (int)paged_div(off, sc.head);
+  off -= w.h * sc.head;
   w.i = 0;
   if (!p.causal || ph.whole_batch) {  // units of equal cost
     const int c = max(1, paged_unit_tiles(p, ph, w.s, 0));
@@ -478,6 +497,7 @@ __device__ __forceinline__ void paged_produce_k(const PagedParams& p, const Page
       mbar_arrive(&sm.item_full[is]);
     }
   };
+  paged_walk_begin(p, ph, sm.scan, walk);
   PagedItem it = paged_next(p, ph, walk);
   publish(0, it);
   PagedPages pages;
