@@ -39,7 +39,6 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kItemRing = 8;  // even: an item's slot belongs to one warpgroup
-constexpr int kDecodeThreads = 384;
 constexpr int kCompute = 256;  // threads of the compute warps
 constexpr int kSBufs = 4;      // S buffers, shared out among the groups
 // A row's reference maximum before it has seen a key: finite, so that the
@@ -170,7 +169,7 @@ __device__ __forceinline__ float reduce_cols(const float (&x)[N], Op op) {
 }
 
 template <int D, int N>
-__global__ void __launch_bounds__(kDecodeThreads, 1)
+__global__ void __launch_bounds__(kPagedThreads, 1)
     fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tq,
                            const __grid_constant__ CUtensorMap tk,
                            const __grid_constant__ CUtensorMap tv, const PagedParams p,
@@ -220,7 +219,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   }
   // Q rows the boxes do not fill (N past the unit's heads) stay zero: their
   // columns of S are never used, and cost nothing as zeros.
-  for (int i = tid; i < (int)sizeof(sm.q) / 16; i += kDecodeThreads)
+  for (int i = tid; i < (int)sizeof(sm.q) / 16; i += kPagedThreads)
     reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   tc_fence_before();
@@ -234,6 +233,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 
   if (warp == kWarpLoad) {
     // ------------------------------------------------------------ Q and K
+    setmaxnreg_dec<kPagedRegsLoad>();
     int n_q = 0;  // units loaded
     paged_produce_k<D, S, kItemRing>(p, ph, sm, &tk, walk, Cfg::kGroups, [&](const PagedItem& it) {
       const int qb = n_q & 1;
@@ -253,9 +253,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     __syncwarp();
   } else if (warp == kWarpLoadV) {
     // ------------------------------------------------------------ V
+    setmaxnreg_dec<kPagedRegsLoad>();
     paged_produce_v<D, S, kItemRing>(p, sm, &tv);
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ products
+    setmaxnreg_dec<kPagedRegsLoad>();
     if (lane_id() == 0) {
       const uint32_t id_s = idesc_bf16(128, N, false, false);
       const uint32_t id_o = idesc_bf16(128, N, true, false);
@@ -366,6 +368,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     __syncwarp();
   } else if (warp < 8) {
     // ------------------------------------------------------------ compute
+    setmaxnreg_inc<kPagedRegsCompute>();
     const int wg = warp >> 2, key_t = tid & 127, lane = tid & 31;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const float c2 = p.scale_log2, ninf = __int_as_float(0xff800000);
@@ -599,6 +602,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
       }
       // (The next unit's first vote comes before P is written again.)
     }
+  } else {
+    // Idle: its registers go to the compute warps.
+    setmaxnreg_dec<kPagedRegsLoad>();
   }
 
   tc_fence_before();
@@ -731,12 +737,11 @@ int launch_decode(const PagedMaps& t, const PagedParams& p, const PagedPhase& ph
   static_assert(sizeof(DecodeSmem<D, N>) + 1024 <= 232448,
                 "decode shared memory above the 227 KB a CTA may have");
   cudaLaunchConfig_t c = base;
-  c.blockDim = dim3(kDecodeThreads, 1, 1);
+  c.blockDim = dim3(kPagedThreads, 1, 1);
   c.dynamicSmemBytes = sizeof(DecodeSmem<D, N>) + 1024;
-  if (cudaFuncSetAttribute(fa_paged_decode_kernel<D, N>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)c.dynamicSmemBytes) != cudaSuccess ||
-      cudaLaunchKernelEx(&c, fa_paged_decode_kernel<D, N>, t.q, t.k, t.v, p, ph) != cudaSuccess) {
+  if (paged_kernel_ready(fa_paged_decode_kernel<D, N>, c.dynamicSmemBytes) != FA_OK)
+    return FA_ERR_LAUNCH;
+  if (cudaLaunchKernelEx(&c, fa_paged_decode_kernel<D, N>, t.q, t.k, t.v, p, ph) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
   }

@@ -82,6 +82,14 @@ __device__ __forceinline__ PagedRow paged_row(const int* cu_q, const int* seq_le
 // timing.  Every CTA derives its range from the tables itself: no launch
 // needs the lengths on the host.
 
+// Registers of the paged kernels' twelve warps: launched with kPagedRegs a
+// thread, of which the third warpgroup (loads, products, one idle warp) hands
+// some to the two that compute.  The launchers refuse a kernel compiled with
+// fewer, whose setmaxnreg.inc would wait for registers that do not exist.
+constexpr int kPagedThreads = 384, kPagedRegs = 168, kPagedRegsCompute = 200, kPagedRegsLoad = 104;
+static_assert(2 * 128 * kPagedRegsCompute + 128 * kPagedRegsLoad <= kPagedThreads * kPagedRegs,
+              "register split above the launch's total");
+
 // Wait without the abort shortcut: used while winding down.
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);
@@ -487,7 +495,11 @@ __device__ __forceinline__ void paged_produce_k(const PagedParams& p, const Page
     r.total = walk.total;
     *reinterpret_cast<PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes) = r;
   }
-  auto publish = [&](int m, const PagedItem& it) {
+  // Publishes the walk's next segment as item m; false at the list's end (or
+  // after a failed wait).  Only this warp writes the records, so it can read
+  // them again later.
+  auto publish = [&](int m) -> bool {
+    const PagedItem it = paged_next(p, ph, walk);
     const int is = m % kRing;
     if (m >= kRing)
       ok = mbar_wait(&sm.item_empty[is], (m / kRing - 1) & 1, p.status, abortf, kSitePgItemEmpty);
@@ -496,44 +508,41 @@ __device__ __forceinline__ void paged_produce_k(const PagedParams& p, const Page
       sm.item[is] = it;
       mbar_arrive(&sm.item_full[is]);
     }
+    __syncwarp();
+    return ok && !it.end;
   };
   paged_walk_begin(p, ph, sm.scan, walk);
-  PagedItem it = paged_next(p, ph, walk);
-  publish(0, it);
-  PagedPages pages;
-  if (!it.end) paged_pages_begin(p, it, pages);
-  for (int m = 0; ok && !it.end; ++m) {
-    PagedItem after;
-    PagedPages after_pages;
+  PagedPages pages, after;
+  int m = 0;
+  bool more = publish(0);
+  if (more) paged_pages_begin(p, sm.item[0], pages);
+  for (; more; ++m) {
+    const int nj = sm.item[m % kRing].nj, h = sm.item[m % kRing].h;
+    int key = sm.item[m % kRing].key;
     auto look_ahead = [&] {
-      after = paged_next(p, ph, walk);
-      publish(m + 1, after);
-      if (!after.end) paged_pages_begin(p, after, after_pages);
+      more = publish(m + 1);
+      if (more) paged_pages_begin(p, sm.item[(m + 1) % kRing], after);
     };
-    if (it.nj == 0) {
+    if (nj == 0) {
       look_ahead();
     } else {
-      ok = load_q(it);
+      ok = load_q(sm.item[m % kRing]);
       ok = __all_sync(0xffffffffu, ok);
     }
-    for (int j = 0; j < it.nj && ok; ++j, c += 2) {
+    for (int j = 0; j < nj && ok; ++j, c += 2, key += kTile) {
       const int slot = c % S;
       if (c >= S)
         ok = mbar_wait(&sm.kv_empty[slot], (c / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      paged_load_tile<D>(p, box, tk, pages, it.h, it.key + j * kTile, sm.kv[slot],
-                         &sm.kv_full[slot]);
+      paged_load_tile<D>(p, box, tk, pages, h, key, sm.kv[slot], &sm.kv_full[slot]);
       if (j == 0) look_ahead();
     }
-    it = after;
-    pages = after_pages;
-    if (ok && it.end)
-      for (int e = 1; e < ends && ok; ++e) publish(m + 1 + e, it);
+    if (!ok) break;
+    pages = after;
   }
-  // A CTA without work has published one end so far.
-  if (ok && walk.tiles == 0 && walk.first)
-    for (int e = 1; e < ends && ok; ++e) publish(e, it);
+  // Item m is the first end.
+  for (int e = 1; e < ends && ok; ++e) publish(m + e);
   if (!ok && lane == 0) {
     // Let the copies already issued land before the CTA exits.
     for (int cc = c - 2; cc >= 0 && cc > c - 2 - S; cc -= 2)
@@ -550,8 +559,10 @@ __device__ __forceinline__ void paged_produce_v(const PagedParams& p, Smem& sm,
   const PagedBox box = paged_box<D>(p);
   bool ok = true;
   int c = 1;
-  // Item m, and its page numbers, if it has been published (or: waited for).
-  auto take = [&](int m, bool wait, PagedItem& it, PagedPages& pages) -> bool {
+  // Takes item m if it has been published (or: waits for it).
+  int nj, h, key, end, nj2, h2, key2, end2 = 1;
+  PagedPages pages, after;
+  auto take = [&](int m, bool wait, int& nj, int& h, int& key, int& end, PagedPages& pages) -> bool {
     const int is = m % kRing;
     bool there = mbar_test_wait(&sm.item_full[is], (m / kRing) & 1);
     if (!there && wait) {
@@ -561,34 +572,30 @@ __device__ __forceinline__ void paged_produce_v(const PagedParams& p, Smem& sm,
     there = __all_sync(0xffffffffu, there);
     ok = __all_sync(0xffffffffu, ok);
     if (!there) return false;
-    it = sm.item[is];
+    const PagedItem& it = sm.item[is];
+    nj = it.nj, h = it.h, key = it.key, end = it.end;
+    if (!end) paged_pages_begin(p, it, pages);
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.item_empty[is]);
-    if (!it.end) paged_pages_begin(p, it, pages);
     return true;
   };
-  PagedItem it;
-  PagedPages pages;
-  it.end = 1;
-  take(0, true, it, pages);
-  for (int m = 0; ok && !it.end; ++m) {
-    PagedItem after;
-    PagedPages after_pages;
+  end = 1;
+  take(0, true, nj, h, key, end, pages);
+  for (int m = 0; ok && !end; ++m) {
     bool have = false;
-    after.end = 1;
-    for (int j = 0; j < it.nj && ok; ++j, c += 2) {
+    for (int j = 0; j < nj && ok; ++j, c += 2, key += kTile) {
       const int slot = c % S;
       if (c >= S)
         ok = mbar_wait(&sm.kv_empty[slot], (c / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      paged_load_tile<D>(p, box, tv, pages, it.h, it.key + j * kTile, sm.kv[slot],
-                         &sm.kv_full[slot]);
-      if (!have) have = take(m + 1, false, after, after_pages);
+      paged_load_tile<D>(p, box, tv, pages, h, key, sm.kv[slot], &sm.kv_full[slot]);
+      if (!have) have = take(m + 1, false, nj2, h2, key2, end2, after);
     }
-    if (ok && !have) take(m + 1, true, after, after_pages);
-    it = after;
-    pages = after_pages;
+    if (ok && !have) take(m + 1, true, nj2, h2, key2, end2, after);
+    if (!ok) break;
+    nj = nj2, h = h2, key = key2, end = end2;
+    pages = after;
   }
   if (!ok && lane == 0) {
     for (int cc = c - 2; cc >= 0 && cc > c - 2 - S; cc -= 2)

@@ -24,12 +24,11 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kItemRing = 4;
-constexpr int kPromptThreads = 384;
 
 template <int D>
 struct PromptCfg {
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr uint32_t kTmemCols = 512;
   static __device__ __forceinline__ uint32_t col_s(int t) { return (uint32_t)t * 128u; }
   static __device__ __forceinline__ uint32_t col_o(int t) { return 256u + (uint32_t)t * D; }
@@ -39,6 +38,7 @@ template <int D>
 struct alignas(1024) PromptSmem {
   uint8_t q[2][PromptCfg<D>::kTileBytes];
   uint8_t kv[PromptCfg<D>::kStages][PromptCfg<D>::kTileBytes];
+  uint8_t out[8][4096];  // a softmax warp's 32 rows x 128 bytes on their way out
   uint64_t q_full, q_empty;
   uint64_t kv_full[PromptCfg<D>::kStages], kv_empty[PromptCfg<D>::kStages];
   uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2];
@@ -62,8 +62,97 @@ __device__ __forceinline__ int tile_steps(const PagedParams& p, const PagedPhase
   return x <= 0 ? 0 : min((x + kTile - 1) / kTile, it.nj);
 }
 
+// A softmax warp's rows of O out of tensor memory (at colO; ~0: zeros), times
+// `own`, plus `pre` times row `row` of pre_o (if given), to row dst_row (none
+// if negative) of `wide` (fp32) or of o (bf16).  A thread has a row, but rows
+// are stored by lanes that share them: 128 bytes of the warp's 32 rows at a
+// time through `out`, 16-byte chunk c of row r at c ^ (r % 8).  (A thread
+// storing its own row wrote 16 of its 256 or 512 bytes at a time: 10,000
+// cycles a unit.)  Not inlined: the softmax loop around it needs every
+// register, and addresses computed here would be kept through it.
+template <int D>
+__device__ __noinline__ void store_rows(uint32_t colO, float own, float pre, long long row,
+                                        long long dst_row, uint8_t* out, float* wide,
+                                        const float* pre_o, __nv_bfloat16* o) {
+  const int lane = (int)lane_id(), e = lane & 7;
+  uint8_t* const mine = out + lane * 128;
+  if (wide != nullptr || pre_o != nullptr) {
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = 0u;
+      if (colO != ~0u) {
+        tmem_ld32(colO + c * 32, w);
+        tmem_wait_ld(w);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        w[i] = own == 0.f ? 0u : __float_as_uint(__uint_as_float(w[i]) * own);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint4*>(mine + ((i ^ (lane & 7)) << 4)) =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      __syncwarp();
+#pragma unroll 2
+      for (int i = 0; i < 8; ++i) {
+        const int rr = i * 4 + lane / 8;
+        const long long to = __shfl_sync(0xffffffffu, dst_row, rr);
+        const long long from = __shfl_sync(0xffffffffu, row, rr);
+        const float f = __shfl_sync(0xffffffffu, pre, rr);
+        if (to < 0) continue;
+        float4 x = *reinterpret_cast<const float4*>(out + rr * 128 + ((e ^ (rr & 7)) << 4));
+        const int col = c * 32 + e * 4;
+        if (f != 0.f) {
+          const float4 y = *reinterpret_cast<const float4*>(pre_o + from * D + col);
+          x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+        }
+        if (wide != nullptr)
+          *reinterpret_cast<float4*>(wide + to * D + col) = x;
+        else
+          *reinterpret_cast<uint2*>(o + to * D + col) =
+              make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+      }
+      __syncwarp();
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = 0u;
+      if (colO != ~0u) {
+        tmem_ld32(colO + c * 64 + h * 32, w);
+        tmem_wait_ld(w);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        w[i] = own == 0.f ? 0u
+                          : pack_bf16x2(__uint_as_float(w[2 * i]) * own,
+                                        __uint_as_float(w[2 * i + 1]) * own);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(mine + (((4 * h + i) ^ (lane & 7)) << 4)) =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    __syncwarp();
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+      const int rr = i * 4 + lane / 8;
+      const long long to = __shfl_sync(0xffffffffu, dst_row, rr);
+      if (to >= 0)
+        *reinterpret_cast<uint4*>(o + to * D + c * 64 + e * 8) =
+            *reinterpret_cast<const uint4*>(out + rr * 128 + ((e ^ (rr & 7)) << 4));
+    }
+    __syncwarp();
+  }
+}
+
 template <int D, bool kNeg>
-__global__ void __launch_bounds__(kPromptThreads, 1)
+__global__ void __launch_bounds__(kPagedThreads, 1)
     fa_paged_prompt_kernel(const __grid_constant__ CUtensorMap tq,
                            const __grid_constant__ CUtensorMap tk,
                            const __grid_constant__ CUtensorMap tv, const PagedParams p,
@@ -112,7 +201,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (ph.tile_tokens * p.G < kTile) {
     // Rows no box fills: any finite values do (their results are not stored),
     // zeros never move the running maximum.
-    for (int i = tid; i < (int)sizeof(sm.q) / 16; i += kPromptThreads)
+    for (int i = tid; i < (int)sizeof(sm.q) / 16; i += kPagedThreads)
       reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
   }
@@ -136,6 +225,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
   if (warp == kWarpLoad) {
     // ------------------------------------------------------------ Q and K
+    setmaxnreg_dec<kPagedRegsLoad>();
     int n_q = 0;  // units loaded
     paged_produce_k<D, S, kItemRing>(p, ph, sm, &tk, walk, 1, [&](const PagedItem& it) {
       if (n_q > 0 &&
@@ -155,9 +245,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     __syncwarp();
   } else if (warp == kWarpLoadV) {
     // ------------------------------------------------------------ V
+    setmaxnreg_dec<kPagedRegsLoad>();
     paged_produce_v<D, S, kItemRing>(p, sm, &tv);
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ products
+    setmaxnreg_dec<kPagedRegsLoad>();
     if (lane_id() == 0) {
       const uint32_t id_s = idesc_bf16(128, 128, false, false);
       const uint32_t id_o = idesc_bf16(128, D, false, true);
@@ -257,6 +349,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     __syncwarp();
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax
+    setmaxnreg_inc<kPagedRegsCompute>();
     const int t = warp >> 2;  // Q tile
     const int r = tid & 127;  // row of the tile
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -341,42 +434,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         tc_fence_after();
       }
       const long long slot_row = ((long long)blockIdx.x * 2 + it.slot) * ph.slot_rows + t * kTile + r;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t w[32];
-        if (n_t > 0) {
-          tmem_ld32(colO + c * 32, w);
-          tmem_wait_ld(w);
-        }
-        if (!valid) continue;
-        float x[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = own == 0.f ? 0.f : __uint_as_float(w[i]) * own;
-        if (pre != 0.f) {
-          const float4* src = reinterpret_cast<const float4*>(ph.pre_o + row * D + c * 32);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 v = src[i];
-            x[4 * i] += pre * v.x, x[4 * i + 1] += pre * v.y;
-            x[4 * i + 2] += pre * v.z, x[4 * i + 3] += pre * v.w;
-          }
-        }
-        if (it.slot >= 0 || ph.out_o) {
-          float* dst = (it.slot >= 0 ? ph.slot_o + slot_row * D : ph.out_o + row * D) + c * 32;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            reinterpret_cast<float4*>(dst)[i] =
-                make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-        } else {
-          uint4 v[4];
-          uint32_t* o = reinterpret_cast<uint32_t*>(v);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-          uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + c * 32);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dst[i] = v[i];
-        }
-      }
+      store_rows<D>(n_t > 0 ? colO : ~0u, own, pre, row, valid ? (it.slot >= 0 ? slot_row : row) : -1,
+                    sm.out[warp], it.slot >= 0 ? ph.slot_o : ph.out_o,
+                    it.first ? ph.pre_o : nullptr, p.o);
       if (n_t > 0) {
         // O_t may now be overwritten by the next unit's first product.
         tc_fence_before();
@@ -392,6 +452,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           p.lse[row] = lse2 == ninf ? ninf : lse2 * kLn2;
       }
     }
+  } else {
+    // Idle: its registers go to the compute warps.
+    setmaxnreg_dec<kPagedRegsLoad>();
   }
 
   tc_fence_before();
@@ -408,12 +471,11 @@ int launch_prompt(const PagedMaps& t, const PagedParams& p, const PagedPhase& ph
   static_assert(sizeof(PromptSmem<D>) + 1024 <= 232448,
                 "prompt shared memory above the 227 KB a CTA may have");
   cudaLaunchConfig_t c = base;
-  c.blockDim = dim3(kPromptThreads, 1, 1);
+  c.blockDim = dim3(kPagedThreads, 1, 1);
   c.dynamicSmemBytes = sizeof(PromptSmem<D>) + 1024;
-  if (cudaFuncSetAttribute(fa_paged_prompt_kernel<D, kNeg>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)c.dynamicSmemBytes) != cudaSuccess ||
-      cudaLaunchKernelEx(&c, fa_paged_prompt_kernel<D, kNeg>, t.q, t.k, t.v, p, ph) !=
+  if (paged_kernel_ready(fa_paged_prompt_kernel<D, kNeg>, c.dynamicSmemBytes) != FA_OK)
+    return FA_ERR_LAUNCH;
+  if (cudaLaunchKernelEx(&c, fa_paged_prompt_kernel<D, kNeg>, t.q, t.k, t.v, p, ph) !=
           cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
