@@ -616,11 +616,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 }
 
 // Joins the parts of the units that were shared between CTAs.  The blocks of
-// a column of the grid look at one boundary between CTAs; they have work if it
-// is the first inside its unit.  The column's warps are spread over the
-// unit's rows, several to a row when the rows are few (decoding, where a unit
-// may have a part in every CTA); parts are added in list order within a warp
-// and the warps' sums in order, so the result does not depend on timing.
+// a column of the grid look at one boundary between CTAs; the columns of the
+// boundaries inside a unit share its rows, several warps to a row when the
+// rows are few; parts are added in list order within a warp and the warps'
+// sums in order, so the result does not depend on timing.
 constexpr int kMergeWarps = 8;
 
 template <int D>
@@ -634,18 +633,19 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
   const PagedRec rec = *reinterpret_cast<const PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes);
   if (!rec.split) return;
   const PagedShare parts(rec.total, p.ctas);
-  const long long before = parts.lo((int)blockIdx.x - 1);
-  if (before > rec.unit_start) return;  // an earlier boundary has the unit
+  const int c0 = parts.owner(rec.unit_start);  // the unit's first CTA, in its last segment's slot
+  const int c1 = parts.owner(rec.unit_end - 1);
+  const int n = c1 - c0 + 1;
+  const int slot0 = parts.lo(c0) < rec.unit_start ? 1 : 0;
+  // Block `y` of the unit's `ny`.
+  const int ny = (n - 1) * (int)gridDim.y;
+  const int y = ((int)blockIdx.x - c0 - 1) * (int)gridDim.y + (int)blockIdx.y;
   const float ninf = __int_as_float(0xff800000);
   const int rows = rec.ntok * p.G;
   int share = 1;  // warps to a row
-  while (share < kMergeWarps && 2 * share * rows <= (int)gridDim.y * kMergeWarps) share *= 2;
+  while (share < kMergeWarps && 2 * share * rows <= ny * kMergeWarps && 2 * share <= n) share *= 2;
   const int per_block = kMergeWarps / share, sub = warp % share;
-  const int c0 = (int)blockIdx.x - 1;  // the unit's first CTA, in its last segment's slot
-  const int c1 = parts.owner(rec.unit_end - 1);
-  const int n = c1 - c0 + 1;
-  const int slot0 = before < rec.unit_start ? 1 : 0;
-  for (int r0 = (int)blockIdx.y * per_block; r0 < rows; r0 += (int)gridDim.y * per_block) {
+  for (int r0 = y * per_block; r0 < rows; r0 += ny * per_block) {
     const int r = r0 + warp / share;
     const bool valid = r < rows;
     // Row r -> token and head, and its place in a slot: Q tiles of
