@@ -262,42 +262,58 @@ struct PagedParams {
   char* workspace;  // PagedWorkspace
 };
 
-// How a call runs: the rows of a unit in the attention of the sequences'
-// own keys and, with share, of the shared prefix (rows of the whole batch).
+// How a call runs: the rows of a unit in the attention of the sequences' own
+// keys (16, 32 or 64: the decode kernel; 256: the prompt kernel), and in that
+// of the shared prefix by the rows of the whole batch.  In a batch of long and
+// short sequences, those of up to small_rows rows go to the decode kernel and
+// the others to the prompt kernel: 30 decoding sequences and two prompt chunks
+// of 500 tokens took 88 us on the prompt kernel alone, whose Q tiles a
+// decoding sequence leaves almost empty.  A batch counts as mixed when its
+// rows are fewer than a prompt unit per sequence on average but max_q says
+// that one sequence has more than a decode unit, unless max_q makes all of
+// them equal.
 struct PagedForm {
-  int rows;         // 16, 32, 64: the decode kernel; 256: the prompt kernel
-  int share;        // the prefix is attended once for the batch
-  int prefix_rows;
+  int rows, small_rows, share, prefix_rows;
 };
 inline int paged_unit_rows(long long rows) {
   return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= kPagedDecodeRows ? 64 : kPairRows));
 }
-inline PagedForm paged_form(int T, int G, int max_q, int prefix_len) {
+inline PagedForm paged_form(int T, int B, int G, int max_q, int prefix_len) {
   PagedForm f;
   f.rows = paged_unit_rows((long long)(max_q < T ? max_q : T) * G);
+  f.small_rows = 0;
+  if (f.rows == kPairRows && B > 1 && G <= kPagedDecodeRows &&
+      (long long)T * G < (long long)kPairRows * B && (long long)B * max_q > T)
+    f.small_rows = paged_unit_rows(G);
   f.share = prefix_len > 0 ? 1 : 0;
   f.prefix_rows = paged_unit_rows((long long)T * G);
   return f;
 }
 
-// Byte offsets of the paged forward's workspace, 256-byte aligned: the split
-// records of the CTAs, their partial results (two slots each: fp32 O rows,
-// then the rows' logsumexp), and with a shared prefix its results, fp32
+// Byte offsets of the paged forward's workspace, 256-byte aligned: for the
+// units of `rows` (or prefix_rows) rows and for those of small_rows, the split
+// records of the CTAs and their partial results (two slots each: fp32 O rows,
+// then the rows' logsumexp); with a shared prefix its results, fp32
 // [T][Hq][d] and [T][Hq].
 struct PagedWorkspace {
-  size_t rec, slot_o, slot_lse, pre_o, pre_lse, total;
+  size_t rec[2], slot_o[2], slot_lse[2], pre_o, pre_lse, total;
 };
 constexpr size_t kPagedRecBytes = 64;
 inline PagedWorkspace paged_workspace_layout(int T, int Hq, int d, const PagedForm& f) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  const int rows = f.share && f.prefix_rows > f.rows ? f.prefix_rows : f.rows;
-  const size_t slots = (size_t)kPagedMaxCtas * 2 * (size_t)rows;
   PagedWorkspace w;
-  w.rec = 0;
-  w.slot_o = up(kPagedMaxCtas * kPagedRecBytes);
-  w.slot_lse = w.slot_o + up(slots * (size_t)d * sizeof(float));
-  w.pre_o = w.slot_lse + up(slots * sizeof(float));
+  size_t at = 0;
+  for (int k = 0; k < 2; ++k) {
+    const int rows = k == 1 ? f.small_rows
+                            : (f.share && f.prefix_rows > f.rows ? f.prefix_rows : f.rows);
+    const size_t slots = (size_t)kPagedMaxCtas * 2 * (size_t)rows;
+    w.rec[k] = at;
+    w.slot_o[k] = at + up(rows > 0 ? kPagedMaxCtas * kPagedRecBytes : 0);
+    w.slot_lse[k] = w.slot_o[k] + up(slots * (size_t)d * sizeof(float));
+    at = w.slot_lse[k] + up(slots * sizeof(float));
+  }
   const size_t pre = f.share ? (size_t)T * (size_t)Hq : 0;
+  w.pre_o = at;
   w.pre_lse = w.pre_o + up(pre * (size_t)d * sizeof(float));
   w.total = w.pre_lse + up(pre * sizeof(float));
   return w;

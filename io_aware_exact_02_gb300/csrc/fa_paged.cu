@@ -624,7 +624,9 @@ constexpr int kMergeWarps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const PagedParams p,
-                                                                          const PagedPhase ph) {
+                                                                          const PagedPhase ph0,
+                                                                          const PagedPhase ph1) {
+  const PagedPhase& ph = blockIdx.z == 0 ? ph0 : ph1;
   launch_dependents();
   wait_prior_grid();
   constexpr int kPer = D / 32;
@@ -739,7 +741,7 @@ int launch_decode(const PagedMaps& t, const PagedParams& p, const PagedPhase& ph
   cudaLaunchConfig_t c = base;
   c.blockDim = dim3(kPagedThreads, 1, 1);
   c.dynamicSmemBytes = sizeof(DecodeSmem<D, N>) + 1024;
-  if (paged_kernel_ready(fa_paged_decode_kernel<D, N>, c.dynamicSmemBytes) != FA_OK)
+  if (paged_kernel_ready<fa_paged_decode_kernel<D, N>>(c.dynamicSmemBytes) != FA_OK)
     return FA_ERR_LAUNCH;
   if (cudaLaunchKernelEx(&c, fa_paged_decode_kernel<D, N>, t.q, t.k, t.v, p, ph) != cudaSuccess) {
     cudaGetLastError();
@@ -748,22 +750,41 @@ int launch_decode(const PagedMaps& t, const PagedParams& p, const PagedPhase& ph
   return FA_OK;
 }
 
+// The merge of one phase's split units, or of two phases' (ph1 not null).
 template <int D>
-int launch_merge(const PagedParams& p, const PagedPhase& ph, const cudaLaunchConfig_t& base) {
+int launch_merge(const PagedParams& p, const PagedPhase& ph0, const PagedPhase* ph1,
+                 const cudaLaunchConfig_t& base) {
   cudaLaunchConfig_t c = base;
   c.blockDim = dim3(32 * kMergeWarps, 1, 1);
   c.dynamicSmemBytes = 0;
-  c.gridDim = dim3((unsigned)p.ctas, ph.slot_rows <= kPagedDecodeRows ? 4 : 16, 1);
-  if (cudaLaunchKernelEx(&c, fa_paged_merge_kernel<D>, p, ph) != cudaSuccess) {
+  c.gridDim = dim3((unsigned)p.ctas, ph0.slot_rows <= kPagedDecodeRows ? 4 : 16, ph1 ? 2 : 1);
+  if (cudaLaunchKernelEx(&c, fa_paged_merge_kernel<D>, p, ph0, ph1 ? *ph1 : ph0) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
   }
   return FA_OK;
 }
 
-// One phase: its attention kernel, then the merge of its split units.
+// One phase's attention kernel; fills in the phase's units of `rows` rows.
 template <int D>
-int launch_phase(const PagedParams& p, PagedPhase ph, int rows, cudaStream_t stream) {
+int launch_phase(const PagedParams& p, PagedPhase& ph, int rows, PagedMaps& t,
+                 const cudaLaunchConfig_t& c) {
+  const int tile_rows = rows <= kPagedDecodeRows ? rows : kTile;
+  ph.tile_tokens = tile_rows / p.G;
+  ph.unit_tokens = rows <= kPagedDecodeRows ? ph.tile_tokens : 2 * ph.tile_tokens;
+  ph.slot_rows = rows;
+  int rc = make_tmap_rows(p.q, p.Hq, p.T, p.q_stride, D, p.G, ph.tile_tokens, &t.q);
+  if (rc != FA_OK) return rc;
+  switch (rows) {
+    case 16: return launch_decode<D, 16>(t, p, ph, c);
+    case 32: return launch_decode<D, 32>(t, p, ph, c);
+    case 64: return launch_decode<D, 64>(t, p, ph, c);
+    default: return launch_paged_prompt(t, p, ph, D, c);
+  }
+}
+
+template <int D>
+int launch_paged_d(const PagedParams& p, cudaStream_t stream) {
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -772,48 +793,42 @@ int launch_phase(const PagedParams& p, PagedPhase ph, int rows, cudaStream_t str
   c.stream = stream;
   c.attrs = pdl;
   c.numAttrs = 1;
-  const int tile_rows = rows <= kPagedDecodeRows ? rows : kTile;
-  ph.tile_tokens = tile_rows / p.G;
-  ph.unit_tokens = rows <= kPagedDecodeRows ? ph.tile_tokens : 2 * ph.tile_tokens;
-  ph.slot_rows = rows;
+  const PagedForm f = paged_form(p.T, p.B, p.G, p.max_q, p.prefix_len);
+  const PagedWorkspace w = paged_workspace_layout(p.T, p.Hq, D, f);
+  const int box = p.page_size < kTile ? p.page_size : kTile;
   PagedMaps t;
   int rc;
-  if ((rc = make_tmap_rows(p.q, p.Hq, p.T, p.q_stride, D, p.G, ph.tile_tokens, &t.q)) != FA_OK ||
-      (rc = make_tmap_bhnd_rows(p.k_pages, p.num_pages * p.Hkv, p.page_size, D,
-                                p.page_size < kTile ? p.page_size : kTile, &t.k)) != FA_OK ||
-      (rc = make_tmap_bhnd_rows(p.v_pages, p.num_pages * p.Hkv, p.page_size, D,
-                                p.page_size < kTile ? p.page_size : kTile, &t.v)) != FA_OK)
+  if ((rc = make_tmap_bhnd_rows(p.k_pages, p.num_pages * p.Hkv, p.page_size, D, box, &t.k)) != FA_OK ||
+      (rc = make_tmap_bhnd_rows(p.v_pages, p.num_pages * p.Hkv, p.page_size, D, box, &t.v)) != FA_OK)
     return rc;
-  switch (rows) {
-    case 16: rc = launch_decode<D, 16>(t, p, ph, c); break;
-    case 32: rc = launch_decode<D, 32>(t, p, ph, c); break;
-    case 64: rc = launch_decode<D, 64>(t, p, ph, c); break;
-    default: rc = launch_paged_prompt(t, p, ph, D, c); break;
+  PagedPhase ph[2] = {};
+  for (int k = 0; k < 2; ++k) {
+    ph[k].rec = p.workspace + w.rec[k];
+    ph[k].slot_o = reinterpret_cast<float*>(p.workspace + w.slot_o[k]);
+    ph[k].slot_lse = reinterpret_cast<float*>(p.workspace + w.slot_lse[k]);
+    ph[k].n_max = 0x7fffffff;
   }
-  if (rc != FA_OK) return rc;
-  return launch_merge<D>(p, ph, c);
-}
-
-template <int D>
-int launch_paged_d(const PagedParams& p, cudaStream_t stream) {
-  const PagedForm f = paged_form(p.T, p.G, p.max_q, p.prefix_len);
-  const PagedWorkspace w = paged_workspace_layout(p.T, p.Hq, D, f);
-  PagedPhase ph = {};
-  ph.rec = p.workspace + w.rec;
-  ph.slot_o = reinterpret_cast<float*>(p.workspace + w.slot_o);
-  ph.slot_lse = reinterpret_cast<float*>(p.workspace + w.slot_lse);
   if (f.share) {
-    PagedPhase pre = ph;
+    PagedPhase pre = ph[0];
     pre.whole_batch = 1;
     pre.out_o = reinterpret_cast<float*>(p.workspace + w.pre_o);
     pre.out_lse = reinterpret_cast<float*>(p.workspace + w.pre_lse);
-    const int rc = launch_phase<D>(p, pre, f.prefix_rows, stream);
-    if (rc != FA_OK) return rc;
-    ph.key0 = p.prefix_len;
-    ph.pre_o = pre.out_o;
-    ph.pre_lse = pre.out_lse;
+    if ((rc = launch_phase<D>(p, pre, f.prefix_rows, t, c)) != FA_OK) return rc;
+    if ((rc = launch_merge<D>(p, pre, nullptr, c)) != FA_OK) return rc;
+    for (int k = 0; k < 2; ++k) {
+      ph[k].key0 = p.prefix_len;
+      ph[k].pre_o = pre.out_o;
+      ph[k].pre_lse = pre.out_lse;
+    }
   }
-  return launch_phase<D>(p, ph, f.rows, stream);
+  const bool mixed = f.small_rows > 0;
+  if (mixed) {
+    ph[1].n_max = f.small_rows / p.G;
+    ph[0].n_min = ph[1].n_max + 1;
+    if ((rc = launch_phase<D>(p, ph[1], f.small_rows, t, c)) != FA_OK) return rc;
+  }
+  if ((rc = launch_phase<D>(p, ph[0], f.rows, t, c)) != FA_OK) return rc;
+  return launch_merge<D>(p, ph[0], mixed ? &ph[1] : nullptr, c);
 }
 
 }  // namespace

@@ -106,6 +106,7 @@ struct PagedPhase {
   int unit_tokens;     // query tokens of a unit
   int tile_tokens;     // query tokens of a Q tile (decode: the unit's)
   int slot_rows;       // rows of a slot: 16 .. 64, or 256
+  int n_min, n_max;    // sequences of that many new tokens take part
   char* rec;           // PagedRec per CTA
   float* slot_o;       // [CTA][2][slot_rows][d]
   float* slot_lse;     // [CTA][2][slot_rows], log2 units
@@ -146,6 +147,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, const PagedP
     report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedRows);
     s.t0 = s.n = 0;
   }
+  if (s.n < ph.n_min || s.n > ph.n_max) s.n = 0;
   if (s.n > 0 && (s.len < 0 || s.len > (p.max_pages << p.page_shift))) {
     report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedLength);
     s.len = s.len < 0 ? 0 : p.max_pages << p.page_shift;
@@ -166,7 +168,7 @@ __device__ __forceinline__ int paged_unit_tiles(const PagedParams& p, const Page
   return x <= 0 ? 0 : (x + kTile - 1) / kTile;
 }
 __device__ __forceinline__ int paged_units(const PagedPhase& ph, const PagedSeq& s) {
-  return (s.n + ph.unit_tokens - 1) / ph.unit_tokens;
+  return s.n <= ph.unit_tokens ? (s.n > 0) : (s.n + ph.unit_tokens - 1) / ph.unit_tokens;
 }
 // Tiles of one head of a sequence.
 __device__ __forceinline__ long long paged_head_cost(const PagedParams& p, const PagedPhase& ph,
@@ -236,23 +238,37 @@ struct PagedScan {
   int b;
 };
 
-// All threads of the CTA: the list's length and the sequence that holds the
-// CTA's first tile, by one scan of the sequences' costs where a thread has a
-// sequence at most, else by a sum and a second pass.
+// The cost of sequence b (0 past the last), and of one of its heads.
+__device__ __forceinline__ long long paged_cost(const PagedParams& p, const PagedPhase& ph, int b,
+                                                int B, PagedSeq& s, long long& head) {
+  head = 0;
+  if (b < B) {
+    s = paged_seq(p, ph, b);
+    head = paged_head_cost(p, ph, s);
+  }
+  return head * p.Hkv;
+}
+__device__ __forceinline__ long long warp_scan(long long x) {  // inclusive
+  const int lane = (int)lane_id();
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// The list's length and the sequence that holds the CTA's first tile.  Up to
+// 32 sequences are left to the K warp alone (paged_walk_begin), a lane each.
+// More take all threads of the CTA: one scan of the sequences' costs where a
+// thread has one at most, else a sum and a second pass.
 __device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhase& ph,
                                            PagedScan& sc, PagedWalk& w) {
-  const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31, nw = nt >> 5;
   const int B = ph.whole_batch ? 1 : p.B;
+  if (B <= 32) return;
+  const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31, nw = nt >> 5;
   PagedSeq s;
-  long long head = 0, cost = 0;
-  auto look = [&](int b) {
-    cost = 0;
-    if (b < B) {
-      s = paged_seq(p, ph, b);
-      head = paged_head_cost(p, ph, s);
-      cost = head * p.Hkv;
-    }
-  };
+  long long head;
   // The sum of the costs of the warps before this one's and of all.
   auto sums = [&](long long of_warp, long long& before, long long& all) {
     if (lane == 31) sc.warp_sum[warp] = of_warp;
@@ -263,27 +279,16 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhas
       all += sc.warp_sum[i];
     }
   };
-  auto scan = [&](long long x) {  // inclusive, over the warp
-#pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    return x;
-  };
   long long total = 0, before, all, inc = 0;
   if (B > nt) {
-    for (int b = tid; b < B; b += nt) {
-      look(b);
-      inc += cost;
-    }
-    sums(scan(inc), before, total);
+    for (int b = tid; b < B; b += nt) inc += paged_cost(p, ph, b, B, s, head);
+    sums(warp_scan(inc), before, total);
     __syncthreads();
   }
   long long run = 0;
   for (int b0 = 0; b0 < B; b0 += nt) {
-    look(b0 + tid);
-    inc = scan(cost);
+    const long long cost = paged_cost(p, ph, b0 + tid, B, s, head);
+    inc = warp_scan(cost);
     sums(inc, before, all);
     if (B <= nt) total = all;
     const PagedShare share(total, gridDim.x);
@@ -308,13 +313,33 @@ __device__ __forceinline__ void paged_walk_begin(const PagedParams& p, const Pag
                                                  const PagedScan& sc, PagedWalk& w) {
   w.first = true;
   w.tiles = 0;
-  if (w.g >= w.hi) return;  // idle CTA
-  w.b = sc.b;
-  w.s = sc.s;
+  const int B = ph.whole_batch ? 1 : p.B;
+  long long head, off;
+  if (B <= 32) {
+    const long long cost = paged_cost(p, ph, (int)lane_id(), B, w.s, head);
+    const long long inc = warp_scan(cost);
+    w.total = __shfl_sync(0xffffffffu, inc, 31);
+    const PagedShare share(w.total, gridDim.x);
+    w.g = share.lo(blockIdx.x);
+    w.hi = share.lo(blockIdx.x + 1);
+    if (w.g >= w.hi) return;  // idle CTA
+    const unsigned at = __ballot_sync(0xffffffffu, inc - cost <= w.g && w.g < inc);
+    w.b = __ffs((int)at) - 1;
+    w.s.t0 = __shfl_sync(0xffffffffu, w.s.t0, w.b);
+    w.s.n = __shfl_sync(0xffffffffu, w.s.n, w.b);
+    w.s.len = __shfl_sync(0xffffffffu, w.s.len, w.b);
+    head = __shfl_sync(0xffffffffu, head, w.b);
+    off = w.g - __shfl_sync(0xffffffffu, inc - cost, w.b);
+  } else {
+    if (w.g >= w.hi) return;  // idle CTA
+    w.b = sc.b;
+    w.s = sc.s;
+    head = sc.head;
+    off = w.g - sc.excl;
+  }
   w.units = paged_units(ph, w.s);
-  long long off = w.g - sc.excl;
-  w.h = (int)paged_div(off, sc.head);
-  off -= w.h * sc.head;
+  w.h = (int)paged_div(off, head);
+  off -= w.h * head;
   w.i = 0;
   if (!p.causal || ph.whole_batch) {  // units of equal cost
     const int c = max(1, paged_unit_tiles(p, ph, w.s, 0));
@@ -386,14 +411,12 @@ __device__ __forceinline__ PagedItem paged_next(const PagedParams& p, const Page
 __device__ __forceinline__ int paged_prefix_limit(const PagedParams& p, int t) {
   if (t >= p.T) return 0;
   // The largest b with cu_q[b] <= t, b = t first: one token per sequence.
-  int lo = -1, hi = p.B;  // cu_q[lo] <= t < cu_q[hi], as far as known
-  if (t < p.B && p.cu_q[t] <= t) {
-    lo = t;
-    if (p.cu_q[t + 1] > t) hi = t + 1;
-  }
-  if (lo < 0 && p.cu_q[0] > t) return 0;
-  if (p.cu_q[p.B] <= t) return 0;  // a padding row
-  if (lo < 0) lo = 0;
+  const int g = min(t, p.B - 1);
+  const int first = p.cu_q[0], end = p.cu_q[p.B], at = p.cu_q[g], after = p.cu_q[g + 1];
+  if (first > t || end <= t) return 0;  // a padding row
+  int lo = 0, hi = p.B;  // cu_q[lo] <= t < cu_q[hi]
+  if (at <= t) lo = g;
+  if (after > t) hi = g + 1;
   while (hi - lo > 1) {
     const int mid = lo + (hi - lo) / 2;
     if (p.cu_q[mid] <= t)
@@ -439,11 +462,12 @@ struct PagedBox {
 };
 template <int D>
 __device__ __forceinline__ PagedBox paged_box(const PagedParams& p) {
-  const int lane = (int)lane_id(), rows = min(p.page_size, kTile), per = kTile / rows;
-  const int half = lane / per;
+  const int lane = (int)lane_id(), rows = min(p.page_size, kTile);
+  const int shift = max(7 - p.page_shift, 0);  // log2 of the tile's pages
+  const int half = lane >> shift;
   PagedBox b;
   b.on = half < D / 64;
-  b.sub = lane % per;
+  b.sub = lane & ((1 << shift) - 1);
   b.x = half * 64;
   b.dst = half * (kTile * 128) + b.sub * rows * 128;
   b.in_page = (p.page_size - 1) & ~(rows - 1);
@@ -490,11 +514,6 @@ __device__ __forceinline__ void paged_produce_k(const PagedParams& p, const Page
   const PagedBox box = paged_box<D>(p);
   bool ok = true;
   int c = 0;  // ring uses
-  if (walk.g >= walk.hi && lane == 0) {
-    PagedRec r = {};
-    r.total = walk.total;
-    *reinterpret_cast<PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes) = r;
-  }
   // Publishes the walk's next segment as item m; false at the list's end (or
   // after a failed wait).  Only this warp writes the records, so it can read
   // them again later.
@@ -512,6 +531,11 @@ __device__ __forceinline__ void paged_produce_k(const PagedParams& p, const Page
     return ok && !it.end;
   };
   paged_walk_begin(p, ph, sm.scan, walk);
+  if (walk.g >= walk.hi && lane == 0) {
+    PagedRec r = {};
+    r.total = walk.total;
+    *reinterpret_cast<PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes) = r;
+  }
   PagedPages pages, after;
   int m = 0;
   bool more = publish(0);

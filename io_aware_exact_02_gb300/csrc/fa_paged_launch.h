@@ -1,6 +1,8 @@
 // fa_paged_launch.h -- what the two paged attention kernels' launchers share.
 #pragma once
 
+#include <atomic>
+
 #include "fa_internal.h"
 #include "fa_paged.cuh"
 
@@ -12,9 +14,17 @@ struct PagedMaps {
 };
 
 // Sets the kernel's shared memory on the current device and checks that it has
-// the registers its warpgroups split.
-template <class Kernel>
-int paged_kernel_ready(Kernel* kernel, size_t smem) {
+// the registers its warpgroups split, once per device.
+template <auto* kernel>
+int paged_kernel_ready(size_t smem) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_LAUNCH;
+  }
+  static std::atomic<unsigned long long> ready{0};  // one per kernel, a bit per device
+  const unsigned long long bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (ready.load(std::memory_order_relaxed) & bit) return FA_OK;
   cudaFuncAttributes attr;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
           cudaSuccess ||
@@ -22,7 +32,9 @@ int paged_kernel_ready(Kernel* kernel, size_t smem) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
   }
-  return attr.numRegs < kPagedRegs ? FA_ERR_LAUNCH : FA_OK;
+  if (attr.numRegs < kPagedRegs) return FA_ERR_LAUNCH;
+  ready.fetch_or(bit, std::memory_order_relaxed);
+  return FA_OK;
 }
 
 // The prompt kernel (fa_paged_prompt.cu): units of two 128-row Q tiles.

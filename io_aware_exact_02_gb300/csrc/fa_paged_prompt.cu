@@ -64,7 +64,8 @@ __device__ __forceinline__ int tile_steps(const PagedParams& p, const PagedPhase
 
 // A softmax warp's rows of O out of tensor memory (at colO; ~0: zeros), times
 // `own`, plus `pre` times row `row` of pre_o (if given), to row dst_row (none
-// if negative) of `wide` (fp32) or of o (bf16).  A thread has a row, but rows
+// if negative) of `wide` (fp32) or of o (bf16); slot: the warp's first row where
+// wide is a slot.  A thread has a row, but rows
 // are stored by lanes that share them: 128 bytes of the warp's 32 rows at a
 // time through `out`, 16-byte chunk c of row r at c ^ (r % 8).  (A thread
 // storing its own row wrote 16 of its 256 or 512 bytes at a time: 10,000
@@ -72,10 +73,41 @@ __device__ __forceinline__ int tile_steps(const PagedParams& p, const PagedPhase
 // register, and addresses computed here would be kept through it.
 template <int D>
 __device__ __noinline__ void store_rows(uint32_t colO, float own, float pre, long long row,
-                                        long long dst_row, uint8_t* out, float* wide,
+                                        long long dst_row, uint8_t* out, float* wide, float* slot,
                                         const float* pre_o, __nv_bfloat16* o) {
   const int lane = (int)lane_id(), e = lane & 7;
   uint8_t* const mine = out + lane * 128;
+  if (slot != nullptr && pre_o == nullptr) {
+    // The warp's 32 rows of a slot lie one after another, and rows that are
+    // none may be written too.
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = 0u;
+      if (colO != ~0u) {
+        tmem_ld32(colO + c * 32, w);
+        tmem_wait_ld(w);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = own == 0.f ? 0.f : __uint_as_float(w[4 * i + k]) * own;
+        *reinterpret_cast<float4*>(mine + ((i ^ (lane & 7)) << 4)) =
+            make_float4(x[0], x[1], x[2], x[3]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int rr = i * 4 + lane / 8;
+        *reinterpret_cast<float4*>(slot + rr * D + c * 32 + e * 4) =
+            *reinterpret_cast<const float4*>(out + rr * 128 + ((e ^ (rr & 7)) << 4));
+      }
+      __syncwarp();
+    }
+    return;
+  }
   if (wide != nullptr || pre_o != nullptr) {
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
@@ -139,7 +171,7 @@ __device__ __noinline__ void store_rows(uint32_t colO, float own, float pre, lon
             make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
     __syncwarp();
-#pragma unroll 2
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int rr = i * 4 + lane / 8;
       const long long to = __shfl_sync(0xffffffffu, dst_row, rr);
@@ -436,6 +468,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       const long long slot_row = ((long long)blockIdx.x * 2 + it.slot) * ph.slot_rows + t * kTile + r;
       store_rows<D>(n_t > 0 ? colO : ~0u, own, pre, row, valid ? (it.slot >= 0 ? slot_row : row) : -1,
                     sm.out[warp], it.slot >= 0 ? ph.slot_o : ph.out_o,
+                    it.slot >= 0 ? ph.slot_o + (slot_row - lane_id()) * D : nullptr,
                     it.first ? ph.pre_o : nullptr, p.o);
       if (n_t > 0) {
         // O_t may now be overwritten by the next unit's first product.
@@ -473,7 +506,7 @@ int launch_prompt(const PagedMaps& t, const PagedParams& p, const PagedPhase& ph
   cudaLaunchConfig_t c = base;
   c.blockDim = dim3(kPagedThreads, 1, 1);
   c.dynamicSmemBytes = sizeof(PromptSmem<D>) + 1024;
-  if (paged_kernel_ready(fa_paged_prompt_kernel<D, kNeg>, c.dynamicSmemBytes) != FA_OK)
+  if (paged_kernel_ready<fa_paged_prompt_kernel<D, kNeg>>(c.dynamicSmemBytes) != FA_OK)
     return FA_ERR_LAUNCH;
   if (cudaLaunchKernelEx(&c, fa_paged_prompt_kernel<D, kNeg>, t.q, t.k, t.v, p, ph) !=
           cudaSuccess) {

@@ -479,19 +479,6 @@ def _checked_cache(k_pages, v_pages, page_table, seq_lens, cu_q, device):
             _checked("cu_q", cu_q, (B + 1,), _I32, device)), shape, B, width
 
 
-def _call_on(device, fn, *args):
-    """The library call with `device` current, on its current stream."""
-    f = getattr(load(), fn)
-    stream = torch._C._cuda_getCurrentRawStream(device)
-    if torch.cuda.current_device() == device:
-        rc = f(*args, stream)
-    else:
-        with torch.cuda.device(device):
-            rc = f(*args, stream)
-    if rc != FA_OK:
-        _check(fn, rc)
-
-
 def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_q, q=None, q_out=None, rope=None,
               interleaved: bool = False):
     """Append packed rows k, v (T, Hkv, d) to the paged cache, rotating keys
@@ -525,9 +512,16 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_q, q=None, q_out=
             raise ValueError("rope must have shape (length, rope_dim)")
         rope_len, rope_dim = rope.shape
         rope_ptr = _checked("rope", rope, (rope_len, rope_dim), _F32, dev)
-    _call_on(dev, "fa_kv_append", q_ptr, k_ptr, v_ptr, q_out_ptr, kp, vp, table, lens, cu,
-             rope_ptr, T, B, Hq, Hkv, d, qs, ks, vs, qos, num_pages, page_size, width, rope_dim,
-             rope_len, 1 if interleaved else 0)
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_q, q, q_out, rope,
+                             interleaved)
+    rc = load().fa_kv_append(q_ptr, k_ptr, v_ptr, q_out_ptr, kp, vp, table, lens, cu,
+                             rope_ptr, T, B, Hq, Hkv, d, qs, ks, vs, qos, num_pages, page_size,
+                             width, rope_dim, rope_len, 1 if interleaved else 0,
+                             torch._C._cuda_getCurrentRawStream(dev))
+    if rc != FA_OK:
+        _check("fa_kv_append", rc)
     return q_out
 
 
@@ -559,14 +553,30 @@ def _fwd_paged(fn, q, k_pages, v_pages, page_table, seq_lens, cu_q, prefix_pages
         n = prefix_pages.shape[0]
         prefix_len = n * page_size
         prefix = (_checked("prefix_pages", prefix_pages, (n,), _I32, dev), prefix_len)
-    if workspace is None:
-        workspace = torch.empty(max(1, fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len)),
-                                dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != dev:
+    if workspace is not None and workspace.get_device() != dev:
         _refuse("workspace", workspace, workspace.shape, workspace.dtype, dev)
-    _call_on(dev, fn, q_ptr, kp, vp, o_ptr, lse_ptr, table, lens, cu, *prefix, T, B, Hq, Hkv, d,
-             qs, num_pages, page_size, width, max_q, 1 if causal else 0, scale,
-             workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _fwd_paged(fn, q, k_pages, v_pages, page_table, seq_lens, cu_q, prefix_pages,
+                              max_q, causal, scale, out, lse, workspace)
+    lib, stream = load(), torch._C._cuda_getCurrentRawStream(dev)
+    if workspace is None:
+        # From torch's allocator without a tensor around it, which costs more
+        # than a single-token call's launch; it is the stream's again as soon
+        # as the call is enqueued.
+        ws_bytes = lib.fa_fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len)
+        ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(max(ws_bytes, 1), stream)
+    else:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    try:
+        rc = getattr(lib, fn)(q_ptr, kp, vp, o_ptr, lse_ptr, table, lens, cu, *prefix, T, B, Hq,
+                              Hkv, d, qs, num_pages, page_size, width, max_q, 1 if causal else 0,
+                              scale, ws, ws_bytes, stream)
+    finally:
+        if workspace is None:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
+    if rc != FA_OK:
+        _check(fn, rc)
     return out, lse
 
 

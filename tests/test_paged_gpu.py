@@ -50,6 +50,14 @@ CASES = [
     (48, 1, 128, 16, [520], [9]),
     (5, 5, 64, 16, list(range(1, 41)), [1] * 40),  # more sequences than a warp
     (8, 1, 64, 16, [60 + 13 * i for i in range(70)], [1 + i % 3 for i in range(70)]),
+    # long and short sequences in one call
+    (8, 2, 128, 16, [300, 17, 0, 600, 400] + [90 + i for i in range(9)], [90, 1, 0, 1, 150] + [1] * 9),
+    (16, 2, 64, 64, [400] * 20, [1, 2, 3, 40] * 5),
+    (40, 1, 64, 32, [333, 100, 40, 9], [1, 30, 2, 1]),
+    (96, 1, 128, 16, [333, 100, 40], [1, 30, 1]),
+    # more sequences than a CTA has threads
+    (2, 1, 64, 16, [1 + (7 * i) % 150 for i in range(900)], [1] * 900),
+    (2, 2, 64, 16, [1 + (7 * i) % 150 for i in range(450)], [i % 2 for i in range(450)]),
 ]
 
 
@@ -106,6 +114,7 @@ PREFIX = [
     (8, 1, 128, 32, 1056, [1056 + i for i in range(1, 60)], [1] * 59),
     (4, 1, 128, 16, 2000, [2100, 2001, 2300, 2050], [60, 1, 200, 50]),
     (8, 2, 64, 16, 160, [161, 0, 200], [1, 0, 1]),     # an empty sequence
+    (8, 2, 128, 16, 320, [400, 321, 330, 500, 322, 390], [60, 1, 1, 1, 2, 1]),  # long and short
     (8, 2, 128, 16, 160, [161, 100, 160, 30], [1, 4, 1, 2]),  # shorter than the prefix
 ]
 
