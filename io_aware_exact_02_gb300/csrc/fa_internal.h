@@ -263,7 +263,7 @@ struct PagedParams {
 };
 
 // How a call runs: the rows of a unit in the attention of the sequences' own
-// keys (16, 32 or 64: the decode kernel; 256: the prompt kernel), and in that
+// keys (8, 16, 32 or 64: the decode kernel; 256: the prompt kernel), and in that
 // of the shared prefix by the rows of the whole batch.  In a batch of long and
 // short sequences, those of up to small_rows rows go to the decode kernel and
 // the others to the prompt kernel: 30 decoding sequences and two prompt chunks
@@ -276,7 +276,7 @@ struct PagedForm {
   int rows, small_rows, share, prefix_rows;
 };
 inline int paged_unit_rows(long long rows) {
-  return rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= kPagedDecodeRows ? 64 : kPairRows));
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= kPagedDecodeRows ? 64 : kPairRows));
 }
 inline PagedForm paged_form(int T, int B, int G, int max_q, int prefix_len) {
   PagedForm f;

@@ -24,7 +24,7 @@
 //
 // Warps: 0-3 and 4-7 compute (and write results), 8 and 10 load K and V (TMA: a
 // lane per page box), 9 issues the products, each as soon as its operands are
-// there, 11 is idle.
+// there, 11 clears what lies past a unit's keys.
 // K and V stream through one ring of 32 KB (d = 128) tiles in the order K0 V0
 // K1 V1 ..., across units; four S buffers let S run ahead of P V, into the
 // next units.
@@ -40,20 +40,27 @@ namespace {
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kItemRing = 8;  // even: an item's slot belongs to one warpgroup
 constexpr int kCompute = 256;  // threads of the compute warps
-constexpr int kSBufs = 4;      // S buffers, shared out among the groups
+constexpr int kSBufs = 4;      // S buffers, two for each group
 // A row's reference maximum before it has seen a key: finite, so that the
 // exponent of a masked score is -inf and not NaN.
 constexpr float kNoRef = -3.0e38f;
 
-template <int D, int N>
+template <int D, int R>
 struct DecodeCfg {
+  static constexpr int N = R < 16 ? 16 : R;  // columns of the products
   static constexpr int kTileBytes = kTile * D * 2;
-  // As many ring slots as the 227 KB allow beside Q and P.
-  static constexpr int kStages =
-      D == 128 ? (N == 16 ? 6 : (N == 32 ? 5 : 4)) : (N == 16 ? 12 : 10);
+  // As many ring slots as the 227 KB allow beside Q and P; an even number, so
+  // that K always takes the even slots and V the odd ones, and the use before
+  // in a K tile's slot is a K tile whose S is issued before (in a V tile's, a
+  // V tile whose P V is): a barrier is only ever tested for the phase after
+  // one that is known to have completed.
+  static constexpr int kStages = D == 128 ? (N == 16 ? 6 : 4) : (N == 16 ? 12 : 10);
+  static_assert(kStages % 2 == 0, "K and V slots");
   // The warpgroups split a unit's columns (else they take units in turn).
   static constexpr bool kHalves = N == 64;
-  static constexpr int kCols = kHalves ? N / 2 : N;  // columns of a thread
+  // Columns of a thread: of 16, only the 8 that have rows, where that is enough
+  // (the others of P stay whatever they are, and of O are not read).
+  static constexpr int kCols = kHalves ? N / 2 : R;
   static constexpr uint32_t kTmemCols = 8 * N;  // 4 S buffers, 2 O (a power of two)
   static __device__ __forceinline__ uint32_t col_s(int i) { return (uint32_t)i * N; }
   // O of the units of parity i.
@@ -61,24 +68,28 @@ struct DecodeCfg {
   // The threads that work on a unit together, and their named barrier.
   static constexpr int kGroups = kHalves ? 1 : 2;
   static constexpr int kGroup = kCompute / kGroups;
-  // A group's n-th tile uses its S buffer n % kSPer and its P buffer n % 2.
-  static constexpr int kSPer = kSBufs / kGroups, kPBufs = 2 * kGroups;
+  // A group's n-th tile uses its S buffer n % 2 and its P buffer n % 2.  S of
+  // tile n is issued only after P V of tile n - 2.
+  static constexpr int kSPer = 2, kPBufs = 2 * kGroups;
   static __device__ __forceinline__ int barrier(int wg) { return kHalves ? 1 : 2 + wg; }
 };
 
-template <int D, int N>
+template <int D, int R>
 struct alignas(1024) DecodeSmem {
-  uint8_t kv[DecodeCfg<D, N>::kStages][DecodeCfg<D, N>::kTileBytes];
+  using Cfg = DecodeCfg<D, R>;
+  static constexpr int N = Cfg::N;
+  uint8_t kv[Cfg::kStages][Cfg::kTileBytes];
   uint8_t q[2][N * D * 2];       // [d / 64][N rows][128 B], 128B-swizzled
-  uint8_t pt[DecodeCfg<D, N>::kPBufs][N * kTile * 2];  // P: [2 blocks of 64 keys][N rows][128 B], swizzled
+  uint8_t pt[Cfg::kPBufs][N * kTile * 2];  // P: [2 blocks of 64 keys][N rows][128 B], swizzled
   float4 top[2][N];              // column maxima of a warpgroup's four warps
   float sum[2][4][N];            // column sums of a warpgroup's four warps
   float ref[2][N];               // reference maxima of the unit
   float f_own[2][N], f_pre[2][N];  // weights of O and of pre_o
   int lim[2][N];                 // keys row n sees end here
   uint64_t q_full[2], q_empty[2];
-  uint64_t kv_full[DecodeCfg<D, N>::kStages], kv_empty[DecodeCfg<D, N>::kStages];
-  uint64_t s_full[kSBufs], p_full[DecodeCfg<D, N>::kPBufs], pv_done[DecodeCfg<D, N>::kPBufs];
+  uint64_t kv_full[Cfg::kStages], kv_empty[Cfg::kStages];
+  uint64_t tail_full[Cfg::kStages];  // V tiles with keys past their unit's: loaded, not cleared
+  uint64_t s_full[kSBufs], p_full[Cfg::kPBufs], pv_done[Cfg::kPBufs];
   uint64_t o_full[2];
   uint64_t item_full[kItemRing], item_empty[kItemRing];
   uint64_t drain;
@@ -134,20 +145,18 @@ __device__ __forceinline__ void store_cols(uint32_t addr, const float (&x)[N]) {
   uint32_t r[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) r[i] = __float_as_uint(x[i]);
-  if constexpr (N == 16)
+  if constexpr (N == 8)
+    tmem_st8(addr, r);
+  else if constexpr (N == 16)
     tmem_st16(addr, r);
   else
     tmem_st32(addr, r);
   tmem_wait_st();
 }
 
-// Reduces each of N columns (16 or 32) over the warp's 32 lanes, halving the
-// columns a lane holds at every step (N shuffles in all, not 5 N).  Returns
-// the reduction of column col_of_lane<N>().
-template <int N>
-__device__ __forceinline__ int col_of_lane() {
-  return (int)lane_id() >> (N == 16 ? 1 : 0);
-}
+// Reduces each of N columns (8, 16 or 32) over the warp's 32 lanes, halving the
+// columns a lane holds at every step (about N shuffles in all, not 5 N).
+// Returns the reduction of column lane / (32 / N).
 template <int N, class Op>
 __device__ __forceinline__ float reduce_cols(const float (&x)[N], Op op) {
   float y[N];
@@ -164,21 +173,22 @@ __device__ __forceinline__ float reduce_cols(const float (&x)[N], Op op) {
       y[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, bit));
     }
   }
-  if constexpr (N == 16) y[0] = op(y[0], __shfl_xor_sync(0xffffffffu, y[0], 1));
+#pragma unroll
+  for (int bit = 16 / N; bit >= 1; bit /= 2) y[0] = op(y[0], __shfl_xor_sync(0xffffffffu, y[0], bit));
   return y[0];
 }
 
-template <int D, int N>
+template <int D, int R>
 __global__ void __launch_bounds__(kPagedThreads, 1)
     fa_paged_decode_kernel(const __grid_constant__ CUtensorMap tq,
                            const __grid_constant__ CUtensorMap tk,
                            const __grid_constant__ CUtensorMap tv, const PagedParams p,
                            const PagedPhase ph) {
-  using Cfg = DecodeCfg<D, N>;
-  constexpr int S = Cfg::kStages, NC = Cfg::kCols;
+  using Cfg = DecodeCfg<D, R>;
+  constexpr int S = Cfg::kStages, N = Cfg::N, NC = Cfg::kCols;
   constexpr bool kHalves = Cfg::kHalves;
   extern __shared__ uint8_t smem_raw[];
-  DecodeSmem<D, N>& sm = *reinterpret_cast<DecodeSmem<D, N>*>(
+  DecodeSmem<D, R>& sm = *reinterpret_cast<DecodeSmem<D, R>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abortf = &sm.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5;
@@ -188,6 +198,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     for (int s = 0; s < S; ++s) {
       mbar_init(&sm.kv_full[s], 1);
       mbar_init(&sm.kv_empty[s], 1);
+      mbar_init(&sm.tail_full[s], 1);
     }
     for (int i = 0; i < kSBufs; ++i) mbar_init(&sm.s_full[i], 1);
     for (int i = 0; i < Cfg::kPBufs; ++i) {
@@ -201,8 +212,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     }
     for (int i = 0; i < kItemRing; ++i) {
       mbar_init(&sm.item_full[i], 1);
-      // Read by the issuing thread, the V warp and the group's warps.
-      mbar_init(&sm.item_empty[i], 2 + Cfg::kGroup / 32);
+      // Read by the issuing thread, the V and the tail warp, the group's warps.
+      mbar_init(&sm.item_empty[i], 3 + Cfg::kGroup / 32);
     }
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -254,82 +265,69 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   } else if (warp == kWarpLoadV) {
     // ------------------------------------------------------------ V
     setmaxnreg_dec<kPagedRegsLoad>();
-    paged_produce_v<D, S, kItemRing>(p, sm, &tv);
+    paged_produce_v<D, S, kItemRing>(p, sm, &tv, sm.tail_full);
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ products
     setmaxnreg_dec<kPagedRegsLoad>();
     if (lane_id() == 0) {
       const uint32_t id_s = idesc_bf16(128, N, false, false);
       const uint32_t id_o = idesc_bf16(128, N, true, false);
-      int m = 0;                        // items read
-      int gs = 0, gp = 0;               // S and P V products issued, over all units
-      int ns[2] = {0, 0}, np[2] = {0, 0};  // and by group
-      bool have = false, end = false;   // have: a unit whose S products are not all issued
-      int s_nj = 0, s_j = 0, s_n = -1;  // that unit: tiles, tiles issued, its number
-      int s_m = 0, s_u = 0;             // its item's, its group
-      int p_nj = 0, p_j = 0, p_n = -1;  // the unit of the next P V product
-      int ob = 0, p_u = 0;              // its O, its group
+      // The units whose S products are not all issued: the oldest and, if it
+      // is the other group's, the next (whose first S can then be issued and
+      // worked on before the oldest unit is through).
+      struct Cursor {
+        int nj, j, tile0, q, u;  // tiles, issued, its first tile, Q use, group; nj = 0: none
+      } cur = {0, 0, 0, 0, 0}, nxt = {0, 0, 0, 0, 0};
+      int m = 0, units = 0;                // items read, units with keys among them
+      int ns[2] = {0, 0}, np[2] = {0, 0};  // S and P V products issued, by group
+      int gp = 0;                          // P V products issued
+      int p_nj = 0, p_j = 0, p_n = 0;      // the unit of the next P V product
+      int ob = 0, p_u = 0;                 // its O, its group
+      bool end = false;
       uint32_t idle = 0;
       unsigned long long t0 = 0;
+      // S of the cursor's next tile if its K (and Q) has arrived and its
+      // buffer's last S has been read (that tile's P V is issued).
+      auto try_s = [&](Cursor& k) -> bool {
+        if (k.nj == 0 || (k.u ? ns[1] - np[1] : ns[0] - np[0]) >= Cfg::kSPer) return false;
+        const int c = 2 * (k.tile0 + k.j), slot = c % S, qb = k.q & 1;
+        if (!mbar_test_wait(&sm.kv_full[slot], (c / S) & 1)) return false;
+        if (k.j == 0 && !mbar_test_wait(&sm.q_full[qb], (k.q >> 1) & 1)) return false;
+        const int sb = k.u * Cfg::kSPer + ((k.u ? ns[1]++ : ns[0]++) & 1);
+        tc_fence_after();
+        const uint64_t kd = desc_here(sdesc_sw128(smem_u32(sm.kv[slot]), 16, 1024));
+        const uint64_t qd = desc_here(sdesc_sw128(smem_u32(sm.q[qb]), 16, 1024));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(tmem + Cfg::col_s(sb), desc_plus(kd, (kk >> 2) * (kTile * 128) + (kk & 3) * 32),
+                 desc_plus(qd, (kk >> 2) * (N * 128) + (kk & 3) * 32), id_s, kk > 0);
+        tc_commit(&sm.s_full[sb]);
+        tc_commit(&sm.kv_empty[slot]);
+        if (++k.j == k.nj) {
+          tc_commit(&sm.q_empty[qb]);
+          k.nj = 0;
+        }
+        return true;
+      };
       for (;;) {
         bool did = false;
-        // The next unit with keys.
-        if (!have && !end && mbar_test_wait(&sm.item_full[m % kItemRing], (m / kItemRing) & 1)) {
-          const PagedItem& it = sm.item[m % kItemRing];
-          end = it.end != 0;
-          if (!end && it.nj > 0) {
-            have = true;
-            s_nj = it.nj;
-            s_j = 0;
-            s_m = m;
-            s_u = kHalves ? 0 : m & 1;
-            ++s_n;
-          }
-          mbar_arrive(&sm.item_empty[m % kItemRing]);
-          ++m;
-          did = true;
+        // The oldest P V product not issued: P is there, and V.
+        if (p_j == p_nj && p_n < units) {
+          p_nj = sm.of_unit[p_n & 7] >> 1;
+          ob = sm.of_unit[p_n & 7] & 1;
+          p_u = kHalves ? 0 : ob;
+          p_j = 0;
+          ++p_n;
         }
-        // S of the next tile: its K (and Q) has arrived and its buffer's last
-        // S has been read (that tile's P V is issued).
-        if (have && (s_u ? ns[1] - np[1] : ns[0] - np[0]) < Cfg::kSPer && mbar_test_wait(&sm.kv_full[(2 * gs) % S], ((2 * gs) / S) & 1) &&
-            (s_j > 0 || mbar_test_wait(&sm.q_full[s_n & 1], (s_n >> 1) & 1))) {
-          const int slot = (2 * gs) % S, qb = s_n & 1;
-          const int sb = s_u * Cfg::kSPer + (s_u ? ns[1]++ : ns[0]++) % Cfg::kSPer;
-          tc_fence_after();
-          const uint64_t kd = desc_here(sdesc_sw128(smem_u32(sm.kv[slot]), 16, 1024));
-          const uint64_t qd = desc_here(sdesc_sw128(smem_u32(sm.q[qb]), 16, 1024));
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + Cfg::col_s(sb), desc_plus(kd, (kk >> 2) * (kTile * 128) + (kk & 3) * 32),
-                   desc_plus(qd, (kk >> 2) * (N * 128) + (kk & 3) * 32), id_s, kk > 0);
-          tc_commit(&sm.s_full[sb]);
-          tc_commit(&sm.kv_empty[slot]);
-          if (s_j == 0) sm.of_unit[s_n & 7] = 2 * s_nj + (s_m & 1);
-          ++gs;
-          if (++s_j == s_nj) {
-            tc_commit(&sm.q_empty[qb]);
-            have = false;
-          }
-          did = true;
-        }
-        // P V of the oldest tile whose S is issued.
-        if (gp < gs) {
-          if (p_j == p_nj) {
-            ++p_n;
-            p_nj = sm.of_unit[p_n & 7] >> 1;
-            ob = sm.of_unit[p_n & 7] & 1;
-            p_u = kHalves ? 0 : ob;
-            p_j = 0;
-          }
-          // The unit's first product overwrites its O.  The group that wrote
-          // this P has by then read the O of the unit before in that place.
+        if (p_j < p_nj) {
           const int n = p_u ? np[1] : np[0], pb = 2 * p_u + (n & 1), c = 2 * gp + 1, slot = c % S;
           if (mbar_test_wait(&sm.p_full[pb], (n >> 1) & 1) &&
               mbar_test_wait(&sm.kv_full[slot], (c / S) & 1)) {
             tc_fence_after();
             // V^T: the tile's 64-channel blocks along M.  At d = 64 there is
             // one block; the product's upper 64 rows repeat the tile 8 keys on
-            // and are never read.
+            // and are never read.  The unit's first product overwrites its O,
+            // which the group that wrote this P has read for its last unit.
             const uint64_t vd =
                 desc_here(sdesc_sw128(smem_u32(sm.kv[slot]), D == 128 ? kTile * 128 : 1024, 1024));
             const uint64_t pd = desc_here(sdesc_sw128(smem_u32(sm.pt[pb]), 16, 1024));
@@ -345,8 +343,36 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             if (++p_j == p_nj) tc_commit(&sm.o_full[ob]);
             did = true;
           }
-        } else if (end && !have) {
+        } else if (end && cur.nj == 0 && p_n == units) {
           break;
+        }
+        if (cur.nj == 0) {
+          cur = nxt;
+          nxt.nj = 0;
+        }
+        did |= try_s(cur);
+        if (nxt.nj > 0) {
+          // Ahead of the oldest unit only once that has its Q, and as far as
+          // the use before of the tile's slot has had its S issued.
+          if (cur.nj == 0 || (nxt.u != cur.u && nxt.q == cur.q + 1 && cur.j > 0 &&
+                              nxt.tile0 + nxt.j - S / 2 < cur.tile0 + cur.j))
+            did |= try_s(nxt);
+        } else if (!end && mbar_test_wait(&sm.item_full[m % kItemRing], (m / kItemRing) & 1)) {
+          // The next segment; one without keys has no products.
+          const PagedItem& it = sm.item[m % kItemRing];
+          end = it.end != 0;
+          if (!end && it.nj > 0) {
+            nxt.nj = it.nj;
+            nxt.j = 0;
+            nxt.tile0 = it.tile0;
+            nxt.q = units;
+            nxt.u = kHalves ? 0 : m & 1;
+            sm.of_unit[units & 7] = 2 * it.nj + (m & 1);
+            ++units;
+          }
+          mbar_arrive(&sm.item_empty[m % kItemRing]);
+          ++m;
+          did = true;
         }
         // Nothing was ready: give up after the time limit, or with the CTA.
         if (did) {
@@ -395,11 +421,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       __syncwarp();
       if (!fail && lane == 0) mbar_arrive(&sm.item_empty[m % kItemRing]);
       const int rows = it.end ? 0 : it.ntok * p.G;
-      if (!bound_ok(it.end || (it.tok0 >= 0 && it.tok0 + it.ntok <= p.T && rows <= N && it.h < p.Hkv),
+      if (!bound_ok(it.end || (it.tok0 >= 0 && it.tok0 + it.ntok <= p.T && rows <= R && it.h < p.Hkv),
                     p.status, abortf, kChkPgItem))
         fail = true;
       // Keys of the unit's rows (0 for the columns past them).
-      if (!fail && !it.end && row < N) {
+      if (!fail && !it.end && row < R) {
         int lim = 0;
         if (row < rows) {
           if (ph.whole_batch)
@@ -449,11 +475,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
         float over = s[0] - ref[0];
 #pragma unroll
         for (int n = 1; n < NC; ++n) over = fmaxf(over, s[n] - ref[n]);
-        if (vote_any(bar, Cfg::kGroup, over > kRescaleSlack || fail)) {
+        // (A unit's first tile has a reference to find in any case.)
+        if (j == 0 || vote_any(bar, Cfg::kGroup, over > kRescaleSlack || fail)) {
           // Some score outgrew the reference: move every row's to its maximum.
           const float x = reduce_cols<NC>(s, [](float a, float b) { return fmaxf(a, b); });
-          if (NC == 32 || (lane & 1) == 0)
-            reinterpret_cast<float*>(&sm.top[buf][col0 + col_of_lane<NC>()])[warp & 3] = x;
+          if (lane % (32 / NC) == 0)
+            reinterpret_cast<float*>(&sm.top[buf][col0 + lane / (32 / NC)])[warp & 3] = x;
           if (vote_any(bar, Cfg::kGroup, fail)) {
             fail = true;
             break;
@@ -487,9 +514,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             }
           }
         }
-        // P's buffer is free once the product before last has read it.
-        if (!fail && n_t >= 2)
-          fail = !mbar_wait(&sm.pv_done[pb], ((n_t >> 1) - 1) & 1, p.status, abortf, kSitePgPvDone);
+        // P's buffer is free: this S was issued after the product before last,
+        // which read it, and products complete in order.
         if (!fail) {
           uint8_t* const pt = pt0 + (n_t & 1) * (N * kTile * 2);
 #pragma unroll
@@ -499,19 +525,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
             *reinterpret_cast<__nv_bfloat16*>(pt + n * 128 + ((pchunk ^ (n & 7)) << 4)) =
                 __float2bfloat16(x);
           }
-          if (it.key + (j + 1) * kTile > it.k_hi && key >= it.k_hi) {
-            // Slots past the unit's keys may hold anything, and 0 * NaN is
-            // NaN: their value rows become zero.
-            const int c = 2 * (it.tile0 + j) + 1, slot = c % S;
-            fail = !mbar_wait(&sm.kv_full[slot], (c / S) & 1, p.status, abortf, kSitePgKvFull);
-            if (!fail) {
-#pragma unroll
-              for (int h = 0; h < D / 64; ++h)
-                for (int i = 0; i < 8; ++i)
-                  *reinterpret_cast<uint4*>(sm.kv[slot] + h * (kTile * 128) + key_t * 128 + i * 16) =
-                      make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
           fence_proxy_async_smem();
           mbar_arrive(&sm.p_full[pb]);
         }
@@ -519,12 +532,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       // ------------------------------------------------------ the unit's result
       {
         const float x = reduce_cols<NC>(l, [](float a, float b) { return a + b; });
-        if (NC == 32 || (lane & 1) == 0) sm.sum[buf][warp & 3][col0 + col_of_lane<NC>()] = x;
+        if (lane % (32 / NC) == 0) sm.sum[buf][warp & 3][col0 + lane / (32 / NC)] = x;
         if (key_t < NC) sm.ref[buf][col0 + key_t] = my_ref;
       }
       if (vote_any(bar, Cfg::kGroup, fail)) break;
       const bool merge = it.first && ph.pre_o != nullptr;
-      if (row < N) {
+      if (row < R) {
         const float sum = (sm.sum[buf][0][row] + sm.sum[buf][1][row]) +
                           (sm.sum[buf][2][row] + sm.sum[buf][3][row]);
         float lse2 = sum == 0.f ? ninf : sm.ref[buf][row] + __log2f(sum);
@@ -603,8 +616,40 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
       // (The next unit's first vote comes before P is written again.)
     }
   } else {
-    // Idle: its registers go to the compute warps.
+    // ------------------------------------------------------------ tails
+    // Slots past a unit's keys may hold anything, and 0 * NaN is NaN: this
+    // warp clears those value rows of a unit's last tile when it has arrived,
+    // and hands the tile on.
     setmaxnreg_dec<kPagedRegsLoad>();
+    const int lane = (int)lane_id();
+    uint32_t parity = 0;  // of tail_full, a bit per slot
+    bool ok = true;
+    for (int m = 0; ok; ++m) {
+      const int is = m % kItemRing;
+      ok = mbar_wait(&sm.item_full[is], (m / kItemRing) & 1, p.status, abortf, kSitePgItemFull);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const PagedItem& it = sm.item[is];
+      const int end = it.end, nj = it.nj, slot = (2 * (it.tile0 + nj) - 1) % S;
+      const int rows = it.k_hi - (it.key + (nj - 1) * kTile);  // of the last tile
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[is]);
+      if (end) break;
+      if (nj == 0 || rows >= kTile) continue;
+      ok = mbar_wait(&sm.tail_full[slot], (parity >> slot) & 1, p.status, abortf, kSitePgKvFull);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      parity ^= 1u << slot;
+      for (int i = rows * 8 + lane; i < kTile * 8; i += 32)
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+          *reinterpret_cast<uint4*>(sm.kv[slot] + h * (kTile * 128) + i * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.kv_full[slot]);
+    }
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -630,7 +675,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
   launch_dependents();
   wait_prior_grid();
   constexpr int kPer = D / 32;
-  __shared__ float part_o[kMergeWarps][D], part_l[kMergeWarps];
+  __shared__ float part_o[kMergeWarps][D], part_l[kMergeWarps], part_m[kMergeWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const PagedRec rec = *reinterpret_cast<const PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes);
   if (!rec.split) return;
@@ -657,44 +702,52 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
     auto slot_of = [&](int i) -> long long {
       return ((long long)(c0 + i) * 2 + (i == 0 ? slot0 : 0)) * ph.slot_rows + row;
     };
-    float m = ninf;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, ph.slot_lse[slot_of(i)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float acc[kPer], sum = 0.f;
+    // One pass over the parts, kBatch of them in flight, with the running
+    // maximum of their logsumexp.
+    constexpr int kBatch = 4;
+    float m = ninf, acc[kPer], sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-    if (m != ninf) {
-      constexpr int kBatch = 4;
-      for (int i0 = sub; i0 < n; i0 += kBatch * share) {
-        float v[kBatch][kPer], w[kBatch];
+    for (int i0 = sub; i0 < n; i0 += kBatch * share) {
+      float v[kBatch][kPer], w[kBatch], top = m;
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int i = i0 + b * share;
-          w[b] = ninf;
+      for (int b = 0; b < kBatch; ++b) {
+        const int i = i0 + b * share;
+        w[b] = ninf;
 #pragma unroll
-          for (int e = 0; e < kPer; ++e) v[b][e] = 0.f;
-          if (i < n) {
-            const long long s = slot_of(i);
-            w[b] = ph.slot_lse[s];
-            const float* src = ph.slot_o + s * D + lane * kPer;
-            if constexpr (kPer == 4) {
-              const float4 x = *reinterpret_cast<const float4*>(src);
-              v[b][0] = x.x, v[b][1] = x.y, v[b][kPer - 2] = x.z, v[b][kPer - 1] = x.w;
-            } else {
-              const float2 x = *reinterpret_cast<const float2*>(src);
-              v[b][0] = x.x, v[b][1] = x.y;
-            }
+        for (int e = 0; e < kPer; ++e) v[b][e] = 0.f;
+        if (i < n) {
+          const long long s = slot_of(i);
+          w[b] = ph.slot_lse[s];
+          const float* src = ph.slot_o + s * D + lane * kPer;
+          if constexpr (kPer == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src);
+            v[b][0] = x.x, v[b][1] = x.y, v[b][kPer - 2] = x.z, v[b][kPer - 1] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(src);
+            v[b][0] = x.x, v[b][1] = x.y;
           }
         }
+      }
+      bool none = true;  // (of a NaN, `top` would not tell)
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const float e = exp2f(w[b] - m);
-          sum += e;
-          if (e != 0.f) {
+      for (int b = 0; b < kBatch; ++b) {
+        top = fmaxf(top, w[b]);
+        none = none && w[b] == ninf;
+      }
+      if (none) continue;
+      const float old = exp2f(m - top);
+      m = top;
+      sum *= old;
 #pragma unroll
-            for (int x = 0; x < kPer; ++x) acc[x] += e * v[b][x];
-          }
+      for (int x = 0; x < kPer; ++x) acc[x] *= old;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const float e = exp2f(w[b] - m);
+        sum += e;
+        if (e != 0.f) {
+#pragma unroll
+          for (int x = 0; x < kPer; ++x) acc[x] += e * v[b][x];
         }
       }
     }
@@ -702,20 +755,32 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
       __syncthreads();  // the last rows' parts were read
 #pragma unroll
       for (int e = 0; e < kPer; ++e) part_o[warp][lane * kPer + e] = acc[e];
-      if (lane == 0) part_l[warp] = sum;
+      if (lane == 0) part_l[warp] = sum, part_m[warp] = m;
       __syncthreads();
       if (sub == 0) {
-        for (int w = 1; w < share; ++w) {
-          sum += part_l[warp + w];
+        float top = m;
+        for (int w = 1; w < share; ++w) top = fmaxf(top, part_m[warp + w]);
+        if (top == ninf) {
+          for (int w = 1; w < share; ++w) sum += part_l[warp + w];  // 0, or NaN
+        } else {
+          const float own = exp2f(m - top);
+          m = top;
+          sum *= own;
 #pragma unroll
-          for (int e = 0; e < kPer; ++e) acc[e] += part_o[warp + w][lane * kPer + e];
+          for (int e = 0; e < kPer; ++e) acc[e] *= own;
+          for (int w = 1; w < share; ++w) {
+            const float f = exp2f(part_m[warp + w] - top);
+            sum += f * part_l[warp + w];
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) acc[e] += f * part_o[warp + w][lane * kPer + e];
+          }
         }
       }
     }
     if (!valid || sub != 0) continue;
-    const float inv = m == ninf ? 0.f : 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const long long out = (long long)(rec.tok0 + tok) * p.Hq + rec.h * p.G + head;
-    const float lse2 = m == ninf ? ninf : m + log2f(sum);
+    const float lse2 = sum == 0.f ? ninf : m + log2f(sum);
     int no_abort = 0;
     if (!bound_ok(rec.tok0 + tok < p.T && rec.h < p.Hkv, p.status, &no_abort, kChkPgRow)) continue;
     if (ph.out_o) {
@@ -728,22 +793,22 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
 #pragma unroll
       for (int e = 0; e < kPer; e += 2)
         *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-      if (lane == 0) p.lse[out] = m == ninf ? ninf : lse2 * kLn2;
+      if (lane == 0) p.lse[out] = lse2 == ninf ? ninf : lse2 * kLn2;
     }
   }
 }
 
-template <int D, int N>
+template <int D, int R>
 int launch_decode(const PagedMaps& t, const PagedParams& p, const PagedPhase& ph,
                   const cudaLaunchConfig_t& base) {
-  static_assert(sizeof(DecodeSmem<D, N>) + 1024 <= 232448,
+  static_assert(sizeof(DecodeSmem<D, R>) + 1024 <= 232448,
                 "decode shared memory above the 227 KB a CTA may have");
   cudaLaunchConfig_t c = base;
   c.blockDim = dim3(kPagedThreads, 1, 1);
-  c.dynamicSmemBytes = sizeof(DecodeSmem<D, N>) + 1024;
-  if (paged_kernel_ready<fa_paged_decode_kernel<D, N>>(c.dynamicSmemBytes) != FA_OK)
+  c.dynamicSmemBytes = sizeof(DecodeSmem<D, R>) + 1024;
+  if (paged_kernel_ready<fa_paged_decode_kernel<D, R>>(c.dynamicSmemBytes) != FA_OK)
     return FA_ERR_LAUNCH;
-  if (cudaLaunchKernelEx(&c, fa_paged_decode_kernel<D, N>, t.q, t.k, t.v, p, ph) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&c, fa_paged_decode_kernel<D, R>, t.q, t.k, t.v, p, ph) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
   }
@@ -757,7 +822,7 @@ int launch_merge(const PagedParams& p, const PagedPhase& ph0, const PagedPhase* 
   cudaLaunchConfig_t c = base;
   c.blockDim = dim3(32 * kMergeWarps, 1, 1);
   c.dynamicSmemBytes = 0;
-  c.gridDim = dim3((unsigned)p.ctas, ph0.slot_rows <= kPagedDecodeRows ? 4 : 16, ph1 ? 2 : 1);
+  c.gridDim = dim3((unsigned)p.ctas, ph0.slot_rows <= kPagedDecodeRows ? 4 : 8, ph1 ? 2 : 1);
   if (cudaLaunchKernelEx(&c, fa_paged_merge_kernel<D>, p, ph0, ph1 ? *ph1 : ph0) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
@@ -776,6 +841,7 @@ int launch_phase(const PagedParams& p, PagedPhase& ph, int rows, PagedMaps& t,
   int rc = make_tmap_rows(p.q, p.Hq, p.T, p.q_stride, D, p.G, ph.tile_tokens, &t.q);
   if (rc != FA_OK) return rc;
   switch (rows) {
+    case 8: return launch_decode<D, 8>(t, p, ph, c);
     case 16: return launch_decode<D, 16>(t, p, ph, c);
     case 32: return launch_decode<D, 32>(t, p, ph, c);
     case 64: return launch_decode<D, 64>(t, p, ph, c);

@@ -575,18 +575,22 @@ __device__ __forceinline__ void paged_produce_k(const PagedParams& p, const Page
   __syncwarp();
 }
 
+// tail: the barriers (one per slot) of tiles that reach past their unit's keys,
+// or null: such tiles are no different.
 template <int D, int S, int kRing, class Smem>
 __device__ __forceinline__ void paged_produce_v(const PagedParams& p, Smem& sm,
-                                                const CUtensorMap* tv) {
+                                                const CUtensorMap* tv, uint64_t* tail) {
   volatile int* abortf = &sm.abort_flag;
   const int lane = (int)lane_id();
   const PagedBox box = paged_box<D>(p);
   bool ok = true;
   int c = 1;
   // Takes item m if it has been published (or: waits for it).
-  int nj, h, key, end, nj2, h2, key2, end2 = 1;
+  int nj, h, key, hi, end, nj2, h2, key2, hi2, end2 = 1;
   PagedPages pages, after;
-  auto take = [&](int m, bool wait, int& nj, int& h, int& key, int& end, PagedPages& pages) -> bool {
+  uint32_t on_tail = 0;  // slots whose last use completes on tail's barrier
+  auto take = [&](int m, bool wait, int& nj, int& h, int& key, int& hi, int& end,
+                  PagedPages& pages) -> bool {
     const int is = m % kRing;
     bool there = mbar_test_wait(&sm.item_full[is], (m / kRing) & 1);
     if (!there && wait) {
@@ -597,14 +601,14 @@ __device__ __forceinline__ void paged_produce_v(const PagedParams& p, Smem& sm,
     ok = __all_sync(0xffffffffu, ok);
     if (!there) return false;
     const PagedItem& it = sm.item[is];
-    nj = it.nj, h = it.h, key = it.key, end = it.end;
+    nj = it.nj, h = it.h, key = it.key, hi = it.k_hi, end = it.end;
     if (!end) paged_pages_begin(p, it, pages);
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.item_empty[is]);
     return true;
   };
   end = 1;
-  take(0, true, nj, h, key, end, pages);
+  take(0, true, nj, h, key, hi, end, pages);
   for (int m = 0; ok && !end; ++m) {
     bool have = false;
     for (int j = 0; j < nj && ok; ++j, c += 2, key += kTile) {
@@ -613,17 +617,28 @@ __device__ __forceinline__ void paged_produce_v(const PagedParams& p, Smem& sm,
         ok = mbar_wait(&sm.kv_empty[slot], (c / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      paged_load_tile<D>(p, box, tv, pages, h, key, sm.kv[slot], &sm.kv_full[slot]);
-      if (!have) have = take(m + 1, false, nj2, h2, key2, end2, after);
+      const bool last = tail != nullptr && key + kTile > hi;
+      on_tail = (on_tail & ~(1u << slot)) | ((uint32_t)last << slot);
+      paged_load_tile<D>(p, box, tv, pages, h, key, sm.kv[slot],
+                         last ? &tail[slot] : &sm.kv_full[slot]);
+      if (!have) have = take(m + 1, false, nj2, h2, key2, hi2, end2, after);
     }
-    if (ok && !have) take(m + 1, true, nj2, h2, key2, end2, after);
+    if (ok && !have) take(m + 1, true, nj2, h2, key2, hi2, end2, after);
     if (!ok) break;
-    nj = nj2, h = h2, key = key2, end = end2;
+    nj = nj2, h = h2, key = key2, hi = hi2, end = end2;
     pages = after;
   }
   if (!ok && lane == 0) {
-    for (int cc = c - 2; cc >= 0 && cc > c - 2 - S; cc -= 2)
-      drain_wait(&sm.kv_full[cc % S], (cc / S) & 1);
+    for (int cc = c - 2; cc >= 0 && cc > c - 2 - S; cc -= 2) {
+      const int slot = cc % S;
+      if ((on_tail >> slot) & 1) {
+        // Its phase is not counted here: whichever is under way ends.
+        drain_wait(&tail[slot], 0);
+        drain_wait(&tail[slot], 1);
+      } else {
+        drain_wait(&sm.kv_full[slot], (cc / S) & 1);
+      }
+    }
   }
   __syncwarp();
 }

@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   } else if (warp == kWarpLoadV) {
     // ------------------------------------------------------------ V
     setmaxnreg_dec<kPagedRegsLoad>();
-    paged_produce_v<D, S, kItemRing>(p, sm, &tv);
+    paged_produce_v<D, S, kItemRing>(p, sm, &tv, nullptr);
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ products
     setmaxnreg_dec<kPagedRegsLoad>();

@@ -100,6 +100,21 @@ def test_fused_projection_slices(G, nq):
     attend(x)
 
 
+@pytest.mark.parametrize("d,Hq,Hkv,page,nq", [(128, 8, 4, 16, 1), (64, 8, 8, 32, 3), (128, 32, 2, 64, 2),
+                                             (128, 12, 1, 16, 5), (64, 4, 4, 16, 30)])
+def test_many_ragged_units_per_cta_are_right_and_repeatable(d, Hq, Hkv, page, nq):
+    """Hundreds of units of one to a dozen key tiles, so that every CTA goes
+    through many: against fp64 once, then bitwise the same every time."""
+    lens = [1 + (i * i * 37 + 11 * i) % 1500 for i in range(150)]
+    x = Batch(Hq, Hkv, d, page, lens, [min(n, nq) for n in lens], seed=nq)
+    o, lse = attend(x)
+    o, lse = o.clone(), lse.clone()
+    for _ in range(30):
+        a, b = fa.fwd_paged(*x.args(), max_q=nq, out=x.out, lse=x.lse)
+        assert torch.equal(a, o) and torch.equal(b, lse)
+    fa.check_device_status()
+
+
 def test_long_sequence_decode():
     attend(Batch(8, 2, 128, 64, [20000, 3], [1, 1], seed=1))
     attend(Batch(4, 1, 64, 16, [30001], [2], seed=2))
