@@ -12,6 +12,7 @@ dv are contiguous bf16 (B, H, N, d) on a CUDA device, lse is contiguous fp32
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -92,6 +93,8 @@ _lib = None
 def load(path: str | None = None):
     """Load libfa.so (once) and declare its signatures.  Raises if missing."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -447,7 +450,7 @@ def _refuse(name, t, shape, dtype, device):
 
 def _checked(name, t, shape, dtype, device):
     """The data pointer of a contiguous tensor of that shape, type and device."""
-    if (not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not dtype
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device
             or t.shape != shape or not t.is_contiguous()):
         _refuse(name, t, shape, dtype, device)
     return t.data_ptr()
@@ -456,7 +459,7 @@ def _checked(name, t, shape, dtype, device):
 def _checked_rows(name, t, T, H, d, device):
     """Data pointer and row stride of packed rows (T, H, d) bf16 whose heads
     are contiguous."""
-    if (not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not _BF16
+    if (not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != device
             or t.shape != (T, H, d)):
         _refuse(name, t, (T, H, d), _BF16, device)
     row, head, one = t.stride()
@@ -525,7 +528,9 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_q, q=None, q_out=
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
 def fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len=0) -> int:
+    """Bytes of workspace for these sizes (0 where they are invalid)."""
     return int(load().fa_fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len))
 
 
@@ -538,7 +543,7 @@ def _fwd_paged(fn, q, k_pages, v_pages, page_table, seq_lens, cu_q, prefix_pages
         k_pages, v_pages, page_table, seq_lens, cu_q, dev)
     T, Hq, _ = q.shape
     q_ptr, qs = _checked_rows("q", q, T, Hq, d, dev)
-    scale = default_scale(d) if scale is None else float(scale)
+    scale = d ** -0.5 if scale is None else float(scale)
     max_q = T if max_q is None else int(max_q)
     if out is None:  # rows of no sequence are not written
         out = torch.zeros((T, Hq, d), dtype=_BF16, device=q.device)
@@ -564,7 +569,7 @@ def _fwd_paged(fn, q, k_pages, v_pages, page_table, seq_lens, cu_q, prefix_pages
         # From torch's allocator without a tensor around it, which costs more
         # than a single-token call's launch; it is the stream's again as soon
         # as the call is enqueued.
-        ws_bytes = lib.fa_fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len)
+        ws_bytes = fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len)
         ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(max(ws_bytes, 1), stream)
     else:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
