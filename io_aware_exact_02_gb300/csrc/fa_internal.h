@@ -262,23 +262,29 @@ struct PagedParams {
   char* workspace;  // PagedWorkspace
 };
 
-// How a call runs: the rows of a unit in the attention of the sequences' own
-// keys (8, 16, 32 or 64: the decode kernel; 256: the prompt kernel), and in that
-// of the shared prefix by the rows of the whole batch.  In a batch of long and
-// short sequences, those of up to small_rows rows go to the decode kernel and
-// the others to the prompt kernel: 30 decoding sequences and two prompt chunks
-// of 500 tokens took 88 us on the prompt kernel alone, whose Q tiles a
-// decoding sequence leaves almost empty.  A batch counts as mixed when its
-// rows are fewer than a prompt unit per sequence on average but max_q says
-// that one sequence has more than a decode unit, unless max_q makes all of
-// them equal.
+// How a call runs.  rows: of a unit in the attention of the sequences' own keys
+// (8, 16, 32 or 64: the decode kernel; 256: the prompt kernel); prefix_rows: in
+// that of the shared prefix by the rows of the whole batch.
+//
+// In a batch of long and short sequences, those of up to small_rows rows go to
+// the decode kernel and the others to the prompt kernel, whose Q tiles a
+// decoding sequence leaves almost empty (30 decoding sequences and two chunks
+// of 500 tokens took 88 us on the prompt kernel alone).  A batch counts as
+// mixed when its rows are fewer than a prompt unit per sequence on average but
+// max_q says that one sequence has more than a decode unit, unless max_q makes
+// all of them equal.
+//
+// duo: a prompt and a decode kernel side by side in one launch (for decode
+// units of at most 16 rows): the two kinds of a mixed batch, or the prefix and
+// the sequences' own keys when these are the decode kernel's, joined by a warp
+// per row, which pays up to some ten thousand rows.
 struct PagedForm {
-  int rows, small_rows, share, prefix_rows;
+  int rows, small_rows, share, prefix_rows, duo;
 };
 inline int paged_unit_rows(long long rows) {
   return rows <= 8 ? 8 : rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= kPagedDecodeRows ? 64 : kPairRows));
 }
-inline PagedForm paged_form(int T, int B, int G, int max_q, int prefix_len) {
+inline PagedForm paged_form(int T, int B, int Hq, int G, int max_q, int prefix_len) {
   PagedForm f;
   f.rows = paged_unit_rows((long long)(max_q < T ? max_q : T) * G);
   f.small_rows = 0;
@@ -287,35 +293,53 @@ inline PagedForm paged_form(int T, int B, int G, int max_q, int prefix_len) {
     f.small_rows = paged_unit_rows(G);
   f.share = prefix_len > 0 ? 1 : 0;
   f.prefix_rows = paged_unit_rows((long long)T * G);
+  if (f.share)
+    f.duo = f.rows <= 16 && f.prefix_rows == kPairRows && (long long)T * Hq <= 16384;
+  else
+    f.duo = f.small_rows > 0 && f.small_rows <= 16;
   return f;
 }
 
-// Byte offsets of the paged forward's workspace, 256-byte aligned: for the
-// units of `rows` (or prefix_rows) rows and for those of small_rows, the split
-// records of the CTAs and their partial results (two slots each: fp32 O rows,
-// then the rows' logsumexp); with a shared prefix its results, fp32
-// [T][Hq][d] and [T][Hq].
+// Byte offsets of the paged forward's workspace, 256-byte aligned: for each of
+// two phases of a call the split records of the CTAs and their partial results
+// (two slots each: fp32 O rows, then the rows' logsumexp); with a shared prefix
+// its results, fp32 [T][Hq][d] and [T][Hq]; in a duo the phases' CTA counts,
+// and with a prefix the results of the sequences' own keys and where their
+// tiles begin.
 struct PagedWorkspace {
-  size_t rec[2], slot_o[2], slot_lse[2], pre_o, pre_lse, total;
+  size_t rec[2], slot_o[2], slot_lse[2], pre_o, pre_lse, own_o, own_lse, seq_start, ctas, total;
 };
 constexpr size_t kPagedRecBytes = 64;
-inline PagedWorkspace paged_workspace_layout(int T, int Hq, int d, const PagedForm& f) {
+inline PagedWorkspace paged_workspace_layout(int T, int B, int Hq, int d, const PagedForm& f) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  int rows[2] = {f.rows, f.small_rows};
+  if (f.share && f.duo) {
+    rows[0] = f.prefix_rows;
+    rows[1] = f.rows;
+  } else if (f.share && f.prefix_rows > f.rows) {
+    rows[0] = f.prefix_rows;
+  }
   PagedWorkspace w;
   size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += up(bytes);
+    return here;
+  };
   for (int k = 0; k < 2; ++k) {
-    const int rows = k == 1 ? f.small_rows
-                            : (f.share && f.prefix_rows > f.rows ? f.prefix_rows : f.rows);
-    const size_t slots = (size_t)kPagedMaxCtas * 2 * (size_t)rows;
-    w.rec[k] = at;
-    w.slot_o[k] = at + up(rows > 0 ? kPagedMaxCtas * kPagedRecBytes : 0);
-    w.slot_lse[k] = w.slot_o[k] + up(slots * (size_t)d * sizeof(float));
-    at = w.slot_lse[k] + up(slots * sizeof(float));
+    const size_t slots = (size_t)kPagedMaxCtas * 2 * (size_t)rows[k];
+    w.rec[k] = take(rows[k] > 0 ? kPagedMaxCtas * kPagedRecBytes : 0);
+    w.slot_o[k] = take(slots * (size_t)d * sizeof(float));
+    w.slot_lse[k] = take(slots * sizeof(float));
   }
-  const size_t pre = f.share ? (size_t)T * (size_t)Hq : 0;
-  w.pre_o = at;
-  w.pre_lse = w.pre_o + up(pre * (size_t)d * sizeof(float));
-  w.total = w.pre_lse + up(pre * sizeof(float));
+  const size_t pre = f.share ? (size_t)T * (size_t)Hq : 0, own = f.duo ? pre : 0;
+  w.pre_o = take(pre * (size_t)d * sizeof(float));
+  w.pre_lse = take(pre * sizeof(float));
+  w.own_o = take(own * (size_t)d * sizeof(float));
+  w.own_lse = take(own * sizeof(float));
+  w.seq_start = take(own > 0 ? (size_t)B * sizeof(long long) : 0);
+  w.ctas = take(f.duo ? 2 * sizeof(int) : 0);
+  w.total = at;
   return w;
 }
 

@@ -11,6 +11,8 @@
 
 namespace fa {
 
+constexpr float kLn2 = 0.69314718055994530942f;
+
 // Sites recorded with FA_ERR_PAGE.
 enum : int {
   kSitePagedRows = 301,  // cu_q not ascending within [0, T]
@@ -108,6 +110,8 @@ struct PagedPhase {
   int slot_rows;       // rows of a slot: 16 .. 64, or 256
   int n_min, n_max;    // sequences of that many new tokens take part
   char* rec;           // PagedRec per CTA
+  int* ctas;           // how many CTAs share the phase's list, where not all do; or null
+  long long* seq_start;  // [B], written: where each sequence's tiles begin in the list; or null
   float* slot_o;       // [CTA][2][slot_rows][d]
   float* slot_lse;     // [CTA][2][slot_rows], log2 units
   const float* pre_o;  // results to merge in ([T][Hq][d], [T][Hq], log2 units), or null
@@ -263,7 +267,7 @@ __device__ __forceinline__ long long warp_scan(long long x) {  // inclusive
 // More take all threads of the CTA: one scan of the sequences' costs where a
 // thread has one at most, else a sum and a second pass.
 __device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhase& ph,
-                                           PagedScan& sc, PagedWalk& w) {
+                                           PagedScan& sc, PagedWalk& w, int cta, int ctas) {
   const int B = ph.whole_batch ? 1 : p.B;
   if (B <= 32) return;
   const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31, nw = nt >> 5;
@@ -291,11 +295,13 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhas
     inc = warp_scan(cost);
     sums(inc, before, all);
     if (B <= nt) total = all;
-    const PagedShare share(total, gridDim.x);
+    const PagedShare share(total, ctas);
     w.total = total;
-    w.g = share.lo(blockIdx.x);
-    w.hi = share.lo(blockIdx.x + 1);
+    w.g = share.lo(cta);
+    w.hi = share.lo(cta + 1);
     const long long excl = run + before + inc - cost;
+    const bool writes = ph.seq_start != nullptr && cta == 0;
+    if (writes && b0 + tid < B) ph.seq_start[b0 + tid] = excl;
     if (cost > 0 && excl <= w.g && w.g < excl + cost) {
       sc.b = b0 + tid;
       sc.excl = excl;
@@ -304,13 +310,32 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhas
     }
     run += all;
     __syncthreads();
-    if (w.g < run) break;  // found
+    if (w.g < run && !writes) break;  // found
   }
+}
+
+// The lengths of two phases' lists, by every warp for itself.
+__device__ __forceinline__ void paged_totals(const PagedParams& p, const PagedPhase& pa,
+                                             const PagedPhase& pb, long long& ta, long long& tb) {
+  ta = tb = 0;
+  PagedSeq s;
+  long long head;
+  for (int b = (int)lane_id(); b < p.B; b += 32) {
+    if (!pa.whole_batch) ta += paged_cost(p, pa, b, p.B, s, head);
+    tb += paged_cost(p, pb, b, p.B, s, head);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    ta += __shfl_xor_sync(0xffffffffu, ta, o);
+    tb += __shfl_xor_sync(0xffffffffu, tb, o);
+  }
+  if (pa.whole_batch) ta = paged_cost(p, pa, 0, 1, s, head);
 }
 
 // The K warp's start of the walk.
 __device__ __forceinline__ void paged_walk_begin(const PagedParams& p, const PagedPhase& ph,
-                                                 const PagedScan& sc, PagedWalk& w) {
+                                                 const PagedScan& sc, PagedWalk& w, int cta,
+                                                 int ctas) {
   w.first = true;
   w.tiles = 0;
   const int B = ph.whole_batch ? 1 : p.B;
@@ -319,9 +344,11 @@ __device__ __forceinline__ void paged_walk_begin(const PagedParams& p, const Pag
     const long long cost = paged_cost(p, ph, (int)lane_id(), B, w.s, head);
     const long long inc = warp_scan(cost);
     w.total = __shfl_sync(0xffffffffu, inc, 31);
-    const PagedShare share(w.total, gridDim.x);
-    w.g = share.lo(blockIdx.x);
-    w.hi = share.lo(blockIdx.x + 1);
+    if (ph.seq_start != nullptr && cta == 0 && (int)lane_id() < B)
+      ph.seq_start[lane_id()] = inc - cost;
+    const PagedShare share(w.total, ctas);
+    w.g = share.lo(cta);
+    w.hi = share.lo(cta + 1);
     if (w.g >= w.hi) return;  // idle CTA
     const unsigned at = __ballot_sync(0xffffffffu, inc - cost <= w.g && w.g < inc);
     w.b = __ffs((int)at) - 1;
@@ -357,7 +384,7 @@ __device__ __forceinline__ void paged_walk_begin(const PagedParams& p, const Pag
 
 // The walk's next segment.
 __device__ __forceinline__ PagedItem paged_next(const PagedParams& p, const PagedPhase& ph,
-                                                PagedWalk& w) {
+                                                PagedWalk& w, int cta) {
   PagedItem it;
   it.end = w.g >= w.hi ? 1 : 0;
   if (it.end) return it;
@@ -385,7 +412,7 @@ __device__ __forceinline__ PagedItem paged_next(const PagedParams& p, const Page
     r.tok0 = it.tok0;
     r.ntok = it.ntok;
     r.h = it.h;
-    *reinterpret_cast<PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes) = r;
+    *reinterpret_cast<PagedRec*>(ph.rec + cta * kPagedRecBytes) = r;
   }
   w.first = false;
   w.g += take;
@@ -508,7 +535,7 @@ __device__ __forceinline__ void paged_load_tile(const PagedParams& p, const Page
 template <int D, int S, int kRing, class Smem, class LoadQ>
 __device__ __forceinline__ void paged_produce_k(const PagedParams& p, const PagedPhase& ph,
                                                 Smem& sm, const CUtensorMap* tk, PagedWalk& walk,
-                                                int ends, LoadQ&& load_q) {
+                                                int cta, int ctas, int ends, LoadQ&& load_q) {
   volatile int* abortf = &sm.abort_flag;
   const int lane = (int)lane_id();
   const PagedBox box = paged_box<D>(p);
@@ -518,7 +545,7 @@ __device__ __forceinline__ void paged_produce_k(const PagedParams& p, const Page
   // after a failed wait).  Only this warp writes the records, so it can read
   // them again later.
   auto publish = [&](int m) -> bool {
-    const PagedItem it = paged_next(p, ph, walk);
+    const PagedItem it = paged_next(p, ph, walk, cta);
     const int is = m % kRing;
     if (m >= kRing)
       ok = mbar_wait(&sm.item_empty[is], (m / kRing - 1) & 1, p.status, abortf, kSitePgItemEmpty);
@@ -530,11 +557,11 @@ __device__ __forceinline__ void paged_produce_k(const PagedParams& p, const Page
     __syncwarp();
     return ok && !it.end;
   };
-  paged_walk_begin(p, ph, sm.scan, walk);
+  paged_walk_begin(p, ph, sm.scan, walk, cta, ctas);
   if (walk.g >= walk.hi && lane == 0) {
     PagedRec r = {};
     r.total = walk.total;
-    *reinterpret_cast<PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes) = r;
+    *reinterpret_cast<PagedRec*>(ph.rec + cta * kPagedRecBytes) = r;
   }
   PagedPages pages, after;
   int m = 0;

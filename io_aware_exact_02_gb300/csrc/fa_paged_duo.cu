@@ -1,0 +1,89 @@
+// fa_paged_duo.cu -- two phases of a paged call side by side: some CTAs run the
+// kernel for many query rows (fa_paged_prompt.cuh), the others the one for few
+// (fa_paged_decode.cuh).  The first is bound by the tensor core and, when there
+// is little of it, by its own latencies, the second by memory, so together they
+// take little longer than the longer one: the prompt chunks and the decoding
+// sequences of a mixed batch, or a shared prefix and the sequences' own keys.
+//
+// Every CTA works out both lists' lengths and the same split of the CTAs, in
+// proportion to the time the lists take: a step of the prompt kernel (two Q
+// tiles, a key tile) about 1.6 us, a tile of the decode kernel about 1.0 us
+// when other CTAs compute meanwhile.
+#include "fa_paged_decode.cuh"
+#include "fa_paged_launch.h"
+#include "fa_paged_prompt.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kStepWeight = 16, kTileWeight = 10;
+
+template <int D, int R, bool kNeg>
+__global__ void __launch_bounds__(kPagedThreads, 1)
+    fa_paged_duo_kernel(const __grid_constant__ CUtensorMap tqa,
+                        const __grid_constant__ CUtensorMap tqb,
+                        const __grid_constant__ CUtensorMap tk,
+                        const __grid_constant__ CUtensorMap tv, const PagedParams p,
+                        const PagedPhase pa, const PagedPhase pb) {
+  extern __shared__ uint8_t smem_raw[];
+  launch_dependents();
+  wait_prior_grid();
+  long long ta, tb;
+  paged_totals(p, pa, pb, ta, tb);
+  const int ctas = gridDim.x;
+  int na = 0;
+  if (ta > 0) {
+    const long long wa = ta * kStepWeight, wb = tb * kTileWeight;
+    na = (int)paged_div(wa * ctas + (wa + wb) / 2, wa + wb);
+    na = tb > 0 ? max(1, min(na, ctas - 1)) : ctas;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *pa.ctas = na;
+    *pb.ctas = ctas - na;
+  }
+  if ((int)blockIdx.x < na)
+    prompt_cta<D, kNeg, true>(&tqa, &tk, &tv, p, pa, blockIdx.x, na, smem_raw);
+  else
+    decode_cta<D, R, true>(&tqb, &tk, &tv, p, pb, blockIdx.x - na, ctas - na, smem_raw);
+}
+
+template <int D, int R, bool kNeg>
+int launch(const PagedMaps& t, const CUtensorMap& tq_b, const PagedParams& p,
+           const PagedPhase& pa, const PagedPhase& pb, const cudaLaunchConfig_t& base) {
+  cudaLaunchConfig_t c = base;
+  c.blockDim = dim3(kPagedThreads, 1, 1);
+  const size_t a = sizeof(PromptSmem<D>), b = sizeof(DecodeSmem<D, R>);
+  c.dynamicSmemBytes = (a > b ? a : b) + 1024;
+  if (paged_kernel_ready<fa_paged_duo_kernel<D, R, kNeg>>(c.dynamicSmemBytes) != FA_OK)
+    return FA_ERR_LAUNCH;
+  if (cudaLaunchKernelEx(&c, fa_paged_duo_kernel<D, R, kNeg>, t.q, tq_b, t.k, t.v, p, pa, pb) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_LAUNCH;
+  }
+  return FA_OK;
+}
+
+template <int D, bool kNeg>
+int launch_rows(const PagedMaps& t, const CUtensorMap& tq_b, const PagedParams& p,
+                const PagedPhase& pa, const PagedPhase& pb, const cudaLaunchConfig_t& c) {
+  if (pb.slot_rows == 8) return launch<D, 8, kNeg>(t, tq_b, p, pa, pb, c);
+  if (pb.slot_rows == 16) return launch<D, 16, kNeg>(t, tq_b, p, pa, pb, c);
+  return FA_ERR_LAUNCH;
+}
+
+}  // namespace
+
+int launch_paged_duo(const PagedMaps& t, const CUtensorMap& tq_b, const PagedParams& params,
+                     const PagedPhase& pa, const PagedPhase& pb, int d,
+                     const cudaLaunchConfig_t& c) {
+  PagedParams p = params;
+  if (p.scale_log2 == 0.f) p.scale_log2 = 1.17549435e-38f;  // as the prompt kernel takes it
+  if (p.scale_log2 < 0.f)
+    return d == 128 ? launch_rows<128, true>(t, tq_b, p, pa, pb, c)
+                    : launch_rows<64, true>(t, tq_b, p, pa, pb, c);
+  return d == 128 ? launch_rows<128, false>(t, tq_b, p, pa, pb, c)
+                  : launch_rows<64, false>(t, tq_b, p, pa, pb, c);
+}
+
+}  // namespace fa
