@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
   if ((int)blockIdx.x >= ctas) return;
   const PagedRec rec = *reinterpret_cast<const PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes);
   if (!rec.split) return;
-  const PagedShare parts(rec.total, ctas);
+  const PagedShare parts(rec.total, ctas, paged_groups(p, ph, ctas));
   const int c0 = parts.owner(rec.unit_start);  // the unit's first CTA, in its last segment's slot
   const int c1 = parts.owner(rec.unit_end - 1);
   const int n = c1 - c0 + 1;
@@ -175,17 +175,30 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p,
   const long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int t = (int)(r / p.Hq), hq = (int)(r - (long long)t * p.Hq);
   if (t >= p.T) return;
-  const PagedRow at = paged_row(p.cu_q, p.seq_lens, p.B, p.T, t, p.status);
-  if (at.b < 0) return;
+  // What does not depend on the row's sequence, and sequence t in case it is
+  // that (one token each), are loaded together.
+  const int ctas_a = *pa.ctas, ctas_b = *pb.ctas;
+  const long long total_b = reinterpret_cast<const PagedRec*>(pb.rec)->total;
+  const int guess = min(t, p.B - 1);
+  const int g0 = p.cu_q[guess], g1 = p.cu_q[guess + 1];
+  long long start = pb.seq_start[guess];
+  PagedSeq s = paged_seq(p, pb, guess);
+  if (g0 > t || g1 <= t) {
+    const PagedRow at = paged_row(p.cu_q, p.seq_lens, p.B, p.T, t, p.status);
+    if (at.b < 0) return;
+    s = paged_seq(p, pb, at.b);
+    start = pb.seq_start[at.b];
+  }
+  if (s.n == 0) return;  // (tables out of bounds)
   const int h = hq / p.G, gh = hq - h * p.G;
   // The row's unit in each list: its first and last CTA, whether the first
   // part is that CTA's last segment, and the row's place in a slot.
   struct Parts {
     int c0, n, slot0, row;
   };
-  auto parts_of = [&](const PagedPhase& ph, long long total, long long start, int cost,
+  auto parts_of = [&](const PagedPhase& ph, int ctas, long long total, long long start, int cost,
                       int tok) -> Parts {
-    const PagedShare share(total, *ph.ctas);
+    const PagedShare share(total, ctas, paged_groups(p, ph, ctas));
     Parts x;
     x.c0 = share.owner(start);
     x.n = share.owner(start + cost - 1) - x.c0 + 1;
@@ -193,19 +206,16 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p,
     x.row = (tok / ph.tile_tokens) * kTile + (tok % ph.tile_tokens) * p.G + gh;
     return x;
   };
-  PagedSeq s = paged_seq(p, pa, 0);
-  int units = paged_units(pa, s), i = t / pa.unit_tokens;
-  int cost = max(1, paged_unit_tiles(p, pa, s, 0));
-  const Parts A = parts_of(pa, (long long)p.Hkv * units * cost,
-                           ((long long)h * units + i) * cost, cost, t - i * pa.unit_tokens);
-  s = paged_seq(p, pb, at.b);
-  const int tok = t - s.t0;
-  i = tok / pb.unit_tokens;
-  long long start = pb.seq_start[at.b] + h * paged_head_cost(p, pb, s);
-  for (int k = 0; k < i; ++k) start += max(1, paged_unit_tiles(p, pb, s, k));
-  cost = max(1, paged_unit_tiles(p, pb, s, i));
-  const Parts B = parts_of(pb, reinterpret_cast<const PagedRec*>(pb.rec)->total, start, cost,
-                           tok - i * pb.unit_tokens);
+  const PagedSeq all = paged_seq(p, pa, 0);
+  const int units = paged_units(pa, all), ia = t / pa.unit_tokens;
+  const int cost_a = max(1, paged_unit_tiles(p, pa, all, 0));
+  const Parts A = parts_of(pa, ctas_a, (long long)p.Hkv * units * cost_a,
+                           ((long long)h * units + ia) * cost_a, cost_a, t - ia * pa.unit_tokens);
+  const int tok = t - s.t0, ib = tok / pb.unit_tokens;
+  start += h * paged_head_cost(p, pb, s);
+  for (int k = 0; k < ib; ++k) start += max(1, paged_unit_tiles(p, pb, s, k));
+  const int cost_b = max(1, paged_unit_tiles(p, pb, s, ib));
+  const Parts B = parts_of(pb, ctas_b, total_b, start, cost_b, tok - ib * pb.unit_tokens);
   auto src = [&](int k, const float*& o) -> float {
     const bool own = k >= A.n;
     const PagedPhase& ph = own ? pb : pa;

@@ -174,6 +174,13 @@ __device__ __forceinline__ int paged_unit_tiles(const PagedParams& p, const Page
 __device__ __forceinline__ int paged_units(const PagedPhase& ph, const PagedSeq& s) {
   return s.n <= ph.unit_tokens ? (s.n > 0) : (s.n + ph.unit_tokens - 1) / ph.unit_tokens;
 }
+// Groups of the list's split: the units of the whole batch, if each can have a
+// CTA, else one.
+__device__ __forceinline__ int paged_groups(const PagedParams& p, const PagedPhase& ph, int ctas) {
+  if (!ph.whole_batch) return 1;
+  const long long units = (long long)p.Hkv * ((p.T + ph.unit_tokens - 1) / ph.unit_tokens);
+  return units <= ctas ? (int)units : 1;
+}
 // Tiles of one head of a sequence.
 __device__ __forceinline__ long long paged_head_cost(const PagedParams& p, const PagedPhase& ph,
                                                      const PagedSeq& s) {
@@ -194,21 +201,29 @@ __device__ __forceinline__ long long paged_div(long long a, long long b) {
 
 // CTA c's range of the list is [lo(c), lo(c + 1)): equal ranges, the first
 // `more` of them one tile longer; with fewer tiles than CTAs the first ones
-// take one each.
+// take one each.  A list of `groups` units of equal cost, no more than there
+// are CTAs, is dealt unit by unit to as many CTAs each, so that no CTA has
+// parts of two (a second segment costs a prompt CTA 10 us and more).
 struct PagedShare {
-  long long total, each;
-  int more;
-  __device__ __forceinline__ PagedShare(long long t, int ctas) : total(t) {
-    each = paged_div(t, ctas);
-    more = (int)(t - each * ctas);
+  long long total, per, each;  // tiles: in all, of a group, of a CTA
+  int k, more;                 // CTAs of a group
+  __device__ __forceinline__ PagedShare(long long t, int ctas, int groups) : total(t) {
+    per = groups > 1 ? paged_div(t, groups) : t;
+    k = groups > 1 ? ctas / groups : ctas;
+    each = paged_div(per, k);
+    more = (int)(per - each * k);
   }
   __device__ __forceinline__ long long lo(int c) const {
-    return each * c + (c < more ? c : more);
+    const int g = per == total ? 0 : c / k, r = c - g * k;
+    const long long x = g * per + each * r + (r < more ? r : more);
+    return x < total ? x : total;
   }
   // The CTA whose range holds tile x of the list.
   __device__ __forceinline__ int owner(long long x) const {
+    const int g = per == total ? 0 : (int)paged_div(x, per);
+    x -= g * per;
     const long long head = (each + 1) * more;
-    return x < head ? (int)paged_div(x, each + 1) : more + (int)paged_div(x - head, each);
+    return g * k + (x < head ? (int)paged_div(x, each + 1) : more + (int)paged_div(x - head, each));
   }
 };
 
@@ -295,7 +310,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhas
     inc = warp_scan(cost);
     sums(inc, before, all);
     if (B <= nt) total = all;
-    const PagedShare share(total, ctas);
+    const PagedShare share(total, ctas, 1);
     w.total = total;
     w.g = share.lo(cta);
     w.hi = share.lo(cta + 1);
@@ -314,22 +329,29 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhas
   }
 }
 
-// The lengths of two phases' lists, by every warp for itself.
-__device__ __forceinline__ void paged_totals(const PagedParams& p, const PagedPhase& pa,
-                                             const PagedPhase& pb, long long& ta, long long& tb) {
-  ta = tb = 0;
-  PagedSeq s;
-  long long head;
-  for (int b = (int)lane_id(); b < p.B; b += 32) {
-    if (!pa.whole_batch) ta += paged_cost(p, pa, b, p.B, s, head);
-    tb += paged_cost(p, pb, b, p.B, s, head);
+// The work in two phases' lists, tiles times the one weight and units times the
+// other, by every warp for itself.
+struct PagedWeight {
+  int tile, unit;
+};
+__device__ __forceinline__ void paged_weights(const PagedParams& p, const PagedPhase& pa,
+                                              PagedWeight a, const PagedPhase& pb, PagedWeight b,
+                                              long long& wa, long long& wb) {
+  auto weigh = [&](const PagedPhase& ph, PagedWeight w, int i) -> long long {
+    const PagedSeq s = paged_seq(p, ph, i);
+    return (paged_head_cost(p, ph, s) * w.tile + (long long)paged_units(ph, s) * w.unit) * p.Hkv;
+  };
+  wa = wb = 0;
+  for (int i = (int)lane_id(); i < p.B; i += 32) {
+    if (!pa.whole_batch) wa += weigh(pa, a, i);
+    wb += weigh(pb, b, i);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    ta += __shfl_xor_sync(0xffffffffu, ta, o);
-    tb += __shfl_xor_sync(0xffffffffu, tb, o);
+    wa += __shfl_xor_sync(0xffffffffu, wa, o);
+    wb += __shfl_xor_sync(0xffffffffu, wb, o);
   }
-  if (pa.whole_batch) ta = paged_cost(p, pa, 0, 1, s, head);
+  if (pa.whole_batch) wa = weigh(pa, a, 0);
 }
 
 // The K warp's start of the walk.
@@ -346,7 +368,7 @@ __device__ __forceinline__ void paged_walk_begin(const PagedParams& p, const Pag
     w.total = __shfl_sync(0xffffffffu, inc, 31);
     if (ph.seq_start != nullptr && cta == 0 && (int)lane_id() < B)
       ph.seq_start[lane_id()] = inc - cost;
-    const PagedShare share(w.total, ctas);
+    const PagedShare share(w.total, ctas, paged_groups(p, ph, ctas));
     w.g = share.lo(cta);
     w.hi = share.lo(cta + 1);
     if (w.g >= w.hi) return;  // idle CTA
@@ -385,7 +407,7 @@ __device__ __forceinline__ void paged_walk_begin(const PagedParams& p, const Pag
 // The walk's next segment.
 __device__ __forceinline__ PagedItem paged_next(const PagedParams& p, const PagedPhase& ph,
                                                 PagedWalk& w, int cta) {
-  PagedItem it;
+  PagedItem it = {};
   it.end = w.g >= w.hi ? 1 : 0;
   if (it.end) return it;
   const int tiles = paged_unit_tiles(p, ph, w.s, w.i), cost = max(1, tiles);

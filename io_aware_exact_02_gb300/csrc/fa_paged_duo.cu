@@ -5,10 +5,10 @@
 // take little longer than the longer one: the prompt chunks and the decoding
 // sequences of a mixed batch, or a shared prefix and the sequences' own keys.
 //
-// Every CTA works out both lists' lengths and the same split of the CTAs, in
-// proportion to the time the lists take: a step of the prompt kernel (two Q
-// tiles, a key tile) about 1.6 us, a tile of the decode kernel about 1.0 us
-// when other CTAs compute meanwhile.
+// Every CTA works out the same split of the CTAs, in proportion to the time the
+// two lists take: a step of the prompt kernel (two Q tiles, a key tile) 1.6 us
+// and the end of a unit 6 us, a tile of the decode kernel 1.0 us on half of the
+// SMs (76 CTAs read 5.1 of the 5.4 TB/s that 152 read) and a unit's end 1 us.
 #include "fa_paged_decode.cuh"
 #include "fa_paged_launch.h"
 #include "fa_paged_prompt.cuh"
@@ -16,7 +16,7 @@
 namespace fa {
 namespace {
 
-constexpr int kStepWeight = 16, kTileWeight = 10;
+constexpr PagedWeight kPromptWeight = {16, 60}, kDecodeWeight = {10, 10};  // 0.1 us
 
 template <int D, int R, bool kNeg>
 __global__ void __launch_bounds__(kPagedThreads, 1)
@@ -28,14 +28,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   launch_dependents();
   wait_prior_grid();
-  long long ta, tb;
-  paged_totals(p, pa, pb, ta, tb);
+  long long wa, wb;
+  paged_weights(p, pa, kPromptWeight, pb, kDecodeWeight, wa, wb);
   const int ctas = gridDim.x;
   int na = 0;
-  if (ta > 0) {
-    const long long wa = ta * kStepWeight, wb = tb * kTileWeight;
+  if (wa > 0) {
     na = (int)paged_div(wa * ctas + (wa + wb) / 2, wa + wb);
-    na = tb > 0 ? max(1, min(na, ctas - 1)) : ctas;
+    // A multiple of the units of a shared prefix, where there are CTAs enough.
+    const int groups = paged_groups(p, pa, ctas - 1);
+    na = (na + groups / 2) / groups * groups;
+    if (na >= ctas) na -= groups;
+    na = wb > 0 ? max(groups, na) : ctas;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *pa.ctas = na;
