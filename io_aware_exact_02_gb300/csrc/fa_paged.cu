@@ -316,13 +316,20 @@ int launch_merge(const PagedParams& p, const PagedPhase& ph0, const PagedPhase* 
   return FA_OK;
 }
 
-// The units of a phase of `rows` rows, and the tensor map of their Q tiles.
+// The units of a phase of `rows` rows, and the tensor maps of their Q tiles and
+// of the prompt kernel's results.
 template <int D>
-int phase_units(const PagedParams& p, PagedPhase& ph, int rows, CUtensorMap* tq) {
+int phase_units(const PagedParams& p, PagedPhase& ph, int rows, PagedMaps& t, CUtensorMap* tq) {
   const int tile_rows = rows <= kPagedDecodeRows ? rows : kTile;
   ph.tile_tokens = tile_rows / p.G;
   ph.unit_tokens = rows <= kPagedDecodeRows ? ph.tile_tokens : 2 * ph.tile_tokens;
   ph.slot_rows = rows;
+  if (rows > kPagedDecodeRows) {
+    ph.box_out = 32 % p.G == 0 && ph.out_o == nullptr;
+    const int rc = make_tmap_rows(p.o, p.Hq, p.T, (long long)p.Hq * D, D, p.G,
+                                  ph.box_out ? 32 / p.G : 1, &t.o);
+    if (rc != FA_OK) return rc;
+  }
   return make_tmap_rows(p.q, p.Hq, p.T, p.q_stride, D, p.G, ph.tile_tokens, tq);
 }
 
@@ -330,7 +337,7 @@ int phase_units(const PagedParams& p, PagedPhase& ph, int rows, CUtensorMap* tq)
 template <int D>
 int launch_phase(const PagedParams& p, PagedPhase& ph, int rows, PagedMaps& t,
                  const cudaLaunchConfig_t& c) {
-  const int rc = phase_units<D>(p, ph, rows, &t.q);
+  const int rc = phase_units<D>(p, ph, rows, t, &t.q);
   if (rc != FA_OK) return rc;
   switch (rows) {
     case 8: return launch_decode<D, 8>(t, p, ph, c);
@@ -381,8 +388,8 @@ int launch_paged_d(const PagedParams& p, cudaStream_t stream) {
       own.out_lse = at(w.own_lse);
       own.seq_start = reinterpret_cast<long long*>(p.workspace + w.seq_start);
       CUtensorMap tq_own;
-      if ((rc = phase_units<D>(p, pre, f.prefix_rows, &t.q)) != FA_OK ||
-          (rc = phase_units<D>(p, own, f.rows, &tq_own)) != FA_OK ||
+      if ((rc = phase_units<D>(p, pre, f.prefix_rows, t, &t.q)) != FA_OK ||
+          (rc = phase_units<D>(p, own, f.rows, t, &tq_own)) != FA_OK ||
           (rc = launch_paged_duo(t, tq_own, p, pre, own, D, c)) != FA_OK)
         return rc;
       c.blockDim = dim3(256, 1, 1);
@@ -408,8 +415,8 @@ int launch_paged_d(const PagedParams& p, cudaStream_t stream) {
   }
   if (f.duo) {
     CUtensorMap tq_small;
-    if ((rc = phase_units<D>(p, ph[0], f.rows, &t.q)) != FA_OK ||
-        (rc = phase_units<D>(p, ph[1], f.small_rows, &tq_small)) != FA_OK ||
+    if ((rc = phase_units<D>(p, ph[0], f.rows, t, &t.q)) != FA_OK ||
+        (rc = phase_units<D>(p, ph[1], f.small_rows, t, &tq_small)) != FA_OK ||
         (rc = launch_paged_duo(t, tq_small, p, ph[0], ph[1], D, c)) != FA_OK)
       return rc;
   } else {

@@ -107,7 +107,8 @@ struct PagedPhase {
   int key0;            // the first key attended (prefix_len after a shared prefix)
   int unit_tokens;     // query tokens of a unit
   int tile_tokens;     // query tokens of a Q tile (decode: the unit's)
-  int slot_rows;       // rows of a slot: 16 .. 64, or 256
+  int slot_rows;       // rows of a slot: 8 .. 64, or 256
+  int box_out;         // 32 rows of a Q tile are whole tokens, and o is bf16: stored as boxes
   int n_min, n_max;    // sequences of that many new tokens take part
   char* rec;           // PagedRec per CTA
   int* ctas;           // how many CTAs share the phase's list, where not all do; or null
@@ -192,9 +193,13 @@ __device__ __forceinline__ long long paged_head_cost(const PagedParams& p, const
   return c;
 }
 
+// The start of a paged kernel is straight-line code that every launch fetches
+// anew, at some 50 ns for eight instructions: what it does more than once is a
+// function or a loop here, not inlined copies.
+
 // a / b of nonnegative numbers; nearly always both fit 32 bits, whose division
 // is several times shorter.
-__device__ __forceinline__ long long paged_div(long long a, long long b) {
+static __device__ __noinline__ long long paged_div(long long a, long long b) {
   if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
   return a / b;
 }
@@ -269,7 +274,7 @@ __device__ __forceinline__ long long paged_cost(const PagedParams& p, const Page
 }
 __device__ __forceinline__ long long warp_scan(long long x) {  // inclusive
   const int lane = (int)lane_id();
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
@@ -346,7 +351,7 @@ __device__ __forceinline__ void paged_weights(const PagedParams& p, const PagedP
     if (!pa.whole_batch) wa += weigh(pa, a, i);
     wb += weigh(pb, b, i);
   }
-#pragma unroll
+#pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) {
     wa += __shfl_xor_sync(0xffffffffu, wa, o);
     wb += __shfl_xor_sync(0xffffffffu, wb, o);

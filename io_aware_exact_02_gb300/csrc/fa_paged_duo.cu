@@ -9,6 +9,11 @@
 // two lists take: a step of the prompt kernel (two Q tiles, a key tile) 1.6 us
 // and the end of a unit 6 us, a tile of the decode kernel 1.0 us on half of the
 // SMs (76 CTAs read 5.1 of the 5.4 TB/s that 152 read) and a unit's end 1 us.
+//
+// Clusters of two CTAs have one kind of work: two neighbouring SMs that run
+// both kinds, whose loops together do not fit what they share of the
+// instruction cache, take 4 us instead of 1.5 for a step of the prompt kernel
+// (and the shared prefix of 16K keys 70 us instead of 60).
 #include "fa_paged_decode.cuh"
 #include "fa_paged_launch.h"
 #include "fa_paged_prompt.cuh"
@@ -23,7 +28,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
     fa_paged_duo_kernel(const __grid_constant__ CUtensorMap tqa,
                         const __grid_constant__ CUtensorMap tqb,
                         const __grid_constant__ CUtensorMap tk,
-                        const __grid_constant__ CUtensorMap tv, const PagedParams p,
+                        const __grid_constant__ CUtensorMap tv,
+                        const __grid_constant__ CUtensorMap to, const PagedParams p,
                         const PagedPhase pa, const PagedPhase pb) {
   extern __shared__ uint8_t smem_raw[];
   launch_dependents();
@@ -34,18 +40,19 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   int na = 0;
   if (wa > 0) {
     na = (int)paged_div(wa * ctas + (wa + wb) / 2, wa + wb);
-    // A multiple of the units of a shared prefix, where there are CTAs enough.
-    const int groups = paged_groups(p, pa, ctas - 1);
-    na = (na + groups / 2) / groups * groups;
-    if (na >= ctas) na -= groups;
-    na = wb > 0 ? max(groups, na) : ctas;
+    // A multiple of the units of a shared prefix, where there are CTAs enough,
+    // and then of two: whole clusters.
+    const int groups = paged_groups(p, pa, ctas - 2);
+    na = max(groups, (na + groups / 2) / groups * groups);
+    if (na > ctas - 2) na -= groups;
+    na = wb > 0 ? (na + 1) & ~1 : ctas;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *pa.ctas = na;
     *pb.ctas = ctas - na;
   }
   if ((int)blockIdx.x < na)
-    prompt_cta<D, kNeg, true>(&tqa, &tk, &tv, p, pa, blockIdx.x, na, smem_raw);
+    prompt_cta<D, kNeg, true>(&tqa, &tk, &tv, &to, p, pa, blockIdx.x, na, smem_raw);
   else
     decode_cta<D, R, true>(&tqb, &tk, &tv, p, pb, blockIdx.x - na, ctas - na, smem_raw);
 }
@@ -55,12 +62,20 @@ int launch(const PagedMaps& t, const CUtensorMap& tq_b, const PagedParams& p,
            const PagedPhase& pa, const PagedPhase& pb, const cudaLaunchConfig_t& base) {
   cudaLaunchConfig_t c = base;
   c.blockDim = dim3(kPagedThreads, 1, 1);
+  c.gridDim.x &= ~1u;
+  cudaLaunchAttribute attrs[2];
+  attrs[0] = base.attrs[0];
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = 2;
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+  c.attrs = attrs;
+  c.numAttrs = 2;
   const size_t a = sizeof(PromptSmem<D>), b = sizeof(DecodeSmem<D, R>);
   c.dynamicSmemBytes = (a > b ? a : b) + 1024;
   if (paged_kernel_ready<fa_paged_duo_kernel<D, R, kNeg>>(c.dynamicSmemBytes) != FA_OK)
     return FA_ERR_LAUNCH;
-  if (cudaLaunchKernelEx(&c, fa_paged_duo_kernel<D, R, kNeg>, t.q, tq_b, t.k, t.v, p, pa, pb) !=
-      cudaSuccess) {
+  if (cudaLaunchKernelEx(&c, fa_paged_duo_kernel<D, R, kNeg>, t.q, tq_b, t.k, t.v, t.o, p, pa,
+                         pb) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
   }

@@ -8,9 +8,10 @@
 
 namespace fa {
 
-// Tensor maps over q (a box per Q tile and 64 channels) and the pages.
+// Tensor maps over q (a box per Q tile and 64 channels), the pages, and o (a
+// box per 32 rows and 64 channels, where a phase stores such: box_out).
 struct PagedMaps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;
 };
 
 // Sets the kernel's shared memory on the current device and checks that it has

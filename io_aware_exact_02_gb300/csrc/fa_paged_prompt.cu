@@ -10,10 +10,11 @@ template <int D, bool kNeg>
 __global__ void __launch_bounds__(kPagedThreads, 1)
     fa_paged_prompt_kernel(const __grid_constant__ CUtensorMap tq,
                            const __grid_constant__ CUtensorMap tk,
-                           const __grid_constant__ CUtensorMap tv, const PagedParams p,
+                           const __grid_constant__ CUtensorMap tv,
+                           const __grid_constant__ CUtensorMap to, const PagedParams p,
                            const PagedPhase ph) {
   extern __shared__ uint8_t smem_raw[];
-  prompt_cta<D, kNeg, false>(&tq, &tk, &tv, p, ph, blockIdx.x, gridDim.x, smem_raw);
+  prompt_cta<D, kNeg, false>(&tq, &tk, &tv, &to, p, ph, blockIdx.x, gridDim.x, smem_raw);
 }
 
 template <int D, bool kNeg>
@@ -26,7 +27,8 @@ int launch_prompt(const PagedMaps& t, const PagedParams& p, const PagedPhase& ph
   c.dynamicSmemBytes = sizeof(PromptSmem<D>) + 1024;
   if (paged_kernel_ready<fa_paged_prompt_kernel<D, kNeg>>(c.dynamicSmemBytes) != FA_OK)
     return FA_ERR_LAUNCH;
-  if (cudaLaunchKernelEx(&c, fa_paged_prompt_kernel<D, kNeg>, t.q, t.k, t.v, p, ph) !=
+  if (cudaLaunchKernelEx(&c, fa_paged_prompt_kernel<D, kNeg>, t.q, t.k, t.v, t.o, p,
+                         ph) !=
           cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;

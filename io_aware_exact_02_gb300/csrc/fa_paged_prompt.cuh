@@ -182,13 +182,57 @@ __device__ __noinline__ void store_rows(uint32_t colO, float own, float pre, lon
   }
 }
 
+// The same for 32 rows of o that are all valid and whole tokens: a box of 64
+// channels at a time, stored by TMA (row r's 16-byte chunk c at c ^ (r % 8), as
+// its swizzle wants it).
+template <int D>
+__device__ __noinline__ void store_box(uint32_t colO, float own, uint8_t* out,
+                                       const CUtensorMap* to, int head, int tok) {
+  const int lane = (int)lane_id();
+  uint8_t* const mine = out + lane * 128;
+#pragma unroll 1
+  for (int c = 0; c < D / 64; ++c) {
+    uint32_t w[2][16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t x[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = 0u;
+      if (colO != ~0u) {
+        tmem_ld32(colO + c * 64 + h * 32, x);
+        tmem_wait_ld(x);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        w[h][i] = own == 0.f ? 0u
+                             : pack_bf16x2(__uint_as_float(x[2 * i]) * own,
+                                           __uint_as_float(x[2 * i + 1]) * own);
+    }
+    if (c > 0) {
+      if (lane == 0) bulk_wait_group_read0();
+      __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      *reinterpret_cast<uint4*>(mine + ((i ^ (lane & 7)) << 4)) =
+          make_uint4(w[i / 4][4 * (i % 4)], w[i / 4][4 * (i % 4) + 1], w[i / 4][4 * (i % 4) + 2],
+                     w[i / 4][4 * (i % 4) + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(to, out, c * 64, head, tok);
+      bulk_commit_group();
+    }
+  }
+}
+
 // The prompt kernel's work on CTA `cta` of the `ctas` that share the phase's
 // list.  kStarted: the caller has waited for the prior grid.
 template <int D, bool kNeg, bool kStarted>
 __device__ __forceinline__ void prompt_cta(const CUtensorMap* tq, const CUtensorMap* tk,
-                                           const CUtensorMap* tv, const PagedParams& p,
-                                           const PagedPhase& ph, int cta, int ctas,
-                                           uint8_t* smem_raw) {
+                                           const CUtensorMap* tv, const CUtensorMap* to,
+                                           const PagedParams& p, const PagedPhase& ph, int cta,
+                                           int ctas, uint8_t* smem_raw) {
   using Cfg = PromptCfg<D>;
   constexpr int S = Cfg::kStages;
   PromptSmem<D>& sm = *reinterpret_cast<PromptSmem<D>*>(
@@ -467,6 +511,15 @@ __device__ __forceinline__ void prompt_cta(const CUtensorMap* tq, const CUtensor
         tc_fence_after();
       }
       const long long slot_row = ((long long)cta * 2 + it.slot) * ph.slot_rows + t * kTile + r;
+      if (lane_id() == 0) bulk_wait_group_read0();  // of the last unit's boxes
+      __syncwarp();
+      // A warp's 32 rows are whole tokens; all of them are the unit's.
+      const bool box = ph.box_out && it.slot < 0 && !(it.first && ph.pre_o != nullptr) &&
+                       __all_sync(0xffffffffu, valid);
+      if (box)
+        store_box<D>(n_t > 0 ? colO : ~0u, own, sm.out[warp], to, it.h * p.G,
+                     it.tok0 + t * ph.tile_tokens + (warp & 3) * (32 / p.G));
+      else
       store_rows<D>(n_t > 0 ? colO : ~0u, own, pre, row, valid ? (it.slot >= 0 ? slot_row : row) : -1,
                     sm.out[warp], it.slot >= 0 ? ph.slot_o : ph.out_o,
                     it.slot >= 0 ? ph.slot_o + (slot_row - lane_id()) * D : nullptr,
@@ -486,6 +539,8 @@ __device__ __forceinline__ void prompt_cta(const CUtensorMap* tq, const CUtensor
           p.lse[row] = lse2 == ninf ? ninf : lse2 * kLn2;
       }
     }
+    if (lane_id() == 0) bulk_wait_group0();
+    __syncwarp();
   } else {
     // Idle: its registers go to the compute warps.
     setmaxnreg_dec<kPagedRegsLoad>();
