@@ -769,7 +769,7 @@ size_t fa_fwd_paged_workspace_size(int T, int B, int Hq, int Hkv, int d, int max
   int shift;
   if (paged_shape(T, B, Hq, Hkv, d, 1, 16, 1, &shift) != FA_OK) return 0;
   if (Hq % Hkv != 0 || Hq / Hkv > 128 || max_q < 1 || prefix_len < 0) return 0;
-  return paged_workspace_layout(T, B, Hq, d, paged_form(T, B, Hq, Hq / Hkv, max_q, prefix_len))
+  return paged_workspace_layout(T, Hq, Hkv, d, paged_form(T, B, Hq, Hq / Hkv, max_q, prefix_len))
       .total;
 }
 

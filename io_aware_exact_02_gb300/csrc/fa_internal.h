@@ -304,13 +304,13 @@ inline PagedForm paged_form(int T, int B, int Hq, int G, int max_q, int prefix_l
 // two phases of a call the split records of the CTAs and their partial results
 // (two slots each: fp32 O rows, then the rows' logsumexp); with a shared prefix
 // its results, fp32 [T][Hq][d] and [T][Hq]; in a duo the phases' CTA counts,
-// and with a prefix the results of the sequences' own keys and where their
-// tiles begin.
+// and with a prefix the results of the sequences' own keys and which slots hold
+// the parts of each phase's units (8 bytes a token and key/value head).
 struct PagedWorkspace {
-  size_t rec[2], slot_o[2], slot_lse[2], pre_o, pre_lse, own_o, own_lse, seq_start, ctas, total;
+  size_t rec[2], slot_o[2], slot_lse[2], pre_o, pre_lse, own_o, own_lse, parts[2], ctas, total;
 };
 constexpr size_t kPagedRecBytes = 64;
-inline PagedWorkspace paged_workspace_layout(int T, int B, int Hq, int d, const PagedForm& f) {
+inline PagedWorkspace paged_workspace_layout(int T, int Hq, int Hkv, int d, const PagedForm& f) {
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   int rows[2] = {f.rows, f.small_rows};
   if (f.share && f.duo) {
@@ -337,7 +337,7 @@ inline PagedWorkspace paged_workspace_layout(int T, int B, int Hq, int d, const 
   w.pre_lse = take(pre * sizeof(float));
   w.own_o = take(own * (size_t)d * sizeof(float));
   w.own_lse = take(own * sizeof(float));
-  w.seq_start = take(own > 0 ? (size_t)B * sizeof(long long) : 0);
+  for (int k = 0; k < 2; ++k) w.parts[k] = take(own > 0 ? (size_t)T * (size_t)Hkv * 8 : 0);
   w.ctas = take(f.duo ? 2 * sizeof(int) : 0);
   w.total = at;
   return w;

@@ -38,14 +38,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
   __shared__ float part_o[kMergeWarps][D], part_l[kMergeWarps], part_m[kMergeWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ctas = ph.ctas ? *ph.ctas : p.ctas;
-  if ((int)blockIdx.x >= ctas) return;
   const PagedRec rec = *reinterpret_cast<const PagedRec*>(ph.rec + blockIdx.x * kPagedRecBytes);
-  if (!rec.split) return;
-  const PagedShare parts(rec.total, ctas, paged_groups(p, ph, ctas));
-  const int c0 = parts.owner(rec.unit_start);  // the unit's first CTA, in its last segment's slot
-  const int c1 = parts.owner(rec.unit_end - 1);
-  const int n = c1 - c0 + 1;
-  const int slot0 = parts.lo(c0) < rec.unit_start ? 1 : 0;
+  if ((int)blockIdx.x >= ctas || !rec.split) return;
+  const int c0 = rec.slot >> 1, n = rec.n;
   // Block `y` of the unit's `ny`.
   const int ny = (n - 1) * (int)gridDim.y;
   const int y = ((int)blockIdx.x - c0 - 1) * (int)gridDim.y + (int)blockIdx.y;
@@ -62,7 +57,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
     const int tok = valid ? r / p.G : 0, head = valid ? r % p.G : 0;
     const int row = (tok / ph.tile_tokens) * kTile + (tok % ph.tile_tokens) * p.G + head;
     auto slot_of = [&](int i) -> long long {
-      return ((long long)(c0 + i) * 2 + (i == 0 ? slot0 : 0)) * ph.slot_rows + row;
+      return (long long)(i == 0 ? rec.slot : 2 * (c0 + i)) * ph.slot_rows + row;
     };
     // One pass over the parts, kBatch of them in flight, with the running
     // maximum of their logsumexp.
@@ -161,71 +156,46 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
 }
 
 // Joins each row's parts of the shared prefix (pa) and of its sequence's own
-// keys (pb), which one launch computed side by side: a warp per row finds the
-// row's units in the two lists and adds up their parts, as the merge kernel
-// does.
+// keys (pb), which one launch computed side by side: a warp per row adds them
+// up as the merge kernel does.  The attention kernels left word of each unit's
+// slots; to find them again from the tables took the row's warp 6 us, most of
+// it divisions and the fetching of their code.
 template <int D>
 __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p,
                                                             const PagedPhase pa,
                                                             const PagedPhase pb) {
   launch_dependents();
-  wait_prior_grid();
   constexpr int kPer = D / 32;
   const int lane = threadIdx.x & 31;
-  const long long r = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int t = (int)(r / p.Hq), hq = (int)(r - (long long)t * p.Hq);
+  const int r = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);  // T * Hq rows: some ten thousand
+  const int t = r / p.Hq, hq = r - t * p.Hq;
   if (t >= p.T) return;
-  // What does not depend on the row's sequence, and sequence t in case it is
-  // that (one token each), are loaded together.
-  const int ctas_a = *pa.ctas, ctas_b = *pb.ctas;
-  const long long total_b = reinterpret_cast<const PagedRec*>(pb.rec)->total;
-  const int guess = min(t, p.B - 1);
-  const int g0 = p.cu_q[guess], g1 = p.cu_q[guess + 1];
-  long long start = pb.seq_start[guess];
-  PagedSeq s = paged_seq(p, pb, guess);
-  if (g0 > t || g1 <= t) {
-    const PagedRow at = paged_row(p.cu_q, p.seq_lens, p.B, p.T, t, p.status);
-    if (at.b < 0) return;
-    s = paged_seq(p, pb, at.b);
-    start = pb.seq_start[at.b];
-  }
-  if (s.n == 0) return;  // (tables out of bounds)
   const int h = hq / p.G, gh = hq - h * p.G;
-  // The row's unit in each list: its first and last CTA, whether the first
-  // part is that CTA's last segment, and the row's place in a slot.
+  const int tok0 = t / pa.unit_tokens * pa.unit_tokens, tile = (t - tok0) / pa.tile_tokens;
+  wait_prior_grid();
+  const int first = p.cu_q[0], end = p.cu_q[p.B];
+  const uint2 ua = pa.parts[(long long)tok0 * p.Hkv + h], ub = pb.parts[(long long)t * p.Hkv + h];
+  if (t < first || t >= end) return;  // a padding row
   struct Parts {
-    int c0, n, slot0, row;
+    int slot, n, row;
   };
-  auto parts_of = [&](const PagedPhase& ph, int ctas, long long total, long long start, int cost,
-                      int tok) -> Parts {
-    const PagedShare share(total, ctas, paged_groups(p, ph, ctas));
-    Parts x;
-    x.c0 = share.owner(start);
-    x.n = share.owner(start + cost - 1) - x.c0 + 1;
-    x.slot0 = share.lo(x.c0) < start ? 1 : 0;
-    x.row = (tok / ph.tile_tokens) * kTile + (tok % ph.tile_tokens) * p.G + gh;
-    return x;
-  };
-  const PagedSeq all = paged_seq(p, pa, 0);
-  const int units = paged_units(pa, all), ia = t / pa.unit_tokens;
-  const int cost_a = max(1, paged_unit_tiles(p, pa, all, 0));
-  const Parts A = parts_of(pa, ctas_a, (long long)p.Hkv * units * cost_a,
-                           ((long long)h * units + ia) * cost_a, cost_a, t - ia * pa.unit_tokens);
-  const int tok = t - s.t0, ib = tok / pb.unit_tokens;
-  start += h * paged_head_cost(p, pb, s);
-  for (int k = 0; k < ib; ++k) start += max(1, paged_unit_tiles(p, pb, s, k));
-  const int cost_b = max(1, paged_unit_tiles(p, pb, s, ib));
-  const Parts B = parts_of(pb, ctas_b, total_b, start, cost_b, tok - ib * pb.unit_tokens);
+  const Parts A = {(int)(ua.x & 0xffff), (int)(ua.x >> 16),
+                   tile * kTile + (t - tok0 - tile * pa.tile_tokens) * p.G + gh};
+  const Parts B = {(int)(ub.x & 0xffff), (int)(ub.x >> 16), (int)ub.y + gh};
+  // (Of a sequence whose tables are out of bounds nothing was written.)
+  if (B.n < 1 || B.slot + 2 * B.n > 2 * kPagedMaxCtas || (unsigned)B.row >= (unsigned)pb.slot_rows)
+    return;
   auto src = [&](int k, const float*& o) -> float {
     const bool own = k >= A.n;
     const PagedPhase& ph = own ? pb : pa;
     const Parts& x = own ? B : A;
     const int c = own ? k - A.n : k;
     if (x.n == 1) {  // the whole unit
-      o = ph.out_o + r * D;
+      o = ph.out_o + (long long)r * D;
       return ph.out_lse[r];
     }
-    const long long row = ((long long)(x.c0 + c) * 2 + (c == 0 ? x.slot0 : 0)) * ph.slot_rows + x.row;
+    const long long row =
+        (long long)(c == 0 ? x.slot : (x.slot & ~1) + 2 * c) * ph.slot_rows + x.row;
     o = ph.slot_o + row * D;
     return ph.slot_lse[row];
   };
@@ -277,7 +247,7 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p,
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  __nv_bfloat16* dst = p.o + r * D + lane * kPer;
+  __nv_bfloat16* dst = p.o + (long long)r * D + lane * kPer;
 #pragma unroll
   for (int e = 0; e < kPer; e += 2)
     *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
@@ -359,7 +329,7 @@ int launch_paged_d(const PagedParams& p, cudaStream_t stream) {
   c.attrs = pdl;
   c.numAttrs = 1;
   const PagedForm f = paged_form(p.T, p.B, p.Hq, p.G, p.max_q, p.prefix_len);
-  const PagedWorkspace w = paged_workspace_layout(p.T, p.B, p.Hq, D, f);
+  const PagedWorkspace w = paged_workspace_layout(p.T, p.Hq, p.Hkv, D, f);
   const int box = p.page_size < kTile ? p.page_size : kTile;
   PagedMaps t;
   int rc;
@@ -386,7 +356,8 @@ int launch_paged_d(const PagedParams& p, cudaStream_t stream) {
       own.key0 = p.prefix_len;
       own.out_o = at(w.own_o);
       own.out_lse = at(w.own_lse);
-      own.seq_start = reinterpret_cast<long long*>(p.workspace + w.seq_start);
+      pre.parts = reinterpret_cast<uint2*>(p.workspace + w.parts[0]);
+      own.parts = reinterpret_cast<uint2*>(p.workspace + w.parts[1]);
       CUtensorMap tq_own;
       if ((rc = phase_units<D>(p, pre, f.prefix_rows, t, &t.q)) != FA_OK ||
           (rc = phase_units<D>(p, own, f.rows, t, &tq_own)) != FA_OK ||

@@ -112,7 +112,7 @@ struct PagedPhase {
   int n_min, n_max;    // sequences of that many new tokens take part
   char* rec;           // PagedRec per CTA
   int* ctas;           // how many CTAs share the phase's list, where not all do; or null
-  long long* seq_start;  // [B], written: where each sequence's tiles begin in the list; or null
+  uint2* parts;        // [T][Hkv], written: PagedParts of the units; or null
   float* slot_o;       // [CTA][2][slot_rows][d]
   float* slot_lse;     // [CTA][2][slot_rows], log2 units
   const float* pre_o;  // results to merge in ([T][Hq][d], [T][Hq], log2 units), or null
@@ -123,13 +123,19 @@ struct PagedPhase {
 
 // What the merge kernel needs to know of a CTA's first unit.
 struct PagedRec {
-  long long total;       // tiles in the list
-  long long unit_start;  // the unit's first tile in the list
-  long long unit_end;
-  int split;             // the unit began in an earlier CTA
+  int split;        // the unit began in an earlier CTA
+  int slot, n;      // its first slot, and how many there are: the next CTAs' slots 0 follow
   int tok0, ntok, h;
 };
 static_assert(sizeof(PagedRec) <= kPagedRecBytes, "record size");
+
+// What the join kernel needs to know of a row's unit: x: its first slot, and
+// 2^16 times the number of its slots (1: the whole unit is in out_o); y: where
+// the token's rows begin in a slot.  Of a shared prefix's units only the first
+// token has one.
+__device__ __forceinline__ uint2 paged_parts(int slot, int n, int row) {
+  return make_uint2((uint32_t)slot | (uint32_t)n << 16, (uint32_t)row);
+}
 
 struct PagedSeq {
   int t0, n, len;  // first row, new tokens, keys
@@ -212,6 +218,7 @@ static __device__ __noinline__ long long paged_div(long long a, long long b) {
 struct PagedShare {
   long long total, per, each;  // tiles: in all, of a group, of a CTA
   int k, more;                 // CTAs of a group
+  PagedShare() = default;
   __device__ __forceinline__ PagedShare(long long t, int ctas, int groups) : total(t) {
     per = groups > 1 ? paged_div(t, groups) : t;
     k = groups > 1 ? ctas / groups : ctas;
@@ -249,7 +256,9 @@ struct PagedItem {
 
 // A CTA's walk along its range of the list.
 struct PagedWalk {
-  long long g, hi, total;
+  long long g, hi;
+  long long start, end;  // of the last segment's unit, in the list
+  PagedShare share;
   int b, h, i, tile, units, tiles;
   PagedSeq s;
   bool first;
@@ -315,13 +324,10 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhas
     inc = warp_scan(cost);
     sums(inc, before, all);
     if (B <= nt) total = all;
-    const PagedShare share(total, ctas, 1);
-    w.total = total;
-    w.g = share.lo(cta);
-    w.hi = share.lo(cta + 1);
+    w.share = PagedShare(total, ctas, 1);
+    w.g = w.share.lo(cta);
+    w.hi = w.share.lo(cta + 1);
     const long long excl = run + before + inc - cost;
-    const bool writes = ph.seq_start != nullptr && cta == 0;
-    if (writes && b0 + tid < B) ph.seq_start[b0 + tid] = excl;
     if (cost > 0 && excl <= w.g && w.g < excl + cost) {
       sc.b = b0 + tid;
       sc.excl = excl;
@@ -330,7 +336,7 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhas
     }
     run += all;
     __syncthreads();
-    if (w.g < run && !writes) break;  // found
+    if (w.g < run) break;  // found
   }
 }
 
@@ -370,12 +376,9 @@ __device__ __forceinline__ void paged_walk_begin(const PagedParams& p, const Pag
   if (B <= 32) {
     const long long cost = paged_cost(p, ph, (int)lane_id(), B, w.s, head);
     const long long inc = warp_scan(cost);
-    w.total = __shfl_sync(0xffffffffu, inc, 31);
-    if (ph.seq_start != nullptr && cta == 0 && (int)lane_id() < B)
-      ph.seq_start[lane_id()] = inc - cost;
-    const PagedShare share(w.total, ctas, paged_groups(p, ph, ctas));
-    w.g = share.lo(cta);
-    w.hi = share.lo(cta + 1);
+    w.share = PagedShare(__shfl_sync(0xffffffffu, inc, 31), ctas, paged_groups(p, ph, ctas));
+    w.g = w.share.lo(cta);
+    w.hi = w.share.lo(cta + 1);
     if (w.g >= w.hi) return;  // idle CTA
     const unsigned at = __ballot_sync(0xffffffffu, inc - cost <= w.g && w.g < inc);
     w.b = __ffs((int)at) - 1;
@@ -430,17 +433,8 @@ __device__ __forceinline__ PagedItem paged_next(const PagedParams& p, const Page
   it.first = w.tile == 0;
   it.tile0 = w.tiles;
   w.tiles += it.nj;
-  if (w.first && lane_id() == 0) {
-    PagedRec r;
-    r.total = w.total;
-    r.unit_start = w.g - w.tile;
-    r.unit_end = r.unit_start + cost;
-    r.split = w.tile > 0;
-    r.tok0 = it.tok0;
-    r.ntok = it.ntok;
-    r.h = it.h;
-    *reinterpret_cast<PagedRec*>(ph.rec + cta * kPagedRecBytes) = r;
-  }
+  w.start = w.g - w.tile;
+  w.end = w.start + cost;
   w.first = false;
   w.g += take;
   w.tile += take;
@@ -585,11 +579,33 @@ __device__ __forceinline__ void paged_produce_k(const PagedParams& p, const Page
     return ok && !it.end;
   };
   paged_walk_begin(p, ph, sm.scan, walk, cta, ctas);
-  if (walk.g >= walk.hi && lane == 0) {
-    PagedRec r = {};
-    r.total = walk.total;
-    *reinterpret_cast<PagedRec*>(ph.rec + cta * kPagedRecBytes) = r;
-  }
+  // What the kernels that join parts need to know, once the segment's loads
+  // are on the way: of the CTA's first unit, and of a unit that begins here.
+  auto describe = [&](const PagedItem& it, bool first) {
+    const bool begins = it.first != 0;
+    if (first && begins && lane == 0) reinterpret_cast<PagedRec*>(ph.rec + cta * kPagedRecBytes)->split = 0;
+    if (begins ? ph.parts == nullptr : !first) return;
+    int c0 = cta, n = 1;
+    if (it.slot >= 0) {
+      if (!begins) c0 = walk.share.owner(walk.start);
+      n = walk.share.owner(walk.end - 1) - c0 + 1;
+    }
+    if (!begins) {
+      PagedRec r;
+      r.split = 1;
+      r.slot = 2 * c0 + (walk.share.lo(c0) < walk.start ? 1 : 0);
+      r.n = n;
+      r.tok0 = it.tok0;
+      r.ntok = it.ntok;
+      r.h = it.h;
+      if (lane == 0) *reinterpret_cast<PagedRec*>(ph.rec + cta * kPagedRecBytes) = r;
+    } else if (lane < (ph.whole_batch ? 1 : it.ntok)) {
+      ph.parts[(long long)(it.tok0 + lane) * p.Hkv + it.h] =
+          paged_parts(2 * cta + max(it.slot, 0), n, lane * p.G);
+    }
+  };
+  if (walk.g >= walk.hi && lane == 0)
+    reinterpret_cast<PagedRec*>(ph.rec + cta * kPagedRecBytes)->split = 0;
   PagedPages pages, after;
   int m = 0;
   bool more = publish(0);
@@ -598,6 +614,7 @@ __device__ __forceinline__ void paged_produce_k(const PagedParams& p, const Page
     const int nj = sm.item[m % kRing].nj, h = sm.item[m % kRing].h;
     int key = sm.item[m % kRing].key;
     auto look_ahead = [&] {
+      describe(sm.item[m % kRing], m == 0);
       more = publish(m + 1);
       if (more) paged_pages_begin(p, sm.item[(m + 1) % kRing], after);
     };
