@@ -64,6 +64,7 @@ constexpr int kAppendThreads = 128;
 
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads) fa_kv_append_kernel(const KvAppendParams p) {
+  launch_dependents();
   wait_prior_grid();
   constexpr int kPairs = D / 16;                   // chunk pairs of a head
   constexpr int kRows = kAppendThreads / kPairs;   // heads in one sweep of the CTA
