@@ -465,7 +465,7 @@ def _checked_rows(name, t, T, H, d, device):
     row, head, one = t.stride()
     if (one != 1 and d > 1) or (head != d and H > 1):
         raise ValueError("%s must have contiguous heads" % name)
-    return t.data_ptr(), row if T > 1 else max(row, H * d)
+    return t.data_ptr(), row if T > 1 else H * d  # (a single row has any stride)
 
 
 def _checked_cache(k_pages, v_pages, page_table, seq_lens, cu_q, device):
@@ -558,8 +558,11 @@ def _fwd_paged(fn, q, k_pages, v_pages, page_table, seq_lens, cu_q, prefix_pages
         n = prefix_pages.shape[0]
         prefix_len = n * page_size
         prefix = (_checked("prefix_pages", prefix_pages, (n,), _I32, dev), prefix_len)
-    if workspace is not None and workspace.get_device() != dev:
-        _refuse("workspace", workspace, workspace.shape, workspace.dtype, dev)
+    if workspace is not None and (not isinstance(workspace, torch.Tensor)
+                                  or workspace.get_device() != dev
+                                  or not workspace.is_contiguous()):
+        _refuse("workspace", workspace, getattr(workspace, "shape", ()),
+                getattr(workspace, "dtype", None), dev)
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             return _fwd_paged(fn, q, k_pages, v_pages, page_table, seq_lens, cu_q, prefix_pages,

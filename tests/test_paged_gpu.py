@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from io_aware_exact_02_gb300 import build, fa
-from paged_common import BF16, FP32, Batch
+from paged_common import BF16, FP32, Batch, compare, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -444,3 +444,110 @@ def test_cache_past_32_bit_offsets():
     fa.kv_append(k, k, kp, vp, table, x.seq_lens, x.cu_q)
     fa.check_device_status()
     assert torch.equal(vp[8300, :, 399 - 256], k[0]) and torch.equal(kp[8500, :, 299 - 256], k[3])
+
+
+# ------------------------------------------------- less usual calls
+
+def test_a_single_row_may_have_any_stride():
+    x = Batch(8, 2, 128, 16, [77], [1], seed=8)
+    wide = torch.zeros(3, 8 * 128 + 3, dtype=torch.bfloat16, device="cuda")
+    q = wide.as_strided((1, 8, 128), (8 * 128 + 3, 128, 1))
+    q.copy_(x.q)
+    x.q = q
+    attend(x)
+    k = torch.ones(1, 2, 128 + 8, dtype=torch.bfloat16, device="cuda").as_strided((1, 2, 128), (5, 128, 1))
+    got = fa.kv_append(k, k, x.k_pages, x.v_pages, x.table, x.seq_lens, x.cu_q, q=q, q_out=q)
+    fa.check_device_status()
+    assert got is q and torch.equal(q, x.q_host.cuda())
+
+
+def test_workspace_is_checked():
+    x = Batch(8, 2, 128, 16, [77], [1], seed=8)
+    n = fa.fwd_paged_workspace_size(1, 1, 8, 2, 128, 1)
+    call = lambda ws: fa.fwd_paged(*x.args(), max_q=1, out=x.out, lse=x.lse, workspace=ws)  # noqa: E731
+    with pytest.raises(ValueError, match="workspace"):
+        call(torch.empty(n))
+    with pytest.raises(ValueError, match="workspace"):
+        call(torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2])
+    with pytest.raises(ValueError, match="workspace"):
+        call(n)
+    with pytest.raises(RuntimeError, match="fa_fwd_paged"):
+        call(torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
+    o, lse = call(torch.empty(n, dtype=torch.uint8, device="cuda"))
+    x.check(o, lse, True, 1 / math.sqrt(128))
+
+
+def test_captured_graphs_with_their_own_workspaces_replayed_together():
+    """Captures that leave the workspace to the allocator: each graph has its
+    own, so two of them may run at once, beside eager calls."""
+    xs = [Batch(8, 2, 128, 16, [900, 40, 333], [1, 1, 1], seed=1),
+          Batch(8, 2, 128, 16, [700, 641, 800], [1, 2, 1], seed=3, prefix=640),
+          Batch(8, 1, 64, 32, [700, 650], [90, 70], seed=2)]
+
+    def call(x):
+        kw = dict(max_q=max(x.nq), out=x.out, lse=x.lse)
+        if x.prefix:
+            return fa.fwd_paged_prefix(*x.args(), x.prefix_pages, **kw)
+        return fa.fwd_paged(*x.args(), **kw)
+
+    want, graphs, streams = [], [], []
+    for x in xs:
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            a, b = call(x)
+            want.append((a.clone(), b.clone()))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            call(x)
+        graphs.append(g)
+        streams.append(s)
+    eager = Batch(8, 2, 128, 16, [500, 600], [1, 30], seed=4)
+    first = [t.clone() for t in call(eager)]
+    for _ in range(20):
+        for x in xs:
+            x.out.zero_(), x.lse.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        again = call(eager)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+        for x, (a, b) in zip(xs, want):
+            n = x.cu[-1]
+            assert torch.equal(x.out[:n], a[:n]) and torch.equal(x.lse[:n], b[:n])
+    fa.check_device_status()
+
+
+def test_sequences_may_share_pages_in_their_tables():
+    """Two sequences whose tables name the same pages, one of them twice."""
+    x = Batch(8, 2, 64, 16, [100, 100, 90], [1, 3, 2], seed=12)
+    x.table[1] = x.table[0]
+    x.keys[1], x.vals[1] = x.keys[0], x.vals[0]
+    x.table[2, 1] = x.table[2, 0]
+    for y in (x.keys, x.vals):
+        y[2] = torch.cat([y[2][:16], y[2][:16], y[2][32:]])
+    attend(x)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 64), (12, 2, 128)])
+def test_long_prompt_sampled_rows(Hq, Hkv, d):
+    """A prompt of thousands of rows after thousands of keys: a sample of rows
+    at the tiles' edges."""
+    n, L = 3000, 7001
+    x = Batch(Hq, Hkv, d, 64, [L], [n], seed=Hq)
+    o, lse = fa.fwd_paged(*x.args(), max_q=n)
+    fa.check_device_status()
+    for r in (0, 1, 31, 63, 64, 127, 128, 500, 1499, 2047, 2048, 2998, 2999):
+        keys = L - n + r + 1
+        ref = reference(x.q_host[r:r + 1], x.keys[0][:keys], x.vals[0][:keys], True, 1 / math.sqrt(d))
+        compare(o[r:r + 1].cpu(), lse[r:r + 1].cpu(), ref, r)
+
+
+def test_more_sequences_than_rows_can_fill():
+    """A batch whose sequences mostly have no new token, padded to a width."""
+    lens = [(i * 53) % 400 for i in range(300)]
+    nq = [1 if i % 7 == 3 and lens[i] > 0 else 0 for i in range(300)]
+    attend(Batch(16, 4, 128, 16, lens, nq, seed=13, pad=5))
