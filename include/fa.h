@@ -304,7 +304,14 @@ int fa_kv_append(const void* q, const void* k, const void* v, void* q_out, void*
  *   workspace: device buffer of fa_fwd_paged_workspace_size(...) bytes,
  *         256-byte aligned (may be NULL where that is 0).  Two calls in flight
  *         at once need two workspaces.
- * Keys in slots past a sequence's length are never used, whatever they hold.
+ * Keys and values in slots past a sequence's length are never used, whatever
+ * they hold.  A key that the causal mask hides from a row is not used by it
+ * either; its value row is multiplied by a probability of 0 and so has to be
+ * finite, as in the other forward calls.
+ * Errors: FA_ERR_ARG, FA_ERR_UNSUPPORTED_D, FA_ERR_ALIGN (16 bytes for q, o,
+ * lse and the pages; 4 for the tables), FA_ERR_WORKSPACE, FA_ERR_DEVICE,
+ * FA_ERR_LAUNCH; with anything but FA_OK nothing was launched, unless it is
+ * FA_ERR_LAUNCH.
  */
 size_t fa_fwd_paged_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_q,
                                    int prefix_len);
@@ -319,7 +326,8 @@ int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* 
  * keys (a positive multiple of page_size, at most max_pages pages), held once
  * in the pages prefix_pages[0 .. prefix_len / page_size): their attention is
  * computed once for the query rows of the whole batch and merged with each
- * sequence's own by logsumexp.  seq_lens and positions count the prefix; the first prefix_len /
+ * sequence's own by logsumexp.  seq_lens and positions count the prefix (a
+ * sequence shorter than it has its first keys); the first prefix_len /
  * page_size entries of each page_table row stand for the prefix and are not
  * read.  Other arguments, results and errors as fa_fwd_paged, with the
  * workspace size for the same prefix_len.
@@ -370,8 +378,9 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  * receives the identifier of the wait or check that raised it (0 if none):
  * 101-199 a wait of the forward kernel, 201-299 one of the backward main
  * kernel, 301-304 the paged cache's tables (row ranges, lengths, positions,
- * page numbers), 1101-1199 a bounds check of the forward kernels, 1201-1299 one of
- * the backward kernels, FA_SITE_SELFTEST and FA_SITE_SELFTEST_BOUNDS the self
+ * page numbers), 311-399 a wait of a paged attention kernel, 1101-1199 a bounds
+ * check of the forward kernels, 1201-1299 one of the backward kernels,
+ * 1301-1399 one of the paged attention kernels, FA_SITE_SELFTEST and FA_SITE_SELFTEST_BOUNDS the self
  * tests'.
  */
 int fa_device_status(void* stream, int* site);

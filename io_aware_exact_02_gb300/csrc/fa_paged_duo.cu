@@ -13,7 +13,7 @@
 // Clusters of two CTAs have one kind of work: two neighbouring SMs that run
 // both kinds, whose loops together do not fit what they share of the
 // instruction cache, take 4 us instead of 1.5 for a step of the prompt kernel
-// (and the shared prefix of 16K keys 70 us instead of 60).
+// (a call behind a shared prefix of 16K keys 67 us instead of 58).
 #include "fa_paged_decode.cuh"
 #include "fa_paged_launch.h"
 #include "fa_paged_prompt.cuh"

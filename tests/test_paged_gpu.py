@@ -551,3 +551,26 @@ def test_more_sequences_than_rows_can_fill():
     lens = [(i * 53) % 400 for i in range(300)]
     nq = [1 if i % 7 == 3 and lens[i] > 0 else 0 for i in range(300)]
     attend(Batch(16, 4, 128, 16, lens, nq, seed=13, pad=5))
+
+
+@pytest.mark.parametrize("nq", [[1, 1, 1], [5, 3, 9], [150, 1, 40]])
+@pytest.mark.parametrize("prefix", [0, 160])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_bad_query_spoils_its_own_row_only(nq, prefix, bad):
+    x = Batch(8, 2, 128, 16, [500, 300, 260], nq, seed=14, prefix=prefix)
+    want = [t.clone() for t in attend(x, prefix=prefix > 0)]
+    row = x.cu[1]
+    x.q[row, 3, 7] = bad
+    kw = dict(max_q=max(nq), out=x.out, lse=x.lse)
+    if prefix:
+        o, lse = fa.fwd_paged_prefix(*x.args(), x.prefix_pages, **kw)
+    else:
+        o, lse = fa.fwd_paged(*x.args(), **kw)
+    fa.check_device_status()
+    keep = torch.ones(x.T, 8, dtype=torch.bool, device="cuda")
+    keep[row, 3] = False
+    assert torch.isnan(lse[row, 3]) and torch.isnan(o[row, 3]).all()
+    # What shares its tile may rescale at other moments: two roundings of
+    # values below 4, and of the probabilities.
+    assert (o[keep].float() - want[0][keep].float()).abs().max() <= 8 * BF16
+    assert (lse[keep] - want[1][keep]).abs().max() <= 1e-4
