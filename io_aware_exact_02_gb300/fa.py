@@ -430,9 +430,11 @@ def rope_table(length: int, rope_dim: int, base: float = 10000.0, device="cuda")
 
 
 # The paged-cache calls serve single tokens, where the call itself is what a
-# step costs: their checks look at each tensor once, and only a failed one
-# finds out what is wrong with it.
+# step costs: they look at their tensors once, in one condition, and only a
+# call that fails it finds out what is wrong (_refuse_call).
 _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_current_device = torch.cuda.current_device
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _refuse(name, t, shape, dtype, device):
@@ -448,38 +450,52 @@ def _refuse(name, t, shape, dtype, device):
     raise ValueError("%s must be contiguous" % name)
 
 
-def _checked(name, t, shape, dtype, device):
-    """The data pointer of a contiguous tensor of that shape, type and device."""
+def _check_one(name, t, shape, dtype, device):
     if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device
             or t.shape != shape or not t.is_contiguous()):
         _refuse(name, t, shape, dtype, device)
-    return t.data_ptr()
 
 
-def _checked_rows(name, t, T, H, d, device):
-    """Data pointer and row stride of packed rows (T, H, d) bf16 whose heads
-    are contiguous."""
+def _check_rows(name, t, T, H, d, device):
     if (not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != device
             or t.shape != (T, H, d)):
         _refuse(name, t, (T, H, d), _BF16, device)
-    row, head, one = t.stride()
+    _, head, one = t.stride()
     if (one != 1 and d > 1) or (head != d and H > 1):
         raise ValueError("%s must have contiguous heads" % name)
-    return t.data_ptr(), row if T > 1 else H * d  # (a single row has any stride)
 
 
-def _checked_cache(k_pages, v_pages, page_table, seq_lens, cu_q, device):
-    """Data pointers and sizes of the cache and its tables."""
+def _refuse_call(name, lead, heads, rows, k_pages, v_pages, page_table, seq_lens, cu_q, others):
+    """Raises what is wrong with a call of the paged cache.  lead: its first
+    rows; heads: their number, None: the cache's; rows, others: more packed
+    rows (name, tensor, heads) and contiguous tensors (name, tensor, shape,
+    type)."""
+    if not isinstance(lead, torch.Tensor) or not lead.is_cuda or lead.dim() != 3:
+        raise ValueError("%s must be a CUDA tensor of shape (T, %s, d)" % (name, heads))
+    dev, T = lead.get_device(), lead.shape[0]
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
         raise ValueError("k_pages must have shape (num_pages, Hkv, page_size, d)")
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must have shape (B, max_pages)")
     shape, (B, width) = k_pages.shape, page_table.shape
-    return (_checked("k_pages", k_pages, shape, _BF16, device),
-            _checked("v_pages", v_pages, shape, _BF16, device),
-            _checked("page_table", page_table, (B, width), _I32, device),
-            _checked("seq_lens", seq_lens, (B,), _I32, device),
-            _checked("cu_q", cu_q, (B + 1,), _I32, device)), shape, B, width
+    _, Hkv, page_size, d = shape
+    for n, t, s, dt in (("k_pages", k_pages, shape, _BF16), ("v_pages", v_pages, shape, _BF16),
+                        ("page_table", page_table, (B, width), _I32),
+                        ("seq_lens", seq_lens, (B,), _I32), ("cu_q", cu_q, (B + 1,), _I32)):
+        _check_one(n, t, s, dt, dev)
+    _check_rows(name, lead, T, Hkv if heads == "Hkv" else lead.shape[1], d, dev)
+    for n, t, h in rows:
+        if t is not None:
+            if not isinstance(t, torch.Tensor) or t.dim() != 3:
+                raise ValueError("%s must have shape (T, %s, d)" % (n, h or "Hq"))
+            _check_rows(n, t, T, t.shape[1] if h is None else h, d, dev)
+    for n, t, s, dt in others:
+        if t is not None:
+            if not isinstance(t, torch.Tensor) or t.dim() != len(s):
+                raise ValueError("%s must have shape (%s)" % (n, ", ".join(map(str, s))))
+            _check_one(n, t, tuple(t.shape[i] if isinstance(x, str) else x
+                                   for i, x in enumerate(s)), dt, dev)
+    raise ValueError("arguments of other types, shapes or devices than the call takes")
 
 
 def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_q, q=None, q_out=None, rope=None,
@@ -489,40 +505,65 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_q, q=None, q_out=
     rotation).  Sequence b's rows are cu_q[b] .. cu_q[b+1]-1 and end at
     position seq_lens[b]-1.  Returns the rotated queries (``q_out``,
     allocated if not given; it may be ``q``), or None without q."""
-    if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 3:
-        raise ValueError("k must be a CUDA tensor of shape (T, Hkv, d)")
-    dev = k.get_device()
-    (kp, vp, table, lens, cu), (num_pages, Hkv, page_size, d), B, width = _checked_cache(
-        k_pages, v_pages, page_table, seq_lens, cu_q, dev)
-    T = k.shape[0]
-    k_ptr, ks = _checked_rows("k", k, T, Hkv, d, dev)
-    v_ptr, vs = _checked_rows("v", v, T, Hkv, d, dev)
-    q_ptr = q_out_ptr = None
     Hq = qs = qos = rope_len = rope_dim = 0
-    if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dim() != 3:
-            raise ValueError("q must have shape (T, Hq, d)")
-        Hq = q.shape[1]
-        q_ptr, qs = _checked_rows("q", q, T, Hq, d, dev)
-        if q_out is None:  # rows of no sequence are not written
-            q_out = torch.zeros((T, Hq, d), dtype=_BF16, device=q.device)
-        q_out_ptr, qos = _checked_rows("q_out", q_out, T, Hq, d, dev)
-    elif q_out is not None:
+    q_ptr = q_out_ptr = rope_ptr = None
+    try:
+        dev, pool, table = k.get_device(), k_pages.shape, page_table.shape
+        num_pages, Hkv, page_size, d = pool
+        B, width = table
+        T = k.shape[0]
+        rows = (T, Hkv, d)
+        ks, head, one = k.stride()
+        vs, vhead, vone = v.stride()
+        ok = (dev >= 0 and k.shape == rows and v.shape == rows and v_pages.shape == pool
+              and seq_lens.shape == (B,) and cu_q.shape == (B + 1,)
+              and k.dtype is _BF16 and v.dtype is _BF16 and k_pages.dtype is _BF16
+              and v_pages.dtype is _BF16 and page_table.dtype is _I32 and seq_lens.dtype is _I32
+              and cu_q.dtype is _I32
+              and v.get_device() == dev and k_pages.get_device() == dev
+              and v_pages.get_device() == dev and page_table.get_device() == dev
+              and seq_lens.get_device() == dev and cu_q.get_device() == dev
+              and one == 1 and vone == 1 and (Hkv == 1 or head == vhead == d)
+              and k_pages.is_contiguous() and v_pages.is_contiguous()
+              and page_table.is_contiguous() and seq_lens.is_contiguous() and cu_q.is_contiguous())
+        if ok and q is not None:
+            Hq = q.shape[1]
+            if q_out is None:  # rows of no sequence are not written
+                q_out = torch.zeros((T, Hq, d), dtype=_BF16, device=q.device)
+            rows = (T, Hq, d)
+            qs, head, one = q.stride()
+            qos, ohead, oone = q_out.stride()
+            ok = (q.shape == rows and q_out.shape == rows and q.dtype is _BF16
+                  and q_out.dtype is _BF16 and q.get_device() == dev and q_out.get_device() == dev
+                  and one == 1 and oone == 1 and (Hq == 1 or head == ohead == d))
+            q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
+        if ok and rope is not None:
+            rope_len, rope_dim = rope.shape
+            ok = rope.dtype is _F32 and rope.get_device() == dev and rope.is_contiguous()
+            rope_ptr = rope.data_ptr()
+    except (AttributeError, TypeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        h = k_pages.shape[1] if getattr(k_pages, "ndim", 0) == 4 else "Hkv"
+        _refuse_call("k", k, "Hkv", (("v", v, h), ("q", q, None),
+                                     ("q_out", q_out, q.shape[1] if getattr(q, "ndim", 0) == 3
+                                      else None)),
+                     k_pages, v_pages, page_table, seq_lens, cu_q,
+                     (("rope", rope, ("length", "rope_dim"), _F32),))
+    if q is None and q_out is not None:
         raise ValueError("q_out needs q")
-    rope_ptr = None
-    if rope is not None:
-        if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
-            raise ValueError("rope must have shape (length, rope_dim)")
-        rope_len, rope_dim = rope.shape
-        rope_ptr = _checked("rope", rope, (rope_len, rope_dim), _F32, dev)
-    if torch.cuda.current_device() != dev:
+    if T == 1:  # a single row has any stride
+        ks = vs = Hkv * d
+        qs = qos = Hq * d
+    if _current_device() != dev:
         with torch.cuda.device(dev):
             return kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_q, q, q_out, rope,
                              interleaved)
-    rc = load().fa_kv_append(q_ptr, k_ptr, v_ptr, q_out_ptr, kp, vp, table, lens, cu,
-                             rope_ptr, T, B, Hq, Hkv, d, qs, ks, vs, qos, num_pages, page_size,
-                             width, rope_dim, rope_len, 1 if interleaved else 0,
-                             torch._C._cuda_getCurrentRawStream(dev))
+    rc = (_lib or load()).fa_kv_append(
+        q_ptr, k.data_ptr(), v.data_ptr(), q_out_ptr, k_pages.data_ptr(), v_pages.data_ptr(),
+        page_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), rope_ptr, T, B, Hq, Hkv, d,
+        qs, ks, vs, qos, num_pages, page_size, width, rope_dim, rope_len,
+        1 if interleaved else 0, _current_stream(dev))
     if rc != FA_OK:
         _check("fa_kv_append", rc)
     return q_out
@@ -536,38 +577,56 @@ def fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len=0) -> int:
 
 def _fwd_paged(fn, q, k_pages, v_pages, page_table, seq_lens, cu_q, prefix_pages, max_q, causal,
                scale, out, lse, workspace):
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
-        raise ValueError("q must be a CUDA tensor of shape (T, Hq, d)")
-    dev = q.get_device()
-    (kp, vp, table, lens, cu), (num_pages, Hkv, page_size, d), B, width = _checked_cache(
-        k_pages, v_pages, page_table, seq_lens, cu_q, dev)
-    T, Hq, _ = q.shape
-    q_ptr, qs = _checked_rows("q", q, T, Hq, d, dev)
-    scale = d ** -0.5 if scale is None else float(scale)
-    max_q = T if max_q is None else int(max_q)
-    if out is None:  # rows of no sequence are not written
-        out = torch.zeros((T, Hq, d), dtype=_BF16, device=q.device)
-    if lse is None:
-        lse = torch.full((T, Hq), -math.inf, dtype=_F32, device=q.device)
-    o_ptr = _checked("out", out, (T, Hq, d), _BF16, dev)
-    lse_ptr = _checked("lse", lse, (T, Hq), _F32, dev)
-    prefix, prefix_len = (), 0
-    if prefix_pages is not None:
-        if not isinstance(prefix_pages, torch.Tensor) or prefix_pages.dim() != 1:
-            raise ValueError("prefix_pages must have shape (pages,)")
-        n = prefix_pages.shape[0]
-        prefix_len = n * page_size
-        prefix = (_checked("prefix_pages", prefix_pages, (n,), _I32, dev), prefix_len)
+    prefix_len, prefix = 0, ()
+    try:
+        dev, pool, table = q.get_device(), k_pages.shape, page_table.shape
+        num_pages, Hkv, page_size, d = pool
+        B, width = table
+        T, Hq, _ = rows = q.shape
+        qs, head, one = q.stride()
+        ok = (dev >= 0 and rows[2] == d and v_pages.shape == pool
+              and seq_lens.shape == (B,) and cu_q.shape == (B + 1,)
+              and q.dtype is _BF16 and k_pages.dtype is _BF16 and v_pages.dtype is _BF16
+              and page_table.dtype is _I32 and seq_lens.dtype is _I32 and cu_q.dtype is _I32
+              and k_pages.get_device() == dev and v_pages.get_device() == dev
+              and page_table.get_device() == dev and seq_lens.get_device() == dev
+              and cu_q.get_device() == dev and one == 1 and (Hq == 1 or head == d)
+              and k_pages.is_contiguous() and v_pages.is_contiguous()
+              and page_table.is_contiguous() and seq_lens.is_contiguous() and cu_q.is_contiguous())
+        if ok and out is None:  # rows of no sequence are not written
+            out = torch.zeros(rows, dtype=_BF16, device=q.device)
+        if ok and lse is None:
+            lse = torch.full((T, Hq), -math.inf, dtype=_F32, device=q.device)
+        ok = (ok and out.shape == rows and out.dtype is _BF16 and out.get_device() == dev
+              and out.is_contiguous() and lse.shape == (T, Hq) and lse.dtype is _F32
+              and lse.get_device() == dev and lse.is_contiguous())
+        if prefix_pages is not None:
+            n, = prefix_pages.shape
+            prefix_len = n * page_size
+            prefix = prefix_pages.data_ptr(), prefix_len
+            ok = (ok and prefix_pages.dtype is _I32 and prefix_pages.get_device() == dev
+                  and prefix_pages.is_contiguous())
+    except (AttributeError, TypeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        shape = q.shape if getattr(q, "ndim", 0) == 3 else ("T", "Hq", "d")
+        _refuse_call("q", q, "Hq", (), k_pages, v_pages, page_table, seq_lens, cu_q,
+                     (("out", out, tuple(shape), _BF16), ("lse", lse, tuple(shape[:2]), _F32),
+                      ("prefix_pages", prefix_pages, ("pages",), _I32)))
     if workspace is not None and (not isinstance(workspace, torch.Tensor)
                                   or workspace.get_device() != dev
                                   or not workspace.is_contiguous()):
         _refuse("workspace", workspace, getattr(workspace, "shape", ()),
                 getattr(workspace, "dtype", None), dev)
-    if torch.cuda.current_device() != dev:
+    if T == 1:  # a single row has any stride
+        qs = Hq * d
+    scale = d ** -0.5 if scale is None else float(scale)
+    max_q = T if max_q is None else int(max_q)
+    if _current_device() != dev:
         with torch.cuda.device(dev):
             return _fwd_paged(fn, q, k_pages, v_pages, page_table, seq_lens, cu_q, prefix_pages,
                               max_q, causal, scale, out, lse, workspace)
-    lib, stream = load(), torch._C._cuda_getCurrentRawStream(dev)
+    lib, stream = _lib or load(), _current_stream(dev)
     if workspace is None:
         # From torch's allocator without a tensor around it, which costs more
         # than a single-token call's launch; it is the stream's again as soon
@@ -577,9 +636,11 @@ def _fwd_paged(fn, q, k_pages, v_pages, page_table, seq_lens, cu_q, prefix_pages
     else:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     try:
-        rc = getattr(lib, fn)(q_ptr, kp, vp, o_ptr, lse_ptr, table, lens, cu, *prefix, T, B, Hq,
-                              Hkv, d, qs, num_pages, page_size, width, max_q, 1 if causal else 0,
-                              scale, ws, ws_bytes, stream)
+        rc = getattr(lib, fn)(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                              out.data_ptr(), lse.data_ptr(), page_table.data_ptr(),
+                              seq_lens.data_ptr(), cu_q.data_ptr(), *prefix, T, B, Hq, Hkv, d, qs,
+                              num_pages, page_size, width, max_q, 1 if causal else 0, scale, ws,
+                              ws_bytes, stream)
     finally:
         if workspace is None:
             torch._C._cuda_cudaCachingAllocator_raw_delete(ws)

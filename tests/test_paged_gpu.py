@@ -574,3 +574,64 @@ def test_a_bad_query_spoils_its_own_row_only(nq, prefix, bad):
     # values below 4, and of the probabilities.
     assert (o[keep].float() - want[0][keep].float()).abs().max() <= 8 * BF16
     assert (lse[keep] - want[1][keep]).abs().max() <= 1e-4
+
+
+WRONG = {  # argument -> what is wrong with it
+    "type": lambda t: t.double() if t.is_floating_point() else t.long(),
+    "device": lambda t: t.cpu(),
+    "shape": lambda t: torch.cat([t, t], t.dim() - 1),
+    "rank": lambda t: t[None],
+    "none": lambda t: None,
+    "list": lambda t: [1, 2],
+    "strides": lambda t: torch.stack([t, t], t.dim()).select(t.dim(), 0),
+}
+
+
+@pytest.mark.parametrize("how", sorted(WRONG))
+@pytest.mark.parametrize("what", ["k", "v", "k_pages", "v_pages", "page_table", "seq_lens", "cu_q",
+                                  "q", "q_out", "rope"])
+def test_append_refuses(what, how):
+    x = Batch(8, 2, 128, 16, [60, 70], [2, 1], seed=15)
+    k = torch.ones(3, 2, 128, dtype=torch.bfloat16, device="cuda")
+    kw = dict(k=k, v=k.clone(), k_pages=x.k_pages, v_pages=x.v_pages, page_table=x.table,
+              seq_lens=x.seq_lens, cu_q=x.cu_q, q=x.q, q_out=x.q.clone(), rope=fa.rope_table(80, 128))
+    fa.kv_append(**kw)
+    if how == "none" and what in ("q_out", "rope"):
+        pytest.skip("optional")
+    before = x.k_pages.view(torch.int16).clone(), kw["q_out"].clone()
+    kw[what] = WRONG[how](kw[what])
+    if what == "page_table" and how == "shape":
+        kw[what] = x.table.repeat(2, 1)  # (a wider one would be right)
+    with pytest.raises((ValueError, RuntimeError)) as e:
+        fa.kv_append(**kw)
+    # (the sizes come from the table, the pages and k: another argument may be
+    # the one that does not fit them)
+    named = {"k_pages": ("k_pages", "v_pages", "k "), "page_table": ("page_table", "seq_lens")}.get(what, (what,))
+    if isinstance(e.value, ValueError):
+        assert any(n in str(e.value) for n in named + ("q_out needs q",)), e.value
+    fa.check_device_status()
+    assert torch.equal(x.k_pages.view(torch.int16), before[0])
+    if what != "q_out":
+        assert torch.equal(kw["q_out"], before[1])
+
+
+@pytest.mark.parametrize("how", sorted(WRONG))
+@pytest.mark.parametrize("what", ["q", "k_pages", "v_pages", "page_table", "seq_lens", "cu_q",
+                                  "prefix_pages", "out", "lse"])
+def test_attention_refuses(what, how):
+    x = Batch(8, 2, 128, 16, [60, 70], [2, 1], seed=15, prefix=32)
+    kw = dict(q=x.q, k_pages=x.k_pages, v_pages=x.v_pages, page_table=x.table,
+              seq_lens=x.seq_lens, cu_q=x.cu_q, prefix_pages=x.prefix_pages, out=x.out, lse=x.lse)
+    if how == "none" and what in ("out", "lse", "prefix_pages"):
+        pytest.skip("optional, or another call")
+    kw[what] = WRONG[how](kw[what])
+    if what == "prefix_pages" and how == "shape":
+        kw[what] = x.prefix_pages.repeat(40)  # more pages than the table is wide
+    if what == "page_table" and how == "shape":
+        kw[what] = x.table.repeat(2, 1)  # (a wider one would be right)
+    with pytest.raises((ValueError, RuntimeError)) as e:
+        fa.fwd_paged_prefix(**kw)
+    if isinstance(e.value, ValueError):
+        assert any(n in str(e.value) for n in (what, "q has shape", "v_pages", "seq_lens")), e.value
+    fa.check_device_status()
+    assert torch.all(x.out == 7.0) and torch.all(x.lse == 7.0)
