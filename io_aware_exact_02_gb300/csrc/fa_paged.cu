@@ -242,49 +242,59 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p,
     return ph.slot_lse[row];
   };
   const int n = A.n + B.n;
-  constexpr int kBatch = 4;
   const float ninf = __int_as_float(0xff800000);
   float m = ninf, acc[kPer], sum = 0.f;
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  for (int k0 = 0; k0 < n; k0 += kBatch) {
-    float v[kBatch][kPer], w[kBatch], top = m;
-    bool none = true;
+  // 32 parts at a time: a lane finds one and weighs it, then all lanes add up
+  // the parts, kBatch of them in flight (the first before their weights).
+  constexpr int kBatch = 6;
+#pragma unroll 1
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    const float* o = pa.out_o;
+    float w = ninf;
+    if (k0 + lane < n) w = src(k0 + lane, o);
+    const int cnt = min(32, n - k0);
+    float f = 0.f;
+#pragma unroll 1
+    for (int j0 = 0; j0 < cnt; j0 += kBatch) {
+      float v[kBatch][kPer];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      w[b] = ninf;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) v[b][e] = 0.f;
-      if (k0 + b < n) {
-        const float* o;
-        w[b] = src(k0 + b, o);
+      for (int b = 0; b < kBatch; ++b) {
+        const float* from = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), min(j0 + b, cnt - 1)));
         if constexpr (kPer == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(o + lane * kPer);
+          const float4 x = *reinterpret_cast<const float4*>(from + lane * kPer);
           v[b][0] = x.x, v[b][1] = x.y, v[b][kPer - 2] = x.z, v[b][kPer - 1] = x.w;
         } else {
-          const float2 x = *reinterpret_cast<const float2*>(o + lane * kPer);
+          const float2 x = *reinterpret_cast<const float2*>(from + lane * kPer);
           v[b][0] = x.x, v[b][1] = x.y;
         }
       }
-    }
+      if (j0 == 0) {
+        float top = w;
+#pragma unroll 1
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        top = fmaxf(top, m);
+        // (of a NaN, `top` would not tell)
+        if (__all_sync(0xffffffffu, w == ninf)) break;
+        const float old = exp2f(m - top);
+        m = top;
+        f = exp2f(w - m);
+        float fs = f;
+#pragma unroll 1
+        for (int x = 16; x > 0; x >>= 1) fs += __shfl_xor_sync(0xffffffffu, fs, x);
+        sum = sum * old + fs;
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      top = fmaxf(top, w[b]);
-      none = none && w[b] == ninf;
-    }
-    if (none) continue;
-    const float old = exp2f(m - top);
-    m = top;
-    sum *= old;
+        for (int e = 0; e < kPer; ++e) acc[e] *= old;
+      }
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] *= old;
+      for (int b = 0; b < kBatch; ++b) {
+        const float fb = __shfl_sync(0xffffffffu, f, min(j0 + b, 31));
+        if (j0 + b < cnt && fb != 0.f) {
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const float f = exp2f(w[b] - m);
-      sum += f;
-      if (f != 0.f) {
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] += f * v[b][e];
+          for (int e = 0; e < kPer; ++e) acc[e] += fb * v[b][e];
+        }
       }
     }
   }
