@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p,
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
   // 32 parts at a time: a lane finds one and weighs it, then all lanes add up
   // the parts, kBatch of them in flight (the first before their weights).
-  constexpr int kBatch = 6;
+  constexpr int kBatch = 12;
 #pragma unroll 1
   for (int k0 = 0; k0 < n; k0 += 32) {
     const float* o = pa.out_o;
