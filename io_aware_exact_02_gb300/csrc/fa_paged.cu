@@ -48,12 +48,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
   const int rows = rec.ntok * p.G;
   int share = 1;  // warps to a row
   while (share < kMergeWarps && 2 * share * rows <= ny * kMergeWarps && 2 * share <= n) share *= 2;
-  // Row r -> token and head, and its place in a slot: Q tiles of tile_tokens
-  // tokens, 128 rows apart.
-  auto place = [&](int r, int& tok, int& head) -> int {
-    tok = r / p.G, head = r % p.G;
-    return (tok / ph.tile_tokens) * kTile + (tok % ph.tile_tokens) * p.G + head;
-  };
+  // Row r's place in a slot: two Q tiles at most, 128 rows apart.
+  const int tile_rows = ph.tile_tokens * p.G;
+  auto place = [&](int r) { return r < tile_rows ? r : kTile + r - tile_rows; };
   auto load = [&](long long slot_row, float (&v)[kPer]) {
     const float* src = ph.slot_o + slot_row * D + lane * kPer;
     if constexpr (kPer == 4) {
@@ -64,7 +61,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
       v[0] = x.x, v[1] = x.y;
     }
   };
-  auto store = [&](int tok, int head, const float (&acc)[kPer], float m, float sum) {
+  auto store = [&](int r, const float (&acc)[kPer], float m, float sum) {
+    const int tok = (int)((unsigned)r / (unsigned)p.G), head = r - tok * p.G;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const long long out = (long long)(rec.tok0 + tok) * p.Hq + rec.h * p.G + head;
     const float lse2 = sum == 0.f ? ninf : m + log2f(sum);
@@ -84,16 +82,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
     }
   };
   if (n == 2 && share == 1) {
-    // Many rows of two parts (a prompt's): four rows of a warp in flight, which
-    // takes 40 MB of parts (prompt chunks of 4,096 rows) from 16 to 12 us.
-    constexpr int kRows = 4;
+    // Many rows of two parts (a prompt's): two rows of a warp in flight.  (Four
+    // were slower, by the longer code: prompt chunks of 4,096 rows 177 us
+    // instead of 174.)
+    constexpr int kRows = 2;
     const int step = ny * kMergeWarps;
     for (int r0 = y * kMergeWarps + warp; r0 < rows; r0 += kRows * step) {
       float v[kRows][2][kPer], w[kRows][2];
-      int tok[kRows], head[kRows];
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
-        const int row = place(min(r0 + k * step, rows - 1), tok[k], head[k]);
+        const int row = place(min(r0 + k * step, rows - 1));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const long long s = (long long)(i == 0 ? rec.slot : 2 * (c0 + 1)) * ph.slot_rows + row;
@@ -111,7 +109,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
 #pragma unroll
         for (int x = 0; x < kPer; ++x)
           acc[x] = (a != 0.f ? a * v[k][0][x] : 0.f) + (b != 0.f ? b * v[k][1][x] : 0.f);
-        store(tok[k], head[k], acc, m, a + b);
+        store(r0 + k * step, acc, m, a + b);
       }
     }
     return;
@@ -120,8 +118,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
   for (int r0 = y * per_block; r0 < rows; r0 += ny * per_block) {
     const int r = r0 + warp / share;
     const bool valid = r < rows;
-    int tok, head;
-    const int row = place(valid ? r : 0, tok, head);
+    const int row = place(valid ? r : 0);
     auto slot_of = [&](int i) -> long long {
       return (long long)(i == 0 ? rec.slot : 2 * (c0 + i)) * ph.slot_rows + row;
     };
@@ -193,7 +190,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
         }
       }
     }
-    if (valid && sub == 0) store(tok, head, acc, m, sum);
+    if (valid && sub == 0) store(r, acc, m, sum);
   }
 }
 
