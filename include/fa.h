@@ -340,6 +340,17 @@ int fa_fwd_paged_prefix(const void* q, const void* k_pages, const void* v_pages,
                         size_t workspace_bytes, void* stream);
 
 /*
+ * The calls of the paged cache with their arguments as 8-byte words, in the
+ * order of the prototypes: for callers that pay by the argument, as a Python
+ * binding does (2 of the 4 us that a call takes).  Pointers and integers are
+ * 64-bit integers, scale is a double.  n: the number of words, 26 for
+ * fa_kv_append, 23 for fa_fwd_paged, 25 for fa_fwd_paged_prefix.  FA_ERR_ARG
+ * for another n, or an int that does not fit; all else as in the calls.
+ */
+int fa_kv_append_words(const void* args, int n);
+int fa_fwd_paged_words(const void* args, int n);
+
+/*
  * Size of the scratch array fa_bwd_noalloc uses: 32 MiB of static device
  * data on every GPU that loads the library, held until the process exits.
  */

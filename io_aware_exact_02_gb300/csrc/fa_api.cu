@@ -6,6 +6,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <cstring>
 #include <cstddef>
 #include <cstdint>
 #include <cstdlib>
@@ -605,6 +606,35 @@ int fwd_paged_impl(const void* q, const void* k_pages, const void* v_pages, void
   return launch_fwd_paged(p, d, static_cast<cudaStream_t>(stream));
 }
 
+// Reads a call's arguments from an array of 8-byte words, one after another
+// (which need not be aligned); ok turns false on an int that does not fit.
+struct ArgWords {
+  const char* at;
+  bool ok = true;
+  explicit ArgWords(const void* args) : at(static_cast<const char*>(args)) {}
+  long long word() {
+    long long x;
+    memcpy(&x, at, sizeof(x));
+    at += sizeof(x);
+    return x;
+  }
+  template <typename T>
+  T* ptr() {
+    return reinterpret_cast<T*>(static_cast<uintptr_t>(word()));
+  }
+  int i32() {
+    const long long x = word();
+    ok = ok && x == static_cast<int>(x);
+    return static_cast<int>(x);
+  }
+  float f32() {
+    double x;
+    memcpy(&x, at, sizeof(x));
+    at += sizeof(x);
+    return static_cast<float>(x);
+  }
+};
+
 }  // namespace
 
 }  // namespace fa
@@ -790,6 +820,47 @@ int fa_fwd_paged_prefix(const void* q, const void* k_pages, const void* v_pages,
                         int max_q, int causal, float scale, void* workspace,
                         size_t workspace_bytes, void* stream) {
   if (!prefix_pages) return FA_ERR_ARG;
+  return fwd_paged_impl(q, k_pages, v_pages, o, lse, page_table, seq_lens, cu_q, prefix_pages,
+                        prefix_len, T, B, Hq, Hkv, d, q_stride, num_pages, page_size, max_pages,
+                        max_q, causal, scale, workspace, workspace_bytes, stream);
+}
+
+int fa_kv_append_words(const void* args, int n) {
+  if (!args || n != 26) return FA_ERR_ARG;
+  ArgWords a(args);
+  const void *q = a.ptr<void>(), *k = a.ptr<void>(), *v = a.ptr<void>();
+  void *q_out = a.ptr<void>(), *k_pages = a.ptr<void>(), *v_pages = a.ptr<void>();
+  const int *page_table = a.ptr<int>(), *seq_lens = a.ptr<int>(), *cu_q = a.ptr<int>();
+  const float* rope = a.ptr<float>();
+  const int T = a.i32(), B = a.i32(), Hq = a.i32(), Hkv = a.i32(), d = a.i32();
+  const long long qs = a.word(), ks = a.word(), vs = a.word(), qos = a.word();
+  const int num_pages = a.i32(), page_size = a.i32(), max_pages = a.i32(), rope_dim = a.i32(),
+            rope_len = a.i32(), interleaved = a.i32();
+  void* stream = a.ptr<void>();
+  if (!a.ok) return FA_ERR_ARG;
+  return kv_append_impl(q, k, v, q_out, k_pages, v_pages, page_table, seq_lens, cu_q, rope, T, B,
+                        Hq, Hkv, d, qs, ks, vs, qos, num_pages, page_size, max_pages, rope_dim,
+                        rope_len, interleaved, stream);
+}
+
+int fa_fwd_paged_words(const void* args, int n) {
+  if (!args || (n != 23 && n != 25)) return FA_ERR_ARG;
+  ArgWords a(args);
+  const void *q = a.ptr<void>(), *k_pages = a.ptr<void>(), *v_pages = a.ptr<void>();
+  void* o = a.ptr<void>();
+  float* lse = a.ptr<float>();
+  const int *page_table = a.ptr<int>(), *seq_lens = a.ptr<int>(), *cu_q = a.ptr<int>();
+  const int* prefix_pages = n == 25 ? a.ptr<int>() : nullptr;
+  const int prefix_len = n == 25 ? a.i32() : 0;
+  const int T = a.i32(), B = a.i32(), Hq = a.i32(), Hkv = a.i32(), d = a.i32();
+  const long long q_stride = a.word();
+  const int num_pages = a.i32(), page_size = a.i32(), max_pages = a.i32(), max_q = a.i32(),
+            causal = a.i32();
+  const float scale = a.f32();
+  void* workspace = a.ptr<void>();
+  const size_t workspace_bytes = static_cast<size_t>(a.word());
+  void* stream = a.ptr<void>();
+  if (!a.ok || (n == 25 && !prefix_pages)) return FA_ERR_ARG;
   return fwd_paged_impl(q, k_pages, v_pages, o, lse, page_table, seq_lens, cu_q, prefix_pages,
                         prefix_len, T, B, Hq, Hkv, d, q_stride, num_pages, page_size, max_pages,
                         max_q, causal, scale, workspace, workspace_bytes, stream);

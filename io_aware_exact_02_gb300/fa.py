@@ -15,6 +15,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 import threading
 
 import torch
@@ -69,6 +70,8 @@ SIGNATURES = {
     "fa_fwd_paged_workspace_size": (_sz, [_i] * 7),
     "fa_fwd_paged": (_i, [_vp] * 8 + [_i] * 5 + [_ll] + [_i] * 5 + [_f, _vp, _sz, _vp]),
     "fa_fwd_paged_prefix": (_i, [_vp] * 9 + [_i] * 6 + [_ll] + [_i] * 5 + [_f, _vp, _sz, _vp]),
+    "fa_kv_append_words": (_i, [ctypes.c_char_p, _i]),
+    "fa_fwd_paged_words": (_i, [ctypes.c_char_p, _i]),
     "fa_device_status": (_i, [_vp, _ip]),
     "fa_selftest_timeout": (_i, [_i, _vp]),
     "fa_checks_enabled": (_i, []),
@@ -433,6 +436,10 @@ def rope_table(length: int, rope_dim: int, base: float = 10000.0, device="cuda")
 # step costs: they look at their tensors once, in one condition, and only a
 # call that fails it finds out what is wrong (_refuse_call).
 _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+# The arguments of fa_kv_append, fa_fwd_paged and fa_fwd_paged_prefix as words.
+_APPEND_WORDS = struct.Struct("=10Q5q4q6qQ").pack
+_PAGED_WORDS = struct.Struct("=8Q5qq5qdQQQ").pack
+_PREFIX_WORDS = struct.Struct("=8QQq5qq5qdQQQ").pack
 _current_device = torch.cuda.current_device
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -506,7 +513,7 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_q, q=None, q_out=
     position seq_lens[b]-1.  Returns the rotated queries (``q_out``,
     allocated if not given; it may be ``q``), or None without q."""
     Hq = qs = qos = rope_len = rope_dim = 0
-    q_ptr = q_out_ptr = rope_ptr = None
+    q_ptr = q_out_ptr = rope_ptr = 0
     try:
         dev, pool, table = k.get_device(), k_pages.shape, page_table.shape
         num_pages, Hkv, page_size, d = pool
@@ -559,11 +566,11 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_q, q=None, q_out=
         with torch.cuda.device(dev):
             return kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_q, q, q_out, rope,
                              interleaved)
-    rc = (_lib or load()).fa_kv_append(
+    rc = (_lib or load()).fa_kv_append_words(_APPEND_WORDS(
         q_ptr, k.data_ptr(), v.data_ptr(), q_out_ptr, k_pages.data_ptr(), v_pages.data_ptr(),
         page_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), rope_ptr, T, B, Hq, Hkv, d,
         qs, ks, vs, qos, num_pages, page_size, width, rope_dim, rope_len,
-        1 if interleaved else 0, _current_stream(dev))
+        1 if interleaved else 0, _current_stream(dev)), 26)
     if rc != FA_OK:
         _check("fa_kv_append", rc)
     return q_out
@@ -636,11 +643,11 @@ def _fwd_paged(fn, q, k_pages, v_pages, page_table, seq_lens, cu_q, prefix_pages
     else:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     try:
-        rc = getattr(lib, fn)(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-                              out.data_ptr(), lse.data_ptr(), page_table.data_ptr(),
-                              seq_lens.data_ptr(), cu_q.data_ptr(), *prefix, T, B, Hq, Hkv, d, qs,
-                              num_pages, page_size, width, max_q, 1 if causal else 0, scale, ws,
-                              ws_bytes, stream)
+        rc = lib.fa_fwd_paged_words((_PREFIX_WORDS if prefix else _PAGED_WORDS)(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
+            page_table.data_ptr(), seq_lens.data_ptr(), cu_q.data_ptr(), *prefix, T, B, Hq, Hkv, d,
+            qs, num_pages, page_size, width, max_q, 1 if causal else 0, scale, ws, ws_bytes,
+            stream), 25 if prefix else 23)
     finally:
         if workspace is None:
             torch._C._cuda_cudaCachingAllocator_raw_delete(ws)

@@ -1,6 +1,9 @@
 """The paged-cache entry points without a GPU: every bad argument is refused
 with its code before a device is touched, and the binding's own checks."""
 import ctypes
+import math
+import re
+import struct
 
 import pytest
 import torch
@@ -136,3 +139,41 @@ def test_rope_table_values():
     ref = torch.tensor([angle], dtype=torch.float64)
     assert abs(t[p, i].item() - ref.cos().item()) <= 2.0 ** -24
     assert abs(t[p, 16 + i].item() - ref.sin().item()) <= 2.0 ** -24
+
+
+# The same calls with their arguments as words.
+
+def words(fmt, *args):
+    return struct.pack(fmt, *args)
+
+
+APPEND_ARGS = [FAKE] * 10 + [3, 2, 4, 2, 64] + [4 * 64, 2 * 64, 2 * 64, 4 * 64] + [8, 16, 4, 64, 32, 0] + [0]
+PAGED_ARGS = [FAKE] * 8 + [3, 2, 4, 2, 64, 4 * 64, 8, 16, 4, 2, 1, 0.125, FAKE, 1 << 40, 0]
+PREFIX_ARGS = [FAKE] * 9 + [32] + PAGED_ARGS[8:]
+
+
+@pytest.mark.parametrize("name,fmt,args", [
+    ("fa_kv_append_words", "=10Q5q4q6qQ", APPEND_ARGS),
+    ("fa_fwd_paged_words", "=8Q5qq5qdQQQ", PAGED_ARGS),
+    ("fa_fwd_paged_words", "=8QQq5qq5qdQQQ", PREFIX_ARGS)])
+def test_words(lib, name, fmt, args):
+    call = getattr(lib, name)
+    n = len(args)
+    expect_device(lambda: call(words(fmt, *args), n))
+    for wrong in (0, -1, n - 1, n + 1, n + 2):
+        if name == "fa_kv_append_words" or wrong not in (23, 25):
+            assert call(words(fmt, *args) + bytes(64), wrong) == fa.FA_ERR_ARG
+    assert call(None, n) == fa.FA_ERR_ARG
+    kinds = "".join(c * int(k or 1) for k, c in re.findall(r"(\d*)([Qqd])", fmt))
+    assert len(kinds) == n
+    strides = {"fa_kv_append_words": (15, 16, 17, 18)}.get(name, (13,) if n == 23 else (15,))
+    for i, kind in enumerate(kinds):
+        if kind == "q" and i not in strides:  # an int that only fits 64 bits
+            assert call(words(fmt, *args[:i], (1 << 32) + args[i], *args[i + 1:]), n) == fa.FA_ERR_ARG
+            assert call(words(fmt, *args[:i], -1, *args[i + 1:]), n) in (
+                fa.FA_ERR_ARG, fa.FA_ERR_UNSUPPORTED_D)
+        elif kind == "Q" and i < 8:  # a pointer
+            got = call(words(fmt, *args[:i], FAKE + 1, *args[i + 1:]), n)
+            assert got == fa.FA_ERR_ALIGN, i
+        elif kind == "d":
+            assert call(words(fmt, *args[:i], math.nan, *args[i + 1:]), n) == fa.FA_ERR_ARG

@@ -635,3 +635,41 @@ def test_attention_refuses(what, how):
         assert any(n in str(e.value) for n in (what, "q has shape", "v_pages", "seq_lens")), e.value
     fa.check_device_status()
     assert torch.all(x.out == 7.0) and torch.all(x.lse == 7.0)
+
+
+def test_the_calls_and_their_words_agree():
+    """The C calls, argument by argument, against the binding, which passes
+    words."""
+    lib = fa.load()
+    x = Batch(8, 2, 128, 16, [300, 200, 177], [1, 40, 2], seed=16, prefix=160, fused=True)
+    T, B, width = x.T, x.B, x.table.shape[1]
+    rope = fa.rope_table(400, 64)
+    k = torch.randn(T, 2, 128, device="cuda").to(torch.bfloat16)
+    a, b = (x.k_pages.clone(), x.v_pages.clone()), (x.k_pages.clone(), x.v_pages.clone())
+    q_out = torch.zeros(T, 8, 128, dtype=torch.bfloat16, device="cuda")
+    want = fa.kv_append(k, k, *a, x.table, x.seq_lens, x.cu_q, q=x.q, rope=rope, interleaved=True)
+    p = lambda t: t.data_ptr()  # noqa: E731
+    stream = torch.cuda.current_stream().cuda_stream
+    tables = p(x.table), p(x.seq_lens), p(x.cu_q)
+    rc = lib.fa_kv_append(p(x.q), p(k), p(k), p(q_out), p(b[0]), p(b[1]), *tables, p(rope), T, B, 8,
+                          2, 128, x.q.stride(0), 256, 256, 1024, x.k_pages.shape[0], 16, width, 64,
+                          400, 1, stream)
+    assert rc == fa.FA_OK
+    fa.check_device_status()
+    assert torch.equal(q_out, want)
+    for i in range(2):
+        assert torch.equal(a[i].view(torch.int16), b[i].view(torch.int16))
+    for prefix in (False, True):
+        extra = (p(x.prefix_pages), 160) if prefix else ()
+        if prefix:
+            o, lse = fa.fwd_paged_prefix(*x.args(), x.prefix_pages, max_q=40, scale=0.07)
+        else:
+            o, lse = fa.fwd_paged(*x.args(), max_q=40, scale=0.07)
+        n = fa.fwd_paged_workspace_size(T, B, 8, 2, 128, 40, 160 if prefix else 0)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        fn = lib.fa_fwd_paged_prefix if prefix else lib.fa_fwd_paged
+        rc = fn(p(x.q), p(x.k_pages), p(x.v_pages), p(x.out), p(x.lse), *tables, *extra, T, B, 8, 2,
+                128, x.q.stride(0), x.k_pages.shape[0], 16, width, 40, 1, 0.07, p(ws), n, stream)
+        assert rc == fa.FA_OK
+        fa.check_device_status()
+        assert torch.equal(o, x.out) and torch.equal(lse, x.lse)
