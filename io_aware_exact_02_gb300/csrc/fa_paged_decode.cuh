@@ -24,6 +24,12 @@
 // Warps: 0-3 and 4-7 compute (and write results), 8 and 10 load K and V (TMA: a
 // lane per page box), 9 issues the products, each as soon as its operands are
 // there, 11 clears what lies past a unit's keys.
+//
+// Bound by memory, and by latency where there is little to read.  With 32
+// query and 8 key/value heads, d = 128, one row a sequence, the merge included:
+// 64 sequences of up to 4K keys in pages of 16 take 101 us (6.1 TB/s of the 6.8
+// that a copy reaches), 8 of up to 32K 160 us (6.7 TB/s), one of 1,000 keys
+// 10.8 us (5 until its first products, 0.7 a tile, 2.6 for the merge).
 // K and V stream through one ring of 32 KB (d = 128) tiles in the order K0 V0
 // K1 V1 ..., across units; four S buffers let S run ahead of P V, into the
 // next units.

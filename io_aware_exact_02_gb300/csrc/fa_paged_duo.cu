@@ -14,6 +14,10 @@
 // both kinds, whose loops together do not fit what they share of the
 // instruction cache, take 4 us instead of 1.5 for a step of the prompt kernel
 // (a call behind a shared prefix of 16K keys 67 us instead of 58).
+//
+// With 32 query and 8 key/value heads, d = 128, the merge or join included: two
+// chunks of 500 rows among 30 single ones, up to 2,500 keys each, 60 us; 64
+// sequences of up to 500 own keys behind 16K shared ones 52 us.
 #include "fa_paged_decode.cuh"
 #include "fa_paged_launch.h"
 #include "fa_paged_prompt.cuh"
