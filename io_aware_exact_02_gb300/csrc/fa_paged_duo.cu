@@ -8,7 +8,7 @@
 // Every CTA works out the same split of the CTAs, in proportion to the time the
 // two lists take: a step of the prompt kernel (two Q tiles, a key tile) 1.6 us
 // and the end of a unit 6 us, a tile of the decode kernel 1.0 us on half of the
-// SMs (76 CTAs read 5.1 of the 5.4 TB/s that 152 read) and a unit's end 1 us.
+// SMs (76 CTAs read 5.1 of the 5.4 TB/s that 152 read) and a unit's end 1.5 us.
 //
 // Clusters of two CTAs have one kind of work: two neighbouring SMs that run
 // both kinds, whose loops together do not fit what they share of the
@@ -17,7 +17,7 @@
 //
 // With 32 query and 8 key/value heads, d = 128, the merge or join included: two
 // chunks of 500 rows among 30 single ones, up to 2,500 keys each, 60 us; 64
-// sequences of up to 500 own keys behind 16K shared ones 52 us.
+// sequences of up to 500 own keys behind 16K shared ones 50 us.
 #include "fa_paged_decode.cuh"
 #include "fa_paged_launch.h"
 #include "fa_paged_prompt.cuh"
@@ -25,7 +25,7 @@
 namespace fa {
 namespace {
 
-constexpr PagedWeight kPromptWeight = {16, 60}, kDecodeWeight = {10, 10};  // 0.1 us
+constexpr PagedWeight kPromptWeight = {16, 60}, kDecodeWeight = {10, 15};  // 0.1 us
 
 template <int D, int R, bool kNeg>
 __global__ void __launch_bounds__(kPagedThreads, 1)
