@@ -205,9 +205,28 @@ __device__ __forceinline__ long long paged_head_cost(const PagedParams& p, const
 
 // a / b of nonnegative numbers; nearly always both fit 32 bits, whose division
 // is several times shorter.
-static __device__ __noinline__ long long paged_div(long long a, long long b) {
+static __host__ __device__ __noinline__ long long paged_div(long long a, long long b) {
   if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
   return a / b;
+}
+
+// Two lists side by side: the CTAs, of `ctas` (even, at least 4), that take the
+// list of weight wa, the others taking that of weight wb; in proportion to the
+// weights, and both multiples of two (whole clusters).  A list with work always
+// has a cluster, however little of the whole its work is: a list without CTAs
+// would leave its rows unwritten.  groups (at most ctas - 2): the units of the
+// first list that are dealt whole (PagedShare), whose CTAs are a multiple of
+// them before they are made even.
+__host__ __device__ __forceinline__ int paged_duo_split(long long wa, long long wb, int ctas,
+                                                        int groups) {
+  if (wa <= 0) return 0;
+  if (wb <= 0) return ctas;
+  int na = (int)paged_div(wa * ctas + (wa + wb) / 2, wa + wb);
+  na = (na + groups / 2) / groups * groups;
+  if (na < groups) na = groups;
+  if (na > ctas - 2) na -= groups;
+  na = (na + 1) & ~1;
+  return na < ctas - 2 ? na : ctas - 2;
 }
 
 // CTA c's range of the list is [lo(c), lo(c + 1)): equal ranges, the first

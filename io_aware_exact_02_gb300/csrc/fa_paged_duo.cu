@@ -41,16 +41,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1)
   long long wa, wb;
   paged_weights(p, pa, kPromptWeight, pb, kDecodeWeight, wa, wb);
   const int ctas = gridDim.x;
-  int na = 0;
-  if (wa > 0) {
-    na = (int)paged_div(wa * ctas + (wa + wb) / 2, wa + wb);
-    // A multiple of the units of a shared prefix, where there are CTAs enough,
-    // and then of two: whole clusters.
-    const int groups = paged_groups(p, pa, ctas - 2);
-    na = max(groups, (na + groups / 2) / groups * groups);
-    if (na > ctas - 2) na -= groups;
-    na = wb > 0 ? (na + 1) & ~1 : ctas;
-  }
+  const int na = paged_duo_split(wa, wb, ctas, paged_groups(p, pa, ctas - 2));
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *pa.ctas = na;
     *pb.ctas = ctas - na;
