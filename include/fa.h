@@ -64,9 +64,9 @@ extern "C" {
                                       than its per-warpgroup register split
                                       needs (nothing is launched then) */
 #define FA_ERR_TIMEOUT (-7)        /* a kernel's pipeline wait timed out (reported by fa_device_status) */
-#define FA_ERR_BOUNDS (-8)         /* bounds-checked build only: a kernel computed a tile, mask
-                                      or row index outside its array and stopped before using it
-                                      (reported by fa_device_status) */
+#define FA_ERR_BOUNDS (-8)         /* a kernel computed a tile, mask or row index outside its array
+                                      and stopped before using it (reported by fa_device_status);
+                                      but for site 1303, in the bounds-checked build only */
 #define FA_ERR_PAGE (-9)           /* a paged cache's device-side tables hold a row range, length,
                                       position or page number outside its bounds (reported by
                                       fa_device_status) */
@@ -383,7 +383,9 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  * Synchronises `stream`, then returns and clears the status word of the
  * current device: FA_OK, FA_ERR_TIMEOUT if a kernel gave up on a pipeline
  * wait since the last call, FA_ERR_BOUNDS if a kernel of the bounds-checked
- * build caught an out-of-range index, FA_ERR_PAGE if a paged-cache kernel met
+ * build caught an out-of-range index (or any build's kernel that joins a shared
+ * prefix with the sequences' own keys met a row that the attention before it
+ * left out, site 1303), FA_ERR_PAGE if a paged-cache kernel met
  * a table entry outside its bounds, or FA_ERR_LAUNCH if the stream holds a
  * CUDA error.  The first error recorded wins.  If `site` is not NULL it
  * receives the identifier of the wait or check that raised it (0 if none):
@@ -391,8 +393,8 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  * kernel, 301-304 the paged cache's tables (row ranges, lengths, positions,
  * page numbers), 311-399 a wait of a paged attention kernel, 1101-1199 a bounds
  * check of the forward kernels, 1201-1299 one of the backward kernels,
- * 1301-1399 one of the paged attention kernels, FA_SITE_SELFTEST and FA_SITE_SELFTEST_BOUNDS the self
- * tests'.
+ * 1301-1399 one of the paged attention kernels, FA_SITE_SELFTEST and
+ * FA_SITE_SELFTEST_BOUNDS the self tests'.
  */
 int fa_device_status(void* stream, int* site);
 

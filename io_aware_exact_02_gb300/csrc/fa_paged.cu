@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p,
   const int h = hq / p.G, gh = hq - h * p.G;
   const int tok0 = t / pa.unit_tokens * pa.unit_tokens, tile = (t - tok0) / pa.tile_tokens;
   wait_prior_grid();
-  const int first = p.cu_q[0], end = p.cu_q[p.B];
+  const int first = p.cu_q[0], end = p.cu_q[p.B], ctas_a = *pa.ctas, ctas_b = *pb.ctas;
   const uint2 ua = pa.parts[(long long)tok0 * p.Hkv + h], ub = pb.parts[(long long)t * p.Hkv + h];
   if (t < first || t >= end) return;  // a padding row
   struct Parts {
@@ -226,9 +226,15 @@ __global__ void __launch_bounds__(256) fa_paged_join_kernel(const PagedParams p,
   const Parts A = {(int)(ua.x & 0xffff), (int)(ua.x >> 16),
                    tile * kTile + (t - tok0 - tile * pa.tile_tokens) * p.G + gh};
   const Parts B = {(int)(ub.x & 0xffff), (int)(ub.x >> 16), (int)ub.y + gh};
-  // (Of a sequence whose tables are out of bounds nothing was written.)
-  if (B.n < 1 || B.slot + 2 * B.n > 2 * kPagedMaxCtas || (unsigned)B.row >= (unsigned)pb.slot_rows)
+  // A word that cannot be was not written: the row gets no result but an error
+  // (already recorded where bad tables or a failed wait are the reason).  Words
+  // left by an earlier call in the same workspace may pass; they point into it.
+  if (!paged_parts_ok(A.slot, A.n, A.row, ctas_a, pa.slot_rows) ||
+      !paged_parts_ok(B.slot, B.n, B.row, ctas_b, pb.slot_rows)) {
+    int abort_flag = 0;
+    if (lane == 0) report_status(p.status, &abort_flag, FA_ERR_BOUNDS, kChkPgParts);
     return;
+  }
   auto src = [&](int k, const float*& o) -> float {
     const bool own = k >= A.n;
     const PagedPhase& ph = own ? pb : pa;

@@ -28,7 +28,8 @@ enum : int {
 // Bounds checks of the checked build.
 enum : int {
   kChkPgItem = 1301,  // a unit's rows or head
-  kChkPgRow           // an output row
+  kChkPgRow,          // an output row
+  kChkPgParts         // (in every build) where a row's parts lie, as the join kernel read it
 };
 
 struct PagedRow {
@@ -135,6 +136,14 @@ static_assert(sizeof(PagedRec) <= kPagedRecBytes, "record size");
 // token has one.
 __device__ __forceinline__ uint2 paged_parts(int slot, int n, int row) {
   return make_uint2((uint32_t)slot | (uint32_t)n << 16, (uint32_t)row);
+}
+// Whether n slots from `slot` on, and a row of each, can be what one of `ctas`
+// CTAs left: a unit without a word (of a sequence whose tables are out of
+// bounds, or of a CTA that gave up on a wait) leaves whatever the workspace
+// held, and that is not to be followed out of it.
+__host__ __device__ __forceinline__ bool paged_parts_ok(int slot, int n, int row, int ctas,
+                                                        int slot_rows) {
+  return n >= 1 && slot >= 0 && slot / 2 + n <= ctas && row >= 0 && row < slot_rows;
 }
 
 struct PagedSeq {

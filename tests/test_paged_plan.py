@@ -1,5 +1,6 @@
 """The paged cache's plan of a call, its host-callable functions compiled into
-a program that runs on the CPU: how two lists of work share the CTAs."""
+a program that runs on the CPU: how two lists of work share the CTAs, and which words about a
+unit's parts are followed."""
 import os
 import subprocess
 
@@ -43,7 +44,28 @@ static int split() {
   return 0;
 }
 
-int main() { return split(); }
+// A word is taken for one exactly when it has slots and they lie in the
+// workspace of the CTAs: all values of its 16-bit halves, as garbage may hold.
+static int parts() {
+  const int all[] = {0, 2, 76, 150, 152, kPagedMaxCtas};
+  for (int ctas : all)
+    for (int slot = 0; slot < 65536; slot += slot < 700 ? 1 : 97)
+      for (int n = 0; n < 65536; n += n < 700 ? 1 : 97) {
+        // Where the join reads: the first slot, then the next CTAs' slots 0.
+        long long last = n > 1 ? (slot & ~1) + 2ll * (n - 1) : slot;
+        if (last < slot) last = slot;
+        const bool inside = n >= 1 && slot < 2 * ctas && last < 2 * ctas;
+        if (paged_parts_ok(slot, n, 0, ctas, 8) != inside) return bad("parts", slot, n, ctas, 8, !inside);
+      }
+  const int rows[] = {-2147483647 - 1, -1, 0, 7, 8, 255, 256, 2147483647};
+  for (int row : rows)
+    for (int slot_rows : {8, 16, 256})
+      if (paged_parts_ok(3, 2, row, 152, slot_rows) != (row >= 0 && row < slot_rows))
+        return bad("row", 3, 2, row, slot_rows, 0);
+  return 0;
+}
+
+int main(int argc, char** argv) { return argv[1][0] == 's' ? split() : parts(); }
 """
 
 
@@ -58,6 +80,7 @@ def program(tmp_path_factory):
     return out
 
 
-def test_a_list_with_work_has_ctas(program):
-    r = subprocess.run([program], capture_output=True, text=True, timeout=120)
+@pytest.mark.parametrize("what", ["split", "parts"])
+def test_plan(program, what):
+    r = subprocess.run([program, what], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout

@@ -1,0 +1,64 @@
+"""The paged cache's device-side tables on the GPU: entries out of bounds are
+recorded, and the other sequences' results stay right."""
+import math
+
+import pytest
+import torch
+
+from io_aware_exact_02_gb300 import build, fa
+from paged_common import Batch, compare, reference
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return fa.load()
+
+
+def sound(x, o, lse, but):
+    """The results of all sequences but some."""
+    for b in range(x.B):
+        rows = slice(x.cu[b], x.cu[b + 1])
+        if b in but or x.nq[b] == 0:
+            continue
+        ref = reference(x.q_host[rows], x.keys[b], x.vals[b], True, 1 / math.sqrt(x.d))
+        compare(o[rows].cpu(), lse[rows].cpu(), ref, b)
+
+
+# Tokens of the sequences: all single, all of four (behind a prefix: both lists
+# side by side), chunks, and chunks among single ones.
+ROWS = [[1] * 20, [4] * 20, [70] * 20, [90, 150] + [1] * 18]
+
+
+@pytest.mark.parametrize("prefix", [0, 320])
+@pytest.mark.parametrize("nq", ROWS)
+@pytest.mark.parametrize("bad", [1 << 20, 2147483647, -1, -(1 << 31)])
+def test_a_bad_length_spoils_its_own_sequence_only(nq, prefix, bad):
+    x = Batch(8, 2, 128, 16, [500 + 7 * i for i in range(20)], nq, seed=1, prefix=prefix)
+    lens = x.seq_lens.clone()
+    lens[5] = bad
+    args = x.q, x.k_pages, x.v_pages, x.table, lens, x.cu_q
+    args += (x.prefix_pages,) if prefix else ()
+    o, lse = (fa.fwd_paged_prefix if prefix else fa.fwd_paged)(*args, max_q=max(nq))
+    assert fa.device_status() == (fa.FA_ERR_PAGE, 302)
+    sound(x, o, lse, (5,))
+
+
+@pytest.mark.parametrize("fill", [0, 1, 255])
+def test_rows_of_no_sequence_behind_a_prefix(fill):
+    """Row ranges that leave rows to no sequence, in the form of the call that
+    joins a prefix with the sequences' own keys, over a workspace that holds
+    anything: an error, and nothing is written to those rows."""
+    B, n = 20, 4
+    x = Batch(8, 2, 128, 16, [330 + 7 * i for i in range(B)], [n] * B, seed=fill, pad=2, prefix=320)
+    cu = x.cu_q.clone()
+    cu[7] = 500  # sequences 6 and 7 are none: rows 24 to 31
+    ws = torch.full((fa.fwd_paged_workspace_size(x.T, B, 8, 2, 128, n, 320),), fill,
+                    dtype=torch.uint8, device="cuda")
+    o, lse = fa.fwd_paged_prefix(x.q, x.k_pages, x.v_pages, x.table, x.seq_lens, cu, x.prefix_pages,
+                                 max_q=n, out=x.out, lse=x.lse, workspace=ws)
+    assert fa.device_status() == (fa.FA_ERR_PAGE, 301)
+    for rows in (slice(24, 32), slice(80, 82)):
+        assert torch.all(o[rows] == 7.0) and torch.all(lse[rows] == 7.0)
