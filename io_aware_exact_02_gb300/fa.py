@@ -673,6 +673,8 @@ def fwd_paged_prefix(q, k_pages, v_pages, page_table, seq_lens, cu_q, prefix_pag
     """fwd_paged for a batch whose sequences all begin with the keys of
     ``prefix_pages`` (int32, in order), whose attention is computed once for
     all rows.  Lengths and positions count the prefix.  Returns (o, lse)."""
+    if prefix_pages is None:  # (fwd_paged is the call without a prefix)
+        raise ValueError("prefix_pages must be a CUDA tensor of shape (pages,)")
     return _fwd_paged("fa_fwd_paged_prefix", q, k_pages, v_pages, page_table, seq_lens, cu_q,
                       prefix_pages, max_q, causal, scale, out, lse, workspace)
 

@@ -62,3 +62,13 @@ def test_rows_of_no_sequence_behind_a_prefix(fill):
     assert fa.device_status() == (fa.FA_ERR_PAGE, 301)
     for rows in (slice(24, 32), slice(80, 82)):
         assert torch.all(o[rows] == 7.0) and torch.all(lse[rows] == 7.0)
+
+
+def test_a_prefix_call_without_a_prefix_is_refused():
+    x = Batch(8, 2, 128, 16, [60, 70], [2, 1], seed=15)
+    with pytest.raises(ValueError, match="prefix_pages"):
+        fa.fwd_paged_prefix(*x.args(), None, out=x.out, lse=x.lse)
+    with pytest.raises(RuntimeError, match="fa_fwd_paged_prefix"):  # an empty one
+        fa.fwd_paged_prefix(*x.args(), x.prefix_pages, out=x.out, lse=x.lse)
+    assert torch.all(x.out == 7.0) and torch.all(x.lse == 7.0)
+    fa.check_device_status()
