@@ -261,7 +261,9 @@ int fa_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* lse,
  * not ascending in [0, T], a length above max_pages * page_size, a position
  * outside the cache or the rotation table, a page number outside
  * [0, num_pages)) records FA_ERR_PAGE in the status word; nothing is read or
- * written through it, and the results of that sequence are unspecified.
+ * written through it, and the results of that sequence are unspecified (those
+ * of all sequences where the row ranges are not ascending in [0, T]: the ranges
+ * say whose a row is).
  * Table entries past a sequence's last page are not read.
  */
 

@@ -37,6 +37,11 @@ struct PagedRow {
   int pos;  // its position in the sequence
 };
 
+// Whether rows t0 .. t1 - 1 can be a sequence's.
+__device__ __forceinline__ bool paged_range_ok(int t0, int t1, int T) {
+  return t0 >= 0 && t1 >= t0 && t1 <= T;
+}
+
 // The sequence of row t: the largest b with cu_q[b] <= t, found by a
 // warp-wide search over 32 probes a step (all lanes of the warp call it with
 // the same t).  Rows at and past cu_q[B] belong to none.
@@ -62,7 +67,7 @@ __device__ __forceinline__ PagedRow paged_row(const int* cu_q, const int* seq_le
   r.pos = 0;
   if (before || lo >= B) return r;
   const int t0 = cu_q[lo], t1 = cu_q[lo + 1];
-  if (t0 > t || t1 <= t || t1 > T) {
+  if (t0 > t || t1 <= t || !paged_range_ok(t0, t1, T)) {
     int abort_flag = 0;
     if (lane == 0) report_status(status, &abort_flag, FA_ERR_PAGE, kSitePagedRows);
     return r;
@@ -163,7 +168,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, const PagedP
   s.n = t1 - t0;
   s.len = p.seq_lens[b];
   int abort_flag = 0;
-  if (t0 < 0 || t1 < t0 || t1 > p.T) {
+  if (!paged_range_ok(t0, t1, p.T)) {
     report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedRows);
     s.t0 = s.n = 0;
   }

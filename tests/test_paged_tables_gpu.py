@@ -72,3 +72,49 @@ def test_a_prefix_call_without_a_prefix_is_refused():
         fa.fwd_paged_prefix(*x.args(), x.prefix_pages, out=x.out, lse=x.lse)
     assert torch.all(x.out == 7.0) and torch.all(x.lse == 7.0)
     fa.check_device_status()
+
+
+def append(T, cu, lens, d=64):
+    """Appends T rows of ones; returns the status and how many (row, key/value
+    head) pairs were written."""
+    B = len(lens)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    kp = torch.zeros(4 * B, 2, 16, d, dtype=torch.bfloat16, device="cuda")
+    vp = kp.clone()
+    table = torch.arange(4 * B, dtype=torch.int32, device="cuda").reshape(B, 4).contiguous()
+    k = torch.ones(T, 2, d, dtype=torch.bfloat16, device="cuda")
+    fa.kv_append(k, k, kp, vp, table, i32(lens), i32(cu))
+    status = fa.device_status()
+    assert torch.equal(kp, vp)
+    return status, int(kp[..., 0].sum().item())
+
+
+@pytest.mark.parametrize("T,cu", [
+    (8, (0, 5, 3, 8)),               # descending between two sound ranges
+    (3, (-5, 1, 2, 3)),              # beginning before the rows
+    (3, (-1, 0, 2, 3)),
+    (3, (0, 1, 3, 900)),             # ending past them, in a sequence of no row
+    (3, (0, 1, 3, 2)),
+    (3, (0, 0, 2147483647, 3)),
+    (3, (0, 0, -(1 << 31), 3)),
+    (1, (0, 1) + (1,) * 399 + (2,)),  # the last of more sequences than a CTA has threads
+    (2, (0,) * 700 + (3, 2)),
+])
+def test_append_reports_every_bad_row_range(T, cu):
+    status, _ = append(T, cu, (20,) * (len(cu) - 1))
+    assert status == (fa.FA_ERR_PAGE, 301)
+
+
+def test_append_writes_no_row_of_a_bad_range():
+    # rows 0 of [-5, 1) and 2 of [2, 900) are not written, row 1 of [1, 2) is
+    status, written = append(3, (-5, 1, 2, 900), (20, 20, 20))
+    assert status == (fa.FA_ERR_PAGE, 301) and written == 2
+
+
+@pytest.mark.parametrize("T,cu", [
+    (3, (0, 1, 2, 3)), (3, (1, 1, 2, 2)), (3, (3, 3, 3, 3)), (3, (0, 0, 0, 3)), (1, (0,) * 700 + (1,)),
+    (300, tuple(range(301))),
+])
+def test_append_reports_no_sound_row_range(T, cu):
+    status, written = append(T, cu, (20,) * (len(cu) - 1))
+    assert status == (fa.FA_OK, 0) and written == 2 * (cu[-1] - cu[0])
