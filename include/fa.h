@@ -253,7 +253,8 @@ int fa_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* lse,
  * writes.  seq_lens: [B] int32, each sequence's keys with its new tokens
  * included; row t of sequence b is position
  *     pos(t) = seq_lens[b] - (cu_q[b+1] - t).
- * Both calls take the same tables: append, then attend.
+ * Both calls take the same tables: append, then attend.  T and B are at least 1;
+ * a step without new tokens needs no call.
  *
  * The tables are device memory, read by the kernels only, so a call can be
  * captured into a graph and replayed with other lengths and pages.  Their

@@ -236,8 +236,8 @@ int launch_kv_append(const KvAppendParams& p, int d, cudaStream_t stream);
 // CTAs that share a call's work at most (one per SM; GB300 has 152), which
 // sizes the workspace without a device.
 constexpr int kPagedMaxCtas = 160;
-// Most query rows of a unit in the decode kernel and rows of a unit in the
-// prompt kernel (two 128-row Q tiles).
+// Most query rows of a unit in the decode kernel; a unit of the prompt kernel has
+// kPairRows (two 128-row Q tiles).
 constexpr int kPagedDecodeRows = 64;
 
 struct PagedParams {

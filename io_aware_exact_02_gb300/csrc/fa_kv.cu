@@ -13,8 +13,10 @@
 //
 // Bound by memory: q, k and v are read once and written once; the table rows
 // (4 * rope_dim bytes) are shared by all heads of a row.  16,384 rows of 32
-// query and 8 key/value heads, d = 128: 61 us, 6.7 TB/s of the 6.8 that a copy
-// reaches; one row: 2.5 us, a launch and three loads that wait for one another.
+// query and 8 key/value heads, d = 128: 61 us, 6.7 TB/s of the 6.8 that a
+// copy reaches; one row: 2.6 us, a launch and four rounds of loads of which each
+// waits for the one before: the row ranges; the row's own and its length; the
+// page number; the rotation table and the inputs.
 #include <cuda_bf16.h>
 
 #include "fa_internal.h"
@@ -60,8 +62,8 @@ __device__ __forceinline__ void load8(const float* src, float* dst) {
 // One CTA per row.  A thread owns the same two 8-channel chunks of every
 // kRows-th head: the chunks p and p + rope_dim/16 that hold a pair's two
 // halves (or two neighbouring chunks), so that it reads its part of the table
-// once.  The inputs do not depend on the row's sequence and are loaded before
-// it is looked up.
+// once.  The inputs are loaded last, when the row's place is known: a row of no
+// sequence reads none.
 constexpr int kAppendThreads = 128;
 
 template <int D>

@@ -118,7 +118,7 @@ struct PagedPhase {
   int n_min, n_max;    // sequences of that many new tokens take part
   char* rec;           // PagedRec per CTA
   int* ctas;           // how many CTAs share the phase's list, where not all do; or null
-  uint2* parts;        // [T][Hkv], written: PagedParts of the units; or null
+  uint2* parts;        // [T][Hkv], written: paged_parts of the units; or null
   float* slot_o;       // [CTA][2][slot_rows][d]
   float* slot_lse;     // [CTA][2][slot_rows], log2 units
   const float* pre_o;  // results to merge in ([T][Hq][d], [T][Hq], log2 units), or null

@@ -9,6 +9,10 @@
 // two lists take: a step of the prompt kernel (two Q tiles, a key tile) 1.6 us
 // and the end of a unit 6 us, a tile of the decode kernel 1.0 us on half of the
 // SMs (76 CTAs read 5.1 of the 5.4 TB/s that 152 read) and a unit's end 1.5 us.
+// These were measured at d = 128 with units of 8 rows, a unit's end behind shared
+// prefixes of 2K and 16K keys, and serve d = 64 and units of 16 rows too, where
+// they have not been measured apart: they decide how well the two kinds end
+// together, never the result, and a list with work has CTAs whatever they say.
 //
 // Clusters of two CTAs have one kind of work: two neighbouring SMs that run
 // both kinds, whose loops together do not fit what they share of the

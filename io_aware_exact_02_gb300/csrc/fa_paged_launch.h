@@ -43,7 +43,7 @@ int launch_paged_prompt(const PagedMaps& t, const PagedParams& p, const PagedPha
                         const cudaLaunchConfig_t& base);
 
 // Both kernels side by side (fa_paged_duo.cu): phase pa's units of 256 rows
-// (Q map t.q) and phase pb's of 8 to 64 (tq_b).
+// (Q map t.q) and phase pb's of 8 or 16 (tq_b).
 int launch_paged_duo(const PagedMaps& t, const CUtensorMap& tq_b, const PagedParams& p,
                      const PagedPhase& pa, const PagedPhase& pb, int d,
                      const cudaLaunchConfig_t& base);

@@ -511,7 +511,9 @@ def kv_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_q, q=None, q_out=
     (and q, if given) by the table ``rope`` (see rope_table; None: no
     rotation).  Sequence b's rows are cu_q[b] .. cu_q[b+1]-1 and end at
     position seq_lens[b]-1.  Returns the rotated queries (``q_out``,
-    allocated if not given; it may be ``q``), or None without q."""
+    allocated if not given; it may be ``q``), or None without q.  Rows of no
+    sequence are left as they are; a ``q_out`` of the call's own is filled with
+    zeros first, which for one token costs more than the call."""
     Hq = qs = qos = rope_len = rope_dim = 0
     q_ptr = q_out_ptr = rope_ptr = 0
     try:
@@ -662,7 +664,9 @@ def fwd_paged(q, k_pages, v_pages, page_table, seq_lens, cu_q, max_q=None, causa
     rows of sequence b are its last cu_q[b+1] - cu_q[b] positions of
     seq_lens[b].  ``max_q``: the most rows of a sequence (None: T), which
     decides the kernel and never the result.  Returns (o, lse), (T, Hq, d)
-    and (T, Hq)."""
+    and (T, Hq).  Rows of no sequence are left as they are; outputs that are not
+    given are filled with 0 and -inf first, which for one token costs more than
+    the call."""
     return _fwd_paged("fa_fwd_paged", q, k_pages, v_pages, page_table, seq_lens, cu_q, None,
                       max_q, causal, scale, out, lse, workspace)
 
