@@ -70,6 +70,17 @@ def test_mixed_batches_of_very_uneven_work(case, causal):
     check(x, o, lse, causal)
 
 
+@pytest.mark.parametrize("max_q", [1, 16, 64, 126, 1000, 2147483647, None])
+@pytest.mark.parametrize("lens,nq", [([9000, 100, 100, 90], [126, 1, 1, 1]),
+                                     ([32768, 100], [126, 1]),
+                                     ([130] + [4000] * 20, [126] + [1] * 20)])
+def test_max_q_is_only_a_hint_for_uneven_work(lens, nq, max_q):
+    x = Batch(4, 1, 128, 32, lens, nq, seed=len(lens))
+    o, lse = fa.fwd_paged(*x.args(), max_q=max_q, out=x.out, lse=x.lse)
+    fa.check_device_status()
+    check(x, o, lse)
+
+
 @pytest.mark.parametrize("Hq,Hkv,d,page,prefix,lens", [
     (8, 2, 128, 16, 16384, [16385 + i % 3 for i in range(20)]),  # all of the work is the prefix's
     (8, 2, 128, 16, 16, [5000 + 31 * i for i in range(20)]),     # nearly none of it is
