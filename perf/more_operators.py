@@ -351,7 +351,6 @@ def _prepare_pool(case, g):
     else:
         shape = (caches, pages, case["Hkv"], el // case["Hkv"])
         s["cache"] = torch.randint(0, 256, shape, generator=g, device="cuda", dtype=torch.uint8)
-    s["pools"] = list(s["cache"].unbind(0))
     return s
 
 
@@ -382,10 +381,10 @@ def run(s):
             return {"o": o, "lse": lse}
         if op == "fork":
             fa.pages_fork(s["parents"], s["children"], s["page_table"], s["seq_lens"], s["refs"],
-                          s["pools"], case["page"])
+                          s["cache"], case["page"])
             fa.pages_free(s["children"], s["page_table"], s["seq_lens"], s["refs"], case["page"])
         else:
-            fa.pages_compact(s["page_table"], s["seq_lens"], s["refs"], s["pools"], case["page"])
+            fa.pages_compact(s["page_table"], s["seq_lens"], s["refs"], s["cache"], case["page"])
         return {"page_table": s["page_table"], "seq_lens": s["seq_lens"], "refs": s["refs"],
                 "cache": s["cache"]}
     return {"append4": _append, "attn4": _attend, "fork": _fork, "compact": _compact}[op](s)
