@@ -343,15 +343,78 @@ int fa_fwd_paged_prefix(const void* q, const void* k_pages, const void* v_pages,
                         size_t workspace_bytes, void* stream);
 
 /*
+ * The paged cache in 4 bits (no counterpart on the pages): keys and values of
+ * a layer in one pool of 4.5 bits a number, for contexts whose reading is what
+ * a step costs.  Tables, rows and positions are those of the calls above.
+ *
+ * Numbers.  A group of 16 channels of a key or value row is held as 16 E2M1
+ * codes (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives) and one E4M3 scale s:
+ *     y = x * (1 / tensor scale),  s = E4M3(max |y| / 6),  code = E2M1(y / s),
+ *     value = code * s * tensor scale,
+ * each step in fp32, conversions rounded to nearest-even and saturated (a group
+ * with a NaN becomes NaN, infinities 6 * 448 tensor scales; s = 0 holds zeros).
+ * k_scale and v_scale, the tensors' own scales (positive, finite, their
+ * inverses too; 1 where magnitudes lie between 0.1 and 2,000), are the caller's
+ * to keep: all calls on a cache take the same.
+ *
+ * Layout.  pages: [num_pages][Hkv][page_size * 9 d / 8] bytes, 16-byte aligned:
+ * page_size / 16 blocks of 16 keys, of 18 d bytes each:
+ *     K codes  [16 keys][d / 2]     a byte holds channels 2i (low 4 bits), 2i + 1
+ *     V codes  [2][8][4][d / 8]     half of 8 keys, eighth of the channels, pair of
+ *                                   keys, channel: a byte holds keys 2i (low), 2i + 1
+ *     K scales [16 keys][d / 16]
+ *     V scales [d / 16][16 keys]
+ *
+ * fa_kv4_append is fa_kv_append into it: keys are quantised after their
+ * rotation, from fp32.  A byte of V holds a pair of keys: appending to an odd
+ * slot reads the byte and writes the even slot's half back as it was, so no
+ * other call may write that slot meanwhile.
+ *
+ * fa_kv4_read reads rows back: row t of sequence b is position
+ * seq_lens[b] - (cu_q[b+1] - t), as in the append, and k_out, v_out
+ * ([T][Hkv][d] bf16, row strides as in the append) receive the values the
+ * cache stands for, rounded to bf16 once (exact where the tensors' scales are
+ * powers of two).  Rows of no sequence are not written.
+ *
+ * fa_fwd_paged4 is fa_fwd_paged over it, of those values unrounded.  A query
+ * row is scaled by a power of two to fit fp16, in which the products run:
+ * channels below 2^-38 of the row's largest lose bits.  Numbers in slots past a
+ * sequence's length are never used; value rows that the causal mask hides have
+ * to be finite, as in the other forward calls.
+ * Errors of all three: as the call each is a form of, and FA_ERR_ARG for a
+ * tensor scale that is not as above.
+ */
+int fa_kv4_append(const void* q, const void* k, const void* v, void* q_out, void* pages,
+                  const int* page_table, const int* seq_lens, const int* cu_q, const float* rope,
+                  int T, int B, int Hq, int Hkv, int d, long long q_stride, long long k_stride,
+                  long long v_stride, long long q_out_stride, int num_pages, int page_size,
+                  int max_pages, int rope_dim, int rope_len, int interleaved, float k_scale,
+                  float v_scale, void* stream);
+int fa_kv4_read(void* k_out, void* v_out, const void* pages, const int* page_table,
+                const int* seq_lens, const int* cu_q, int T, int B, int Hkv, int d,
+                long long k_out_stride, long long v_out_stride, int num_pages, int page_size,
+                int max_pages, float k_scale, float v_scale, void* stream);
+size_t fa_fwd_paged4_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_q);
+int fa_fwd_paged4(const void* q, const void* pages, void* o, float* lse, const int* page_table,
+                  const int* seq_lens, const int* cu_q, int T, int B, int Hq, int Hkv, int d,
+                  long long q_stride, int num_pages, int page_size, int max_pages, int max_q,
+                  int causal, float scale, float k_scale, float v_scale, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/*
  * The calls of the paged cache with their arguments as 8-byte words, in the
  * order of the prototypes: for callers that pay by the argument, as a Python
  * binding does (2 of the 4 us that a call takes).  Pointers and integers are
- * 64-bit integers, scale is a double.  n: the number of words, 26 for
- * fa_kv_append, 23 for fa_fwd_paged, 25 for fa_fwd_paged_prefix.  FA_ERR_ARG
+ * 64-bit integers, scales are doubles.  n: the number of words, 26 for
+ * fa_kv_append, 23 for fa_fwd_paged, 25 for fa_fwd_paged_prefix, 27 for
+ * fa_kv4_append, 18 for fa_kv4_read, 24 for fa_fwd_paged4.  FA_ERR_ARG
  * for another n, or an int that does not fit; all else as in the calls.
  */
 int fa_kv_append_words(const void* args, int n);
 int fa_fwd_paged_words(const void* args, int n);
+int fa_kv4_append_words(const void* args, int n);
+int fa_kv4_read_words(const void* args, int n);
+int fa_fwd_paged4_words(const void* args, int n);
 
 /*
  * Size of the scratch array fa_bwd_noalloc uses: 32 MiB of static device

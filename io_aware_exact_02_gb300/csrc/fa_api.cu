@@ -496,17 +496,17 @@ bool row_stride_ok(long long stride, int heads, int d) {
   return stride >= (long long)heads * d && stride % 8 == 0 && stride < (1LL << 38);
 }
 
-int kv_append_impl(const void* q, const void* k, const void* v, void* q_out, void* k_pages,
-                   void* v_pages, const int* page_table, const int* seq_lens, const int* cu_q,
-                   const float* rope, int T, int B, int Hq, int Hkv, int d, long long q_stride,
-                   long long k_stride, long long v_stride, long long q_out_stride, int num_pages,
-                   int page_size, int max_pages, int rope_dim, int rope_len, int interleaved,
-                   void* stream) {
-  if (!k || !v || !k_pages || !v_pages || !page_table || !seq_lens || !cu_q) return FA_ERR_ARG;
+// The checks and fields that the appends to both kinds of cache share.
+int kv_append_fields(const void* q, const void* k, const void* v, void* q_out, const int* page_table,
+                     const int* seq_lens, const int* cu_q, const float* rope, int T, int B, int Hq,
+                     int Hkv, int d, long long q_stride, long long k_stride, long long v_stride,
+                     long long q_out_stride, int num_pages, int page_size, int max_pages,
+                     int rope_dim, int rope_len, int interleaved, KvAppendParams& p) {
+  if (!k || !v || !page_table || !seq_lens || !cu_q) return FA_ERR_ARG;
   if ((q == nullptr) != (q_out == nullptr)) return FA_ERR_ARG;
   if (interleaved != 0 && interleaved != 1) return FA_ERR_ARG;
-  KvAppendParams p;
-  int rc = paged_shape(T, B, q ? Hq : 1, Hkv, d, num_pages, page_size, max_pages, &p.page_shift);
+  const int rc =
+      paged_shape(T, B, q ? Hq : 1, Hkv, d, num_pages, page_size, max_pages, &p.page_shift);
   if (rc != FA_OK) return rc;
   if (rope_dim < 0 || rope_dim > d || rope_dim % 16 != 0) return FA_ERR_ARG;
   if ((rope_dim > 0) != (rope != nullptr) || (rope_dim > 0 && rope_len < 1)) return FA_ERR_ARG;
@@ -514,23 +514,17 @@ int kv_append_impl(const void* q, const void* k, const void* v, void* q_out, voi
   if (q && (!row_stride_ok(q_stride, Hq, d) || !row_stride_ok(q_out_stride, Hq, d)))
     return FA_ERR_ARG;
   if (q == q_out && q && q_stride != q_out_stride) return FA_ERR_ARG;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
-      !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(rope) || !aligned4(page_table) ||
-      !aligned4(seq_lens) || !aligned4(cu_q))
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(rope) ||
+      !aligned4(page_table) || !aligned4(seq_lens) || !aligned4(cu_q))
     return FA_ERR_ALIGN;
-  DeviceState* ds;
-  if ((rc = device_state(&ds)) != FA_OK) return rc;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k = static_cast<const __nv_bfloat16*>(k);
   p.v = static_cast<const __nv_bfloat16*>(v);
   p.q_out = static_cast<__nv_bfloat16*>(q_out);
-  p.k_pages = static_cast<__nv_bfloat16*>(k_pages);
-  p.v_pages = static_cast<__nv_bfloat16*>(v_pages);
   p.page_table = page_table;
   p.seq_lens = seq_lens;
   p.cu_q = cu_q;
   p.rope = rope;
-  p.status = ds->status;
   p.T = T;
   p.B = B;
   p.Hq = Hq;
@@ -545,49 +539,118 @@ int kv_append_impl(const void* q, const void* k, const void* v, void* q_out, voi
   p.rope_dim = rope_dim;
   p.rope_len = rope_len;
   p.interleaved = interleaved;
+  return FA_OK;
+}
+
+int kv_append_impl(const void* q, const void* k, const void* v, void* q_out, void* k_pages,
+                   void* v_pages, const int* page_table, const int* seq_lens, const int* cu_q,
+                   const float* rope, int T, int B, int Hq, int Hkv, int d, long long q_stride,
+                   long long k_stride, long long v_stride, long long q_out_stride, int num_pages,
+                   int page_size, int max_pages, int rope_dim, int rope_len, int interleaved,
+                   void* stream) {
+  if (!k_pages || !v_pages) return FA_ERR_ARG;
+  KvAppendParams p;
+  int rc = kv_append_fields(q, k, v, q_out, page_table, seq_lens, cu_q, rope, T, B, Hq, Hkv, d,
+                            q_stride, k_stride, v_stride, q_out_stride, num_pages, page_size,
+                            max_pages, rope_dim, rope_len, interleaved, p);
+  if (rc != FA_OK) return rc;
+  if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_ALIGN;
+  DeviceState* ds;
+  if ((rc = device_state(&ds)) != FA_OK) return rc;
+  p.k_pages = static_cast<__nv_bfloat16*>(k_pages);
+  p.v_pages = static_cast<__nv_bfloat16*>(v_pages);
+  p.status = ds->status;
   return launch_kv_append(p, d, static_cast<cudaStream_t>(stream));
 }
 
-// Attention over the paged cache; prefix_pages null and prefix_len 0 without
-// a shared prefix.
-int fwd_paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
-                   const int* page_table, const int* seq_lens, const int* cu_q,
-                   const int* prefix_pages, int prefix_len, int T, int B, int Hq, int Hkv, int d,
-                   long long q_stride, int num_pages, int page_size, int max_pages, int max_q,
-                   int causal, float scale, void* workspace, size_t workspace_bytes,
-                   void* stream) {
-  if (!q || !k_pages || !v_pages || !o || !lse || !page_table || !seq_lens || !cu_q)
+// A tensor's own scale in the 4-bit cache, whose inverse has to be finite too.
+bool tensor_scale_ok(float s) { return s > 0.f && std::isfinite(s) && std::isfinite(1.f / s); }
+
+int kv4_append_impl(const void* q, const void* k, const void* v, void* q_out, void* pages,
+                    const int* page_table, const int* seq_lens, const int* cu_q, const float* rope,
+                    int T, int B, int Hq, int Hkv, int d, long long q_stride, long long k_stride,
+                    long long v_stride, long long q_out_stride, int num_pages, int page_size,
+                    int max_pages, int rope_dim, int rope_len, int interleaved, float k_scale,
+                    float v_scale, void* stream) {
+  if (!pages || !tensor_scale_ok(k_scale) || !tensor_scale_ok(v_scale)) return FA_ERR_ARG;
+  Kv4AppendParams p;
+  int rc = kv_append_fields(q, k, v, q_out, page_table, seq_lens, cu_q, rope, T, B, Hq, Hkv, d,
+                            q_stride, k_stride, v_stride, q_out_stride, num_pages, page_size,
+                            max_pages, rope_dim, rope_len, interleaved, p);
+  if (rc != FA_OK) return rc;
+  if (!aligned16(pages)) return FA_ERR_ALIGN;
+  DeviceState* ds;
+  if ((rc = device_state(&ds)) != FA_OK) return rc;
+  p.k_pages = p.v_pages = nullptr;
+  p.pages = static_cast<uint8_t*>(pages);
+  p.k_inv = 1.f / k_scale;
+  p.v_inv = 1.f / v_scale;
+  p.status = ds->status;
+  return launch_kv4_append(p, d, static_cast<cudaStream_t>(stream));
+}
+
+int kv4_read_impl(void* k_out, void* v_out, const void* pages, const int* page_table,
+                  const int* seq_lens, const int* cu_q, int T, int B, int Hkv, int d,
+                  long long k_out_stride, long long v_out_stride, int num_pages, int page_size,
+                  int max_pages, float k_scale, float v_scale, void* stream) {
+  if (!k_out || !v_out || !pages || !page_table || !seq_lens || !cu_q) return FA_ERR_ARG;
+  if (!tensor_scale_ok(k_scale) || !tensor_scale_ok(v_scale)) return FA_ERR_ARG;
+  Kv4ReadParams p;
+  int rc = paged_shape(T, B, 1, Hkv, d, num_pages, page_size, max_pages, &p.page_shift);
+  if (rc != FA_OK) return rc;
+  if (!row_stride_ok(k_out_stride, Hkv, d) || !row_stride_ok(v_out_stride, Hkv, d))
     return FA_ERR_ARG;
+  if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(pages) || !aligned4(page_table) ||
+      !aligned4(seq_lens) || !aligned4(cu_q))
+    return FA_ERR_ALIGN;
+  DeviceState* ds;
+  if ((rc = device_state(&ds)) != FA_OK) return rc;
+  p.pages = static_cast<const uint8_t*>(pages);
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.v_out = static_cast<__nv_bfloat16*>(v_out);
+  p.page_table = page_table;
+  p.seq_lens = seq_lens;
+  p.cu_q = cu_q;
+  p.status = ds->status;
+  p.T = T;
+  p.B = B;
+  p.Hkv = Hkv;
+  p.k_out_stride = k_out_stride;
+  p.v_out_stride = v_out_stride;
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  return launch_kv4_read(p, d, static_cast<cudaStream_t>(stream));
+}
+
+// The checks and fields that the attentions over both kinds of cache share;
+// prefix_pages null and prefix_len 0 without a shared prefix.
+int fwd_paged_fields(const void* q, void* o, float* lse, const int* page_table, const int* seq_lens,
+                     const int* cu_q, const int* prefix_pages, int prefix_len, int T, int B, int Hq,
+                     int Hkv, int d, long long q_stride, int num_pages, int page_size,
+                     int max_pages, int max_q, int causal, float scale, PagedParams& p) {
+  if (!q || !o || !lse || !page_table || !seq_lens || !cu_q) return FA_ERR_ARG;
   if (causal != 0 && causal != 1) return FA_ERR_ARG;
   if (!std::isfinite(scale) || max_q < 1) return FA_ERR_ARG;
-  PagedParams p;
-  int rc = paged_shape(T, B, Hq, Hkv, d, num_pages, page_size, max_pages, &p.page_shift);
+  const int rc = paged_shape(T, B, Hq, Hkv, d, num_pages, page_size, max_pages, &p.page_shift);
   if (rc != FA_OK) return rc;
   if (Hq % Hkv != 0 || Hq / Hkv > 128) return FA_ERR_ARG;
   if (!row_stride_ok(q_stride, Hq, d)) return FA_ERR_ARG;
   if (prefix_pages &&
       (prefix_len < page_size || prefix_len % page_size != 0 || prefix_len / page_size > max_pages))
     return FA_ERR_ARG;
-  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) ||
-      !aligned16(lse) || !aligned4(page_table) || !aligned4(seq_lens) || !aligned4(cu_q) ||
-      !aligned4(prefix_pages))
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned4(page_table) ||
+      !aligned4(seq_lens) || !aligned4(cu_q) || !aligned4(prefix_pages))
     return FA_ERR_ALIGN;
-  const size_t need = fa_fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len);
-  if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-                   workspace_bytes < need))
-    return FA_ERR_WORKSPACE;
-  DeviceState* ds;
-  if ((rc = device_state(&ds)) != FA_OK) return rc;
   p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
-  p.v_pages = static_cast<const __nv_bfloat16*>(v_pages);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.page_table = page_table;
   p.seq_lens = seq_lens;
   p.cu_q = cu_q;
   p.prefix_pages = prefix_pages;
-  p.status = ds->status;
   p.T = T;
   p.B = B;
   p.Hq = Hq;
@@ -601,9 +664,65 @@ int fwd_paged_impl(const void* q, const void* k_pages, const void* v_pages, void
   p.max_q = max_q;
   p.causal = causal;
   p.scale_log2 = scale * 1.4426950408889634f;
+  return FA_OK;
+}
+
+bool workspace_ok(const void* workspace, size_t bytes, size_t need) {
+  return need == 0 || (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0 &&
+                       bytes >= need);
+}
+
+int fwd_paged_impl(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+                   const int* page_table, const int* seq_lens, const int* cu_q,
+                   const int* prefix_pages, int prefix_len, int T, int B, int Hq, int Hkv, int d,
+                   long long q_stride, int num_pages, int page_size, int max_pages, int max_q,
+                   int causal, float scale, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  if (!k_pages || !v_pages) return FA_ERR_ARG;
+  PagedParams p;
+  int rc = fwd_paged_fields(q, o, lse, page_table, seq_lens, cu_q, prefix_pages, prefix_len, T, B,
+                            Hq, Hkv, d, q_stride, num_pages, page_size, max_pages, max_q, causal,
+                            scale, p);
+  if (rc != FA_OK) return rc;
+  if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_ALIGN;
+  if (!workspace_ok(workspace, workspace_bytes,
+                    fa_fwd_paged_workspace_size(T, B, Hq, Hkv, d, max_q, prefix_len)))
+    return FA_ERR_WORKSPACE;
+  DeviceState* ds;
+  if ((rc = device_state(&ds)) != FA_OK) return rc;
+  p.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
+  p.v_pages = static_cast<const __nv_bfloat16*>(v_pages);
+  p.status = ds->status;
   p.ctas = ds->sm_count < kPagedMaxCtas ? ds->sm_count : kPagedMaxCtas;
   p.workspace = static_cast<char*>(workspace);
   return launch_fwd_paged(p, d, static_cast<cudaStream_t>(stream));
+}
+
+int fwd_paged4_impl(const void* q, const void* pages, void* o, float* lse, const int* page_table,
+                    const int* seq_lens, const int* cu_q, int T, int B, int Hq, int Hkv, int d,
+                    long long q_stride, int num_pages, int page_size, int max_pages, int max_q,
+                    int causal, float scale, float k_scale, float v_scale, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (!pages || !tensor_scale_ok(k_scale) || !tensor_scale_ok(v_scale)) return FA_ERR_ARG;
+  Paged4Params p;
+  int rc = fwd_paged_fields(q, o, lse, page_table, seq_lens, cu_q, nullptr, 0, T, B, Hq, Hkv, d,
+                            q_stride, num_pages, page_size, max_pages, max_q, causal, scale, p);
+  if (rc != FA_OK) return rc;
+  if (!aligned16(pages)) return FA_ERR_ALIGN;
+  if (!std::isfinite(p.scale_log2 * k_scale)) return FA_ERR_ARG;
+  if (!workspace_ok(workspace, workspace_bytes,
+                    fa_fwd_paged4_workspace_size(T, B, Hq, Hkv, d, max_q)))
+    return FA_ERR_WORKSPACE;
+  DeviceState* ds;
+  if ((rc = device_state(&ds)) != FA_OK) return rc;
+  p.k_pages = p.v_pages = nullptr;
+  p.pages = static_cast<const uint8_t*>(pages);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.status = ds->status;
+  p.ctas = ds->sm_count < kPagedMaxCtas ? ds->sm_count : kPagedMaxCtas;
+  p.workspace = static_cast<char*>(workspace);
+  return launch_fwd_paged4(p, d, static_cast<cudaStream_t>(stream));
 }
 
 // Reads a call's arguments from an array of 8-byte words, one after another
@@ -823,6 +942,98 @@ int fa_fwd_paged_prefix(const void* q, const void* k_pages, const void* v_pages,
   return fwd_paged_impl(q, k_pages, v_pages, o, lse, page_table, seq_lens, cu_q, prefix_pages,
                         prefix_len, T, B, Hq, Hkv, d, q_stride, num_pages, page_size, max_pages,
                         max_q, causal, scale, workspace, workspace_bytes, stream);
+}
+
+int fa_kv4_append(const void* q, const void* k, const void* v, void* q_out, void* pages,
+                  const int* page_table, const int* seq_lens, const int* cu_q, const float* rope,
+                  int T, int B, int Hq, int Hkv, int d, long long q_stride, long long k_stride,
+                  long long v_stride, long long q_out_stride, int num_pages, int page_size,
+                  int max_pages, int rope_dim, int rope_len, int interleaved, float k_scale,
+                  float v_scale, void* stream) {
+  return kv4_append_impl(q, k, v, q_out, pages, page_table, seq_lens, cu_q, rope, T, B, Hq, Hkv, d,
+                         q_stride, k_stride, v_stride, q_out_stride, num_pages, page_size,
+                         max_pages, rope_dim, rope_len, interleaved, k_scale, v_scale, stream);
+}
+
+int fa_kv4_read(void* k_out, void* v_out, const void* pages, const int* page_table,
+                const int* seq_lens, const int* cu_q, int T, int B, int Hkv, int d,
+                long long k_out_stride, long long v_out_stride, int num_pages, int page_size,
+                int max_pages, float k_scale, float v_scale, void* stream) {
+  return kv4_read_impl(k_out, v_out, pages, page_table, seq_lens, cu_q, T, B, Hkv, d, k_out_stride,
+                       v_out_stride, num_pages, page_size, max_pages, k_scale, v_scale, stream);
+}
+
+size_t fa_fwd_paged4_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_q) {
+  int shift;
+  if (paged_shape(T, B, Hq, Hkv, d, 1, 16, 1, &shift) != FA_OK) return 0;
+  if (Hq % Hkv != 0 || Hq / Hkv > 128 || max_q < 1) return 0;
+  return 0;
+}
+
+int fa_fwd_paged4(const void* q, const void* pages, void* o, float* lse, const int* page_table,
+                  const int* seq_lens, const int* cu_q, int T, int B, int Hq, int Hkv, int d,
+                  long long q_stride, int num_pages, int page_size, int max_pages, int max_q,
+                  int causal, float scale, float k_scale, float v_scale, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  return fwd_paged4_impl(q, pages, o, lse, page_table, seq_lens, cu_q, T, B, Hq, Hkv, d, q_stride,
+                         num_pages, page_size, max_pages, max_q, causal, scale, k_scale, v_scale,
+                         workspace, workspace_bytes, stream);
+}
+
+int fa_kv4_append_words(const void* args, int n) {
+  if (!args || n != 27) return FA_ERR_ARG;
+  ArgWords a(args);
+  const void *q = a.ptr<void>(), *k = a.ptr<void>(), *v = a.ptr<void>();
+  void *q_out = a.ptr<void>(), *pages = a.ptr<void>();
+  const int *page_table = a.ptr<int>(), *seq_lens = a.ptr<int>(), *cu_q = a.ptr<int>();
+  const float* rope = a.ptr<float>();
+  const int T = a.i32(), B = a.i32(), Hq = a.i32(), Hkv = a.i32(), d = a.i32();
+  const long long qs = a.word(), ks = a.word(), vs = a.word(), qos = a.word();
+  const int num_pages = a.i32(), page_size = a.i32(), max_pages = a.i32(), rope_dim = a.i32(),
+            rope_len = a.i32(), interleaved = a.i32();
+  const float k_scale = a.f32(), v_scale = a.f32();
+  void* stream = a.ptr<void>();
+  if (!a.ok) return FA_ERR_ARG;
+  return kv4_append_impl(q, k, v, q_out, pages, page_table, seq_lens, cu_q, rope, T, B, Hq, Hkv, d,
+                         qs, ks, vs, qos, num_pages, page_size, max_pages, rope_dim, rope_len,
+                         interleaved, k_scale, v_scale, stream);
+}
+
+int fa_kv4_read_words(const void* args, int n) {
+  if (!args || n != 18) return FA_ERR_ARG;
+  ArgWords a(args);
+  void *k_out = a.ptr<void>(), *v_out = a.ptr<void>();
+  const void* pages = a.ptr<void>();
+  const int *page_table = a.ptr<int>(), *seq_lens = a.ptr<int>(), *cu_q = a.ptr<int>();
+  const int T = a.i32(), B = a.i32(), Hkv = a.i32(), d = a.i32();
+  const long long ks = a.word(), vs = a.word();
+  const int num_pages = a.i32(), page_size = a.i32(), max_pages = a.i32();
+  const float k_scale = a.f32(), v_scale = a.f32();
+  void* stream = a.ptr<void>();
+  if (!a.ok) return FA_ERR_ARG;
+  return kv4_read_impl(k_out, v_out, pages, page_table, seq_lens, cu_q, T, B, Hkv, d, ks, vs,
+                       num_pages, page_size, max_pages, k_scale, v_scale, stream);
+}
+
+int fa_fwd_paged4_words(const void* args, int n) {
+  if (!args || n != 24) return FA_ERR_ARG;
+  ArgWords a(args);
+  const void *q = a.ptr<void>(), *pages = a.ptr<void>();
+  void* o = a.ptr<void>();
+  float* lse = a.ptr<float>();
+  const int *page_table = a.ptr<int>(), *seq_lens = a.ptr<int>(), *cu_q = a.ptr<int>();
+  const int T = a.i32(), B = a.i32(), Hq = a.i32(), Hkv = a.i32(), d = a.i32();
+  const long long q_stride = a.word();
+  const int num_pages = a.i32(), page_size = a.i32(), max_pages = a.i32(), max_q = a.i32(),
+            causal = a.i32();
+  const float scale = a.f32(), k_scale = a.f32(), v_scale = a.f32();
+  void* workspace = a.ptr<void>();
+  const size_t workspace_bytes = (size_t)a.word();
+  void* stream = a.ptr<void>();
+  if (!a.ok) return FA_ERR_ARG;
+  return fwd_paged4_impl(q, pages, o, lse, page_table, seq_lens, cu_q, T, B, Hq, Hkv, d, q_stride,
+                         num_pages, page_size, max_pages, max_q, causal, scale, k_scale, v_scale,
+                         workspace, workspace_bytes, stream);
 }
 
 int fa_kv_append_words(const void* args, int n) {

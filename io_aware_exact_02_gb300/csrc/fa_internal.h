@@ -233,6 +233,30 @@ struct KvAppendParams {
 };
 int launch_kv_append(const KvAppendParams& p, int d, cudaStream_t stream);
 
+// The cache in 4 bits (fa_kv4_append, fa_kv4_read, fa_fwd_paged4): one pool
+// [num_pages][Hkv][page_size / 16] of blocks (fa_kv4.cuh).  The append's
+// k_pages and v_pages are not used.
+struct Kv4AppendParams : KvAppendParams {
+  uint8_t* pages;
+  float k_inv, v_inv;  // 1 / the tensors' scales
+};
+int launch_kv4_append(const Kv4AppendParams& p, int d, cudaStream_t stream);
+
+struct Kv4ReadParams {
+  const uint8_t* pages;
+  __nv_bfloat16* k_out;
+  __nv_bfloat16* v_out;
+  const int* page_table;
+  const int* seq_lens;
+  const int* cu_q;
+  int* status;
+  int T, B, Hkv;
+  long long k_out_stride, v_out_stride;
+  int num_pages, page_size, page_shift, max_pages;
+  float k_scale, v_scale;
+};
+int launch_kv4_read(const Kv4ReadParams& p, int d, cudaStream_t stream);
+
 // CTAs that share a call's work at most (one per SM; GB300 has 152), which
 // sizes the workspace without a device.
 constexpr int kPagedMaxCtas = 160;
@@ -344,6 +368,13 @@ inline PagedWorkspace paged_workspace_layout(int T, int Hq, int Hkv, int d, cons
 }
 
 int launch_fwd_paged(const PagedParams& p, int d, cudaStream_t stream);
+
+// The same over the cache in 4 bits; k_pages and v_pages are not used.
+struct Paged4Params : PagedParams {
+  const uint8_t* pages;
+  float k_scale, v_scale;  // the tensors' scales
+};
+int launch_fwd_paged4(const Paged4Params& p, int d, cudaStream_t stream);
 
 // A rank-3 tensor map over packed rows [T][heads][d] bf16 with `stride`
 // elements between rows: dims (d, heads, T), box (64, box_heads, box_rows),

@@ -70,6 +70,13 @@ SIGNATURES = {
     "fa_fwd_paged_workspace_size": (_sz, [_i] * 7),
     "fa_fwd_paged": (_i, [_vp] * 8 + [_i] * 5 + [_ll] + [_i] * 5 + [_f, _vp, _sz, _vp]),
     "fa_fwd_paged_prefix": (_i, [_vp] * 9 + [_i] * 6 + [_ll] + [_i] * 5 + [_f, _vp, _sz, _vp]),
+    "fa_kv4_append": (_i, [_vp] * 9 + [_i] * 5 + [_ll] * 4 + [_i] * 6 + [_f] * 2 + [_vp]),
+    "fa_kv4_read": (_i, [_vp] * 6 + [_i] * 4 + [_ll] * 2 + [_i] * 3 + [_f] * 2 + [_vp]),
+    "fa_fwd_paged4_workspace_size": (_sz, [_i] * 6),
+    "fa_fwd_paged4": (_i, [_vp] * 7 + [_i] * 5 + [_ll] + [_i] * 5 + [_f] * 3 + [_vp, _sz, _vp]),
+    "fa_kv4_append_words": (_i, [ctypes.c_char_p, _i]),
+    "fa_kv4_read_words": (_i, [ctypes.c_char_p, _i]),
+    "fa_fwd_paged4_words": (_i, [ctypes.c_char_p, _i]),
     "fa_kv_append_words": (_i, [ctypes.c_char_p, _i]),
     "fa_fwd_paged_words": (_i, [ctypes.c_char_p, _i]),
     "fa_device_status": (_i, [_vp, _ip]),
@@ -435,11 +442,14 @@ def rope_table(length: int, rope_dim: int, base: float = 10000.0, device="cuda")
 # The paged-cache calls serve single tokens, where the call itself is what a
 # step costs: they look at their tensors once, in one condition, and only a
 # call that fails it finds out what is wrong (_refuse_call).
-_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
 # The arguments of fa_kv_append, fa_fwd_paged and fa_fwd_paged_prefix as words.
 _APPEND_WORDS = struct.Struct("=10Q5q4q6qQ").pack
 _PAGED_WORDS = struct.Struct("=8Q5qq5qdQQQ").pack
 _PREFIX_WORDS = struct.Struct("=8QQq5qq5qdQQQ").pack
+_APPEND4_WORDS = struct.Struct("=9Q5q4q6q2dQ").pack
+_READ4_WORDS = struct.Struct("=6Q4q2q3q2dQ").pack
+_PAGED4_WORDS = struct.Struct("=7Q5qq5q3dQQQ").pack
 _current_device = torch.cuda.current_device
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -681,6 +691,218 @@ def fwd_paged_prefix(q, k_pages, v_pages, page_table, seq_lens, cu_q, prefix_pag
         raise ValueError("prefix_pages must be a CUDA tensor of shape (pages,)")
     return _fwd_paged("fa_fwd_paged_prefix", q, k_pages, v_pages, page_table, seq_lens, cu_q,
                       prefix_pages, max_q, causal, scale, out, lse, workspace)
+
+
+def kv4_pages(num_pages: int, Hkv: int, page_size: int, d: int, device="cuda"):
+    """An empty pool of a cache in 4 bits: uint8 (num_pages, Hkv, page_size * 9 d / 8),
+    keys and values of a layer together (the layout is fa.h's)."""
+    return torch.zeros((num_pages, Hkv, page_size * 9 * d // 8), dtype=_U8, device=device)
+
+
+def _refuse_call4(rows, pages, page_table, seq_lens, cu_q, others):
+    """Raises what is wrong with a call of the 4-bit cache.  rows: its packed
+    rows (name, tensor, heads; None: any number), the first of them given."""
+    lead = rows[0][1]
+    if not isinstance(lead, torch.Tensor) or not lead.is_cuda or lead.dim() != 3:
+        raise ValueError("%s must be a CUDA tensor of shape (T, heads, d)" % rows[0][0])
+    dev, T, d = lead.get_device(), lead.shape[0], lead.shape[2]
+    if not isinstance(pages, torch.Tensor) or pages.dim() != 3 or d == 0:
+        raise ValueError("pages must have shape (num_pages, Hkv, page_size * 9 d / 8)")
+    if pages.shape[2] % (18 * d):
+        raise ValueError("pages holds %d bytes a page and head, expected page_size * 9 * %d / 8"
+                         % (pages.shape[2], d))
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must have shape (B, max_pages)")
+    B, width = page_table.shape
+    for n, t, s, dt in (("pages", pages, tuple(pages.shape), _U8),
+                        ("page_table", page_table, (B, width), _I32),
+                        ("seq_lens", seq_lens, (B,), _I32), ("cu_q", cu_q, (B + 1,), _I32)):
+        _check_one(n, t, s, dt, dev)
+    for n, t, h in rows:
+        if t is not None:
+            if not isinstance(t, torch.Tensor) or t.dim() != 3:
+                raise ValueError("%s must have shape (T, heads, d)" % n)
+            _check_rows(n, t, T, t.shape[1] if h is None else h, d, dev)
+    for n, t, s, dt in others:
+        if t is not None:
+            if not isinstance(t, torch.Tensor) or t.dim() != len(s):
+                raise ValueError("%s must have shape (%s)" % (n, ", ".join(map(str, s))))
+            _check_one(n, t, tuple(t.shape[i] if isinstance(x, str) else x
+                                   for i, x in enumerate(s)), dt, dev)
+    raise ValueError("arguments of other types, shapes or devices than the call takes")
+
+
+def _tables_ok(dev, B, pages, page_table, seq_lens, cu_q):
+    return (seq_lens.shape == (B,) and cu_q.shape == (B + 1,)
+            and pages.dtype is _U8 and page_table.dtype is _I32 and seq_lens.dtype is _I32
+            and cu_q.dtype is _I32
+            and pages.get_device() == dev and page_table.get_device() == dev
+            and seq_lens.get_device() == dev and cu_q.get_device() == dev
+            and pages.is_contiguous() and page_table.is_contiguous()
+            and seq_lens.is_contiguous() and cu_q.is_contiguous())
+
+
+def kv4_append(k, v, pages, page_table, seq_lens, cu_q, q=None, q_out=None, rope=None,
+               interleaved: bool = False, k_scale: float = 1.0, v_scale: float = 1.0):
+    """kv_append into a cache held in 4 bits (``pages``, see kv4_pages): keys
+    are quantised after their rotation.  k_scale, v_scale: the tensors' own
+    scales, the same in every call on a cache.  Returns the rotated queries
+    (``q_out``, allocated and zeroed if not given), or None without q."""
+    Hq = qs = qos = rope_len = rope_dim = 0
+    q_ptr = q_out_ptr = rope_ptr = 0
+    try:
+        dev, (T, Hkv, d) = k.get_device(), k.shape
+        num_pages, heads, size = pages.shape
+        B, width = page_table.shape
+        rows = (T, Hkv, d)
+        ks, head, one = k.stride()
+        vs, vhead, vone = v.stride()
+        ok = (dev >= 0 and v.shape == rows and heads == Hkv and d > 0 and size % (18 * d) == 0
+              and k.dtype is _BF16 and v.dtype is _BF16 and v.get_device() == dev
+              and one == 1 and vone == 1 and (Hkv == 1 or head == vhead == d)
+              and _tables_ok(dev, B, pages, page_table, seq_lens, cu_q))
+        if ok and q is not None:
+            Hq = q.shape[1]
+            if q_out is None:  # rows of no sequence are not written
+                q_out = torch.zeros((T, Hq, d), dtype=_BF16, device=q.device)
+            rows = (T, Hq, d)
+            qs, head, one = q.stride()
+            qos, ohead, oone = q_out.stride()
+            ok = (q.shape == rows and q_out.shape == rows and q.dtype is _BF16
+                  and q_out.dtype is _BF16 and q.get_device() == dev and q_out.get_device() == dev
+                  and one == 1 and oone == 1 and (Hq == 1 or head == ohead == d))
+            q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
+        if ok and rope is not None:
+            rope_len, rope_dim = rope.shape
+            ok = rope.dtype is _F32 and rope.get_device() == dev and rope.is_contiguous()
+            rope_ptr = rope.data_ptr()
+    except (AttributeError, TypeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        h = pages.shape[1] if getattr(pages, "ndim", 0) == 3 else None
+        _refuse_call4((("k", k, h), ("v", v, h), ("q", q, None),
+                                     ("q_out", q_out, q.shape[1] if getattr(q, "ndim", 0) == 3
+                                      else None)),
+                      pages, page_table, seq_lens, cu_q,
+                      (("rope", rope, ("length", "rope_dim"), _F32),))
+    if q is None and q_out is not None:
+        raise ValueError("q_out needs q")
+    if T == 1:  # a single row has any stride
+        ks = vs = Hkv * d
+        qs = qos = Hq * d
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return kv4_append(k, v, pages, page_table, seq_lens, cu_q, q, q_out, rope, interleaved,
+                              k_scale, v_scale)
+    rc = (_lib or load()).fa_kv4_append_words(_APPEND4_WORDS(
+        q_ptr, k.data_ptr(), v.data_ptr(), q_out_ptr, pages.data_ptr(), page_table.data_ptr(),
+        seq_lens.data_ptr(), cu_q.data_ptr(), rope_ptr, T, B, Hq, Hkv, d, qs, ks, vs, qos,
+        num_pages, size // (9 * d) * 8, width, rope_dim, rope_len, 1 if interleaved else 0,
+        k_scale, v_scale, _current_stream(dev)), 27)
+    if rc != FA_OK:
+        _check("fa_kv4_append", rc)
+    return q_out
+
+
+def kv4_read(pages, page_table, seq_lens, cu_q, k_out, v_out, k_scale: float = 1.0,
+             v_scale: float = 1.0):
+    """Read rows of a cache held in 4 bits back into k_out and v_out (T, Hkv, d)
+    bf16: row t of sequence b is the position that kv4_append with the same
+    tables writes.  Rows of no sequence are left as they are.  Returns
+    (k_out, v_out)."""
+    try:
+        dev, (T, Hkv, d) = k_out.get_device(), k_out.shape
+        num_pages, heads, size = pages.shape
+        B, width = page_table.shape
+        ks, head, one = k_out.stride()
+        vs, vhead, vone = v_out.stride()
+        ok = (dev >= 0 and v_out.shape == (T, Hkv, d) and heads == Hkv and d > 0
+              and size % (18 * d) == 0 and k_out.dtype is _BF16 and v_out.dtype is _BF16
+              and v_out.get_device() == dev and one == 1 and vone == 1
+              and (Hkv == 1 or head == vhead == d)
+              and _tables_ok(dev, B, pages, page_table, seq_lens, cu_q))
+    except (AttributeError, TypeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        h = pages.shape[1] if getattr(pages, "ndim", 0) == 3 else None
+        _refuse_call4((("k_out", k_out, h), ("v_out", v_out, h)), pages, page_table,
+                      seq_lens, cu_q, ())
+    if T == 1:  # a single row has any stride
+        ks = vs = Hkv * d
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return kv4_read(pages, page_table, seq_lens, cu_q, k_out, v_out, k_scale, v_scale)
+    rc = (_lib or load()).fa_kv4_read_words(_READ4_WORDS(
+        k_out.data_ptr(), v_out.data_ptr(), pages.data_ptr(), page_table.data_ptr(),
+        seq_lens.data_ptr(), cu_q.data_ptr(), T, B, Hkv, d, ks, vs, num_pages,
+        size // (9 * d) * 8, width, k_scale, v_scale, _current_stream(dev)), 18)
+    if rc != FA_OK:
+        _check("fa_kv4_read", rc)
+    return k_out, v_out
+
+
+@functools.lru_cache(maxsize=256)
+def fwd_paged4_workspace_size(T, B, Hq, Hkv, d, max_q) -> int:
+    """Bytes of workspace for these sizes (0 where they are invalid)."""
+    return int(load().fa_fwd_paged4_workspace_size(T, B, Hq, Hkv, d, max_q))
+
+
+def fwd_paged4(q, pages, page_table, seq_lens, cu_q, max_q=None, causal: bool = True,
+               scale: float | None = None, k_scale: float = 1.0, v_scale: float = 1.0, out=None,
+               lse=None, workspace=None):
+    """fwd_paged over a cache held in 4 bits (``pages``, see kv4_pages), with the
+    tensors' scales of the appends.  Returns (o, lse)."""
+    try:
+        dev, (T, Hq, d) = q.get_device(), q.shape
+        num_pages, Hkv, size = pages.shape
+        B, width = page_table.shape
+        qs, head, one = q.stride()
+        ok = (dev >= 0 and d > 0 and size % (18 * d) == 0 and q.dtype is _BF16 and one == 1
+              and (Hq == 1 or head == d) and _tables_ok(dev, B, pages, page_table, seq_lens, cu_q))
+        if ok and out is None:  # rows of no sequence are not written
+            out = torch.zeros((T, Hq, d), dtype=_BF16, device=q.device)
+        if ok and lse is None:
+            lse = torch.full((T, Hq), -math.inf, dtype=_F32, device=q.device)
+        ok = (ok and out.shape == (T, Hq, d) and out.dtype is _BF16 and out.get_device() == dev
+              and out.is_contiguous() and lse.shape == (T, Hq) and lse.dtype is _F32
+              and lse.get_device() == dev and lse.is_contiguous())
+    except (AttributeError, TypeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        shape = q.shape if getattr(q, "ndim", 0) == 3 else ("T", "Hq", "d")
+        _refuse_call4((("q", q, None),), pages, page_table, seq_lens, cu_q,
+                      (("out", out, tuple(shape), _BF16), ("lse", lse, tuple(shape[:2]), _F32)))
+    if workspace is not None and (not isinstance(workspace, torch.Tensor)
+                                  or workspace.get_device() != dev
+                                  or not workspace.is_contiguous()):
+        _refuse("workspace", workspace, getattr(workspace, "shape", ()),
+                getattr(workspace, "dtype", None), dev)
+    if T == 1:  # a single row has any stride
+        qs = Hq * d
+    scale = d ** -0.5 if scale is None else float(scale)
+    max_q = T if max_q is None else int(max_q)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return fwd_paged4(q, pages, page_table, seq_lens, cu_q, max_q, causal, scale, k_scale,
+                              v_scale, out, lse, workspace)
+    lib, stream = _lib or load(), _current_stream(dev)
+    if workspace is None:  # (as in _fwd_paged)
+        ws_bytes = fwd_paged4_workspace_size(T, B, Hq, Hkv, d, max_q)
+        ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(max(ws_bytes, 1), stream)
+    else:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    try:
+        rc = lib.fa_fwd_paged4_words(_PAGED4_WORDS(
+            q.data_ptr(), pages.data_ptr(), out.data_ptr(), lse.data_ptr(), page_table.data_ptr(),
+            seq_lens.data_ptr(), cu_q.data_ptr(), T, B, Hq, Hkv, d, qs, num_pages,
+            size // (9 * d) * 8, width, max_q, 1 if causal else 0, scale, k_scale, v_scale, ws,
+            ws_bytes, stream), 24)
+    finally:
+        if workspace is None:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
+    if rc != FA_OK:
+        _check("fa_fwd_paged4", rc)
+    return out, lse
 
 
 def device_status(stream=None):

@@ -1,0 +1,254 @@
+"""The paged cache in 4 bits on the GPU: appends against the quantisation written
+from its definition, bit for bit; reading back; attention against 64 bits."""
+import math
+
+import pytest
+import torch
+
+import paged4_common as c4
+from io_aware_exact_02_gb300 import build, fa
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return fa.load()
+
+
+# ------------------------------------------------------------------ append
+
+
+def rotated(x, pos, rope, interleaved):
+    """x (n, H, d) fp32 turned by the table's rows pos, every operation rounded."""
+    rd = rope.shape[1]
+    half = rd // 2
+    c, s = rope[pos][:, None, :half], rope[pos][:, None, half:]
+    y = x.clone()
+    a, b = (x[..., 0:rd:2], x[..., 1:rd:2]) if interleaved else (x[..., :half], x[..., half:rd])
+    u, v = a * c - b * s, a * s + b * c
+    if interleaved:
+        y[..., 0:rd:2], y[..., 1:rd:2] = u, v
+    else:
+        y[..., :half], y[..., half:rd] = u, v
+    return y
+
+
+class Append:
+    """New rows of ragged sequences, and the pool the append should leave."""
+
+    def __init__(self, Hq, Hkv, d, page, lens, nq, seed=0, rope=0, interleaved=False, pad=0,
+                 k_scale=1.0, v_scale=1.0, fused=False, data=None):
+        g = torch.Generator().manual_seed(seed)
+        self.Hkv, self.d, self.page, self.interleaved = Hkv, d, page, interleaved
+        self.scales = dict(k_scale=k_scale, v_scale=v_scale)
+        cu = [0]
+        for n in nq:
+            cu.append(cu[-1] + n)
+        T = cu[-1] + pad
+        qkv = torch.randn((T, Hq + 2 * Hkv, d), generator=g) * torch.cat(
+            [torch.ones(Hq), torch.full((Hkv,), k_scale), torch.full((Hkv,), v_scale)])[:, None]
+        if data is not None:
+            qkv = data(qkv)
+        qkv = qkv.to(torch.bfloat16)
+        self.q, self.k, self.v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        dev = qkv.cuda() if fused else None
+        part = (lambda x, lo, hi: dev[:, lo:hi]) if fused else (lambda x, lo, hi: x.cuda().contiguous())
+        self.dq, self.dk, self.dv = (part(self.q, 0, Hq), part(self.k, Hq, Hq + Hkv),
+                                     part(self.v, Hq + Hkv, Hq + 2 * Hkv))
+        counts = [max(1, -(-n // page)) for n in lens]
+        order = torch.randperm(sum(counts) + 2, generator=g)
+        table = torch.full((len(lens), max(counts)), 1 << 30, dtype=torch.int32)
+        pool = torch.randint(0, 256, (sum(counts) + 2, Hkv, page // 16, 18 * d), generator=g,
+                             dtype=torch.uint8)
+        self.pages = pool.flatten(2).cuda()
+        self.rope = None
+        if rope:
+            half = rope // 2
+            ang = torch.arange(max(lens), dtype=torch.float64)[:, None] * 10000.0 ** (
+                -torch.arange(half, dtype=torch.float64) / half)
+            self.rope = torch.cat([ang.cos(), ang.sin()], 1).float()
+        want, at = pool.clone(), 0
+        self.rows = []
+        self.q_want = self.q.float().clone()
+        inv_k, inv_v = (torch.tensor(1.0, dtype=torch.float32) / torch.tensor(x, dtype=torch.float32)
+                        for x in (k_scale, v_scale))
+        for b, (n, L) in enumerate(zip(nq, lens)):
+            ids = order[at:at + counts[b]]
+            table[b, :counts[b]] = ids.to(torch.int32)
+            at += counts[b]
+            if n == 0:
+                continue
+            rows, pos = slice(cu[b], cu[b + 1]), torch.arange(L - n, L)
+            k = self.k[rows].float()
+            if rope:
+                k = rotated(k, pos, self.rope, interleaved)
+                self.q_want[rows] = rotated(self.q[rows].float(), pos, self.rope, interleaved)
+            kc, ks = c4.quantize((k * inv_k).double())
+            vc, vs = c4.quantize((self.v[rows].float() * inv_v).double())
+            self.rows.append((rows, c4.values(kc, ks) * k_scale, c4.values(vc, vs) * v_scale))
+            for i in range(n):
+                p = int(pos[i])
+                blocks = want[ids[p // page], :, p % page // 16]
+                for h in range(Hkv):
+                    c4.put(blocks[h], p % 16, kc[i, h], ks[i, h], vc[i, h], vs[i, h])
+        self.want, self.table, self.lens, self.nq = want.flatten(2), table.cuda(), lens, nq
+        self.seq_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.cu_q = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        self.T, self.Hq, self.end = T, Hq, cu[-1]
+
+    def run(self):
+        return fa.kv4_append(self.dk, self.dv, self.pages, self.table, self.seq_lens, self.cu_q,
+                             q=self.dq, rope=None if self.rope is None else self.rope.cuda(),
+                             interleaved=self.interleaved, **self.scales)
+
+    def check_pool(self):
+        """Bit for bit, but for what no key owns: the odd half of a V byte (and
+        its scale) behind a sequence's last key, when it is even."""
+        got, want = self.pages.cpu().clone(), self.want.clone()
+        d, page = self.d, self.page
+        for b, (n, L) in enumerate(zip(self.nq, self.lens)):
+            if n and L % 2 == 1:
+                page_id = int(self.table[b, (L - 1) // page])
+                r, blk = (L - 1) % 16, (L - 1) % page // 16
+                for x in (got, want):
+                    v = x[page_id].view(self.Hkv, page // 16, 18 * d)[:, blk]
+                    for i in range(8):
+                        o = 8 * d + ((r // 8 * 8 + i) * 4 + r % 8 // 2) * (d // 8)
+                        v[:, o:o + d // 8] &= 15
+        assert torch.equal(got, want), (got != want).nonzero()[:5]
+
+
+APPENDS = [
+    dict(Hq=4, Hkv=2, d=128, page=16, lens=[1, 2, 17, 40], nq=[1, 1, 1, 1], rope=128),
+    dict(Hq=4, Hkv=2, d=64, page=16, lens=[5, 6, 33, 48, 9], nq=[5, 3, 17, 48, 0], rope=64, pad=3),
+    dict(Hq=3, Hkv=3, d=64, page=32, lens=[31, 64, 65], nq=[7, 8, 9], rope=32, interleaved=True),
+    dict(Hq=8, Hkv=1, d=128, page=64, lens=[63, 100], nq=[62, 33], rope=96, fused=True, pad=2),
+    dict(Hq=5, Hkv=5, d=128, page=256, lens=[257, 300], nq=[3, 44], rope=16, k_scale=0.7713, v_scale=0.0613),
+    dict(Hq=2, Hkv=2, d=64, page=128, lens=[130], nq=[129], k_scale=4.0, v_scale=0.0625),
+    dict(Hq=16, Hkv=16, d=128, page=16, lens=[18, 18], nq=[1, 2], rope=128, interleaved=True, fused=True),
+    dict(Hq=2, Hkv=1, d=128, page=16, lens=[31], nq=[30], rope=48),
+    dict(Hq=2, Hkv=1, d=64, page=16, lens=[31], nq=[30], rope=48, interleaved=True),
+]
+
+
+@pytest.mark.parametrize("case", APPENDS)
+def test_append_and_read(case):
+    a = Append(seed=11, **case)
+    q = a.run()
+    fa.check_device_status()
+    a.check_pool()
+    got = q.cpu().float()
+    # (q may be turned with fused products: both roundings of its bf16)
+    tol = c4.BF16 * a.q_want.abs() + 4 * c4.FP32 * 2 * a.q_want.abs().amax(-1, keepdim=True)
+    assert torch.all((got - a.q_want).abs()[:a.end] <= tol[:a.end]) and torch.all(got[a.end:] == 0)
+    k_out = torch.full((a.T, a.Hkv, a.d), 7.0, dtype=torch.bfloat16, device="cuda")
+    v_out = torch.full((a.T, a.Hkv + 1, a.d), 7.0, dtype=torch.bfloat16, device="cuda")[:, 1:]
+    fa.kv4_read(a.pages, a.table, a.seq_lens, a.cu_q, k_out, v_out, **a.scales)
+    fa.check_device_status()
+    for rows, k, v in a.rows:
+        for x, y in ((k_out, k), (v_out, v)):
+            # one rounding of the tensor's scale, of the product, to bf16
+            err = (x[rows].cpu().double() - y).abs()
+            exact = all(math.log2(s) % 1 == 0 for s in a.scales.values())
+            assert torch.all(err <= (0 if exact else c4.BF16 + 3 * c4.FP32) * y.abs())
+    assert torch.all(k_out[a.end:] == 7.0) and torch.all(v_out[a.end:] == 7.0)
+
+
+def test_append_special_numbers():
+    def data(x):
+        x[0, 2, :16] = 0.0                      # an empty group
+        x[1, 2, 16:32] = 1e-5                   # below the smallest scale
+        x[2, 2, 0] = math.inf
+        x[3, 2, 5] = -math.inf
+        x[4, 3, 7] = math.nan
+        x[5, 3, 16:32] = 3e4                    # beyond the largest
+        x[6, 3] = torch.arange(128) * 0.0625 - 4  # many halfway cases
+        x[7, 2, 32:48] = torch.tensor([6.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0] * 2)
+        return x
+    a = Append(2, 1, 128, 16, [8], [8], seed=5, data=data)
+    a.run()
+    fa.check_device_status()
+    k_out = torch.empty((8, 1, 128), dtype=torch.bfloat16, device="cuda")
+    v_out = torch.empty_like(k_out)
+    fa.kv4_read(a.pages, a.table, a.seq_lens, a.cu_q, k_out, v_out)
+    k, v = k_out.cpu().double()[:, 0], v_out.cpu().double()[:, 0]
+    assert torch.all(k[0, :16] == 0) and torch.all(k[1, 16:32] == 0)
+    assert k[2, 0] == 6 * 448 and k[3, 5] == -6 * 448
+    assert torch.all(k[2, 1:16] == 0) and torch.isnan(v[4, :16]).all()
+    assert not torch.isnan(v[4, 16:]).any() and torch.all(v[5, 16:32] == 6 * 448)
+    assert torch.equal(k[7, 32:48], torch.tensor([6, 0, 1, 1, 2, 2, 4, 4] * 2, dtype=torch.float64))
+    (_, kw, vw), = a.rows
+    rows = [0, 1, 6, 7]
+    assert torch.equal(k[rows], kw[rows, 0]) and torch.equal(v[rows], vw[rows, 0])
+
+
+def test_append_in_steps_is_the_whole():
+    """Token by token, odd and even starts, leaves the same pool as one call."""
+    whole = Append(2, 2, 64, 16, [37], [37], seed=3, rope=64)
+    whole.run()
+    rope = whole.rope.cuda()
+    pages = torch.randint(0, 256, whole.pages.shape, dtype=torch.uint8, device="cuda")
+    at = 0
+    for n in (1, 1, 2, 3, 5, 1, 8, 16):
+        rows = slice(at, at + n)
+        at += n
+        lens = torch.tensor([at], dtype=torch.int32, device="cuda")
+        cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+        fa.kv4_append(whole.dk[rows], whole.dv[rows], pages, whole.table, lens, cu, rope=rope)
+    outs = []
+    for p in (whole.pages, pages):
+        k = torch.empty((37, 2, 64), dtype=torch.bfloat16, device="cuda")
+        v = torch.empty_like(k)
+        outs.append(fa.kv4_read(p, whole.table, whole.seq_lens, whole.cu_q, k, v))
+    fa.check_device_status()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+# --------------------------------------------------------------- attention
+
+
+def attend(x, causal=True, scale=None, max_q=None, **kw):
+    o, lse = fa.fwd_paged4(*x.args(), max_q=max_q, causal=causal, scale=scale, out=x.out, lse=x.lse,
+                           **x.scales(), **kw)
+    fa.check_device_status()
+    x.check(o, lse, causal, x.d ** -0.5 if scale is None else scale)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("case", [
+    dict(Hq=4, Hkv=4, d=64, page=16, lens=[1, 2, 15, 16, 17, 33], nq=[1, 1, 1, 1, 1, 1]),
+    dict(Hq=8, Hkv=2, d=128, page=16, lens=[1000], nq=[1]),
+    dict(Hq=8, Hkv=1, d=128, page=32, lens=[300, 0, 129, 128], nq=[1, 1, 0, 2], pad=3),
+    dict(Hq=12, Hkv=2, d=64, page=64, lens=[777, 65], nq=[4, 5], fused=True),
+    dict(Hq=16, Hkv=1, d=128, page=128, lens=[260, 500, 1], nq=[1, 1, 1]),
+    dict(Hq=24, Hkv=1, d=64, page=16, lens=[100, 31], nq=[1, 3]),
+    dict(Hq=17, Hkv=1, d=128, page=16, lens=[50], nq=[2]),
+    dict(Hq=4, Hkv=2, d=128, page=256, lens=[513, 90], nq=[60, 90]),
+    dict(Hq=4, Hkv=1, d=64, page=16, lens=[400, 70, 40], nq=[100, 1, 1], pad=1),
+    dict(Hq=2, Hkv=2, d=128, page=64, lens=[700], nq=[300], k_scale=0.7713, v_scale=0.0613),
+    dict(Hq=6, Hkv=2, d=128, page=16, lens=[5, 3], nq=[5, 7]),
+])
+def test_attention(case, causal):
+    attend(c4.Batch4(seed=21, **case), causal, max_q=max(case["nq"]))
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, 1.0])
+def test_attention_scales(scale):
+    for nq in ([1, 1, 1], [90, 3, 40]):
+        attend(c4.Batch4(4, 2, 64, 16, [90, 91, 100], nq, seed=4), True, scale)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_of_loud_keys(d):
+    """Scores of some hundred: the running maximum keeps moving."""
+    for nq in ([1, 1], [70, 5]):
+        attend(c4.Batch4(8, 2, d, 16, [600, 70], nq, seed=6, spread=20.0))
+
+
+def test_attention_many_sequences():
+    lens = [1 + (37 * i) % 200 for i in range(70)]
+    attend(c4.Batch4(4, 2, 64, 16, lens, [1] * 70, seed=8), max_q=1)
+    nq = [min(n, 1 + (i % 9 == 0) * 40) for i, n in enumerate(lens)]
+    attend(c4.Batch4(4, 1, 128, 16, lens, nq, seed=9), max_q=max(nq))
