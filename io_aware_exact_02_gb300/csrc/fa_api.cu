@@ -967,7 +967,7 @@ size_t fa_fwd_paged4_workspace_size(int T, int B, int Hq, int Hkv, int d, int ma
   int shift;
   if (paged_shape(T, B, Hq, Hkv, d, 1, 16, 1, &shift) != FA_OK) return 0;
   if (Hq % Hkv != 0 || Hq / Hkv > 128 || max_q < 1) return 0;
-  return 0;
+  return paged4_workspace_layout(d, paged4_form(T, B, Hq / Hkv, max_q)).total;
 }
 
 int fa_fwd_paged4(const void* q, const void* pages, void* o, float* lse, const int* page_table,

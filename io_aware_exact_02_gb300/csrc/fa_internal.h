@@ -376,6 +376,54 @@ struct Paged4Params : PagedParams {
 };
 int launch_fwd_paged4(const Paged4Params& p, int d, cudaStream_t stream);
 
+// How a call over the 4-bit cache runs.  Sequences of up to small_tokens new
+// tokens go to the decode kernel, in units of `rows` (8 or 16) query rows of one
+// key/value head; where a token has more, its heads are dealt in `subs` equal
+// runs.  The others go to the prompt kernel.
+constexpr int kPaged4DecodeMost = 64;  // query rows of a sequence and key/value head
+struct Paged4Form {
+  int heads, subs;   // query heads of a decode unit's token; runs of a token's heads
+  int rows;          // 0: no decode phase
+  int small_tokens;
+  int prompt;        // a sequence may have more
+};
+inline Paged4Form paged4_form(int T, int B, int G, int max_q) {
+  Paged4Form f;
+  f.heads = G < 16 ? G : 16;
+  while (G % f.heads != 0) --f.heads;
+  f.subs = G / f.heads;
+  const int most = max_q < T ? max_q : T;
+  f.small_tokens = kPaged4DecodeMost / G > 1 ? kPaged4DecodeMost / G : 1;
+  f.prompt = most > f.small_tokens;
+  const int decode = f.prompt ? (B > 1 && (long long)B * most > T ? f.small_tokens : 0) : most;
+  f.rows = decode == 0 ? 0 : (long long)decode * f.heads <= 8 ? 8 : 16;
+  if (f.rows == 0) f.small_tokens = 0;
+  return f;
+}
+// Its workspace: the two phases' split records and slots.
+struct Paged4Workspace {
+  size_t rec[2], slot_o[2], slot_lse[2], total;
+};
+inline Paged4Workspace paged4_workspace_layout(int d, const Paged4Form& f) {
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  const int rows[2] = {f.rows, f.prompt ? kPairRows : 0};
+  Paged4Workspace w;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += up(bytes);
+    return here;
+  };
+  for (int k = 0; k < 2; ++k) {
+    const size_t slots = (size_t)kPagedMaxCtas * 2 * (size_t)rows[k];
+    w.rec[k] = take(rows[k] > 0 ? kPagedMaxCtas * kPagedRecBytes : 0);
+    w.slot_o[k] = take(slots * (size_t)d * sizeof(float));
+    w.slot_lse[k] = take(slots * sizeof(float));
+  }
+  w.total = at;
+  return w;
+}
+
 // A rank-3 tensor map over packed rows [T][heads][d] bf16 with `stride`
 // elements between rows: dims (d, heads, T), box (64, box_heads, box_rows),
 // 128-byte swizzle, zero fill outside.

@@ -459,6 +459,11 @@ int launch_paged_d(const PagedParams& p, cudaStream_t stream) {
 
 }  // namespace
 
+int launch_paged_merge(const PagedParams& p, const PagedPhase& ph, int d,
+                       const cudaLaunchConfig_t& base) {
+  return d == 128 ? launch_merge<128>(p, ph, nullptr, base) : launch_merge<64>(p, ph, nullptr, base);
+}
+
 int launch_fwd_paged(const PagedParams& p, int d, cudaStream_t stream) {
   return d == 128 ? launch_paged_d<128>(p, stream) : launch_paged_d<64>(p, stream);
 }

@@ -6,6 +6,8 @@
 #include "fa_internal.h"
 #include "fa_kv4.cuh"
 #include "fa_paged.cuh"
+#include "fa_paged4_decode.cuh"
+#include "fa_paged_launch.h"
 #include "sm100_ptx.cuh"
 
 namespace fa {
@@ -14,7 +16,7 @@ namespace {
 constexpr int kWarps = 4;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) fa_paged4_rows_kernel(const Paged4Params p) {
+__global__ void __launch_bounds__(32 * kWarps) fa_paged4_rows_kernel(const Paged4Params p, int n_min) {
   using Block = Kv4Block<D>;
   constexpr int kPer = D / 32;
   __shared__ float qs[kWarps][D];
@@ -29,7 +31,7 @@ __global__ void __launch_bounds__(32 * kWarps) fa_paged4_rows_kernel(const Paged
         report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedRows);
     }
   const PagedRow at = paged_row(p.cu_q, p.seq_lens, p.B, p.T, t, p.status);
-  if (at.b < 0 || hq >= p.Hq) return;
+  if (at.b < 0 || hq >= p.Hq || p.cu_q[at.b + 1] - p.cu_q[at.b] < n_min) return;
   int abort_flag = 0;
   int len = p.seq_lens[at.b];
   const int cap = p.max_pages << p.page_shift;
@@ -114,25 +116,74 @@ __global__ void __launch_bounds__(32 * kWarps) fa_paged4_rows_kernel(const Paged
   if (lane == 0) p.lse[row] = l == 0.f ? ninf : (m + log2f(l)) * kLn2;
 }
 
-}  // namespace
+template <int D, int R>
+__global__ void __launch_bounds__(Decode4Cfg<D, R>::kThreads, 1)
+    fa_paged4_decode_kernel(const Paged4Params p, const PagedPhase ph, int subs) {
+  extern __shared__ uint8_t smem_raw[];
+  decode4_cta<D, R>(p, ph, subs, blockIdx.x, gridDim.x, smem_raw);
+}
 
-int launch_fwd_paged4(const Paged4Params& p, int d, cudaStream_t stream) {
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((unsigned)p.T, (unsigned)((p.Hq + kWarps - 1) / kWarps), 1);
-  c.blockDim = dim3(32 * kWarps, 1, 1);
-  c.stream = stream;
-  c.attrs = pdl;
-  c.numAttrs = 1;
-  const cudaError_t e = d == 128 ? cudaLaunchKernelEx(&c, fa_paged4_rows_kernel<128>, p)
-                                 : cudaLaunchKernelEx(&c, fa_paged4_rows_kernel<64>, p);
-  if (e != cudaSuccess) {
+template <int D, int R>
+int launch_decode(const Paged4Params& p, const PagedPhase& ph, int subs,
+                  const cudaLaunchConfig_t& base) {
+  static_assert(sizeof(Decode4Smem<D, R>) + 128 <= 232448,
+                "shared memory above the 227 KB a CTA may have");
+  cudaLaunchConfig_t c = base;
+  c.blockDim = dim3(Decode4Cfg<D, R>::kThreads, 1, 1);
+  c.dynamicSmemBytes = sizeof(Decode4Smem<D, R>) + 128;
+  if (paged_kernel_ready<fa_paged4_decode_kernel<D, R>, 0>(c.dynamicSmemBytes) != FA_OK)
+    return FA_ERR_LAUNCH;
+  if (cudaLaunchKernelEx(&c, fa_paged4_decode_kernel<D, R>, p, ph, subs) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
   }
   return FA_OK;
+}
+
+template <int D>
+int launch_paged4_d(const Paged4Params& p, cudaStream_t stream) {
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.stream = stream;
+  c.attrs = pdl;
+  c.numAttrs = 1;
+  const Paged4Form f = paged4_form(p.T, p.B, p.G, p.max_q);
+  const Paged4Workspace w = paged4_workspace_layout(D, f);
+  auto at = [&](size_t offset) { return reinterpret_cast<float*>(p.workspace + offset); };
+  int rc;
+  if (f.prompt) {
+    c.gridDim = dim3((unsigned)p.T, (unsigned)((p.Hq + kWarps - 1) / kWarps), 1);
+    c.blockDim = dim3(32 * kWarps, 1, 1);
+    if (cudaLaunchKernelEx(&c, fa_paged4_rows_kernel<D>, p, f.small_tokens + 1) != cudaSuccess) {
+      cudaGetLastError();
+      return FA_ERR_LAUNCH;
+    }
+  }
+  c.gridDim = dim3((unsigned)p.ctas, 1, 1);
+  if (f.rows > 0) {
+    Paged4Params q = p;  // its heads are runs of a token's
+    q.G = f.heads;
+    q.Hkv = p.Hkv * f.subs;
+    PagedPhase ph = {};
+    ph.rec = p.workspace + w.rec[0];
+    ph.slot_o = at(w.slot_o[0]);
+    ph.slot_lse = at(w.slot_lse[0]);
+    ph.n_max = f.prompt ? f.small_tokens : 0x7fffffff;
+    ph.unit_tokens = ph.tile_tokens = f.rows / f.heads;
+    ph.slot_rows = f.rows;
+    rc = f.rows == 8 ? launch_decode<D, 8>(q, ph, f.subs, c) : launch_decode<D, 16>(q, ph, f.subs, c);
+    if (rc != FA_OK) return rc;
+    if ((rc = launch_paged_merge(q, ph, D, c)) != FA_OK) return rc;
+  }
+  return FA_OK;
+}
+
+}  // namespace
+
+int launch_fwd_paged4(const Paged4Params& p, int d, cudaStream_t stream) {
+  return d == 128 ? launch_paged4_d<128>(p, stream) : launch_paged4_d<64>(p, stream);
 }
 
 }  // namespace fa

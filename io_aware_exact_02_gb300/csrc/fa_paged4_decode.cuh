@@ -1,0 +1,558 @@
+// fa_paged4_decode.cuh -- attention over a paged cache held in 4 bits for few
+// query rows to a key/value head.  The list of units and its split over the CTAs
+// are those of fa_paged.cuh, the numbers and their layout those of fa_kv4.cuh.
+//
+// Keys and values are read once and used by 8 or 16 rows, so the kernel's job is
+// to keep memory busy; but 45 bytes a nanosecond and SM are 80 numbers, and each
+// has to be turned into a 16-bit operand of the tensor core.  What that costs
+// decides the form: an operand in shared memory would be written and read
+// there once more (160 and 160 of the 250 bytes a nanosecond that shared memory
+// moves), so the products are mma.sync's, whose operands are registers.  Its
+// rate (measured: 4.1 ns for a 16 x 8 x 16 product on a quarter of an SM) is a
+// third used with 8 rows, two thirds with 16; the conversion of codes (76 pairs
+// a nanosecond and SM) is half used.
+//
+// A warp works alone on blocks of 16 keys of a unit, which arrive in its own ring:
+//     S^T [16 keys x rows] = K [16 x d] Q^T,    O^T [d x rows] += V^T [d x 16] P^T
+// with keys, then channels, along the 16 rows of the product, so that 8 query
+// rows leave none of it unused.  A lane (g, t) = (lane / 4, lane % 4) reads from
+// a block channels t d/4 .. of keys g and g + 8, whose order in the first product
+// is free, and channels g d/8 .. of the key pairs (2t, 2t + 1) and 8 further on:
+// the layout of a block makes each one 16-byte load (d = 64: 8-byte) of
+// consecutive addresses.  P goes from the first product's layout to the
+// second's by a transposition of 8 x 8 matrices among the warp's registers.
+// The running maximum of a row is a warp's own, and moves only when a block's
+// scores exceed it by kRescaleSlack.  At a unit's end the warps' parts are
+// joined through shared memory.
+//
+// Warps: 0 .. W-1 compute, warp W walks the list and loads (a lane per ring), warp
+// W + 1 turns each unit's query rows into fp16, scaled by a power of two each.
+#pragma once
+
+#include "fa_internal.h"
+#include "fa_kv4.cuh"
+#include "fa_paged.cuh"
+#include "fa_softmax.cuh"
+#include "sm100_ptx.cuh"
+
+namespace fa {
+
+// A row's reference maximum before it has seen a key (finite: the exponent of a
+// masked score is -inf and not NaN).
+constexpr float kNoRef4 = -3.0e38f;
+
+// 16-byte aligned bytes (a multiple of 16) to shared memory, completing `bar`'s
+// transaction count.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+// D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16).
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The transpose of an 8 x 8 matrix of 16-bit numbers, two to a lane.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A vote of `threads` threads on named barrier `id`: true for all when true for
+// any.  Also a barrier among them.
+__device__ __forceinline__ bool named_vote(int id, int threads, bool x) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred P, Q;\n\t"
+      "setp.ne.b32 P, %1, 0;\n\t"
+      "barrier.cta.red.or.pred Q, %2, %3, P;\n\t"
+      "selp.b32 %0, 1, 0, Q;\n\t}"
+      : "=r"(r)
+      : "r"((int)x), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+template <int D, int R>
+struct Decode4Cfg {
+  static constexpr int kTiles = R / 8;
+  // That compute: with the other two 16 or 12 warps, of 128 or 168 registers.
+  static constexpr int kWarps = R == 8 ? 14 : 10;
+  static constexpr int kThreads = 32 * (kWarps + 2);
+  static constexpr int kStages = D == 128 ? 4 : 8;  // blocks of a warp's ring
+  static constexpr int kItems = 4;
+};
+
+template <int D, int R>
+struct alignas(128) Decode4Smem {
+  using Cfg = Decode4Cfg<D, R>;
+  static constexpr int W = Cfg::kWarps;
+  uint8_t ring[W][Cfg::kStages][Kv4Block<D>::kBytes];
+  float part_o[W][R][D];  // 16-byte chunk c of row r at c ^ (r / 2 % 4)
+  __half q[2][R][D];
+  float part_m[W][R], part_l[W][R];
+  float c2[2][R];         // a row's factor from products to exponents
+  int lim[2][R];          // the keys that a row sees end here
+  uint64_t full[W][Cfg::kStages], empty[W][Cfg::kStages];
+  uint64_t item_full[Cfg::kItems], item_empty[Cfg::kItems];
+  uint64_t q_full[2], q_empty[2];
+  PagedItem item[Cfg::kItems];
+  PagedScan scan;
+  int abort_flag;
+};
+
+// Blocks of 16 keys of a segment.
+__device__ __forceinline__ int item_blocks(const PagedItem& it) {
+  return it.nj == 0 ? 0 : (min(it.k_hi - it.key, it.nj * kTile) + 15) >> 4;
+}
+
+// The kernel's work on CTA `cta` of `ctas`.  p.Hkv heads of p.G rows each: `subs`
+// of them share a key/value head of the cache.
+template <int D, int R>
+__device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPhase& ph, int subs,
+                                            int cta, int ctas, uint8_t* smem_raw) {
+  using Cfg = Decode4Cfg<D, R>;
+  using Block = Kv4Block<D>;
+  constexpr int W = Cfg::kWarps, S = Cfg::kStages, NT = Cfg::kTiles;
+  Decode4Smem<D, R>& sm = *reinterpret_cast<Decode4Smem<D, R>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  volatile int* abortf = &sm.abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < W * S; i += Cfg::kThreads) {
+    mbar_init(&sm.full[0][0] + i, 1);
+    mbar_init(&sm.empty[0][0] + i, 1);
+  }
+  if (tid == 0) {
+    for (int i = 0; i < Cfg::kItems; ++i) {
+      mbar_init(&sm.item_full[i], 1);
+      mbar_init(&sm.item_empty[i], W + 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.q_empty[i], W);
+    }
+    sm.abort_flag = 0;
+  }
+  fence_mbar_init();
+  __syncthreads();
+  launch_dependents();
+  wait_prior_grid();
+  PagedWalk walk;
+  paged_plan(p, ph, sm.scan, walk, cta, ctas);
+
+  if (warp == W) {
+    // ------------------------------------------------------------ the list, and loads
+    paged_walk_begin(p, ph, sm.scan, walk, cta, ctas);
+    if (walk.g >= walk.hi && lane == 0)
+      reinterpret_cast<PagedRec*>(ph.rec + cta * kPagedRecBytes)->split = 0;
+    bool ok = true;
+    int c = 0;    // this lane's ring uses
+    int off = 0;  // the warp that the segment's first block goes to
+    for (int m = 0; ok; ++m) {
+      const PagedItem it = paged_next(p, ph, walk, cta);
+      const int is = m % Cfg::kItems;
+      if (m >= Cfg::kItems)
+        ok = mbar_wait(&sm.item_empty[is], (m / Cfg::kItems - 1) & 1, p.status, abortf,
+                       kSitePgItemEmpty);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        sm.item[is] = it;
+        mbar_arrive(&sm.item_full[is]);
+      }
+      if (it.end) break;
+      // Block i of the segment is warp (off + i) % W's.
+      const int n = item_blocks(it), h = it.h / subs;
+      const int* const list = p.page_table + (long long)it.b * p.max_pages;
+      auto page_of = [&](int i) { return i < n ? list[(it.key + 16 * i) >> p.page_shift] : 0; };
+      int i = lane < W ? (lane >= off ? lane - off : lane - off + W) : n;
+      int next = page_of(i);
+      while (__any_sync(0xffffffffu, i < n)) {
+        const int page = next;
+        next = page_of(i + W);
+        if (i < n) {
+          const int slot = c % S;
+          if (c >= S)
+            ok = mbar_wait(&sm.empty[lane][slot], (c / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
+          if (ok) {
+            if (page < 0 || page >= p.num_pages) {
+              int abort_flag = 0;
+              report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
+              mbar_arrive(&sm.full[lane][slot]);  // whatever the slot holds
+            } else {
+              const int key = it.key + 16 * i;
+              mbar_arrive_expect_tx(&sm.full[lane][slot], Block::kBytes);
+              bulk_load(sm.ring[lane][slot],
+                        p.pages + kv4_block_at(page, p.Hkv / subs, h, p.page_shift,
+                                               key & (p.page_size - 1), Block::kBytes),
+                        Block::kBytes, &sm.full[lane][slot]);
+            }
+            ++c;
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        i += W;
+      }
+      off = (off + n) % W;
+      // What the merge needs to know of the CTA's first unit.
+      if (m == 0 && lane == 0) {
+        PagedRec r = {};
+        if (!it.first) {
+          const int c0 = walk.share.owner(walk.start);
+          r.split = 1;
+          r.slot = 2 * c0 + (walk.share.lo(c0) < walk.start ? 1 : 0);
+          r.n = walk.share.owner(walk.end - 1) - c0 + 1;
+          r.tok0 = it.tok0;
+          r.ntok = it.ntok;
+          r.h = it.h;
+        }
+        *reinterpret_cast<PagedRec*>(ph.rec + cta * kPagedRecBytes) = r;
+      }
+      __syncwarp();
+    }
+    // After a failure: the copies on their way have to land before the CTA exits.
+    if (!ok && lane < W)
+      for (int k = c - 1; k >= 0 && k >= c - S; --k) drain_wait(&sm.full[lane][k % S], (k / S) & 1);
+    __syncwarp();
+    return;
+  }
+  if (warp == W + 1) {
+    // ------------------------------------------------------------ query rows
+    constexpr int kPer = D / 32;
+    bool ok = true;
+    for (int m = 0; ok; ++m) {
+      const int is = m % Cfg::kItems, qb = m & 1;
+      ok = mbar_wait(&sm.item_full[is], (m / Cfg::kItems) & 1, p.status, abortf, kSitePgItemFull);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int end = sm.item[is].end, rows = sm.item[is].ntok * p.G, tok0 = sm.item[is].tok0,
+                h = sm.item[is].h, pos0 = sm.item[is].pos0, len = sm.item[is].len;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[is]);
+      if (end) break;
+      if (!warp_bound_ok(tok0 >= 0 && rows <= R && tok0 + rows / p.G <= p.T && h < p.Hkv, p.status,
+                         abortf, kChkPgItem))
+        break;
+      float x[R][kPer];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        uint32_t w[kPer / 2];
+#pragma unroll
+        for (int i = 0; i < kPer / 2; ++i) w[i] = 0u;
+        if (r < rows) {
+          const int tok = r / p.G;
+          const __nv_bfloat16* src = p.q + (tok0 + tok) * p.q_stride +
+                                     (long long)(h * p.G + r - tok * p.G) * D + lane * kPer;
+          if constexpr (kPer == 4) {
+            const uint2 u = *reinterpret_cast<const uint2*>(src);
+            w[0] = u.x, w[kPer / 2 - 1] = u.y;
+          } else {
+            w[0] = *reinterpret_cast<const uint32_t*>(src);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kPer / 2; ++i) {
+          x[r][2 * i] = __uint_as_float(w[i] << 16);
+          x[r][2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+      }
+      if (m >= 2) ok = mbar_wait(&sm.q_empty[qb], (m / 2 - 1) & 1, p.status, abortf, kSitePgQEmpty);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) top = fmaxf(top, fabsf(x[r][i]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // The largest to [2^14, 2^15): exponents are exact, and what falls below
+        // fp16's range is 2^-38 of it.  (Zeros, infinities and NaN stay.)
+        int e = 0;
+        if (top > 0.f && top < __int_as_float(0x7f800000))
+          e = min(14 - ((__float_as_int(top) >> 23) - 127), 100);
+        const float f = __int_as_float((e + 127) << 23);
+        uint32_t w[kPer / 2];
+#pragma unroll
+        for (int i = 0; i < kPer / 2; ++i) w[i] = pack_half2(x[r][2 * i] * f, x[r][2 * i + 1] * f);
+        if constexpr (kPer == 4)
+          *reinterpret_cast<uint2*>(&sm.q[qb][r][lane * kPer]) = make_uint2(w[0], w[kPer / 2 - 1]);
+        else
+          *reinterpret_cast<uint32_t*>(&sm.q[qb][r][lane * kPer]) = w[0];
+        if (lane == 0) {
+          sm.c2[qb][r] = r < rows ? p.scale_log2 * p.k_scale * __int_as_float((127 - e) << 23) : 0.f;
+          int lim = 0;
+          if (r < rows) lim = p.causal ? max(0, min(pos0 + r / p.G + 1, len)) : len;
+          sm.lim[qb][r] = lim;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full[qb]);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- compute
+  const int g = lane >> 2, t = lane & 3;
+  const float ninf = __int_as_float(0xff800000);
+  bool fail = false;
+  int c = 0, off = 0;  // ring uses; the warp of the segment's first block
+  for (int m = 0;; ++m) {
+    const int is = m % Cfg::kItems, qb = m & 1;
+    if (!fail)
+      fail = !mbar_wait(&sm.item_full[is], (m / Cfg::kItems) & 1, p.status, abortf, kSitePgItemFull);
+    fail = __any_sync(0xffffffffu, fail);
+    int end = 0, n = 0, key0 = 0, rows = 0, tok0 = 0, head0 = 0, oslot = -1, min_lim = 0, k_hi = 0;
+    if (!fail) {
+      const PagedItem& it = sm.item[is];
+      end = it.end;
+      n = item_blocks(it);
+      key0 = it.key;
+      rows = it.ntok * p.G;
+      tok0 = it.tok0;
+      head0 = it.h * p.G;
+      oslot = it.slot;
+      k_hi = it.k_hi;
+      min_lim = p.causal ? it.pos0 + 1 : it.len;
+    }
+    __syncwarp();
+    if (!fail && lane == 0) mbar_arrive(&sm.item_empty[is]);
+    float ref[NT][2], l[NT][2], c2[NT][2], o[D / 16][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) ref[nt][e] = kNoRef4, l[nt][e] = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+    const int i0 = warp >= off ? warp - off : warp - off + W;
+    off = (off + n) % W;
+    if (!fail && !end) {
+      fail = !mbar_wait(&sm.q_full[qb], (m / 2) & 1, p.status, abortf, kSitePgQFull);
+      fail = __any_sync(0xffffffffu, fail);
+      uint32_t q[NT][D / 16][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4* src = reinterpret_cast<const uint4*>(&sm.q[qb][nt * 8 + g][t * (D / 4)]);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const uint4 x = src[i];
+          q[nt][2 * i][0] = x.x, q[nt][2 * i][1] = x.y;
+          q[nt][2 * i + 1][0] = x.z, q[nt][2 * i + 1][1] = x.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) c2[nt][e] = sm.c2[qb][nt * 8 + 2 * t + e];
+      }
+      for (int i = i0; i < n && !fail; i += W, ++c) {
+        const int slot = c % S, key = key0 + 16 * i;
+        fail = !mbar_wait(&sm.full[warp][slot], (c / S) & 1, p.status, abortf, kSitePgKvFull);
+        fail = __any_sync(0xffffffffu, fail);
+        if (fail) break;
+        const uint8_t* const blk = sm.ring[warp][slot];
+        constexpr int kWords = D / 32;  // of four bytes: a key's, or a value pair's, of this lane
+        uint32_t kw[2][kWords], vw[2][kWords], ks[2], vs[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(blk + Block::k_code(0) + (u * 32 + lane) * 16);
+            const uint4 y = *reinterpret_cast<const uint4*>(blk + Block::v_code(0, 0) + (u * 32 + lane) * 16);
+            kw[u][0] = x.x, kw[u][1] = x.y, kw[u][kWords - 2] = x.z, kw[u][kWords - 1] = x.w;
+            vw[u][0] = y.x, vw[u][1] = y.y, vw[u][kWords - 2] = y.z, vw[u][kWords - 1] = y.w;
+            ks[u] = *reinterpret_cast<const uint16_t*>(blk + Block::k_scale(0) + (u * 32 + lane) * 2);
+            vs[u] = *reinterpret_cast<const uint16_t*>(blk + Block::v_scale(g) + u * 8 + 2 * t);
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(blk + Block::k_code(0) + (u * 32 + lane) * 8);
+            const uint2 y = *reinterpret_cast<const uint2*>(blk + Block::v_code(0, 0) + (u * 32 + lane) * 8);
+            kw[u][0] = x.x, kw[u][1] = x.y;
+            vw[u][0] = y.x, vw[u][1] = y.y;
+            ks[u] = blk[Block::k_scale(0) + u * 32 + lane];
+            vs[u] = *reinterpret_cast<const uint16_t*>(blk + Block::v_scale(g / 2) + u * 8 + 2 * t);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.empty[warp][slot]);
+        float s[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+        {
+          uint32_t sc[2][2];  // of keys g, g + 8: the scales of the lane's one or two groups
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t x = e4m3_to_half(ks[u]);
+            sc[u][0] = __byte_perm(x, x, 0x1010);
+            sc[u][1] = D == 128 ? __byte_perm(x, x, 0x3232) : sc[u][0];
+          }
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              e2m1_to_half(kw[u][w], a[u]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) a[u][e] = half2_mul(a[u][e], sc[u][2 * w / kWords]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t f[4] = {a[0][2 * k], a[1][2 * k], a[0][2 * k + 1], a[1][2 * k + 1]};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_16816(s[nt], f, q[nt][2 * w + k][0], q[nt][2 * w + k][1]);
+            }
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[nt][e] *= c2[nt][e & 1];
+        if (key + 16 > min_lim) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key + g + (e >> 1) * 8 >= sm.lim[qb][nt * 8 + 2 * t + (e & 1)]) s[nt][e] = ninf;
+          if (key + 16 > k_hi) {
+            // Slots past the unit's keys may hold anything, and 0 * NaN is NaN.
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int first = key + u * 8 + 2 * t;
+              if (first >= k_hi) vs[u] = 0u;
+              if (first + 1 >= k_hi) vs[u] &= 0xffu;
+            }
+          }
+        }
+        float over = ninf;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) over = fmaxf(over, s[nt][e] - ref[nt][e & 1]);
+        if (__any_sync(0xffffffffu, over > kRescaleSlack)) {
+          // Some score outgrew the reference: every row's moves to its maximum.
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float top = fmaxf(fmaxf(s[nt][e], s[nt][e + 2]), ref[nt][e]);
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+              const float alpha = ex2_approx(ref[nt][e] - top);
+              ref[nt][e] = top;
+              l[nt][e] *= alpha;
+#pragma unroll
+              for (int mt = 0; mt < D / 16; ++mt) o[mt][nt][e] *= alpha, o[mt][nt][e + 2] *= alpha;
+            }
+        }
+        uint32_t pt[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = ex2_approx(s[nt][e] - ref[nt][e & 1]);
+            l[nt][e & 1] += x[e];
+          }
+          pt[nt][0] = transpose_8x8(pack_half2(x[0], x[1]));
+          pt[nt][1] = transpose_8x8(pack_half2(x[2], x[3]));
+        }
+        const uint32_t v0 = e4m3_to_half(vs[0]), v1 = e4m3_to_half(vs[1]);
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          uint32_t a[2][4];
+          e2m1_to_half(vw[0][w], a[0]);
+          e2m1_to_half(vw[1][w], a[1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[0][e] = half2_mul(a[0][e], v0);
+            a[1][e] = half2_mul(a[1][e], v1);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t f[4] = {a[0][2 * k], a[0][2 * k + 1], a[1][2 * k], a[1][2 * k + 1]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_16816(o[2 * w + k][nt], f, pt[nt][0], pt[nt][1]);
+          }
+        }
+      }
+      if (lane == 0 && !fail) mbar_arrive(&sm.q_empty[qb]);
+    }
+    // ------------------------------------------------------ the unit's result
+    // (Every warp comes to both votes, whatever failed, and all leave together.)
+    if (named_vote(1, 32 * W, fail) || end) break;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], x);
+        const int r = nt * 8 + 2 * t + e;
+        if (g == 0) {
+          sm.part_m[warp][r] = ref[nt][e];
+          sm.part_l[warp][r] = l[nt][e];
+        }
+        if (i0 < n) {
+          // Channels g d/8 .. of the row: o[mt] holds 2 mt (its first half) and 2 mt + 1.
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const int chunk = (g * (D / 32) + i) ^ t;
+            *reinterpret_cast<float4*>(&sm.part_o[warp][r][chunk * 4]) =
+                make_float4(o[2 * i][nt][e], o[2 * i][nt][e + 2], o[2 * i + 1][nt][e],
+                            o[2 * i + 1][nt][e + 2]);
+          }
+        }
+      }
+    named_bar_sync(1, 32 * W);
+    for (int x = tid; x < rows * (D / 2); x += 32 * W) {  // a row to a warp (or half of one)
+      const int r = x / (D / 2), ch = x % (D / 2) * 2;
+      float pm = kNoRef4, pl = 0.f;
+      if (lane < W) pm = sm.part_m[lane][r], pl = sm.part_l[lane][r];
+      float top = pl == 0.f ? kNoRef4 : pm;
+#pragma unroll
+      for (int e = 16; e > 0; e >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
+      const float weight = pl == 0.f ? 0.f : exp2f(pm - top);
+      float sum = pl * weight;
+#pragma unroll
+      for (int e = 16; e > 0; e >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, e);
+      float2 acc = make_float2(0.f, 0.f);
+#pragma unroll 4
+      for (int w = 0; w < W; ++w) {
+        const float f = __shfl_sync(0xffffffffu, weight, w);
+        if (f != 0.f) {
+          const float2 y = *reinterpret_cast<const float2*>(
+              &sm.part_o[w][r][((ch >> 2) ^ ((r >> 1) & 3)) * 4 + (ch & 3)]);
+          acc.x += f * y.x, acc.y += f * y.y;
+        }
+      }
+      const float own = sum == 0.f ? 0.f : p.v_scale / sum;
+      const float lse2 = sum == 0.f ? ninf : top + log2f(sum);
+      const int tok = r / p.G;
+      const long long at = (long long)(tok0 + tok) * p.Hq + head0 + (r - tok * p.G);
+      if (oslot >= 0) {
+        const long long row = ((long long)cta * 2 + oslot) * ph.slot_rows + r;
+        *reinterpret_cast<float2*>(ph.slot_o + row * D + ch) = make_float2(acc.x * own, acc.y * own);
+        if (ch == 0) ph.slot_lse[row] = lse2;
+      } else {
+        *reinterpret_cast<uint32_t*>(p.o + at * D + ch) = pack_bf16x2(acc.x * own, acc.y * own);
+        if (ch == 0) p.lse[at] = lse2 == ninf ? ninf : lse2 * kLn2;
+      }
+    }
+  }
+}
+
+}  // namespace fa

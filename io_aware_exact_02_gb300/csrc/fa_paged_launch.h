@@ -16,7 +16,7 @@ struct PagedMaps {
 
 // Sets the kernel's shared memory on the current device and checks that it has
 // the registers its warpgroups split, once per device.
-template <auto* kernel>
+template <auto* kernel, int kRegs = kPagedRegs>
 int paged_kernel_ready(size_t smem) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -33,7 +33,7 @@ int paged_kernel_ready(size_t smem) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
   }
-  if (attr.numRegs < kPagedRegs) return FA_ERR_LAUNCH;
+  if (attr.numRegs < kRegs) return FA_ERR_LAUNCH;
   ready.fetch_or(bit, std::memory_order_relaxed);
   return FA_OK;
 }
@@ -47,5 +47,9 @@ int launch_paged_prompt(const PagedMaps& t, const PagedParams& p, const PagedPha
 int launch_paged_duo(const PagedMaps& t, const CUtensorMap& tq_b, const PagedParams& p,
                      const PagedPhase& pa, const PagedPhase& pb, int d,
                      const cudaLaunchConfig_t& base);
+
+// The merge of one phase's units that were shared between CTAs (fa_paged.cu).
+int launch_paged_merge(const PagedParams& p, const PagedPhase& ph, int d,
+                       const cudaLaunchConfig_t& base);
 
 }  // namespace fa
