@@ -25,8 +25,9 @@
 // scores exceed it by kRescaleSlack.  At a unit's end the warps' parts are
 // joined through shared memory.
 //
-// Warps: 0 .. W-1 compute, warp W walks the list and loads (a lane per ring), warp
-// W + 1 turns each unit's query rows into fp16, scaled by a power of two each.
+// Warps: 0 .. W-1 load and compute; warp W walks the list and turns each unit's
+// query rows into fp16, scaled by a power of two each.  (One warp loading for all
+// of them bounded the kernel: 70 ns a block.)
 #pragma once
 
 #include "fa_internal.h"
@@ -89,10 +90,13 @@ __device__ __forceinline__ bool named_vote(int id, int threads, bool x) {
 template <int D, int R>
 struct Decode4Cfg {
   static constexpr int kTiles = R / 8;
-  // That compute: with the other two 16 or 12 warps, of 128 or 168 registers.
-  static constexpr int kWarps = R == 8 ? 14 : 10;
-  static constexpr int kThreads = 32 * (kWarps + 2);
-  static constexpr int kStages = D == 128 ? 4 : 8;  // blocks of a warp's ring
+  // With the twelfth, 168 registers a thread: enough for a step of two blocks (the
+  // latencies of one hide behind the other's), but for d = 128 with 16 rows,
+  // whose O alone takes 64.
+  static constexpr int kWarps = 11;  // that compute
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kUnit = D == 128 && R == 16 ? 1 : 2;  // blocks of a step
+  static constexpr int kStages = D == 128 ? (R == 16 ? 4 : 3) : 6;  // steps in a warp's ring
   static constexpr int kItems = 4;
 };
 
@@ -100,13 +104,13 @@ template <int D, int R>
 struct alignas(128) Decode4Smem {
   using Cfg = Decode4Cfg<D, R>;
   static constexpr int W = Cfg::kWarps;
-  uint8_t ring[W][Cfg::kStages][Kv4Block<D>::kBytes];
+  uint8_t ring[W][Cfg::kStages][Cfg::kUnit * Kv4Block<D>::kBytes];
   float part_o[W][R][D];  // 16-byte chunk c of row r at c ^ (r / 2 % 4)
   __half q[2][R][D];
   float part_m[W][R], part_l[W][R];
   float c2[2][R];         // a row's factor from products to exponents
   int lim[2][R];          // the keys that a row sees end here
-  uint64_t full[W][Cfg::kStages], empty[W][Cfg::kStages];
+  uint64_t full[W][Cfg::kStages];
   uint64_t item_full[Cfg::kItems], item_empty[Cfg::kItems];
   uint64_t q_full[2], q_empty[2];
   PagedItem item[Cfg::kItems];
@@ -114,9 +118,9 @@ struct alignas(128) Decode4Smem {
   int abort_flag;
 };
 
-// Blocks of 16 keys of a segment.
-__device__ __forceinline__ int item_blocks(const PagedItem& it) {
-  return it.nj == 0 ? 0 : (min(it.k_hi - it.key, it.nj * kTile) + 15) >> 4;
+// Keys of a segment.
+__device__ __forceinline__ int item_keys(const PagedItem& it) {
+  return it.nj == 0 ? 0 : min(it.k_hi - it.key, it.nj * kTile);
 }
 
 // The kernel's work on CTA `cta` of `ctas`.  p.Hkv heads of p.G rows each: `subs`
@@ -126,19 +130,16 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
                                             int cta, int ctas, uint8_t* smem_raw) {
   using Cfg = Decode4Cfg<D, R>;
   using Block = Kv4Block<D>;
-  constexpr int W = Cfg::kWarps, S = Cfg::kStages, NT = Cfg::kTiles;
+  constexpr int W = Cfg::kWarps, S = Cfg::kStages, NT = Cfg::kTiles, U = Cfg::kUnit;
   Decode4Smem<D, R>& sm = *reinterpret_cast<Decode4Smem<D, R>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   volatile int* abortf = &sm.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int i = tid; i < W * S; i += Cfg::kThreads) {
-    mbar_init(&sm.full[0][0] + i, 1);
-    mbar_init(&sm.empty[0][0] + i, 1);
-  }
+  for (int i = tid; i < W * S; i += Cfg::kThreads) mbar_init(&sm.full[0][0] + i, 1);
   if (tid == 0) {
     for (int i = 0; i < Cfg::kItems; ++i) {
       mbar_init(&sm.item_full[i], 1);
-      mbar_init(&sm.item_empty[i], W + 1);
+      mbar_init(&sm.item_empty[i], W);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 1);
@@ -154,16 +155,15 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
   paged_plan(p, ph, sm.scan, walk, cta, ctas);
 
   if (warp == W) {
-    // ------------------------------------------------------------ the list, and loads
+    // ------------------------------------------------------------ the list, and query rows
+    constexpr int kPer = D / 32;
     paged_walk_begin(p, ph, sm.scan, walk, cta, ctas);
     if (walk.g >= walk.hi && lane == 0)
       reinterpret_cast<PagedRec*>(ph.rec + cta * kPagedRecBytes)->split = 0;
     bool ok = true;
-    int c = 0;    // this lane's ring uses
-    int off = 0;  // the warp that the segment's first block goes to
     for (int m = 0; ok; ++m) {
       const PagedItem it = paged_next(p, ph, walk, cta);
-      const int is = m % Cfg::kItems;
+      const int is = m % Cfg::kItems, qb = m & 1, rows = it.ntok * p.G;
       if (m >= Cfg::kItems)
         ok = mbar_wait(&sm.item_empty[is], (m / Cfg::kItems - 1) & 1, p.status, abortf,
                        kSitePgItemEmpty);
@@ -174,40 +174,32 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
         mbar_arrive(&sm.item_full[is]);
       }
       if (it.end) break;
-      // Block i of the segment is warp (off + i) % W's.
-      const int n = item_blocks(it), h = it.h / subs;
-      const int* const list = p.page_table + (long long)it.b * p.max_pages;
-      auto page_of = [&](int i) { return i < n ? list[(it.key + 16 * i) >> p.page_shift] : 0; };
-      int i = lane < W ? (lane >= off ? lane - off : lane - off + W) : n;
-      int next = page_of(i);
-      while (__any_sync(0xffffffffu, i < n)) {
-        const int page = next;
-        next = page_of(i + W);
-        if (i < n) {
-          const int slot = c % S;
-          if (c >= S)
-            ok = mbar_wait(&sm.empty[lane][slot], (c / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
-          if (ok) {
-            if (page < 0 || page >= p.num_pages) {
-              int abort_flag = 0;
-              report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
-              mbar_arrive(&sm.full[lane][slot]);  // whatever the slot holds
-            } else {
-              const int key = it.key + 16 * i;
-              mbar_arrive_expect_tx(&sm.full[lane][slot], Block::kBytes);
-              bulk_load(sm.ring[lane][slot],
-                        p.pages + kv4_block_at(page, p.Hkv / subs, h, p.page_shift,
-                                               key & (p.page_size - 1), Block::kBytes),
-                        Block::kBytes, &sm.full[lane][slot]);
-            }
-            ++c;
+      if (!warp_bound_ok(it.tok0 >= 0 && rows <= R && it.tok0 + it.ntok <= p.T && it.h < p.Hkv,
+                         p.status, abortf, kChkPgItem))
+        break;
+      float x[R][kPer];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        uint32_t w[kPer / 2];
+#pragma unroll
+        for (int i = 0; i < kPer / 2; ++i) w[i] = 0u;
+        if (r < rows) {
+          const int tok = r / p.G;
+          const __nv_bfloat16* src = p.q + (it.tok0 + tok) * p.q_stride +
+                                     (long long)(it.h * p.G + r - tok * p.G) * D + lane * kPer;
+          if constexpr (kPer == 4) {
+            const uint2 u = *reinterpret_cast<const uint2*>(src);
+            w[0] = u.x, w[kPer / 2 - 1] = u.y;
+          } else {
+            w[0] = *reinterpret_cast<const uint32_t*>(src);
           }
         }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        i += W;
+#pragma unroll
+        for (int i = 0; i < kPer / 2; ++i) {
+          x[r][2 * i] = __uint_as_float(w[i] << 16);
+          x[r][2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
       }
-      off = (off + n) % W;
       // What the merge needs to know of the CTA's first unit.
       if (m == 0 && lane == 0) {
         PagedRec r = {};
@@ -223,53 +215,6 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
         *reinterpret_cast<PagedRec*>(ph.rec + cta * kPagedRecBytes) = r;
       }
       __syncwarp();
-    }
-    // After a failure: the copies on their way have to land before the CTA exits.
-    if (!ok && lane < W)
-      for (int k = c - 1; k >= 0 && k >= c - S; --k) drain_wait(&sm.full[lane][k % S], (k / S) & 1);
-    __syncwarp();
-    return;
-  }
-  if (warp == W + 1) {
-    // ------------------------------------------------------------ query rows
-    constexpr int kPer = D / 32;
-    bool ok = true;
-    for (int m = 0; ok; ++m) {
-      const int is = m % Cfg::kItems, qb = m & 1;
-      ok = mbar_wait(&sm.item_full[is], (m / Cfg::kItems) & 1, p.status, abortf, kSitePgItemFull);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      const int end = sm.item[is].end, rows = sm.item[is].ntok * p.G, tok0 = sm.item[is].tok0,
-                h = sm.item[is].h, pos0 = sm.item[is].pos0, len = sm.item[is].len;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.item_empty[is]);
-      if (end) break;
-      if (!warp_bound_ok(tok0 >= 0 && rows <= R && tok0 + rows / p.G <= p.T && h < p.Hkv, p.status,
-                         abortf, kChkPgItem))
-        break;
-      float x[R][kPer];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        uint32_t w[kPer / 2];
-#pragma unroll
-        for (int i = 0; i < kPer / 2; ++i) w[i] = 0u;
-        if (r < rows) {
-          const int tok = r / p.G;
-          const __nv_bfloat16* src = p.q + (tok0 + tok) * p.q_stride +
-                                     (long long)(h * p.G + r - tok * p.G) * D + lane * kPer;
-          if constexpr (kPer == 4) {
-            const uint2 u = *reinterpret_cast<const uint2*>(src);
-            w[0] = u.x, w[kPer / 2 - 1] = u.y;
-          } else {
-            w[0] = *reinterpret_cast<const uint32_t*>(src);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kPer / 2; ++i) {
-          x[r][2 * i] = __uint_as_float(w[i] << 16);
-          x[r][2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-      }
       if (m >= 2) ok = mbar_wait(&sm.q_empty[qb], (m / 2 - 1) & 1, p.status, abortf, kSitePgQEmpty);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -296,7 +241,7 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
         if (lane == 0) {
           sm.c2[qb][r] = r < rows ? p.scale_log2 * p.k_scale * __int_as_float((127 - e) << 23) : 0.f;
           int lim = 0;
-          if (r < rows) lim = p.causal ? max(0, min(pos0 + r / p.G + 1, len)) : len;
+          if (r < rows) lim = p.causal ? max(0, min(it.pos0 + r / p.G + 1, it.len)) : it.len;
           sm.lim[qb][r] = lim;
         }
       }
@@ -310,27 +255,80 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
   const int g = lane >> 2, t = lane & 3;
   const float ninf = __int_as_float(0xff800000);
   bool fail = false;
-  int c = 0, off = 0;  // ring uses; the warp of the segment's first block
-  for (int m = 0;; ++m) {
-    const int is = m % Cfg::kItems, qb = m & 1;
+  int off = 0;  // the warp of the segment's first step: step i is warp (off + i) % W's
+  int c = 0;    // steps this warp has had
+  int issued = 0;
+  // The current segment: this warp's steps, the first one's first key (the next
+  // one's is 16 U W further on), where their pages are listed, and the numbers
+  // of 32 blocks' pages in the lanes, with the next 32.
+  int end = 0, own = 0, key0 = 0, head = 0, rows = 0, tok0 = 0, head0 = 0, oslot = -1, min_lim = 0,
+      k_hi = 0, pg = 0, pg2 = 0;
+  const int* list = nullptr;
+  auto key_of = [&](int block) -> int {  // the first key of own block U j + b
+    return key0 + 16 * (block / U * (W * U) + block % U);
+  };
+  auto page_at = [&](int block) -> int {
+    const int key = key_of(block);
+    return block < own * U && key < k_hi ? list[key >> p.page_shift] : 0;
+  };
+  // Issues the loads of own step j (c0 steps went before the segment's), a lane
+  // to a block.
+  auto issue = [&](int j, int c0) {
+    const int first = j * U;
+    if (j > 0 && (first & 31) == 0) {
+      pg = pg2;
+      pg2 = page_at(first + 32 + lane);
+    }
+    const int page = __shfl_sync(0xffffffffu, pg, (first + lane) & 31), slot = (c0 + j) % S;
+    const int key = key_of(first + (lane & (U - 1)));
+    const bool on = lane < U && key < k_hi, valid = on && page >= 0 && page < p.num_pages;
+    const unsigned copies = __ballot_sync(0xffffffffu, valid);
+    if (lane == 0) mbar_arrive_expect_tx(&sm.full[warp][slot], __popc(copies) * Block::kBytes);
+    if (on && !valid) {  // (the step takes whatever the slot holds)
+      int abort_flag = 0;
+      report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
+    }
+    __syncwarp();
+    if (valid)
+      bulk_load(sm.ring[warp][slot] + lane * Block::kBytes,
+                p.pages + kv4_block_at(page, p.Hkv / subs, head, p.page_shift,
+                                       key & (p.page_size - 1), Block::kBytes),
+                Block::kBytes, &sm.full[warp][slot]);
+    __syncwarp();
+    ++issued;
+  };
+  // Takes segment m: its record, its pages, and the first loads.
+  auto take = [&](int m) {
+    const int is = m % Cfg::kItems;
     if (!fail)
       fail = !mbar_wait(&sm.item_full[is], (m / Cfg::kItems) & 1, p.status, abortf, kSitePgItemFull);
     fail = __any_sync(0xffffffffu, fail);
-    int end = 0, n = 0, key0 = 0, rows = 0, tok0 = 0, head0 = 0, oslot = -1, min_lim = 0, k_hi = 0;
-    if (!fail) {
-      const PagedItem& it = sm.item[is];
-      end = it.end;
-      n = item_blocks(it);
-      key0 = it.key;
-      rows = it.ntok * p.G;
-      tok0 = it.tok0;
-      head0 = it.h * p.G;
-      oslot = it.slot;
-      k_hi = it.k_hi;
-      min_lim = p.causal ? it.pos0 + 1 : it.len;
-    }
+    end = own = 0;
+    if (fail) return;
+    const PagedItem& it = sm.item[is];
+    end = it.end;
+    const int n = end ? 0 : (item_keys(it) + 16 * U - 1) / (16 * U);
+    const int i0 = warp >= off ? warp - off : warp - off + W;
+    own = i0 < n ? (n - i0 + W - 1) / W : 0;
+    off = (off + n) % W;
+    key0 = it.key + 16 * U * i0;
+    head = it.h / subs;
+    rows = it.ntok * p.G;
+    tok0 = it.tok0;
+    head0 = it.h * p.G;
+    oslot = it.slot;
+    k_hi = it.key + item_keys(it);
+    min_lim = p.causal ? it.pos0 + 1 : it.len;
+    list = p.page_table + (long long)it.b * p.max_pages;
     __syncwarp();
-    if (!fail && lane == 0) mbar_arrive(&sm.item_empty[is]);
+    if (lane == 0) mbar_arrive(&sm.item_empty[is]);
+    pg = page_at(lane);
+    pg2 = page_at(lane + 32);
+    for (int j = 0; j < S && j < own; ++j) issue(j, c);
+  };
+  take(0);
+  for (int m = 0;; ++m) {
+    const int qb = m & 1;
     float ref[NT][2], l[NT][2], c2[NT][2], o[D / 16][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -342,8 +340,6 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
-    const int i0 = warp >= off ? warp - off : warp - off + W;
-    off = (off + n) % W;
     if (!fail && !end) {
       fail = !mbar_wait(&sm.q_full[qb], (m / 2) & 1, p.status, abortf, kSitePgQFull);
       fail = __any_sync(0xffffffffu, fail);
@@ -360,96 +356,114 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
 #pragma unroll
         for (int e = 0; e < 2; ++e) c2[nt][e] = sm.c2[qb][nt * 8 + 2 * t + e];
       }
-      for (int i = i0; i < n && !fail; i += W, ++c) {
-        const int slot = c % S, key = key0 + 16 * i;
+      const int c0 = c;
+      for (int j = 0; j < own && !fail; ++j, ++c) {
+        const int slot = c % S, key = key0 + 16 * U * W * j;
         fail = !mbar_wait(&sm.full[warp][slot], (c / S) & 1, p.status, abortf, kSitePgKvFull);
         fail = __any_sync(0xffffffffu, fail);
         if (fail) break;
-        const uint8_t* const blk = sm.ring[warp][slot];
         constexpr int kWords = D / 32;  // of four bytes: a key's, or a value pair's, of this lane
-        uint32_t kw[2][kWords], vw[2][kWords], ks[2], vs[2];
+        uint32_t kw[U][2][kWords], vw[U][2][kWords], ks[U][2], vs[U][2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if constexpr (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(blk + Block::k_code(0) + (u * 32 + lane) * 16);
-            const uint4 y = *reinterpret_cast<const uint4*>(blk + Block::v_code(0, 0) + (u * 32 + lane) * 16);
-            kw[u][0] = x.x, kw[u][1] = x.y, kw[u][kWords - 2] = x.z, kw[u][kWords - 1] = x.w;
-            vw[u][0] = y.x, vw[u][1] = y.y, vw[u][kWords - 2] = y.z, vw[u][kWords - 1] = y.w;
-            ks[u] = *reinterpret_cast<const uint16_t*>(blk + Block::k_scale(0) + (u * 32 + lane) * 2);
-            vs[u] = *reinterpret_cast<const uint16_t*>(blk + Block::v_scale(g) + u * 8 + 2 * t);
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(blk + Block::k_code(0) + (u * 32 + lane) * 8);
-            const uint2 y = *reinterpret_cast<const uint2*>(blk + Block::v_code(0, 0) + (u * 32 + lane) * 8);
-            kw[u][0] = x.x, kw[u][1] = x.y;
-            vw[u][0] = y.x, vw[u][1] = y.y;
-            ks[u] = blk[Block::k_scale(0) + u * 32 + lane];
-            vs[u] = *reinterpret_cast<const uint16_t*>(blk + Block::v_scale(g / 2) + u * 8 + 2 * t);
+        for (int b = 0; b < U; ++b) {
+          const uint8_t* const blk = sm.ring[warp][slot] + b * Block::kBytes;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if constexpr (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4*>(blk + Block::k_code(0) + (u * 32 + lane) * 16);
+              const uint4 y = *reinterpret_cast<const uint4*>(blk + Block::v_code(0, 0) + (u * 32 + lane) * 16);
+              kw[b][u][0] = x.x, kw[b][u][1] = x.y, kw[b][u][kWords - 2] = x.z, kw[b][u][kWords - 1] = x.w;
+              vw[b][u][0] = y.x, vw[b][u][1] = y.y, vw[b][u][kWords - 2] = y.z, vw[b][u][kWords - 1] = y.w;
+              ks[b][u] = *reinterpret_cast<const uint16_t*>(blk + Block::k_scale(0) + (u * 32 + lane) * 2);
+              vs[b][u] = *reinterpret_cast<const uint16_t*>(blk + Block::v_scale(g) + u * 8 + 2 * t);
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(blk + Block::k_code(0) + (u * 32 + lane) * 8);
+              const uint2 y = *reinterpret_cast<const uint2*>(blk + Block::v_code(0, 0) + (u * 32 + lane) * 8);
+              kw[b][u][0] = x.x, kw[b][u][1] = x.y;
+              vw[b][u][0] = y.x, vw[b][u][1] = y.y;
+              ks[b][u] = blk[Block::k_scale(0) + u * 32 + lane];
+              vs[b][u] = *reinterpret_cast<const uint16_t*>(blk + Block::v_scale(g / 2) + u * 8 + 2 * t);
+            }
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.empty[warp][slot]);
-        float s[NT][4];
+        if (j + S < own) issue(j + S, c0);  // (this slot is free again)
+        float s[U][NT][4];
+        uint32_t sc[U][2][2];  // of keys g, g + 8: the scales of the lane's one or two groups
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int b = 0; b < U; ++b) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-        {
-          uint32_t sc[2][2];  // of keys g, g + 8: the scales of the lane's one or two groups
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[b][nt][e] = 0.f;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const uint32_t x = e4m3_to_half(ks[u]);
-            sc[u][0] = __byte_perm(x, x, 0x1010);
-            sc[u][1] = D == 128 ? __byte_perm(x, x, 0x3232) : sc[u][0];
+            const uint32_t x = e4m3_to_half(ks[b][u]);
+            sc[b][u][0] = __byte_perm(x, x, 0x1010);
+            sc[b][u][1] = D == 128 ? __byte_perm(x, x, 0x3232) : sc[b][u][0];
           }
+        }
 #pragma unroll
-          for (int w = 0; w < kWords; ++w) {
+        for (int w = 0; w < kWords; ++w)
+#pragma unroll
+          for (int b = 0; b < U; ++b) {
             uint32_t a[2][4];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              e2m1_to_half(kw[u][w], a[u]);
+              e2m1_to_half(kw[b][u][w], a[u]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) a[u][e] = half2_mul(a[u][e], sc[u][2 * w / kWords]);
+              for (int e = 0; e < 4; ++e) a[u][e] = half2_mul(a[u][e], sc[b][u][2 * w / kWords]);
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const uint32_t f[4] = {a[0][2 * k], a[1][2 * k], a[0][2 * k + 1], a[1][2 * k + 1]};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_16816(s[nt], f, q[nt][2 * w + k][0], q[nt][2 * w + k][1]);
+              for (int nt = 0; nt < NT; ++nt)
+                mma_16816(s[b][nt], f, q[nt][2 * w + k][0], q[nt][2 * w + k][1]);
             }
           }
-        }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[nt][e] *= c2[nt][e & 1];
-        if (key + 16 > min_lim) {
+        for (int b = 0; b < U; ++b)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (key + g + (e >> 1) * 8 >= sm.lim[qb][nt * 8 + 2 * t + (e & 1)]) s[nt][e] = ninf;
-          if (key + 16 > k_hi) {
-            // Slots past the unit's keys may hold anything, and 0 * NaN is NaN.
+            for (int e = 0; e < 4; ++e) s[b][nt][e] *= c2[nt][e & 1];
+        if (key + 16 * U > min_lim || key + 16 * U > k_hi) {
+#pragma unroll
+          for (int b = 0; b < U; ++b)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int at = key + 16 * b + g + (e >> 1) * 8;
+                if (at >= k_hi || at >= sm.lim[qb][nt * 8 + 2 * t + (e & 1)]) s[b][nt][e] = ninf;
+              }
+          // Slots past the segment's keys may hold anything, and 0 * NaN is NaN.
+#pragma unroll
+          for (int b = 0; b < U; ++b)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              const int first = key + u * 8 + 2 * t;
-              if (first >= k_hi) vs[u] = 0u;
-              if (first + 1 >= k_hi) vs[u] &= 0xffu;
+              const int first = key + 16 * b + u * 8 + 2 * t;
+              if (first >= k_hi) vs[b][u] = 0u;
+              if (first + 1 >= k_hi) vs[b][u] &= 0xffu;
             }
-          }
         }
         float over = ninf;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int b = 0; b < U; ++b)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) over = fmaxf(over, s[nt][e] - ref[nt][e & 1]);
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) over = fmaxf(over, s[b][nt][e] - ref[nt][e & 1]);
         if (__any_sync(0xffffffffu, over > kRescaleSlack)) {
           // Some score outgrew the reference: every row's moves to its maximum.
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float top = fmaxf(fmaxf(s[nt][e], s[nt][e + 2]), ref[nt][e]);
+              float top = ref[nt][e];
+#pragma unroll
+              for (int b = 0; b < U; ++b) top = fmaxf(top, fmaxf(s[b][nt][e], s[b][nt][e + 2]));
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
               const float alpha = ex2_approx(ref[nt][e] - top);
@@ -459,42 +473,51 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
               for (int mt = 0; mt < D / 16; ++mt) o[mt][nt][e] *= alpha, o[mt][nt][e + 2] *= alpha;
             }
         }
-        uint32_t pt[NT][2];
+        uint32_t pt[U][NT][2], v[U][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float x[4];
+        for (int b = 0; b < U; ++b) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[e] = ex2_approx(s[nt][e] - ref[nt][e & 1]);
-            l[nt][e & 1] += x[e];
+          for (int nt = 0; nt < NT; ++nt) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[e] = ex2_approx(s[b][nt][e] - ref[nt][e & 1]);
+              l[nt][e & 1] += x[e];
+            }
+            pt[b][nt][0] = transpose_8x8(pack_half2(x[0], x[1]));
+            pt[b][nt][1] = transpose_8x8(pack_half2(x[2], x[3]));
           }
-          pt[nt][0] = transpose_8x8(pack_half2(x[0], x[1]));
-          pt[nt][1] = transpose_8x8(pack_half2(x[2], x[3]));
+          v[b][0] = e4m3_to_half(vs[b][0]);
+          v[b][1] = e4m3_to_half(vs[b][1]);
         }
-        const uint32_t v0 = e4m3_to_half(vs[0]), v1 = e4m3_to_half(vs[1]);
 #pragma unroll
-        for (int w = 0; w < kWords; ++w) {
-          uint32_t a[2][4];
-          e2m1_to_half(vw[0][w], a[0]);
-          e2m1_to_half(vw[1][w], a[1]);
+        for (int w = 0; w < kWords; ++w)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            a[0][e] = half2_mul(a[0][e], v0);
-            a[1][e] = half2_mul(a[1][e], v1);
+          for (int b = 0; b < U; ++b) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              e2m1_to_half(vw[b][u][w], a[u]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) a[u][e] = half2_mul(a[u][e], v[b][u]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t f[4] = {a[0][2 * k], a[0][2 * k + 1], a[1][2 * k], a[1][2 * k + 1]};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_16816(o[2 * w + k][nt], f, pt[b][nt][0], pt[b][nt][1]);
+            }
           }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t f[4] = {a[0][2 * k], a[0][2 * k + 1], a[1][2 * k], a[1][2 * k + 1]};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_16816(o[2 * w + k][nt], f, pt[nt][0], pt[nt][1]);
-          }
-        }
       }
       if (lane == 0 && !fail) mbar_arrive(&sm.q_empty[qb]);
     }
     // ------------------------------------------------------ the unit's result
+    // The next segment's first loads, before the warps wait for one another.
     // (Every warp comes to both votes, whatever failed, and all leave together.)
-    if (named_vote(1, 32 * W, fail) || end) break;
+    const int was_end = end, n_own = own, r_rows = rows, r_tok0 = tok0, r_head0 = head0,
+              r_slot = oslot;
+    if (!was_end) take(m + 1);
+    if (named_vote(1, 32 * W, fail) || was_end) break;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -506,7 +529,7 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
           sm.part_m[warp][r] = ref[nt][e];
           sm.part_l[warp][r] = l[nt][e];
         }
-        if (i0 < n) {
+        if (n_own > 0) {
           // Channels g d/8 .. of the row: o[mt] holds 2 mt (its first half) and 2 mt + 1.
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
@@ -518,7 +541,7 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
         }
       }
     named_bar_sync(1, 32 * W);
-    for (int x = tid; x < rows * (D / 2); x += 32 * W) {  // a row to a warp (or half of one)
+    for (int x = tid; x < r_rows * (D / 2); x += 32 * W) {  // a row to a warp (or half of one)
       const int r = x / (D / 2), ch = x % (D / 2) * 2;
       float pm = kNoRef4, pl = 0.f;
       if (lane < W) pm = sm.part_m[lane][r], pl = sm.part_l[lane][r];
@@ -542,9 +565,9 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
       const float own = sum == 0.f ? 0.f : p.v_scale / sum;
       const float lse2 = sum == 0.f ? ninf : top + log2f(sum);
       const int tok = r / p.G;
-      const long long at = (long long)(tok0 + tok) * p.Hq + head0 + (r - tok * p.G);
-      if (oslot >= 0) {
-        const long long row = ((long long)cta * 2 + oslot) * ph.slot_rows + r;
+      const long long at = (long long)(r_tok0 + tok) * p.Hq + r_head0 + (r - tok * p.G);
+      if (r_slot >= 0) {
+        const long long row = ((long long)cta * 2 + r_slot) * ph.slot_rows + r;
         *reinterpret_cast<float2*>(ph.slot_o + row * D + ch) = make_float2(acc.x * own, acc.y * own);
         if (ch == 0) ph.slot_lse[row] = lse2;
       } else {
@@ -553,6 +576,8 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
       }
     }
   }
+  // After a failure: the copies on their way have to land before the CTA exits.
+  for (; c < issued; ++c) drain_wait(&sm.full[warp][c % S], (c / S) & 1);
 }
 
 }  // namespace fa
