@@ -380,6 +380,7 @@ int launch_fwd_paged4(const Paged4Params& p, int d, cudaStream_t stream);
 // tokens go to the decode kernel, in units of `rows` (8 or 16) query rows of one
 // key/value head; where a token has more, its heads are dealt in `subs` equal
 // runs.  The others go to the prompt kernel.
+constexpr int kPaged4CtasPerSm = 3;    // of the decode kernel
 constexpr int kPaged4DecodeMost = 64;  // query rows of a sequence and key/value head
 struct Paged4Form {
   int heads, subs;   // query heads of a decode unit's token; runs of a token's heads
@@ -415,8 +416,9 @@ inline Paged4Workspace paged4_workspace_layout(int d, const Paged4Form& f) {
     return here;
   };
   for (int k = 0; k < 2; ++k) {
-    const size_t slots = (size_t)kPagedMaxCtas * 2 * (size_t)rows[k];
-    w.rec[k] = take(rows[k] > 0 ? kPagedMaxCtas * kPagedRecBytes : 0);
+    const size_t ctas = (size_t)kPagedMaxCtas * (k == 0 ? kPaged4CtasPerSm : 1);
+    const size_t slots = ctas * 2 * (size_t)rows[k];
+    w.rec[k] = take(rows[k] > 0 ? ctas * kPagedRecBytes : 0);
     w.slot_o[k] = take(slots * (size_t)d * sizeof(float));
     w.slot_lse[k] = take(slots * sizeof(float));
   }

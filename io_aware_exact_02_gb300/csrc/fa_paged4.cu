@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(32 * kWarps) fa_paged4_rows_kernel(const Paged
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(Decode4Cfg<D, R>::kThreads, 1)
+__global__ void __launch_bounds__(Decode4Cfg<D, R>::kThreads, Decode4Cfg<D, R>::kCtas)
     fa_paged4_decode_kernel(const Paged4Params p, const PagedPhase ph, int subs) {
   extern __shared__ uint8_t smem_raw[];
   decode4_cta<D, R>(p, ph, subs, blockIdx.x, gridDim.x, smem_raw);
@@ -126,8 +126,8 @@ __global__ void __launch_bounds__(Decode4Cfg<D, R>::kThreads, 1)
 template <int D, int R>
 int launch_decode(const Paged4Params& p, const PagedPhase& ph, int subs,
                   const cudaLaunchConfig_t& base) {
-  static_assert(sizeof(Decode4Smem<D, R>) + 128 <= 232448,
-                "shared memory above the 227 KB a CTA may have");
+  static_assert((sizeof(Decode4Smem<D, R>) + 128 + 1024) * Decode4Cfg<D, R>::kCtas <= 233472,
+                "shared memory above the 228 KB of an SM, of which a CTA takes 1 KB more");
   cudaLaunchConfig_t c = base;
   c.blockDim = dim3(Decode4Cfg<D, R>::kThreads, 1, 1);
   c.dynamicSmemBytes = sizeof(Decode4Smem<D, R>) + 128;
@@ -166,6 +166,8 @@ int launch_paged4_d(const Paged4Params& p, cudaStream_t stream) {
     Paged4Params q = p;  // its heads are runs of a token's
     q.G = f.heads;
     q.Hkv = p.Hkv * f.subs;
+    q.ctas = p.ctas * kPaged4CtasPerSm;
+    c.gridDim.x = (unsigned)q.ctas;
     PagedPhase ph = {};
     ph.rec = p.workspace + w.rec[0];
     ph.slot_o = at(w.slot_o[0]);

@@ -38,10 +38,6 @@
 
 namespace fa {
 
-// A row's reference maximum before it has seen a key (finite: the exponent of a
-// masked score is -inf and not NaN).
-constexpr float kNoRef4 = -3.0e38f;
-
 // 16-byte aligned bytes (a multiple of 16) to shared memory, completing `bar`'s
 // transaction count.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -90,13 +86,11 @@ __device__ __forceinline__ bool named_vote(int id, int threads, bool x) {
 template <int D, int R>
 struct Decode4Cfg {
   static constexpr int kTiles = R / 8;
-  // With the twelfth, 168 registers a thread: enough for a step of two blocks (the
-  // latencies of one hide behind the other's), but for d = 128 with 16 rows,
-  // whose O alone takes 64.
-  static constexpr int kWarps = 11;  // that compute
+  static constexpr int kCtas = kPaged4CtasPerSm;  // of an SM
+  static constexpr int kWarps = R == 8 ? 4 : 3;  // that compute
   static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kUnit = D == 128 && R == 16 ? 1 : 2;  // blocks of a step
-  static constexpr int kStages = D == 128 ? (R == 16 ? 4 : 3) : 6;  // steps in a warp's ring
+  static constexpr int kUnit = 2;  // blocks of a step: the latencies of one hide behind the other's
+  static constexpr int kStages = D == 128 ? 2 : 4;  // steps in a warp's ring
   static constexpr int kItems = 4;
 };
 
@@ -106,7 +100,7 @@ struct alignas(128) Decode4Smem {
   static constexpr int W = Cfg::kWarps;
   uint8_t ring[W][Cfg::kStages][Cfg::kUnit * Kv4Block<D>::kBytes];
   float part_o[W][R][D];  // 16-byte chunk c of row r at c ^ (r / 2 % 4)
-  __half q[2][R][D];
+  uint4 q[2][R / 8 * (D / 32)][32];  // [8 rows, 8 of a lane's channels][lane of the product]
   float part_m[W][R], part_l[W][R];
   float c2[2][R];         // a row's factor from products to exponents
   int lim[2][R];          // the keys that a row sees end here
@@ -156,7 +150,6 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
 
   if (warp == W) {
     // ------------------------------------------------------------ the list, and query rows
-    constexpr int kPer = D / 32;
     paged_walk_begin(p, ph, sm.scan, walk, cta, ctas);
     if (walk.g >= walk.hi && lane == 0)
       reinterpret_cast<PagedRec*>(ph.rec + cta * kPagedRecBytes)->split = 0;
@@ -177,28 +170,18 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
       if (!warp_bound_ok(it.tok0 >= 0 && rows <= R && it.tok0 + it.ntok <= p.T && it.h < p.Hkv,
                          p.status, abortf, kChkPgItem))
         break;
-      float x[R][kPer];
+      // Lane (g, t) has channels t d/4 .. of row g of each eight, as the product
+      // takes them.
+      const int g = lane >> 2, t = lane & 3;
+      uint4 x[NT][D / 32];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        uint32_t w[kPer / 2];
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = nt * 8 + g, tok = r / p.G;
+        const __nv_bfloat16* src = p.q + (it.tok0 + tok) * p.q_stride +
+                                   (long long)(it.h * p.G + r - tok * p.G) * D + t * (D / 4);
 #pragma unroll
-        for (int i = 0; i < kPer / 2; ++i) w[i] = 0u;
-        if (r < rows) {
-          const int tok = r / p.G;
-          const __nv_bfloat16* src = p.q + (it.tok0 + tok) * p.q_stride +
-                                     (long long)(it.h * p.G + r - tok * p.G) * D + lane * kPer;
-          if constexpr (kPer == 4) {
-            const uint2 u = *reinterpret_cast<const uint2*>(src);
-            w[0] = u.x, w[kPer / 2 - 1] = u.y;
-          } else {
-            w[0] = *reinterpret_cast<const uint32_t*>(src);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kPer / 2; ++i) {
-          x[r][2 * i] = __uint_as_float(w[i] << 16);
-          x[r][2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        for (int i = 0; i < D / 32; ++i)
+          x[nt][i] = r < rows ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0u, 0u, 0u, 0u);
       }
       // What the merge needs to know of the CTA's first unit.
       if (m == 0 && lane == 0) {
@@ -219,26 +202,30 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float top = 0.f;
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = nt * 8 + g;
+        uint32_t w[D / 8];  // pairs of channels
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) top = fmaxf(top, fabsf(x[r][i]));
+        for (int i = 0; i < D / 32; ++i)
+          w[4 * i] = x[nt][i].x, w[4 * i + 1] = x[nt][i].y, w[4 * i + 2] = x[nt][i].z, w[4 * i + 3] = x[nt][i].w;
+        // The largest magnitude: bf16 numbers compare as the integers they are.
+        uint32_t top = 0u;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // The largest to [2^14, 2^15): exponents are exact, and what falls below
+        for (int i = 0; i < D / 8; ++i) top = max(top, max(w[i] << 16 & 0x7fffffffu, w[i] & 0x7fff0000u));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // It goes to [2^14, 2^15): exponents are exact, and what falls below
         // fp16's range is 2^-38 of it.  (Zeros, infinities and NaN stay.)
         int e = 0;
-        if (top > 0.f && top < __int_as_float(0x7f800000))
-          e = min(14 - ((__float_as_int(top) >> 23) - 127), 100);
+        if (top > 0u && top < 0x7f800000u) e = min(14 - ((int)(top >> 23) - 127), 100);
         const float f = __int_as_float((e + 127) << 23);
-        uint32_t w[kPer / 2];
 #pragma unroll
-        for (int i = 0; i < kPer / 2; ++i) w[i] = pack_half2(x[r][2 * i] * f, x[r][2 * i + 1] * f);
-        if constexpr (kPer == 4)
-          *reinterpret_cast<uint2*>(&sm.q[qb][r][lane * kPer]) = make_uint2(w[0], w[kPer / 2 - 1]);
-        else
-          *reinterpret_cast<uint32_t*>(&sm.q[qb][r][lane * kPer]) = w[0];
-        if (lane == 0) {
+        for (int i = 0; i < D / 8; ++i)
+          w[i] = pack_half2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+          sm.q[qb][nt * (D / 32) + i][lane] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        if (t == 0) {
           sm.c2[qb][r] = r < rows ? p.scale_log2 * p.k_scale * __int_as_float((127 - e) << 23) : 0.f;
           int lim = 0;
           if (r < rows) lim = p.causal ? max(0, min(it.pos0 + r / p.G + 1, it.len)) : it.len;
@@ -262,14 +249,17 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
   // one's is 16 U W further on), where their pages are listed, and the numbers
   // of 32 blocks' pages in the lanes, with the next 32.
   int end = 0, own = 0, key0 = 0, head = 0, rows = 0, tok0 = 0, head0 = 0, oslot = -1, min_lim = 0,
-      k_hi = 0, pg = 0, pg2 = 0;
-  const int* list = nullptr;
+      k_hi = 0, seq = 0, pg = 0, pg2 = 0;
+  int ahead = 0, ahead2 = 0;  // the next segment's pages, if it was looked at
+  bool looked = false;
   auto key_of = [&](int block) -> int {  // the first key of own block U j + b
     return key0 + 16 * (block / U * (W * U) + block % U);
   };
   auto page_at = [&](int block) -> int {
     const int key = key_of(block);
-    return block < own * U && key < k_hi ? list[key >> p.page_shift] : 0;
+    return block < own * U && key < k_hi
+               ? p.page_table[(long long)seq * p.max_pages + (key >> p.page_shift)]
+               : 0;
   };
   // Issues the loads of own step j (c0 steps went before the segment's), a lane
   // to a block.
@@ -297,33 +287,55 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
     __syncwarp();
     ++issued;
   };
+  // The warp's part of a segment: how many steps, and the first one's first key.
+  auto part = [&](const PagedItem& it, int& first_key) -> int {
+    const int n = it.end ? 0 : (item_keys(it) + 16 * U - 1) / (16 * U);
+    const int i0 = warp >= off ? warp - off : warp - off + W;
+    first_key = it.key + 16 * U * i0;
+    return i0 < n ? (n - i0 + W - 1) / W : 0;
+  };
+  // Asks for the pages of segment m, if it is known by now.
+  auto look = [&](int m) {
+    const int is = m % Cfg::kItems;
+    looked = __all_sync(0xffffffffu, mbar_test_wait(&sm.item_full[is], (m / Cfg::kItems) & 1));
+    if (!looked) return;
+    const PagedItem& it = sm.item[is];
+    int first_key;
+    const int steps = part(it, first_key), hi = it.key + item_keys(it);
+    const int* const list = p.page_table + (long long)it.b * p.max_pages;
+    auto at = [&](int block) -> int {
+      const int key = first_key + 16 * (block / U * (W * U) + block % U);
+      return block < steps * U && key < hi ? list[key >> p.page_shift] : 0;
+    };
+    ahead = at(lane);
+    ahead2 = at(lane + 32);
+  };
   // Takes segment m: its record, its pages, and the first loads.
   auto take = [&](int m) {
     const int is = m % Cfg::kItems;
-    if (!fail)
+    if (!fail && !looked)
       fail = !mbar_wait(&sm.item_full[is], (m / Cfg::kItems) & 1, p.status, abortf, kSitePgItemFull);
     fail = __any_sync(0xffffffffu, fail);
     end = own = 0;
     if (fail) return;
+    if (!looked) look(m);
     const PagedItem& it = sm.item[is];
     end = it.end;
-    const int n = end ? 0 : (item_keys(it) + 16 * U - 1) / (16 * U);
-    const int i0 = warp >= off ? warp - off : warp - off + W;
-    own = i0 < n ? (n - i0 + W - 1) / W : 0;
-    off = (off + n) % W;
-    key0 = it.key + 16 * U * i0;
+    own = part(it, key0);
+    off = end ? off : (off + (item_keys(it) + 16 * U - 1) / (16 * U)) % W;
     head = it.h / subs;
     rows = it.ntok * p.G;
     tok0 = it.tok0;
     head0 = it.h * p.G;
     oslot = it.slot;
+    seq = it.b;
     k_hi = it.key + item_keys(it);
     min_lim = p.causal ? it.pos0 + 1 : it.len;
-    list = p.page_table + (long long)it.b * p.max_pages;
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.item_empty[is]);
-    pg = page_at(lane);
-    pg2 = page_at(lane + 32);
+    pg = ahead;
+    pg2 = ahead2;
+    looked = false;
     for (int j = 0; j < S && j < own; ++j) issue(j, c);
   };
   take(0);
@@ -333,7 +345,7 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) ref[nt][e] = kNoRef4, l[nt][e] = 0.f;
+      for (int e = 0; e < 2; ++e) ref[nt][e] = 0.f, l[nt][e] = 0.f;
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
@@ -343,19 +355,10 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
     if (!fail && !end) {
       fail = !mbar_wait(&sm.q_full[qb], (m / 2) & 1, p.status, abortf, kSitePgQFull);
       fail = __any_sync(0xffffffffu, fail);
-      uint32_t q[NT][D / 16][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint4* src = reinterpret_cast<const uint4*>(&sm.q[qb][nt * 8 + g][t * (D / 4)]);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const uint4 x = src[i];
-          q[nt][2 * i][0] = x.x, q[nt][2 * i][1] = x.y;
-          q[nt][2 * i + 1][0] = x.z, q[nt][2 * i + 1][1] = x.w;
-        }
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) c2[nt][e] = sm.c2[qb][nt * 8 + 2 * t + e];
-      }
       const int c0 = c;
       for (int j = 0; j < own && !fail; ++j, ++c) {
         const int slot = c % S, key = key0 + 16 * U * W * j;
@@ -363,31 +366,28 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
         fail = __any_sync(0xffffffffu, fail);
         if (fail) break;
         constexpr int kWords = D / 32;  // of four bytes: a key's, or a value pair's, of this lane
-        uint32_t kw[U][2][kWords], vw[U][2][kWords], ks[U][2], vs[U][2];
+        const uint8_t* const blk = sm.ring[warp][slot];
+        // A lane's 16 (d = 64: 8) bytes of the u-th 32 of a block's codes.
+        auto words = [&](const uint8_t* codes, int u, uint32_t (&w)[kWords]) {
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(codes + (u * 32 + lane) * 16);
+            w[0] = x.x, w[1] = x.y, w[kWords - 2] = x.z, w[kWords - 1] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(codes + (u * 32 + lane) * 8);
+            w[0] = x.x, w[1] = x.y;
+          }
+        };
+        uint32_t kw[U][2][kWords], ks[U][2];
 #pragma unroll
-        for (int b = 0; b < U; ++b) {
-          const uint8_t* const blk = sm.ring[warp][slot] + b * Block::kBytes;
+        for (int b = 0; b < U; ++b)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            if constexpr (D == 128) {
-              const uint4 x = *reinterpret_cast<const uint4*>(blk + Block::k_code(0) + (u * 32 + lane) * 16);
-              const uint4 y = *reinterpret_cast<const uint4*>(blk + Block::v_code(0, 0) + (u * 32 + lane) * 16);
-              kw[b][u][0] = x.x, kw[b][u][1] = x.y, kw[b][u][kWords - 2] = x.z, kw[b][u][kWords - 1] = x.w;
-              vw[b][u][0] = y.x, vw[b][u][1] = y.y, vw[b][u][kWords - 2] = y.z, vw[b][u][kWords - 1] = y.w;
-              ks[b][u] = *reinterpret_cast<const uint16_t*>(blk + Block::k_scale(0) + (u * 32 + lane) * 2);
-              vs[b][u] = *reinterpret_cast<const uint16_t*>(blk + Block::v_scale(g) + u * 8 + 2 * t);
-            } else {
-              const uint2 x = *reinterpret_cast<const uint2*>(blk + Block::k_code(0) + (u * 32 + lane) * 8);
-              const uint2 y = *reinterpret_cast<const uint2*>(blk + Block::v_code(0, 0) + (u * 32 + lane) * 8);
-              kw[b][u][0] = x.x, kw[b][u][1] = x.y;
-              vw[b][u][0] = y.x, vw[b][u][1] = y.y;
-              ks[b][u] = blk[Block::k_scale(0) + u * 32 + lane];
-              vs[b][u] = *reinterpret_cast<const uint16_t*>(blk + Block::v_scale(g / 2) + u * 8 + 2 * t);
-            }
+            words(blk + b * Block::kBytes + Block::k_code(0), u, kw[b][u]);
+            const uint8_t* const sc = blk + b * Block::kBytes + Block::k_scale(0);
+            ks[b][u] = D == 128 ? *reinterpret_cast<const uint16_t*>(sc + (u * 32 + lane) * 2)
+                                : sc[u * 32 + lane];
           }
-        }
-        __syncwarp();
-        if (j + S < own) issue(j + S, c0);  // (this slot is free again)
+        if (!looked) look(m + 1);
         float s[U][NT][4];
         uint32_t sc[U][2][2];  // of keys g, g + 8: the scales of the lane's one or two groups
 #pragma unroll
@@ -404,7 +404,10 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
           }
         }
 #pragma unroll
-        for (int w = 0; w < kWords; ++w)
+        for (int w = 0; w < kWords; ++w) {
+          uint4 q[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) q[nt] = sm.q[qb][nt * kWords + w][lane];
 #pragma unroll
           for (int b = 0; b < U; ++b) {
             uint32_t a[2][4];
@@ -419,15 +422,17 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
               const uint32_t f[4] = {a[0][2 * k], a[1][2 * k], a[0][2 * k + 1], a[1][2 * k + 1]};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma_16816(s[b][nt], f, q[nt][2 * w + k][0], q[nt][2 * w + k][1]);
+                mma_16816(s[b][nt], f, k == 0 ? q[nt].x : q[nt].z, k == 0 ? q[nt].y : q[nt].w);
             }
           }
+        }
+        // Exponents, less the reference.
 #pragma unroll
         for (int b = 0; b < U; ++b)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[b][nt][e] *= c2[nt][e & 1];
+            for (int e = 0; e < 4; ++e) s[b][nt][e] = fmaf(s[b][nt][e], c2[nt][e & 1], -ref[nt][e & 1]);
         if (key + 16 * U > min_lim || key + 16 * U > k_hi) {
 #pragma unroll
           for (int b = 0; b < U; ++b)
@@ -438,6 +443,49 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
                 const int at = key + 16 * b + g + (e >> 1) * 8;
                 if (at >= k_hi || at >= sm.lim[qb][nt * 8 + 2 * t + (e & 1)]) s[b][nt][e] = ninf;
               }
+        }
+        float over = ninf;
+#pragma unroll
+        for (int b = 0; b < U; ++b)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) over = fmax3(over, s[b][nt][e], s[b][nt][e + 1]);
+        if (j == 0 || __any_sync(0xffffffffu, over > kRescaleSlack)) {
+          // The first scores, or some that outgrew the reference: every row's
+          // moves to its maximum.  (A row that the first step's keys, the lowest,
+          // are hidden from sees none of the later ones.)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float up = j == 0 ? ninf : 0.f;
+#pragma unroll
+              for (int b = 0; b < U; ++b) up = fmax3(up, s[b][nt][e], s[b][nt][e + 2]);
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, x));
+              if (up == ninf) up = 0.f;
+              const float alpha = j == 0 ? 1.f : ex2_approx(-up);
+              ref[nt][e] += up;
+              l[nt][e] *= alpha;
+#pragma unroll
+              for (int b = 0; b < U; ++b) s[b][nt][e] -= up, s[b][nt][e + 2] -= up;
+#pragma unroll
+              for (int mt = 0; mt < D / 16; ++mt) o[mt][nt][e] *= alpha, o[mt][nt][e + 2] *= alpha;
+            }
+        }
+        uint32_t vw[U][2][kWords], vs[U][2];
+#pragma unroll
+        for (int b = 0; b < U; ++b)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            words(blk + b * Block::kBytes + Block::v_code(0, 0), u, vw[b][u]);
+            vs[b][u] = *reinterpret_cast<const uint16_t*>(
+                blk + b * Block::kBytes + Block::v_scale(D == 128 ? g : g / 2) + u * 8 + 2 * t);
+          }
+        __syncwarp();
+        if (j + S < own) issue(j + S, c0);  // (this slot is free again)
+        if (key + 16 * U > k_hi) {
           // Slots past the segment's keys may hold anything, and 0 * NaN is NaN.
 #pragma unroll
           for (int b = 0; b < U; ++b)
@@ -448,31 +496,6 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
               if (first + 1 >= k_hi) vs[b][u] &= 0xffu;
             }
         }
-        float over = ninf;
-#pragma unroll
-        for (int b = 0; b < U; ++b)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) over = fmaxf(over, s[b][nt][e] - ref[nt][e & 1]);
-        if (__any_sync(0xffffffffu, over > kRescaleSlack)) {
-          // Some score outgrew the reference: every row's moves to its maximum.
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float top = ref[nt][e];
-#pragma unroll
-              for (int b = 0; b < U; ++b) top = fmaxf(top, fmaxf(s[b][nt][e], s[b][nt][e + 2]));
-#pragma unroll
-              for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-              const float alpha = ex2_approx(ref[nt][e] - top);
-              ref[nt][e] = top;
-              l[nt][e] *= alpha;
-#pragma unroll
-              for (int mt = 0; mt < D / 16; ++mt) o[mt][nt][e] *= alpha, o[mt][nt][e + 2] *= alpha;
-            }
-        }
         uint32_t pt[U][NT][2], v[U][2];
 #pragma unroll
         for (int b = 0; b < U; ++b) {
@@ -481,7 +504,7 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
             float x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              x[e] = ex2_approx(s[b][nt][e] - ref[nt][e & 1]);
+              x[e] = ex2_approx(s[b][nt][e]);
               l[nt][e & 1] += x[e];
             }
             pt[b][nt][0] = transpose_8x8(pack_half2(x[0], x[1]));
@@ -514,7 +537,7 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
     // ------------------------------------------------------ the unit's result
     // The next segment's first loads, before the warps wait for one another.
     // (Every warp comes to both votes, whatever failed, and all leave together.)
-    const int was_end = end, n_own = own, r_rows = rows, r_tok0 = tok0, r_head0 = head0,
+    const int was_end = end, r_rows = rows, r_tok0 = tok0, r_head0 = head0,
               r_slot = oslot;
     if (!was_end) take(m + 1);
     if (named_vote(1, 32 * W, fail) || was_end) break;
@@ -529,8 +552,8 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
           sm.part_m[warp][r] = ref[nt][e];
           sm.part_l[warp][r] = l[nt][e];
         }
-        if (n_own > 0) {
-          // Channels g d/8 .. of the row: o[mt] holds 2 mt (its first half) and 2 mt + 1.
+        // Channels g d/8 .. of the row: o[mt] holds 2 mt (its first half) and 2 mt + 1.
+        if (r < r_rows)
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             const int chunk = (g * (D / 32) + i) ^ t;
@@ -538,29 +561,30 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
                 make_float4(o[2 * i][nt][e], o[2 * i][nt][e + 2], o[2 * i + 1][nt][e],
                             o[2 * i + 1][nt][e + 2]);
           }
-        }
       }
     named_bar_sync(1, 32 * W);
     for (int x = tid; x < r_rows * (D / 2); x += 32 * W) {  // a row to a warp (or half of one)
       const int r = x / (D / 2), ch = x % (D / 2) * 2;
-      float pm = kNoRef4, pl = 0.f;
-      if (lane < W) pm = sm.part_m[lane][r], pl = sm.part_l[lane][r];
-      float top = pl == 0.f ? kNoRef4 : pm;
+      float2 y[W];
 #pragma unroll
-      for (int e = 16; e > 0; e >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
+      for (int w = 0; w < W; ++w)
+        y[w] = *reinterpret_cast<const float2*>(
+            &sm.part_o[w][r][((ch >> 2) ^ ((r >> 1) & 3)) * 4 + (ch & 3)]);
+      // Lane w (of every 16) weighs warp w's part.
+      float pm = ninf, pl = 0.f;
+      if ((lane & 15) < W) pm = sm.part_m[lane & 15][r], pl = sm.part_l[lane & 15][r];
+      float top = pl == 0.f ? ninf : pm;
+#pragma unroll
+      for (int e = 8; e > 0; e >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
       const float weight = pl == 0.f ? 0.f : exp2f(pm - top);
       float sum = pl * weight;
 #pragma unroll
-      for (int e = 16; e > 0; e >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, e);
+      for (int e = 8; e > 0; e >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, e);
       float2 acc = make_float2(0.f, 0.f);
-#pragma unroll 4
+#pragma unroll
       for (int w = 0; w < W; ++w) {
         const float f = __shfl_sync(0xffffffffu, weight, w);
-        if (f != 0.f) {
-          const float2 y = *reinterpret_cast<const float2*>(
-              &sm.part_o[w][r][((ch >> 2) ^ ((r >> 1) & 3)) * 4 + (ch & 3)]);
-          acc.x += f * y.x, acc.y += f * y.y;
-        }
+        acc.x += f * y[w].x, acc.y += f * y[w].y;
       }
       const float own = sum == 0.f ? 0.f : p.v_scale / sum;
       const float lse2 = sum == 0.f ? ninf : top + log2f(sum);
