@@ -334,11 +334,12 @@ int launch_decode(const PagedMaps& t, const PagedParams& p, const PagedPhase& ph
 // The merge of one phase's split units, or of two phases' (ph1 not null).
 template <int D>
 int launch_merge(const PagedParams& p, const PagedPhase& ph0, const PagedPhase* ph1,
-                 const cudaLaunchConfig_t& base) {
+                 const cudaLaunchConfig_t& base, int blocks = 0) {
   cudaLaunchConfig_t c = base;
   c.blockDim = dim3(32 * kMergeWarps, 1, 1);
   c.dynamicSmemBytes = 0;
-  c.gridDim = dim3((unsigned)p.ctas, ph0.slot_rows <= kPagedDecodeRows ? 4 : 8, ph1 ? 2 : 1);
+  if (blocks == 0) blocks = ph0.slot_rows <= kPagedDecodeRows ? 4 : 8;
+  c.gridDim = dim3((unsigned)p.ctas, (unsigned)blocks, ph1 ? 2 : 1);
   if (cudaLaunchKernelEx(&c, fa_paged_merge_kernel<D>, p, ph0, ph1 ? *ph1 : ph0) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
@@ -459,9 +460,10 @@ int launch_paged_d(const PagedParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-int launch_paged_merge(const PagedParams& p, const PagedPhase& ph, int d,
+int launch_paged_merge(const PagedParams& p, const PagedPhase& ph, int d, int blocks,
                        const cudaLaunchConfig_t& base) {
-  return d == 128 ? launch_merge<128>(p, ph, nullptr, base) : launch_merge<64>(p, ph, nullptr, base);
+  return d == 128 ? launch_merge<128>(p, ph, nullptr, base, blocks)
+                  : launch_merge<64>(p, ph, nullptr, base, blocks);
 }
 
 int launch_fwd_paged(const PagedParams& p, int d, cudaStream_t stream) {

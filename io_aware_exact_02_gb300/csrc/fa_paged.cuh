@@ -202,14 +202,17 @@ __device__ __forceinline__ int paged_groups(const PagedParams& p, const PagedPha
   const long long units = (long long)p.Hkv * ((p.T + ph.unit_tokens - 1) / ph.unit_tokens);
   return units <= ctas ? (int)units : 1;
 }
-// Tiles of one head of a sequence.
+// Tiles of one head of a sequence.  kEnd: what the end of a unit costs, in tiles;
+// the kernels over the cache in 4 bits, whose tiles take less, count it.
+template <int kEnd = 0>
 __device__ __forceinline__ long long paged_head_cost(const PagedParams& p, const PagedPhase& ph,
                                                      const PagedSeq& s) {
   const int R = paged_units(ph, s);
   if (R == 0) return 0;
-  if (!p.causal || ph.whole_batch) return (long long)R * max(1, paged_unit_tiles(p, ph, s, 0));
+  if (!p.causal || ph.whole_batch)
+    return (long long)R * (max(1, paged_unit_tiles(p, ph, s, 0)) + kEnd);
   long long c = 0;
-  for (int i = 0; i < R; ++i) c += max(1, paged_unit_tiles(p, ph, s, i));
+  for (int i = 0; i < R; ++i) c += max(1, paged_unit_tiles(p, ph, s, i)) + kEnd;
   return c;
 }
 
@@ -305,12 +308,13 @@ struct PagedScan {
 };
 
 // The cost of sequence b (0 past the last), and of one of its heads.
+template <int kEnd = 0>
 __device__ __forceinline__ long long paged_cost(const PagedParams& p, const PagedPhase& ph, int b,
                                                 int B, PagedSeq& s, long long& head) {
   head = 0;
   if (b < B) {
     s = paged_seq(p, ph, b);
-    head = paged_head_cost(p, ph, s);
+    head = paged_head_cost<kEnd>(p, ph, s);
   }
   return head * p.Hkv;
 }
@@ -328,6 +332,7 @@ __device__ __forceinline__ long long warp_scan(long long x) {  // inclusive
 // 32 sequences are left to the K warp alone (paged_walk_begin), a lane each.
 // More take all threads of the CTA: one scan of the sequences' costs where a
 // thread has one at most, else a sum and a second pass.
+template <int kEnd = 0>
 __device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhase& ph,
                                            PagedScan& sc, PagedWalk& w, int cta, int ctas) {
   const int B = ph.whole_batch ? 1 : p.B;
@@ -347,13 +352,13 @@ __device__ __forceinline__ void paged_plan(const PagedParams& p, const PagedPhas
   };
   long long total = 0, before, all, inc = 0;
   if (B > nt) {
-    for (int b = tid; b < B; b += nt) inc += paged_cost(p, ph, b, B, s, head);
+    for (int b = tid; b < B; b += nt) inc += paged_cost<kEnd>(p, ph, b, B, s, head);
     sums(warp_scan(inc), before, total);
     __syncthreads();
   }
   long long run = 0;
   for (int b0 = 0; b0 < B; b0 += nt) {
-    const long long cost = paged_cost(p, ph, b0 + tid, B, s, head);
+    const long long cost = paged_cost<kEnd>(p, ph, b0 + tid, B, s, head);
     inc = warp_scan(cost);
     sums(inc, before, all);
     if (B <= nt) total = all;
@@ -399,6 +404,7 @@ __device__ __forceinline__ void paged_weights(const PagedParams& p, const PagedP
 }
 
 // The K warp's start of the walk.
+template <int kEnd = 0>
 __device__ __forceinline__ void paged_walk_begin(const PagedParams& p, const PagedPhase& ph,
                                                  const PagedScan& sc, PagedWalk& w, int cta,
                                                  int ctas) {
@@ -407,7 +413,7 @@ __device__ __forceinline__ void paged_walk_begin(const PagedParams& p, const Pag
   const int B = ph.whole_batch ? 1 : p.B;
   long long head, off;
   if (B <= 32) {
-    const long long cost = paged_cost(p, ph, (int)lane_id(), B, w.s, head);
+    const long long cost = paged_cost<kEnd>(p, ph, (int)lane_id(), B, w.s, head);
     const long long inc = warp_scan(cost);
     w.share = PagedShare(__shfl_sync(0xffffffffu, inc, 31), ctas, paged_groups(p, ph, ctas));
     w.g = w.share.lo(cta);
@@ -432,12 +438,12 @@ __device__ __forceinline__ void paged_walk_begin(const PagedParams& p, const Pag
   off -= w.h * head;
   w.i = 0;
   if (!p.causal || ph.whole_batch) {  // units of equal cost
-    const int c = max(1, paged_unit_tiles(p, ph, w.s, 0));
+    const int c = max(1, paged_unit_tiles(p, ph, w.s, 0)) + kEnd;
     w.i = (int)paged_div(off, c);
     off -= (long long)w.i * c;
   } else {
     for (;; ++w.i) {
-      const int c = max(1, paged_unit_tiles(p, ph, w.s, w.i));
+      const int c = max(1, paged_unit_tiles(p, ph, w.s, w.i)) + kEnd;
       if (off < c) break;
       off -= c;
     }
@@ -486,6 +492,56 @@ __device__ __forceinline__ PagedItem paged_next(const PagedParams& p, const Page
     }
   }
   return it;
+}
+
+// The same where a unit's end counts as kEnd tiles, which lie behind the unit's
+// own: a range that has none but such of a unit has no segment of it.
+template <int kEnd>
+__device__ __forceinline__ PagedItem paged_next_weighed(const PagedParams& p, const PagedPhase& ph,
+                                                        PagedWalk& w, int cta) {
+  PagedItem it = {};
+  for (;;) {
+    it.end = w.g >= w.hi ? 1 : 0;
+    if (it.end) return it;
+    const int tiles = paged_unit_tiles(p, ph, w.s, w.i), real = max(1, tiles), cost = real + kEnd;
+    const int take = (int)min((long long)(cost - w.tile), w.hi - w.g);
+    const int own = min(w.tile + take, real) - w.tile;
+    if (own > 0) {
+      it.nj = tiles == 0 ? 0 : own;
+      it.b = w.b;
+      it.h = w.h;
+      it.tok0 = w.s.t0 + w.i * ph.unit_tokens;
+      it.ntok = min(ph.unit_tokens, w.s.n - w.i * ph.unit_tokens);
+      it.key = ph.key0 + w.tile * kTile;
+      it.k_hi = paged_unit_hi(p, ph, w.s, w.i);
+      it.pos0 = w.s.len - w.s.n + w.i * ph.unit_tokens;
+      it.len = w.s.len;
+      it.first = w.tile == 0;
+      it.tile0 = w.tiles;
+      w.tiles += it.nj;
+      w.start = w.g - w.tile;
+      w.end = w.start + real;
+      it.slot = own == real ? -1 : (w.start > w.share.lo(cta) ? 1 : 0);
+    }
+    w.first = false;
+    w.g += take;
+    w.tile += take;
+    if (w.tile == cost && w.g < w.hi) {
+      w.tile = 0;
+      if (++w.i == w.units) {
+        w.i = 0;
+        if (++w.h == p.Hkv) {
+          w.h = 0;
+          do {  // the range's end bounds the walk: a later sequence has tiles
+            ++w.b;
+            w.s = paged_seq(p, ph, w.b);
+          } while (w.s.n == 0 && w.b + 1 < p.B);
+          w.units = paged_units(ph, w.s);
+        }
+      }
+    }
+    if (own > 0) return it;
+  }
 }
 
 // Keys row t of the batch sees of the shared prefix.

@@ -177,7 +177,7 @@ int launch_paged4_d(const Paged4Params& p, cudaStream_t stream) {
     ph.slot_rows = f.rows;
     rc = f.rows == 8 ? launch_decode<D, 8>(q, ph, f.subs, c) : launch_decode<D, 16>(q, ph, f.subs, c);
     if (rc != FA_OK) return rc;
-    if ((rc = launch_paged_merge(q, ph, D, c)) != FA_OK) return rc;
+    if ((rc = launch_paged_merge(q, ph, D, 4, c)) != FA_OK) return rc;
   }
   return FA_OK;
 }

@@ -48,8 +48,9 @@ int launch_paged_duo(const PagedMaps& t, const CUtensorMap& tq_b, const PagedPar
                      const PagedPhase& pa, const PagedPhase& pb, int d,
                      const cudaLaunchConfig_t& base);
 
-// The merge of one phase's units that were shared between CTAs (fa_paged.cu).
-int launch_paged_merge(const PagedParams& p, const PagedPhase& ph, int d,
+// The merge of one phase's units that were shared between CTAs (fa_paged.cu), with
+// `blocks` thread blocks to each boundary between CTAs.
+int launch_paged_merge(const PagedParams& p, const PagedPhase& ph, int d, int blocks,
                        const cudaLaunchConfig_t& base);
 
 }  // namespace fa
