@@ -102,4 +102,18 @@ __device__ __forceinline__ uint32_t kv4_codes(const float* y, float s) {
   return r;
 }
 
+// The power of two that takes a query row, whose largest magnitude has the bits
+// `top` of an fp32 number, to [2^14, 2^15), where fp16 holds every channel but
+// for what is below 2^-38 of that one; as an exponent.  Zeros, infinities and
+// NaN stay.
+__device__ __forceinline__ int kv4_row_exponent(uint32_t top) {
+  return top > 0u && top < 0x7f800000u ? min(14 - ((int)(top >> 23) - 127), 100) : 0;
+}
+__device__ __forceinline__ float kv4_pow2(int e) { return __int_as_float((e + 127) << 23); }
+// The larger of `top` and the magnitudes of a pair of bf16 numbers, as bits of
+// fp32 numbers (which compare as integers).
+__device__ __forceinline__ uint32_t kv4_top(uint32_t top, uint32_t pair) {
+  return max(top, max(pair << 16 & 0x7fffffffu, pair & 0x7fff0000u));
+}
+
 }  // namespace fa

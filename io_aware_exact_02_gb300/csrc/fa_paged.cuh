@@ -544,6 +544,22 @@ __device__ __forceinline__ PagedItem paged_next_weighed(const PagedParams& p, co
   }
 }
 
+// What the merge needs to know of a CTA's first unit, `it` being its first segment,
+// the walk's last.
+__device__ __forceinline__ PagedRec paged4_first_rec(const PagedItem& it, const PagedWalk& w) {
+  PagedRec r = {};  // (a CTA whose first segment begins its unit joins none)
+  if (!it.first) {
+    const int c0 = w.share.owner(w.start);
+    r.split = 1;
+    r.slot = 2 * c0 + (w.share.lo(c0) < w.start ? 1 : 0);
+    r.n = w.share.owner(w.end - 1) - c0 + 1;
+    r.tok0 = it.tok0;
+    r.ntok = it.ntok;
+    r.h = it.h;
+  }
+  return r;
+}
+
 // Keys row t of the batch sees of the shared prefix.
 __device__ __forceinline__ int paged_prefix_limit(const PagedParams& p, int t) {
   if (t >= p.T) return 0;

@@ -62,12 +62,6 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // A vote of `threads` threads on named barrier `id`: true for all when true for
 // any.  Also a barrier among them.
 __device__ __forceinline__ bool named_vote(int id, int threads, bool x) {
@@ -191,17 +185,7 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
       }
       // What the merge needs to know of the CTA's first unit.
       if (m == 0 && lane == 0) {
-        PagedRec r = {};  // (a CTA whose first segment begins its unit joins none)
-        if (!it.first) {
-          const int c0 = walk.share.owner(walk.start);
-          r.split = 1;
-          r.slot = 2 * c0 + (walk.share.lo(c0) < walk.start ? 1 : 0);
-          r.n = walk.share.owner(walk.end - 1) - c0 + 1;
-          r.tok0 = it.tok0;
-          r.ntok = it.ntok;
-          r.h = it.h;
-        }
-        *rec = r;
+        *rec = paged4_first_rec(it, walk);
       }
       __syncwarp();
       if (m >= 2) ok = mbar_wait(&sm.q_empty[qb], (m / 2 - 1) & 1, p.status, abortf, kSitePgQEmpty);
@@ -214,25 +198,21 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
           w[4 * i] = x[nt][i].x, w[4 * i + 1] = x[nt][i].y, w[4 * i + 2] = x[nt][i].z, w[4 * i + 3] = x[nt][i].w;
-        // The largest magnitude: bf16 numbers compare as the integers they are.
         uint32_t top = 0u;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) top = max(top, max(w[i] << 16 & 0x7fffffffu, w[i] & 0x7fff0000u));
+        for (int i = 0; i < D / 8; ++i) top = kv4_top(top, w[i]);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // It goes to [2^14, 2^15): exponents are exact, and what falls below
-        // fp16's range is 2^-38 of it.  (Zeros, infinities and NaN stay.)
-        int e = 0;
-        if (top > 0u && top < 0x7f800000u) e = min(14 - ((int)(top >> 23) - 127), 100);
-        const float f = __int_as_float((e + 127) << 23);
+        const int e = kv4_row_exponent(top);
+        const float f = kv4_pow2(e);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
-          w[i] = pack_half2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+          w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)
           sm.q[qb][nt * (D / 32) + i][lane] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         if (t == 0) {
-          sm.c2[qb][r] = r < rows ? p.scale_log2 * p.k_scale * __int_as_float((127 - e) << 23) : 0.f;
+          sm.c2[qb][r] = r < rows ? p.scale_log2 * p.k_scale * kv4_pow2(-e) : 0.f;
           int lim = 0;
           if (r < rows) lim = p.causal ? max(0, min(it.pos0 + r / p.G + 1, it.len)) : it.len;
           sm.lim[qb][r] = lim;
@@ -513,8 +493,8 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
               x[e] = ex2_approx(s[b][nt][e]);
               l[nt][e & 1] += x[e];
             }
-            pt[b][nt][0] = transpose_8x8(pack_half2(x[0], x[1]));
-            pt[b][nt][1] = transpose_8x8(pack_half2(x[2], x[3]));
+            pt[b][nt][0] = transpose_8x8(pack_f16x2(x[0], x[1]));
+            pt[b][nt][1] = transpose_8x8(pack_f16x2(x[2], x[3]));
           }
           v[b][0] = e4m3_to_half(vs[b][0]);
           v[b][1] = e4m3_to_half(vs[b][1]);

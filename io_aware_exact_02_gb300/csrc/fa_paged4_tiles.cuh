@@ -1,0 +1,247 @@
+// fa_paged4_tiles.cuh -- the prompt kernel's producers over a cache held in 4 bits:
+// the list's segments, the K and V tiles turned into fp16, and the rows of Q.
+//
+// A 128-key tile is eight blocks of fa_kv4.cuh; one warp makes the K tiles, one the
+// V tiles, 16,384 numbers each in the 2,600 cycles that a step of the tensor core
+// takes.  A lane reads 16 bytes (d = 64: 8) of a block's codes at a time, four
+// blocks ahead of those it converts (of the units that share a key/value head
+// all but the first find them in L2), and stores 16 bytes of the tile at a time,
+// in the layout that TMA would leave: [d / 64][128 keys][128 bytes], the 16-byte
+// chunk c of row r at c ^ (r % 8).  Which lane stores which of its pieces first
+// is chosen so that eight lanes meet eight chunks.
+#pragma once
+
+#include "fa_internal.h"
+#include "fa_kv4.cuh"
+#include "fa_paged.cuh"
+#include "sm100_ptx.cuh"
+
+namespace fa {
+
+// Walks the CTA's range of the list and publishes its segments; load_q loads the
+// query rows of those with keys.
+template <int kRing, class Smem, class LoadQ>
+__device__ __forceinline__ void paged4_produce_items(const PagedParams& p, const PagedPhase& ph,
+                                                     Smem& sm, PagedWalk& walk, int cta, int ctas,
+                                                     LoadQ&& load_q) {
+  volatile int* abortf = &sm.abort_flag;
+  PagedRec* const rec = reinterpret_cast<PagedRec*>(ph.rec + cta * kPagedRecBytes);
+  bool ok = true;
+  paged_walk_begin(p, ph, sm.scan, walk, cta, ctas);
+  for (int m = 0; ok; ++m) {
+    const PagedItem it = paged_next(p, ph, walk, cta);
+    const int is = m % kRing;
+    if (m >= kRing)
+      ok = mbar_wait(&sm.item_empty[is], (m / kRing - 1) & 1, p.status, abortf, kSitePgItemEmpty);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    if (lane_id() == 0) {
+      sm.item[is] = it;
+      mbar_arrive(&sm.item_full[is]);
+    }
+    __syncwarp();
+    if (it.end) {
+      if (m == 0 && lane_id() == 0) rec->split = 0;
+      break;
+    }
+    if (it.nj > 0) ok = load_q(it);
+    ok = __all_sync(0xffffffffu, ok);
+    if (m == 0 && lane_id() == 0) *rec = paged4_first_rec(it, walk);
+  }
+  __syncwarp();
+}
+
+// What a lane has read of four blocks: a block's codes of K or V, and scales.
+template <int D>
+struct Raw4 {
+  static constexpr int kWords = D / 32;
+  uint32_t code[4][2][kWords];
+  uint32_t scale[4];  // two 16-bit pieces, of the codes' two
+};
+
+// Reads blocks 4 half .. 4 half + 3 of the tile whose first key is `key` (keys end
+// at k_hi); `page`: lane b holds the page of the tile's block b.
+template <int D, bool kV>
+__device__ __forceinline__ void read_raw4(const Paged4Params& p, int h, int key, int k_hi, int page,
+                                          int half, Raw4<D>& r) {
+  using Block = Kv4Block<D>;
+  const int lane = (int)lane_id(), g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int block = 4 * half + b, at = key + 16 * block;
+    const int id = __shfl_sync(0xffffffffu, page, block);
+    r.scale[b] = 0u;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) r.code[b][u][w] = 0u;
+    if (at >= k_hi) continue;  // past the keys: zeros
+    if (id < 0 || id >= p.num_pages) {
+      int abort_flag = 0;
+      if (lane == 0) report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
+      continue;
+    }
+    const uint8_t* const blk =
+        p.pages + kv4_block_at(id, p.Hkv, h, p.page_shift, at & (p.page_size - 1), Block::kBytes);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t* const src =
+          blk + (kV ? Block::v_code(0, 0) : Block::k_code(0)) + (u * 32 + lane) * (D / 8);
+      if constexpr (D == 128) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
+        r.code[b][u][0] = x.x, r.code[b][u][1] = x.y;
+        r.code[b][u][D / 32 - 2] = x.z, r.code[b][u][D / 32 - 1] = x.w;
+      } else {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+        r.code[b][u][0] = x.x, r.code[b][u][1] = x.y;
+      }
+      uint32_t s;
+      if constexpr (kV) {
+        s = __ldg(reinterpret_cast<const uint16_t*>(blk + Block::v_scale(D == 128 ? g : g / 2) + u * 8 + 2 * t));
+        // Slots past the keys may hold anything, and 0 * NaN is NaN.
+        const int first = at + u * 8 + 2 * t;
+        if (first >= k_hi) s = 0u;
+        if (first + 1 >= k_hi) s &= 0xffu;
+      } else if constexpr (D == 128) {
+        s = __ldg(reinterpret_cast<const uint16_t*>(blk + Block::k_scale(0) + (u * 32 + lane) * 2));
+      } else {
+        s = __ldg(blk + Block::k_scale(0) + u * 32 + lane);
+      }
+      r.scale[b] |= s << (16 * u);
+    }
+  }
+}
+
+// Turns them into rows 64 half .. 64 half + 63 of a tile.
+template <int D, bool kV>
+__device__ __forceinline__ void store_raw4(const Raw4<D>& r, int half, uint8_t* tile) {
+  const int lane = (int)lane_id(), g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t s = e4m3_to_half(r.scale[b] >> (16 * u) & 0xffffu);
+      if constexpr (!kV) {
+        // Key g of these eight, channels t d/4 ..: a word is a chunk of eight.
+        const int row = 64 * half + 16 * b + 8 * u + g;
+        const uint32_t s0 = __byte_perm(s, s, 0x1010), s1 = __byte_perm(s, s, 0x3232);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          // (Lanes of the second 64 channels take the words in another order.)
+          const int w = D == 128 ? i ^ (t >> 1) : i;
+          const uint32_t code = D == 128 && (t >> 1) ? r.code[b][u][i ^ 1] : r.code[b][u][i];
+          const uint32_t sw = D == 128 && i >= 2 ? s1 : s0;  // (w and i are of one half)
+          uint32_t x[4];
+          e2m1_to_half(code, x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = half2_mul(x[e], sw);
+          const int ch = D == 128 ? (t & 1) * 4 + w : 2 * t + w;
+          *reinterpret_cast<uint4*>(tile + (D == 128 ? (t >> 1) * (kTile * 128) : 0) + row * 128 +
+                                    ((ch ^ (row & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+      } else {
+        // Keys 2t and 2t + 1 of these eight, channels g d/8 ..: two words are a
+        // chunk of eight of both.
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          uint32_t x[8];
+          e2m1_to_half(r.code[b][u][2 * i], reinterpret_cast<uint32_t(&)[4]>(x[0]));
+          e2m1_to_half(r.code[b][u][2 * i + 1], reinterpret_cast<uint32_t(&)[4]>(x[4]));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = half2_mul(x[e], s);
+          const int ch = D == 128 ? g * 2 + i : g;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            // (Lanes of odd g store the odd key first.)
+            const int key = k ^ (g & 1), row = 64 * half + 16 * b + 8 * u + 2 * t + key;
+            const uint32_t sel = key ? 0x7632u : 0x5410u;
+            *reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + row * 128 +
+                                      (((ch & 7) ^ (row & 7)) << 4)) =
+                make_uint4(__byte_perm(x[0], x[1], sel), __byte_perm(x[2], x[3], sel),
+                           __byte_perm(x[4], x[5], sel), __byte_perm(x[6], x[7], sel));
+          }
+        }
+      }
+    }
+  }
+}
+
+// The warp that makes the K (or V) tiles of the CTA's segments.
+template <int D, int S, int kRing, bool kV, class Smem>
+__device__ __forceinline__ void paged4_produce_tiles(const Paged4Params& p, Smem& sm) {
+  volatile int* abortf = &sm.abort_flag;
+  const int lane = (int)lane_id();
+  bool ok = true;
+  int c = kV ? 1 : 0;  // ring uses
+  for (int m = 0; ok; ++m) {
+    const int is = m % kRing;
+    ok = mbar_wait(&sm.item_full[is], (m / kRing) & 1, p.status, abortf, kSitePgItemFull);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    const PagedItem& it = sm.item[is];
+    const int end = it.end, nj = it.nj, h = it.h, key0 = it.key, k_hi = it.k_hi, seq = it.b;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.item_empty[is]);
+    if (end) break;
+    if (nj == 0) continue;
+    const int* const list = p.page_table + (long long)seq * p.max_pages;
+    auto pages = [&](int j) -> int {  // of tile j's blocks, in lanes 0 .. 7
+      const int key = key0 + j * kTile + 16 * (lane & 7);
+      return j < nj && key < k_hi ? list[key >> p.page_shift] : 0;
+    };
+    int page = pages(0), next = pages(1);
+    Raw4<D> a, b;
+    read_raw4<D, kV>(p, h, key0, k_hi, page, 0, a);
+    for (int j = 0; j < nj && ok; ++j, c += 2) {
+      const int slot = c % S, key = key0 + j * kTile;
+      read_raw4<D, kV>(p, h, key, k_hi, page, 1, b);
+      if (c >= S)
+        ok = mbar_wait(&sm.kv_empty[slot], (c / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      store_raw4<D, kV>(a, 0, sm.kv[slot]);
+      page = next;
+      next = pages(j + 2);
+      if (j + 1 < nj) read_raw4<D, kV>(p, h, key + kTile, k_hi, page, 0, a);
+      store_raw4<D, kV>(b, 1, sm.kv[slot]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.kv_full[slot]);
+    }
+  }
+  __syncwarp();
+}
+
+// Row r of a Q tile from bf16 to fp16, in place, times the power of two that takes
+// it to fp16's range; returns the factor from products to exponents (c2 that of
+// the row as it was), which is never 0: a zero scale is a tiny one.
+template <int D>
+__device__ __forceinline__ float q_row_to_half(uint8_t* tile, int r, float c2) {
+  uint8_t* const row = tile + r * 128;
+  uint32_t top = 0u;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 x = *reinterpret_cast<const uint4*>(row + (c >> 3) * (kTile * 128) + (c & 7) * 16);
+    top = kv4_top(kv4_top(kv4_top(kv4_top(top, x.x), x.y), x.z), x.w);
+  }
+  const int e = kv4_row_exponent(top);
+  const float f = kv4_pow2(e);
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    // (The chunks' order in the row does not matter here.)
+    uint4* const at = reinterpret_cast<uint4*>(row + (c >> 3) * (kTile * 128) + ((c ^ r) & 7) * 16);
+    const uint4 x = *at;
+    auto turn = [&](uint32_t w) {
+      uint32_t y;
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+          : "=r"(y)
+          : "f"(__uint_as_float(w & 0xffff0000u) * f), "f"(__uint_as_float(w << 16) * f));
+      return y;
+    };
+    *at = make_uint4(turn(x.x), turn(x.y), turn(x.z), turn(x.w));
+  }
+  const float x = c2 * kv4_pow2(-e), tiny = 1.17549435e-38f;
+  return fabsf(x) >= tiny ? x : (c2 < 0.f ? -tiny : tiny);
+}
+
+}  // namespace fa

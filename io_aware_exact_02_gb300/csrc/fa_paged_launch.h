@@ -53,4 +53,8 @@ int launch_paged_duo(const PagedMaps& t, const CUtensorMap& tq_b, const PagedPar
 int launch_paged_merge(const PagedParams& p, const PagedPhase& ph, int d, int blocks,
                        const cudaLaunchConfig_t& base);
 
+// The prompt kernel over a cache in 4 bits (fa_paged4_prompt.cu); completes ph.
+int launch_paged4_prompt(const Paged4Params& p, PagedPhase& ph, int d,
+                         const cudaLaunchConfig_t& base);
+
 }  // namespace fa

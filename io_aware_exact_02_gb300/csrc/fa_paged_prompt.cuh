@@ -21,8 +21,12 @@
 // record and scores).
 #pragma once
 
+#include <type_traits>
+
 #include "fa_internal.h"
+#include "fa_kv4.cuh"
 #include "fa_paged.cuh"
+#include "fa_paged4_tiles.cuh"
 #include "fa_softmax.cuh"
 #include "sm100_ptx.cuh"
 
@@ -44,7 +48,7 @@ struct alignas(1024) PromptSmem {
   uint8_t q[2][PromptCfg<D>::kTileBytes];
   uint8_t kv[PromptCfg<D>::kStages][PromptCfg<D>::kTileBytes];
   uint8_t out[8][4096];  // a softmax warp's 32 rows x 128 bytes on their way out
-  uint64_t q_full, q_empty;
+  uint64_t q_full, q_empty, q_half;
   uint64_t kv_full[PromptCfg<D>::kStages], kv_empty[PromptCfg<D>::kStages];
   uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2];
   uint64_t item_full[kPromptRing], item_empty[kPromptRing];
@@ -234,11 +238,15 @@ __device__ __noinline__ void store_box(uint32_t colO, float own, uint8_t* out,
 
 // The prompt kernel's work on CTA `cta` of the `ctas` that share the phase's
 // list.  kStarted: the caller has waited for the prior grid.
-template <int D, bool kNeg, bool kStarted>
-__device__ __forceinline__ void prompt_cta(const CUtensorMap* tq, const CUtensorMap* tk,
-                                           const CUtensorMap* tv, const CUtensorMap* to,
-                                           const PagedParams& p, const PagedPhase& ph, int cta,
-                                           int ctas, uint8_t* smem_raw) {
+//
+// kFour: over the cache in 4 bits (fa_kv4.cuh).  Warps 10 and 11 turn the codes of
+// V and K into fp16 tiles, warp 8 has the list and Q only; the products run in
+// fp16, and the softmax warps scale each row of Q to its range first.
+template <int D, bool kNeg, bool kStarted, bool kFour = false>
+__device__ __forceinline__ void prompt_cta(
+    const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const CUtensorMap* to,
+    const std::conditional_t<kFour, Paged4Params, PagedParams>& p, const PagedPhase& ph, int cta,
+    int ctas, uint8_t* smem_raw) {
   using Cfg = PromptCfg<D>;
   constexpr int S = Cfg::kStages;
   PromptSmem<D>& sm = *reinterpret_cast<PromptSmem<D>*>(
@@ -250,6 +258,7 @@ __device__ __forceinline__ void prompt_cta(const CUtensorMap* tq, const CUtensor
   if (tid == 0) {
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
+    if constexpr (kFour) mbar_init(&sm.q_half, 256);
     for (int s = 0; s < S; ++s) {
       mbar_init(&sm.kv_full[s], 1);
       mbar_init(&sm.kv_empty[s], 1);
@@ -263,8 +272,9 @@ __device__ __forceinline__ void prompt_cta(const CUtensorMap* tq, const CUtensor
     }
     for (int i = 0; i < kPromptRing; ++i) {
       mbar_init(&sm.item_full[i], 1);
-      // Read by the issuing thread, the V warp and the eight softmax warps.
-      mbar_init(&sm.item_empty[i], 2 + 8);
+      // Read by the issuing thread, the V warp (kFour: and the K warp) and the
+      // eight softmax warps.
+      mbar_init(&sm.item_empty[i], (kFour ? 3 : 2) + 8);
     }
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -276,8 +286,10 @@ __device__ __forceinline__ void prompt_cta(const CUtensorMap* tq, const CUtensor
   }
   if (warp == kWarpLoad && lane_id() == 0) {
     prefetch_tmap(tq);
-    prefetch_tmap(tk);
-    prefetch_tmap(tv);
+    if constexpr (!kFour) {
+      prefetch_tmap(tk);
+      prefetch_tmap(tv);
+    }
   }
   if (ph.tile_tokens * p.G < kTile) {
     // Rows no box fills: any finite values do (their results are not stored),
@@ -310,7 +322,7 @@ __device__ __forceinline__ void prompt_cta(const CUtensorMap* tq, const CUtensor
     // ------------------------------------------------------------ Q and K
     setmaxnreg_dec<kPagedRegsLoad>();
     int n_q = 0;  // units loaded
-    paged_produce_k<D, S, kPromptRing>(p, ph, sm, tk, walk, cta, ctas, 1, [&](const PagedItem& it) {
+    auto load_q = [&](const PagedItem& it) {
       if (n_q > 0 &&
           !mbar_wait(&sm.q_empty, (n_q - 1) & 1, p.status, abortf, kSitePgQEmpty))
         return false;
@@ -323,19 +335,28 @@ __device__ __forceinline__ void prompt_cta(const CUtensorMap* tq, const CUtensor
       }
       ++n_q;
       return true;
-    });
+    };
+    if constexpr (kFour)
+      paged4_produce_items<kPromptRing>(p, ph, sm, walk, cta, ctas, load_q);
+    else
+      paged_produce_k<D, S, kPromptRing>(p, ph, sm, tk, walk, cta, ctas, 1, load_q);
     if (*abortf && lane_id() == 0 && n_q > 0) drain_wait(&sm.q_full, (n_q - 1) & 1);
     __syncwarp();
   } else if (warp == kWarpLoadV) {
     // ------------------------------------------------------------ V
     setmaxnreg_dec<kPagedRegsLoad>();
-    paged_produce_v<D, S, kPromptRing>(p, sm, tv, nullptr);
+    if constexpr (kFour)
+      paged4_produce_tiles<D, S, kPromptRing, true>(p, sm);
+    else
+      paged_produce_v<D, S, kPromptRing>(p, sm, tv, nullptr);
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ products
     setmaxnreg_dec<kPagedRegsLoad>();
     if (lane_id() == 0) {
-      const uint32_t id_s = idesc_bf16(128, 128, false, false);
-      const uint32_t id_o = idesc_bf16(128, D, false, true);
+      // (In the descriptor, fp16 is 0 where bf16 is 1.)
+      constexpr uint32_t kTypes = kFour ? 1u << 7 | 1u << 10 : 0u;
+      const uint32_t id_s = idesc_bf16(128, 128, false, false) & ~kTypes;
+      const uint32_t id_o = idesc_bf16(128, D, false, true) & ~kTypes;
       const uint32_t q_addr[2] = {smem_u32(sm.q[0]), smem_u32(sm.q[1])};
       uint32_t p_par[2] = {0, 0};
       int n_o[2] = {0, 0};  // units whose O_t was begun
@@ -387,7 +408,7 @@ __device__ __forceinline__ void prompt_cta(const CUtensorMap* tq, const CUtensor
         const int n_t[2] = {tile_steps(p, ph, it, 0), tile_steps(p, ph, it, 1)};
         const int nmax = max(n_t[0], n_t[1]);
         if (nmax == 0) continue;
-        ok = mbar_wait(&sm.q_full, n_q & 1, p.status, abortf, kSitePgQFull);
+        ok = mbar_wait(kFour ? &sm.q_half : &sm.q_full, n_q & 1, p.status, abortf, kSitePgQFull);
         if (ok) ok = wait_full(cb);
         if (!ok) break;
         ++n_q;
@@ -439,7 +460,8 @@ __device__ __forceinline__ void prompt_cta(const CUtensorMap* tq, const CUtensor
     const uint32_t colS = tmem + lane_base + Cfg::col_s(t);
     const uint32_t colO = tmem + lane_base + Cfg::col_o(t);
     const float ninf = __int_as_float(0xff800000);
-    const float c2 = p.scale_log2;  // nonzero: a zero scale arrives as a tiny positive one
+    float c2 = p.scale_log2;  // nonzero: a zero scale arrives as a tiny positive one
+    [[maybe_unused]] int n_q = 0;
     const int row_tok = t * ph.tile_tokens + r / p.G, row_head = r % p.G;
     uint32_t s_par = 0;
     int n_o = 0;  // units with keys for this tile
@@ -468,6 +490,17 @@ __device__ __forceinline__ void prompt_cta(const CUtensorMap* tq, const CUtensor
           lim = p.causal ? min(it.pos0 + row_tok + 1, it.len) : it.len;
       }
       float m_ref = ninf, l = 0.f;
+      if constexpr (kFour) {
+        if (nmax > 0) {
+          ok = mbar_wait(&sm.q_full, n_q & 1, p.status, abortf, kSitePgQFull);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          ++n_q;
+          c2 = q_row_to_half<D>(sm.q[t], r, p.scale_log2 * p.k_scale);
+          fence_proxy_async_smem();
+          mbar_arrive(&sm.q_half);
+        }
+      }
       for (int j = 0; j < n_t; ++j) {
         const int key = it.key + j * kTile;
         ok = mbar_wait(&sm.s_full[t], s_par, p.status, abortf, kSitePgSFull);
@@ -489,7 +522,7 @@ __device__ __forceinline__ void prompt_cta(const CUtensorMap* tq, const CUtensor
         s_par ^= 1;
         if (!ok) break;
         tc_fence_after();
-        softmax_tile<D, kNeg, false>(colS, colO, c2, lim - key, j > 0, m_ref, l,
+        softmax_tile<D, kNeg, false, kFour>(colS, colO, c2, lim - key, j > 0, m_ref, l,
                                      [&] { mbar_arrive(&sm.p_half[t]); });
         tc_fence_before();
         mbar_arrive(&sm.p_full[t]);
@@ -501,6 +534,7 @@ __device__ __forceinline__ void prompt_cta(const CUtensorMap* tq, const CUtensor
       const bool any = l > 0.f || l != l;
       float lse2 = any ? m_ref + __log2f(l) : ninf;
       float own = any ? 1.f / l : 0.f, pre = 0.f;
+      if constexpr (kFour) own *= p.v_scale;
       if (it.first && ph.pre_o != nullptr && valid) {
         const float other = ph.pre_lse[row], top = fmaxf(lse2, other);
         if (top != ninf) {
@@ -549,8 +583,9 @@ __device__ __forceinline__ void prompt_cta(const CUtensorMap* tq, const CUtensor
     if (lane_id() == 0) bulk_wait_group0();
     __syncwarp();
   } else {
-    // Idle: its registers go to the compute warps.
+    // Idle, but for K in 4 bits: its registers go to the compute warps.
     setmaxnreg_dec<kPagedRegsLoad>();
+    if constexpr (kFour) paged4_produce_tiles<D, S, kPromptRing, false>(p, sm);
   }
 
   tc_fence_before();

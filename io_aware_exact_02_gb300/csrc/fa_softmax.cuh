@@ -6,7 +6,7 @@
 // past `tlim` (the row's visible keys end there), takes the tile's extreme,
 // moves the row's reference maximum only when the tile's exceeds it by more
 // than kRescaleSlack (log2 units), writes P = 2^(c2 * S - m) over S as bf16
-// pairs (or E4M3 quadruples), adds P's row sum to l, and rescales the row's O
+// (kHalf: fp16) pairs (or E4M3 quadruples), adds P's row sum to l, and rescales the row's O
 // accumulator in tensor memory when the reference moved (cs2680 Lecture 9,
 // sec. 9.4; "Reading CMU 11-868 LLM Systems: FlashAttention", slide pages
 // 12 and 51-52).  O and l share the reference, so O / l and
@@ -20,6 +20,12 @@ namespace fa {
 
 constexpr float kRescaleSlack = 8.0f;  // log2 units
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // colS / colO: this thread's TMEM address of the tile's S and O columns.
 // c2 = scale * log2(e) (nonzero).  may_rescale: O holds earlier tiles'
 // products (false on the row's first key tile, whose O is overwritten).
@@ -32,7 +38,7 @@ constexpr float kRescaleSlack = 8.0f;  // log2 units
 // rescale: it must return once the previous P V product has written O (the
 // caller's S having completed implies that, unless the tensor core computed
 // S ahead of that product).  Warp-collective (TMEM loads and stores).
-template <int D, bool kNeg, bool kFp8, class HalfReady, class BeforeRescale>
+template <int D, bool kNeg, bool kFp8, bool kHalf = false, class HalfReady, class BeforeRescale>
 __device__ __forceinline__ void softmax_tile_w(uint32_t colS, uint32_t colO, float c2, int tlim,
                                                bool may_rescale, float& m_ref, float& l,
                                                HalfReady&& half_ready,
@@ -114,7 +120,7 @@ __device__ __forceinline__ void softmax_tile_w(uint32_t colS, uint32_t colO, flo
           else
             pk8[(c * 32 + i) >> 2] |= two << 16;
         } else {
-          pk[c2i * 16 + i / 2] = pack_bf16x2(p0, p1);
+          pk[c2i * 16 + i / 2] = kHalf ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
         }
       }
     }
@@ -155,11 +161,11 @@ __device__ __forceinline__ void softmax_tile_w(uint32_t colS, uint32_t colO, flo
   }
 }
 
-template <int D, bool kNeg, bool kFp8, class HalfReady>
+template <int D, bool kNeg, bool kFp8, bool kHalf = false, class HalfReady>
 __device__ __forceinline__ void softmax_tile(uint32_t colS, uint32_t colO, float c2, int tlim,
                                              bool may_rescale, float& m_ref, float& l,
                                              HalfReady&& half_ready) {
-  softmax_tile_w<D, kNeg, kFp8>(colS, colO, c2, tlim, may_rescale, m_ref, l, half_ready, [] {});
+  softmax_tile_w<D, kNeg, kFp8, kHalf>(colS, colO, c2, tlim, may_rescale, m_ref, l, half_ready, [] {});
 }
 
 }  // namespace fa
