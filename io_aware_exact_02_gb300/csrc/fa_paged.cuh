@@ -98,6 +98,14 @@ constexpr int kPagedThreads = 384, kPagedRegs = 168, kPagedRegsCompute = 200, kP
 static_assert(2 * 128 * kPagedRegsCompute + 128 * kPagedRegsLoad <= kPagedThreads * kPagedRegs,
               "register split above the launch's total");
 
+// The prompt kernel over the cache in 4 bits has a warpgroup more, which makes the
+// tiles: launched with kPaged4Regs a thread.
+constexpr int kPaged4Threads = 512, kPaged4Regs = 128, kPaged4RegsCompute = 192,
+              kPaged4RegsList = 48, kPaged4RegsTiles = 80;
+static_assert(2 * 128 * kPaged4RegsCompute + 128 * (kPaged4RegsList + kPaged4RegsTiles) <=
+                  kPaged4Threads * kPaged4Regs,
+              "register split above the launch's total");
+
 // Wait without the abort shortcut: used while winding down.
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   const uint32_t a = smem_u32(bar);

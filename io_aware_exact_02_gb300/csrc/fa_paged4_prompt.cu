@@ -7,7 +7,7 @@ namespace fa {
 namespace {
 
 template <int D, bool kNeg>
-__global__ void __launch_bounds__(kPagedThreads, 1)
+__global__ void __launch_bounds__(kPaged4Threads, 1)
     fa_paged4_prompt_kernel(const __grid_constant__ CUtensorMap tq,
                             const __grid_constant__ CUtensorMap to, const Paged4Params p,
                             const PagedPhase ph) {
@@ -20,9 +20,9 @@ template <int D, bool kNeg>
 int launch(const PagedMaps& t, const Paged4Params& p, const PagedPhase& ph,
            const cudaLaunchConfig_t& base) {
   cudaLaunchConfig_t c = base;
-  c.blockDim = dim3(kPagedThreads, 1, 1);
+  c.blockDim = dim3(kPaged4Threads, 1, 1);
   c.dynamicSmemBytes = sizeof(PromptSmem<D>) + 1024;
-  if (paged_kernel_ready<fa_paged4_prompt_kernel<D, kNeg>>(c.dynamicSmemBytes) != FA_OK)
+  if (paged_kernel_ready<fa_paged4_prompt_kernel<D, kNeg>, kPaged4Regs>(c.dynamicSmemBytes) != FA_OK)
     return FA_ERR_LAUNCH;
   if (cudaLaunchKernelEx(&c, fa_paged4_prompt_kernel<D, kNeg>, t.q, t.o, p, ph) != cudaSuccess) {
     cudaGetLastError();

@@ -1,14 +1,15 @@
 // fa_paged4_tiles.cuh -- the prompt kernel's producers over a cache held in 4 bits:
 // the list's segments, the K and V tiles turned into fp16, and the rows of Q.
 //
-// A 128-key tile is eight blocks of fa_kv4.cuh; one warp makes the K tiles, one the
-// V tiles, 16,384 numbers each in the 2,600 cycles that a step of the tensor core
-// takes.  A lane reads 16 bytes (d = 64: 8) of a block's codes at a time, four
-// blocks ahead of those it converts (of the units that share a key/value head
-// all but the first find them in L2), and stores 16 bytes of the tile at a time,
-// in the layout that TMA would leave: [d / 64][128 keys][128 bytes], the 16-byte
-// chunk c of row r at c ^ (r % 8).  Which lane stores which of its pieces first
-// is chosen so that eight lanes meet eight chunks.
+// A 128-key tile is eight blocks of fa_kv4.cuh; four warps, one on each quarter of
+// the SM, make two blocks of each tile, K and V in turn: 8,192 numbers a warp in
+// the 2,600 cycles that a step of the tensor core takes.  (A warp for K and one
+// for V, beside the softmax warps of two of the quarters, took 7,800.)  A lane
+// reads 16 bytes (d = 64: 8) of a block's codes at a time, a step ahead of those
+// it converts, and stores 16 bytes of the tile at a time, in the layout that TMA
+// would leave: [d / 64][128 keys][128 bytes], the 16-byte chunk c of row r at
+// c ^ (r % 8).  Which lane stores which of its pieces first is chosen so that
+// eight lanes meet eight chunks.
 #pragma once
 
 #include "fa_internal.h"
@@ -28,47 +29,56 @@ __device__ __forceinline__ void paged4_produce_items(const PagedParams& p, const
   PagedRec* const rec = reinterpret_cast<PagedRec*>(ph.rec + cta * kPagedRecBytes);
   bool ok = true;
   paged_walk_begin(p, ph, sm.scan, walk, cta, ctas);
-  for (int m = 0; ok; ++m) {
+  // Publishes the walk's next segment as item m; false at the list's end.
+  auto publish = [&](int m) -> bool {
     const PagedItem it = paged_next(p, ph, walk, cta);
     const int is = m % kRing;
     if (m >= kRing)
       ok = mbar_wait(&sm.item_empty[is], (m / kRing - 1) & 1, p.status, abortf, kSitePgItemEmpty);
     ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    if (lane_id() == 0) {
+    if (ok && lane_id() == 0) {
       sm.item[is] = it;
       mbar_arrive(&sm.item_full[is]);
     }
     __syncwarp();
-    if (it.end) {
-      if (m == 0 && lane_id() == 0) rec->split = 0;
-      break;
-    }
+    return ok && !it.end;
+  };
+  bool more = publish(0);
+  if (ok && lane_id() == 0) {
+    if (more)
+      *rec = paged4_first_rec(sm.item[0], walk);
+    else
+      rec->split = 0;
+  }
+  // Item m + 1 is known before item m's query rows have a place.
+  for (int m = 0; more; ++m) {
+    more = publish(m + 1);
+    if (!ok) break;
+    const PagedItem it = sm.item[m % kRing];  // (only this warp writes the records)
     if (it.nj > 0) ok = load_q(it);
     ok = __all_sync(0xffffffffu, ok);
-    if (m == 0 && lane_id() == 0) *rec = paged4_first_rec(it, walk);
+    more = more && ok;
   }
   __syncwarp();
 }
 
-// What a lane has read of four blocks: a block's codes of K or V, and scales.
+// What a lane has read of two blocks: its codes of K or V, and scales.
 template <int D>
 struct Raw4 {
-  static constexpr int kWords = D / 32;
-  uint32_t code[4][2][kWords];
-  uint32_t scale[4];  // two 16-bit pieces, of the codes' two
+  uint32_t code[2][2][D / 32];
+  uint32_t scale[2];  // two 16-bit pieces, of the codes' two
 };
 
-// Reads blocks 4 half .. 4 half + 3 of the tile whose first key is `key` (keys end
-// at k_hi); `page`: lane b holds the page of the tile's block b.
+// Reads blocks 2 part, 2 part + 1 of the tile whose first key is `key` (keys end at
+// k_hi); `page`: lane b holds the page of the tile's block b.
 template <int D, bool kV>
 __device__ __forceinline__ void read_raw4(const Paged4Params& p, int h, int key, int k_hi, int page,
-                                          int half, Raw4<D>& r) {
+                                          int part, Raw4<D>& r) {
   using Block = Kv4Block<D>;
   const int lane = (int)lane_id(), g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const int block = 4 * half + b, at = key + 16 * block;
+  for (int b = 0; b < 2; ++b) {
+    const int block = 2 * part + b, at = key + 16 * block;
     const int id = __shfl_sync(0xffffffffu, page, block);
     r.scale[b] = 0u;
 #pragma unroll
@@ -76,11 +86,7 @@ __device__ __forceinline__ void read_raw4(const Paged4Params& p, int h, int key,
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) r.code[b][u][w] = 0u;
     if (at >= k_hi) continue;  // past the keys: zeros
-    if (id < 0 || id >= p.num_pages) {
-      int abort_flag = 0;
-      if (lane == 0) report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
-      continue;
-    }
+    if (id < 0) continue;      // no page (reported where its number was read)
     const uint8_t* const blk =
         p.pages + kv4_block_at(id, p.Hkv, h, p.page_shift, at & (p.page_size - 1), Block::kBytes);
 #pragma unroll
@@ -112,18 +118,18 @@ __device__ __forceinline__ void read_raw4(const Paged4Params& p, int h, int key,
   }
 }
 
-// Turns them into rows 64 half .. 64 half + 63 of a tile.
+// Turns them into rows 32 part .. 32 part + 31 of a tile.
 template <int D, bool kV>
-__device__ __forceinline__ void store_raw4(const Raw4<D>& r, int half, uint8_t* tile) {
+__device__ __forceinline__ void store_raw4(const Raw4<D>& r, int part, uint8_t* tile) {
   const int lane = (int)lane_id(), g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
+  for (int b = 0; b < 2; ++b) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const uint32_t s = e4m3_to_half(r.scale[b] >> (16 * u) & 0xffffu);
       if constexpr (!kV) {
         // Key g of these eight, channels t d/4 ..: a word is a chunk of eight.
-        const int row = 64 * half + 16 * b + 8 * u + g;
+        const int row = 32 * part + 16 * b + 8 * u + g;
         const uint32_t s0 = __byte_perm(s, s, 0x1010), s1 = __byte_perm(s, s, 0x3232);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
@@ -153,7 +159,7 @@ __device__ __forceinline__ void store_raw4(const Raw4<D>& r, int half, uint8_t* 
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             // (Lanes of odd g store the odd key first.)
-            const int key = k ^ (g & 1), row = 64 * half + 16 * b + 8 * u + 2 * t + key;
+            const int key = k ^ (g & 1), row = 32 * part + 16 * b + 8 * u + 2 * t + key;
             const uint32_t sel = key ? 0x7632u : 0x5410u;
             *reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + row * 128 +
                                       (((ch & 7) ^ (row & 7)) << 4)) =
@@ -166,48 +172,78 @@ __device__ __forceinline__ void store_raw4(const Raw4<D>& r, int half, uint8_t* 
   }
 }
 
-// The warp that makes the K (or V) tiles of the CTA's segments.
-template <int D, int S, int kRing, bool kV, class Smem>
-__device__ __forceinline__ void paged4_produce_tiles(const Paged4Params& p, Smem& sm) {
+// One of the warps that make the tiles of the CTA's segments: part `part` of each.
+template <int D, int S, int kRing, class Smem>
+__device__ __forceinline__ void paged4_produce_tiles(const Paged4Params& p, Smem& sm, int part) {
   volatile int* abortf = &sm.abort_flag;
   const int lane = (int)lane_id();
   bool ok = true;
-  int c = kV ? 1 : 0;  // ring uses
-  for (int m = 0; ok; ++m) {
-    const int is = m % kRing;
-    ok = mbar_wait(&sm.item_full[is], (m / kRing) & 1, p.status, abortf, kSitePgItemFull);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    const PagedItem& it = sm.item[is];
-    const int end = it.end, nj = it.nj, h = it.h, key0 = it.key, k_hi = it.k_hi, seq = it.b;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.item_empty[is]);
-    if (end) break;
-    if (nj == 0) continue;
-    const int* const list = p.page_table + (long long)seq * p.max_pages;
-    auto pages = [&](int j) -> int {  // of tile j's blocks, in lanes 0 .. 7
-      const int key = key0 + j * kTile + 16 * (lane & 7);
-      return j < nj && key < k_hi ? list[key >> p.page_shift] : 0;
-    };
-    int page = pages(0), next = pages(1);
-    Raw4<D> a, b;
-    read_raw4<D, kV>(p, h, key0, k_hi, page, 0, a);
-    for (int j = 0; j < nj && ok; ++j, c += 2) {
-      const int slot = c % S, key = key0 + j * kTile;
-      read_raw4<D, kV>(p, h, key, k_hi, page, 1, b);
-      if (c >= S)
-        ok = mbar_wait(&sm.kv_empty[slot], (c / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      store_raw4<D, kV>(a, 0, sm.kv[slot]);
-      page = next;
-      next = pages(j + 2);
-      if (j + 1 < nj) read_raw4<D, kV>(p, h, key + kTile, k_hi, page, 0, a);
-      store_raw4<D, kV>(b, 1, sm.kv[slot]);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.kv_full[slot]);
+  // The tile that is read next: its segment's place, and its blocks' pages in lanes
+  // 0 .. 7, with those of the tile behind it.
+  int m = -1, j = 0, nj = 0, h = 0, key0 = 0, k_hi = 0, seq = 0, page = 0, next = 0;
+  bool end = false;
+  auto pages = [&](int j) -> int {
+    const int key = key0 + j * kTile + 16 * (lane & 7);
+    if (j >= nj || key >= k_hi) return 0;
+    int id = p.page_table[(long long)seq * p.max_pages + (key >> p.page_shift)];
+    if (id < 0 || id >= p.num_pages) {
+      int abort_flag = 0;
+      report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
+      id = -1;
     }
+    return id;
+  };
+  auto step = [&] {
+    if (++j < nj) {
+      page = next;
+      next = pages(j + 1);
+      return;
+    }
+    do {  // the next segment with keys
+      const int is = ++m % kRing;
+      ok = mbar_wait(&sm.item_full[is], (m / kRing) & 1, p.status, abortf, kSitePgItemFull);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      const PagedItem& it = sm.item[is];
+      end = it.end != 0;
+      nj = it.nj, h = it.h, key0 = it.key, k_hi = it.k_hi, seq = it.b;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.item_empty[is]);
+    } while (!end && nj == 0);
+    j = 0;
+    if (end) return;
+    page = pages(0);
+    next = pages(1);
+  };
+  auto ready = [&](int c) -> bool {
+    if (c >= S)
+      ok = mbar_wait(&sm.kv_empty[c % S], (c / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
+    ok = __all_sync(0xffffffffu, ok);
+    return ok;
+  };
+  auto hand_on = [&](int c) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.kv_full[c % S]);
+  };
+  Raw4<D> k, v;
+  j = -1;
+  step();
+  if (ok && !end) {
+    read_raw4<D, false>(p, h, key0, k_hi, page, part, k);
+    read_raw4<D, true>(p, h, key0, k_hi, page, part, v);
+  }
+  for (int c = 0; ok && !end; c += 2) {
+    if (!ready(c)) break;
+    store_raw4<D, false>(k, part, sm.kv[c % S]);
+    hand_on(c);
+    step();
+    if (!ok) break;
+    if (!end) read_raw4<D, false>(p, h, key0 + j * kTile, k_hi, page, part, k);
+    if (!ready(c + 1)) break;
+    store_raw4<D, true>(v, part, sm.kv[(c + 1) % S]);
+    hand_on(c + 1);
+    if (!end) read_raw4<D, true>(p, h, key0 + j * kTile, k_hi, page, part, v);
   }
   __syncwarp();
 }

@@ -239,9 +239,10 @@ __device__ __noinline__ void store_box(uint32_t colO, float own, uint8_t* out,
 // The prompt kernel's work on CTA `cta` of the `ctas` that share the phase's
 // list.  kStarted: the caller has waited for the prior grid.
 //
-// kFour: over the cache in 4 bits (fa_kv4.cuh).  Warps 10 and 11 turn the codes of
-// V and K into fp16 tiles, warp 8 has the list and Q only; the products run in
-// fp16, and the softmax warps scale each row of Q to its range first.
+// kFour: over the cache in 4 bits (fa_kv4.cuh).  Four more warps, 12-15, turn its
+// codes into fp16 tiles, warp 8 has the list and Q only, 10 is idle too; the
+// products run in fp16, and the softmax warps scale each row of Q to its range
+// first.
 template <int D, bool kNeg, bool kStarted, bool kFour = false>
 __device__ __forceinline__ void prompt_cta(
     const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const CUtensorMap* to,
@@ -253,14 +254,17 @@ __device__ __forceinline__ void prompt_cta(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int* abortf = &sm.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5;
-  constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpLoadV = 10;
+  constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpLoadV = 10, kWarpTiles = 12;
+  constexpr int kThreads = kFour ? kPaged4Threads : kPagedThreads;
+  constexpr int kRegsCompute = kFour ? kPaged4RegsCompute : kPagedRegsCompute;
+  constexpr int kRegsLoad = kFour ? kPaged4RegsList : kPagedRegsLoad;
 
   if (tid == 0) {
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
     if constexpr (kFour) mbar_init(&sm.q_half, 256);
     for (int s = 0; s < S; ++s) {
-      mbar_init(&sm.kv_full[s], 1);
+      mbar_init(&sm.kv_full[s], kFour ? 4 : 1);
       mbar_init(&sm.kv_empty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -272,9 +276,9 @@ __device__ __forceinline__ void prompt_cta(
     }
     for (int i = 0; i < kPromptRing; ++i) {
       mbar_init(&sm.item_full[i], 1);
-      // Read by the issuing thread, the V warp (kFour: and the K warp) and the
-      // eight softmax warps.
-      mbar_init(&sm.item_empty[i], (kFour ? 3 : 2) + 8);
+      // Read by the issuing thread, the V warp (kFour: the four that make tiles)
+      // and the eight softmax warps.
+      mbar_init(&sm.item_empty[i], (kFour ? 5 : 2) + 8);
     }
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -294,7 +298,7 @@ __device__ __forceinline__ void prompt_cta(
   if (ph.tile_tokens * p.G < kTile) {
     // Rows no box fills: any finite values do (their results are not stored),
     // zeros never move the running maximum.
-    for (int i = tid; i < (int)sizeof(sm.q) / 16; i += kPagedThreads)
+    for (int i = tid; i < (int)sizeof(sm.q) / 16; i += kThreads)
       reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
   }
@@ -320,7 +324,7 @@ __device__ __forceinline__ void prompt_cta(
 
   if (warp == kWarpLoad) {
     // ------------------------------------------------------------ Q and K
-    setmaxnreg_dec<kPagedRegsLoad>();
+    setmaxnreg_dec<kRegsLoad>();
     int n_q = 0;  // units loaded
     auto load_q = [&](const PagedItem& it) {
       if (n_q > 0 &&
@@ -344,14 +348,11 @@ __device__ __forceinline__ void prompt_cta(
     __syncwarp();
   } else if (warp == kWarpLoadV) {
     // ------------------------------------------------------------ V
-    setmaxnreg_dec<kPagedRegsLoad>();
-    if constexpr (kFour)
-      paged4_produce_tiles<D, S, kPromptRing, true>(p, sm);
-    else
-      paged_produce_v<D, S, kPromptRing>(p, sm, tv, nullptr);
+    setmaxnreg_dec<kRegsLoad>();
+    if constexpr (!kFour) paged_produce_v<D, S, kPromptRing>(p, sm, tv, nullptr);
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ products
-    setmaxnreg_dec<kPagedRegsLoad>();
+    setmaxnreg_dec<kRegsLoad>();
     if (lane_id() == 0) {
       // (In the descriptor, fp16 is 0 where bf16 is 1.)
       constexpr uint32_t kTypes = kFour ? 1u << 7 | 1u << 10 : 0u;
@@ -453,7 +454,7 @@ __device__ __forceinline__ void prompt_cta(
     __syncwarp();
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax
-    setmaxnreg_inc<kPagedRegsCompute>();
+    setmaxnreg_inc<kRegsCompute>();
     const int t = warp >> 2;  // Q tile
     const int r = tid & 127;  // row of the tile
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -582,10 +583,15 @@ __device__ __forceinline__ void prompt_cta(
     }
     if (lane_id() == 0) bulk_wait_group0();
     __syncwarp();
+  } else if (kFour && warp >= kWarpTiles) {
+    // ------------------------------------------------------------ tiles
+    if constexpr (kFour) {
+      setmaxnreg_dec<kPaged4RegsTiles>();
+      paged4_produce_tiles<D, S, kPromptRing>(p, sm, warp - kWarpTiles);
+    }
   } else {
-    // Idle, but for K in 4 bits: its registers go to the compute warps.
-    setmaxnreg_dec<kPagedRegsLoad>();
-    if constexpr (kFour) paged4_produce_tiles<D, S, kPromptRing, false>(p, sm);
+    // Idle: its registers go to the compute warps.
+    setmaxnreg_dec<kRegsLoad>();
   }
 
   tc_fence_before();
