@@ -39,10 +39,13 @@ struct Kv4Block {
   static __host__ __device__ constexpr int v_scale(int group) { return 17 * D + group * 16; }
 };
 
-// Byte offset of the block of a page's slot.
+// Byte offset of the block of a page's slot: 32-bit factors (num_pages * Hkv is below
+// 2^31, a page's blocks of a head below 2^16 bytes), a 64-bit product.
 __device__ __forceinline__ long long kv4_block_at(int page, int Hkv, int h, int page_shift, int slot,
                                                   int block_bytes) {
-  return ((((long long)page * Hkv + h) << (page_shift - 4)) + (slot >> 4)) * block_bytes;
+  return (long long)((unsigned long long)(uint32_t)(page * Hkv + h) *
+                     (uint32_t)(block_bytes << (page_shift - 4))) +
+         (slot >> 4) * block_bytes;
 }
 
 // Four bytes of two codes each to pairs of fp16, exactly.

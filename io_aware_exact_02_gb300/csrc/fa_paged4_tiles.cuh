@@ -62,15 +62,18 @@ __device__ __forceinline__ void paged4_produce_items(const PagedParams& p, const
   __syncwarp();
 }
 
-// What a lane has read of two blocks: its codes of K or V, and scales.
+// What a lane has read of two blocks: its codes of K or V, and scales with the masks
+// that leave a slot without a key 0 (its codes may be anything, and are finite).
 template <int D>
 struct Raw4 {
   uint32_t code[2][2][D / 32];
-  uint32_t scale[2];  // two 16-bit pieces, of the codes' two
+  uint32_t scale[2][2], mask[2];  // (the second eight keys' mask in the upper half)
 };
 
 // Reads blocks 2 part, 2 part + 1 of the tile whose first key is `key` (keys end at
-// k_hi); `page`: lane b holds the page of the tile's block b.
+// k_hi); `page`: lane b holds the page of the tile's block b.  Straight-line code
+// that looks at nothing it loads: a block past the keys, or without a page, reads
+// page 0.  (With branches around the loads it took the warp 1,200 cycles.)
 template <int D, bool kV>
 __device__ __forceinline__ void read_raw4(const Paged4Params& p, int h, int key, int k_hi, int page,
                                           int part, Raw4<D>& r) {
@@ -79,41 +82,40 @@ __device__ __forceinline__ void read_raw4(const Paged4Params& p, int h, int key,
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     const int block = 2 * part + b, at = key + 16 * block;
-    const int id = __shfl_sync(0xffffffffu, page, block);
-    r.scale[b] = 0u;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w) r.code[b][u][w] = 0u;
-    if (at >= k_hi) continue;  // past the keys: zeros
-    if (id < 0) continue;      // no page (reported where its number was read)
+    int id = __shfl_sync(0xffffffffu, page, block);
+    const bool there = at < k_hi && (unsigned)id < (unsigned)p.num_pages;
+    id = there ? id : 0;
     const uint8_t* const blk =
         p.pages + kv4_block_at(id, p.Hkv, h, p.page_shift, at & (p.page_size - 1), Block::kBytes);
+    const uint8_t* const codes = blk + (kV ? Block::v_code(0, 0) : Block::k_code(0)) + lane * (D / 8);
+    const uint8_t* const scales =
+        blk + (kV ? Block::v_scale(D == 128 ? g : g / 2) + 2 * t
+                  : Block::k_scale(0) + lane * (D == 128 ? 2 : 1));
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const uint8_t* const src =
-          blk + (kV ? Block::v_code(0, 0) : Block::k_code(0)) + (u * 32 + lane) * (D / 8);
       if constexpr (D == 128) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(codes + u * 512));
         r.code[b][u][0] = x.x, r.code[b][u][1] = x.y;
         r.code[b][u][D / 32 - 2] = x.z, r.code[b][u][D / 32 - 1] = x.w;
       } else {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(codes + u * 256));
         r.code[b][u][0] = x.x, r.code[b][u][1] = x.y;
       }
-      uint32_t s;
-      if constexpr (kV) {
-        s = __ldg(reinterpret_cast<const uint16_t*>(blk + Block::v_scale(D == 128 ? g : g / 2) + u * 8 + 2 * t));
-        // Slots past the keys may hold anything, and 0 * NaN is NaN.
-        const int first = at + u * 8 + 2 * t;
-        if (first >= k_hi) s = 0u;
-        if (first + 1 >= k_hi) s &= 0xffu;
-      } else if constexpr (D == 128) {
-        s = __ldg(reinterpret_cast<const uint16_t*>(blk + Block::k_scale(0) + (u * 32 + lane) * 2));
-      } else {
-        s = __ldg(blk + Block::k_scale(0) + u * 32 + lane);
-      }
-      r.scale[b] |= s << (16 * u);
+      if constexpr (kV)
+        r.scale[b][u] = __ldg(reinterpret_cast<const uint16_t*>(scales + u * 8));
+      else if constexpr (D == 128)
+        r.scale[b][u] = __ldg(reinterpret_cast<const uint16_t*>(scales + u * 64));
+      else
+        r.scale[b][u] = __ldg(scales + u * 32);
+    }
+    if constexpr (kV) {
+      // Keys of this lane's pairs 2t, 2t + 1 and 8 further on: a byte of mask each.
+      const int n = k_hi - (at + 2 * t);
+      const uint32_t m = (n > 0 ? 0xffu : 0u) | (n > 1 ? 0xff00u : 0u) | (n > 8 ? 0xff0000u : 0u) |
+                         (n > 9 ? 0xff000000u : 0u);
+      r.mask[b] = there ? m : 0u;
+    } else {
+      r.mask[b] = there ? 0xffffffffu : 0u;
     }
   }
 }
@@ -126,21 +128,22 @@ __device__ __forceinline__ void store_raw4(const Raw4<D>& r, int part, uint8_t* 
   for (int b = 0; b < 2; ++b) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const uint32_t s = e4m3_to_half(r.scale[b] >> (16 * u) & 0xffffu);
+      const uint32_t s = e4m3_to_half(r.scale[b][u] & r.mask[b] >> (16 * u));
       if constexpr (!kV) {
         // Key g of these eight, channels t d/4 ..: a word is a chunk of eight.
         const int row = 32 * part + 16 * b + 8 * u + g;
-        const uint32_t s0 = __byte_perm(s, s, 0x1010), s1 = __byte_perm(s, s, 0x3232);
+        // (Lanes of the second 64 channels take the words of their second group first.)
+        const bool swap = D == 128 && (t >> 1) != 0;
+        const uint32_t lo = __byte_perm(s, s, 0x1010), hi = D == 128 ? __byte_perm(s, s, 0x3232) : lo;
+        const uint32_t s0 = swap ? hi : lo, s1 = swap ? lo : hi;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-          // (Lanes of the second 64 channels take the words in another order.)
-          const int w = D == 128 ? i ^ (t >> 1) : i;
-          const uint32_t code = D == 128 && (t >> 1) ? r.code[b][u][i ^ 1] : r.code[b][u][i];
-          const uint32_t sw = D == 128 && i >= 2 ? s1 : s0;  // (w and i are of one half)
+          const int w = swap ? i ^ 2 : i;
+          const uint32_t code = swap ? r.code[b][u][D == 128 ? i ^ 2 : i] : r.code[b][u][i];
           uint32_t x[4];
           e2m1_to_half(code, x);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = half2_mul(x[e], sw);
+          for (int e = 0; e < 4; ++e) x[e] = half2_mul(x[e], i >= 2 ? s1 : s0);
           const int ch = D == 128 ? (t & 1) * 4 + w : 2 * t + w;
           *reinterpret_cast<uint4*>(tile + (D == 128 ? (t >> 1) * (kTile * 128) : 0) + row * 128 +
                                     ((ch ^ (row & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
@@ -180,20 +183,18 @@ __device__ __forceinline__ void paged4_produce_tiles(const Paged4Params& p, Smem
   bool ok = true;
   // The tile that is read next: its segment's place, and its blocks' pages in lanes
   // 0 .. 7, with those of the tile behind it.
-  int m = -1, j = 0, nj = 0, h = 0, key0 = 0, k_hi = 0, seq = 0, page = 0, next = 0;
+  int m = -1, j = 0, nj = 0, h = 0, key0 = 0, k_hi = 0, page = 0, next = 0;
+  const int* list = nullptr;
   bool end = false;
   auto pages = [&](int j) -> int {
     const int key = key0 + j * kTile + 16 * (lane & 7);
-    if (j >= nj || key >= k_hi) return 0;
-    int id = p.page_table[(long long)seq * p.max_pages + (key >> p.page_shift)];
-    if (id < 0 || id >= p.num_pages) {
-      int abort_flag = 0;
-      report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
-      id = -1;
-    }
-    return id;
+    return j < nj && key < k_hi ? list[key >> p.page_shift] : 0;
   };
   auto step = [&] {
+    if ((unsigned)page >= (unsigned)p.num_pages) {  // of the tile just read
+      int abort_flag = 0;
+      report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
+    }
     if (++j < nj) {
       page = next;
       next = pages(j + 1);
@@ -206,7 +207,8 @@ __device__ __forceinline__ void paged4_produce_tiles(const Paged4Params& p, Smem
       if (!ok) return;
       const PagedItem& it = sm.item[is];
       end = it.end != 0;
-      nj = it.nj, h = it.h, key0 = it.key, k_hi = it.k_hi, seq = it.b;
+      nj = it.nj, h = it.h, key0 = it.key, k_hi = it.k_hi;
+      list = p.page_table + (long long)it.b * p.max_pages;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[is]);
     } while (!end && nj == 0);
@@ -256,15 +258,15 @@ __device__ __forceinline__ float q_row_to_half(uint8_t* tile, int r, float c2) {
   uint8_t* const row = tile + r * 128;
   uint32_t top = 0u;
 #pragma unroll
-  for (int c = 0; c < D / 8; ++c) {
-    const uint4 x = *reinterpret_cast<const uint4*>(row + (c >> 3) * (kTile * 128) + (c & 7) * 16);
+  for (int c = 0; c < D / 8; ++c) {  // (in an order of chunks that meets every bank)
+    const uint4 x =
+        *reinterpret_cast<const uint4*>(row + (c >> 3) * (kTile * 128) + ((c ^ r) & 7) * 16);
     top = kv4_top(kv4_top(kv4_top(kv4_top(top, x.x), x.y), x.z), x.w);
   }
   const int e = kv4_row_exponent(top);
   const float f = kv4_pow2(e);
 #pragma unroll
   for (int c = 0; c < D / 8; ++c) {
-    // (The chunks' order in the row does not matter here.)
     uint4* const at = reinterpret_cast<uint4*>(row + (c >> 3) * (kTile * 128) + ((c ^ r) & 7) * 16);
     const uint4 x = *at;
     auto turn = [&](uint32_t w) {
