@@ -100,8 +100,8 @@ static_assert(2 * 128 * kPagedRegsCompute + 128 * kPagedRegsLoad <= kPagedThread
 
 // The prompt kernel over the cache in 4 bits has a warpgroup more, which makes the
 // tiles: launched with kPaged4Regs a thread.
-constexpr int kPaged4Threads = 512, kPaged4Regs = 128, kPaged4RegsCompute = 176,
-              kPaged4RegsList = 72, kPaged4RegsTiles = 88;
+constexpr int kPaged4Threads = 512, kPaged4Regs = 128, kPaged4RegsCompute = 168,
+              kPaged4RegsList = 72, kPaged4RegsTiles = 104;
 static_assert(2 * 128 * kPaged4RegsCompute + 128 * (kPaged4RegsList + kPaged4RegsTiles) <=
                   kPaged4Threads * kPaged4Regs,
               "register split above the launch's total");
