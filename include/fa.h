@@ -402,6 +402,61 @@ int fa_fwd_paged4(const void* q, const void* pages, void* o, float* lse, const i
                   size_t workspace_bytes, void* stream);
 
 /*
+ * The pages of a paged cache as a whole (no counterpart on the pages): for
+ * sequences that share what they have in common, and pools that shrink.
+ *
+ * A page number stands for the same page in every cache of a model: pools
+ * holds n_pools (0 to 256) device pointers, 16-byte aligned, in host memory, and
+ * page_bytes the bytes of a page in each (a multiple of 16; 2 * Hkv * page_size *
+ * d of a bf16 pool, Hkv * page_size * 9 d / 8 of one in 4 bits).  Both arrays are
+ * read by the call only.  page_table: [rows][max_pages] int32, seq_lens: [rows]
+ * int32, the keys of each row's sequence (0: the row is empty); entries past a
+ * sequence's last page mean nothing.  refs: [num_pages] int32, the sequences that
+ * hold a page; 0: it is free.  page_size as above.  The tables are device memory,
+ * read and written by the kernels only; entries outside their bounds record
+ * FA_ERR_PAGE and are left out, and so are the cases named below.
+ *
+ * fa_pages_copy copies page src[k] to page dst[k] in every pool, k < n (device
+ * memory; the pages of dst distinct, and none of them in src).
+ *
+ * fa_pages_fork makes row children[i] a copy of row parents[i], i < n: the whole
+ * pages are shared (refs + 1), a last page that is not full is copied to a free
+ * one, which the child alone holds: the k-th child that needs one takes the k-th
+ * lowest free page.  A parent may have several children.  A child that is listed
+ * twice, is its own parent, or holds keys is left out (FA_ERR_PAGE; of one listed
+ * twice, one of its forks takes place), as is one for which no page is left (it
+ * stays empty).  workspace: fa_pages_fork_workspace_size bytes of device memory,
+ * 256-byte aligned.
+ *
+ * fa_pages_free empties the rows rows_list[i], i < n: refs - 1 for every page,
+ * length 0.  A row listed twice is freed once.  A page whose count is 0 already
+ * records FA_ERR_PAGE and keeps it.
+ *
+ * fa_pages_compact moves the pages in use (`live` of them) to the numbers below
+ * live: the highest page in use goes to the lowest free one and so on, in every
+ * pool, in refs and in the tables of all rows.  The pages from live on are free
+ * then; their bytes are left as they were.  live, if not NULL, receives the
+ * number (device memory).  workspace: fa_pages_compact_workspace_size bytes.
+ *
+ * Errors: FA_ERR_ARG, FA_ERR_ALIGN (16 bytes for pools and page_bytes, 4 for the
+ * tables), FA_ERR_WORKSPACE, FA_ERR_DEVICE, FA_ERR_LAUNCH.
+ */
+int fa_pages_copy(const void* const* pools, const size_t* page_bytes, int n_pools, const int* src,
+                  const int* dst, int n, int num_pages, void* stream);
+size_t fa_pages_fork_workspace_size(int num_pages, int n);
+int fa_pages_fork(const int* parents, const int* children, int n, int* page_table, int* seq_lens,
+                  int* refs, int rows, int max_pages, int num_pages, int page_size,
+                  const void* const* pools, const size_t* page_bytes, int n_pools, void* workspace,
+                  size_t workspace_bytes, void* stream);
+int fa_pages_free(const int* rows_list, int n, const int* page_table, int* seq_lens, int* refs,
+                  int rows, int max_pages, int num_pages, int page_size, void* stream);
+size_t fa_pages_compact_workspace_size(int num_pages);
+int fa_pages_compact(int* page_table, const int* seq_lens, int* refs, int rows, int max_pages,
+                     int num_pages, int page_size, const void* const* pools,
+                     const size_t* page_bytes, int n_pools, int* live, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
  * The calls of the paged cache with their arguments as 8-byte words, in the
  * order of the prototypes: for callers that pay by the argument, as a Python
  * binding does (2 of the 4 us that a call takes).  Pointers and integers are
@@ -457,7 +512,8 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  * receives the identifier of the wait or check that raised it (0 if none):
  * 101-199 a wait of the forward kernel, 201-299 one of the backward main
  * kernel, 301-304 the paged cache's tables (row ranges, lengths, positions,
- * page numbers), 311-399 a wait of a paged attention kernel, 1101-1199 a bounds
+ * page numbers), 305-307 the calls on its pages (rows, no free page, reference
+ * counts), 311-399 a wait of a paged attention kernel, 1101-1199 a bounds
  * check of the forward kernels, 1201-1299 one of the backward kernels,
  * 1301-1399 one of the paged attention kernels, FA_SITE_SELFTEST and
  * FA_SITE_SELFTEST_BOUNDS the self tests'.

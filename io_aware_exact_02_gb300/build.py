@@ -24,7 +24,7 @@ LIB = os.path.join(HERE, "libfa.so")
 LIB_CHECKED = os.path.join(HERE, "libfa_checked.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 UNITS = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_pair.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_fp8.cu",
-         "fa_kv.cu", "fa_paged.cu", "fa_paged_prompt.cu", "fa_paged_duo.cu", "fa_kv4.cu", "fa_paged4.cu", "fa_paged4_prompt.cu"]
+         "fa_kv.cu", "fa_paged.cu", "fa_paged_prompt.cu", "fa_paged_duo.cu", "fa_kv4.cu", "fa_paged4.cu", "fa_paged4_prompt.cu", "fa_pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler",
          "-fvisibility=default", "--expt-relaxed-constexpr"]

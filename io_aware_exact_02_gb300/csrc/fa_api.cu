@@ -13,6 +13,7 @@
 #include <mutex>
 
 #include "fa_internal.h"
+#include "fa_pages.h"
 #include "sm100_ptx.cuh"
 
 namespace fa {
@@ -725,6 +726,69 @@ int fwd_paged4_impl(const void* q, const void* pages, void* o, float* lse, const
   return launch_fwd_paged4(p, d, static_cast<cudaStream_t>(stream));
 }
 
+// The operators on pages: sizes and tables (rows 0: none), then the caches.
+int pages_shape(int n, int rows, int max_pages, int num_pages, int page_size, PagesParams& p) {
+  if (n < 1 || num_pages < 1) return FA_ERR_ARG;
+  p = PagesParams();
+  p.n = n;
+  p.num_pages = num_pages;
+  p.ranges = (int)(((long long)num_pages + kPagesRange - 1) / kPagesRange);
+  if (rows == 0) return FA_OK;
+  if (rows < 1 || max_pages < 1) return FA_ERR_ARG;
+  p.rows = rows;
+  p.max_pages = max_pages;
+  p.page_size = page_size;
+  return paged_shape(1, rows, 1, 1, 64, num_pages, page_size, max_pages, &p.page_shift);
+}
+
+int pages_pools(const void* const* pools, const size_t* page_bytes, int n_pools, PagesList& list,
+                bool& alike) {
+  if (n_pools < 0 || n_pools > kPagesPools || (n_pools > 0 && (!pools || !page_bytes)))
+    return FA_ERR_ARG;
+  list.n = n_pools;
+  list.chunks = 0;
+  list.stride = 0;
+  list.base[0] = 0;
+  list.bytes[0] = 0;
+  alike = true;
+  long long chunks = 0;
+  for (int i = 0; i < n_pools; ++i) {
+    if (!pools[i] || page_bytes[i] < 1 || page_bytes[i] > ((size_t)1 << 30)) return FA_ERR_ARG;
+    if (!aligned16(pools[i]) || page_bytes[i] % 16 != 0) return FA_ERR_ALIGN;
+    list.base[i] = (unsigned long long)reinterpret_cast<uintptr_t>(pools[i]);
+    list.bytes[i] = (unsigned)page_bytes[i];
+    list.first[i] = (int)chunks;
+    chunks += pages_chunks(page_bytes[i]);
+    if (i == 1) list.stride = (long long)(list.base[1] - list.base[0]);
+    alike = alike && list.bytes[i] == list.bytes[0] &&
+            (long long)(list.base[i] - list.base[0]) == i * list.stride;
+  }
+  if (chunks > 0x7fffffff) return FA_ERR_ARG;
+  list.chunks = (int)chunks;
+  return FA_OK;
+}
+
+PagesAlike pages_alike(const PagesList& list) {
+  PagesAlike a;
+  a.n = list.n;
+  a.chunks = list.chunks;
+  a.stride = list.stride;
+  a.base[0] = list.base[0];
+  a.bytes[0] = list.bytes[0];
+  a.first[0] = 0;
+  return a;
+}
+
+void pages_workspace(PagesParams& p, void* workspace, const PagesWorkspace& w) {
+  char* const at = static_cast<char*>(workspace);
+  p.range_used = reinterpret_cast<int*>(at + w.range_used);
+  p.counts = reinterpret_cast<int*>(at + w.counts);
+  p.from = reinterpret_cast<int*>(at + w.from);
+  p.to = reinterpret_cast<int*>(at + w.to);
+  p.child = reinterpret_cast<PagesChild*>(at + w.child);
+  p.rank = reinterpret_cast<int*>(at + w.rank);
+}
+
 // Reads a call's arguments from an array of 8-byte words, one after another
 // (which need not be aligned); ok turns false on an int that does not fit.
 struct ArgWords {
@@ -1034,6 +1098,110 @@ int fa_fwd_paged4_words(const void* args, int n) {
   return fwd_paged4_impl(q, pages, o, lse, page_table, seq_lens, cu_q, T, B, Hq, Hkv, d, q_stride,
                          num_pages, page_size, max_pages, max_q, causal, scale, k_scale, v_scale,
                          workspace, workspace_bytes, stream);
+}
+
+int fa_pages_copy(const void* const* pools, const size_t* page_bytes, int n_pools, const int* src,
+                  const int* dst, int n, int num_pages, void* stream) {
+  if (!src || !dst) return FA_ERR_ARG;
+  PagesParams p;
+  PagesList list;
+  bool alike;
+  int rc = pages_shape(n, 0, 0, num_pages, 0, p);
+  if (rc == FA_OK) rc = pages_pools(pools, page_bytes, n_pools, list, alike);
+  if (rc != FA_OK) return rc;
+  if (!aligned4(src) || !aligned4(dst)) return FA_ERR_ALIGN;
+  DeviceState* ds;
+  if ((rc = device_state(&ds)) != FA_OK) return rc;
+  p.src = src;
+  p.dst = dst;
+  p.status = ds->status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return alike ? launch_pages_copy(p, pages_alike(list), ds->sm_count, s)
+               : launch_pages_copy(p, list, ds->sm_count, s);
+}
+
+size_t fa_pages_fork_workspace_size(int num_pages, int n) {
+  return num_pages < 1 || n < 1 ? 0 : pages_workspace_layout(num_pages, n).total;
+}
+
+int fa_pages_fork(const int* parents, const int* children, int n, int* page_table, int* seq_lens,
+                  int* refs, int rows, int max_pages, int num_pages, int page_size,
+                  const void* const* pools, const size_t* page_bytes, int n_pools, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+  if (!parents || !children || !page_table || !seq_lens || !refs || rows < 1) return FA_ERR_ARG;
+  PagesParams p;
+  PagesList list;
+  bool alike;
+  int rc = pages_shape(n, rows, max_pages, num_pages, page_size, p);
+  if (rc == FA_OK) rc = pages_pools(pools, page_bytes, n_pools, list, alike);
+  if (rc != FA_OK) return rc;
+  if (!aligned4(parents) || !aligned4(children) || !aligned4(page_table) || !aligned4(seq_lens) ||
+      !aligned4(refs))
+    return FA_ERR_ALIGN;
+  const PagesWorkspace w = pages_workspace_layout(num_pages, n);
+  if (!workspace_ok(workspace, workspace_bytes, w.total)) return FA_ERR_WORKSPACE;
+  DeviceState* ds;
+  if ((rc = device_state(&ds)) != FA_OK) return rc;
+  p.parents = parents;
+  p.children = children;
+  p.page_table = page_table;
+  p.seq_lens = seq_lens;
+  p.refs = refs;
+  p.status = ds->status;
+  pages_workspace(p, workspace, w);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return alike ? launch_pages_fork(p, pages_alike(list), ds->sm_count, s)
+               : launch_pages_fork(p, list, ds->sm_count, s);
+}
+
+int fa_pages_free(const int* rows_list, int n, const int* page_table, int* seq_lens, int* refs,
+                  int rows, int max_pages, int num_pages, int page_size, void* stream) {
+  if (!rows_list || !page_table || !seq_lens || !refs || rows < 1) return FA_ERR_ARG;
+  PagesParams p;
+  int rc = pages_shape(n, rows, max_pages, num_pages, page_size, p);
+  if (rc != FA_OK) return rc;
+  if (!aligned4(rows_list) || !aligned4(page_table) || !aligned4(seq_lens) || !aligned4(refs))
+    return FA_ERR_ALIGN;
+  DeviceState* ds;
+  if ((rc = device_state(&ds)) != FA_OK) return rc;
+  p.parents = rows_list;
+  p.page_table = const_cast<int*>(page_table);
+  p.seq_lens = seq_lens;
+  p.refs = refs;
+  p.status = ds->status;
+  return launch_pages_free(p, static_cast<cudaStream_t>(stream));
+}
+
+size_t fa_pages_compact_workspace_size(int num_pages) {
+  return num_pages < 1 ? 0 : pages_workspace_layout(num_pages, 0).total;
+}
+
+int fa_pages_compact(int* page_table, const int* seq_lens, int* refs, int rows, int max_pages,
+                     int num_pages, int page_size, const void* const* pools,
+                     const size_t* page_bytes, int n_pools, int* live, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (!page_table || !seq_lens || !refs || rows < 1) return FA_ERR_ARG;
+  PagesParams p;
+  PagesList list;
+  bool alike;
+  int rc = pages_shape(1, rows, max_pages, num_pages, page_size, p);
+  if (rc == FA_OK) rc = pages_pools(pools, page_bytes, n_pools, list, alike);
+  if (rc != FA_OK) return rc;
+  if (!aligned4(page_table) || !aligned4(seq_lens) || !aligned4(refs) || !aligned4(live))
+    return FA_ERR_ALIGN;
+  const PagesWorkspace w = pages_workspace_layout(num_pages, 0);
+  if (!workspace_ok(workspace, workspace_bytes, w.total)) return FA_ERR_WORKSPACE;
+  DeviceState* ds;
+  if ((rc = device_state(&ds)) != FA_OK) return rc;
+  p.page_table = page_table;
+  p.seq_lens = const_cast<int*>(seq_lens);
+  p.refs = refs;
+  p.live = live;
+  p.status = ds->status;
+  pages_workspace(p, workspace, w);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return alike ? launch_pages_compact(p, pages_alike(list), ds->sm_count, s)
+               : launch_pages_compact(p, list, ds->sm_count, s);
 }
 
 int fa_kv_append_words(const void* args, int n) {

@@ -44,6 +44,7 @@ FA_NOALLOC_SCRATCH_BYTES = 32 << 20
 # Every symbol include/fa.h declares, with (restype, argtypes).
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _ll = ctypes.c_longlong
+_cp = ctypes.c_char_p
 _ip = ctypes.POINTER(ctypes.c_int)
 SIGNATURES = {
     "fa_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp]),
@@ -74,6 +75,12 @@ SIGNATURES = {
     "fa_kv4_read": (_i, [_vp] * 6 + [_i] * 4 + [_ll] * 2 + [_i] * 3 + [_f] * 2 + [_vp]),
     "fa_fwd_paged4_workspace_size": (_sz, [_i] * 6),
     "fa_fwd_paged4": (_i, [_vp] * 7 + [_i] * 5 + [_ll] + [_i] * 5 + [_f] * 3 + [_vp, _sz, _vp]),
+    "fa_pages_copy": (_i, [_cp, _cp, _i, _vp, _vp, _i, _i, _vp]),
+    "fa_pages_fork_workspace_size": (_sz, [_i, _i]),
+    "fa_pages_fork": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _cp, _cp, _i, _vp, _sz, _vp]),
+    "fa_pages_free": (_i, [_vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _vp]),
+    "fa_pages_compact_workspace_size": (_sz, [_i]),
+    "fa_pages_compact": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _cp, _cp, _i, _vp, _vp, _sz, _vp]),
     "fa_kv4_append_words": (_i, [ctypes.c_char_p, _i]),
     "fa_kv4_read_words": (_i, [ctypes.c_char_p, _i]),
     "fa_fwd_paged4_words": (_i, [ctypes.c_char_p, _i]),
@@ -903,6 +910,168 @@ def fwd_paged4(q, pages, page_table, seq_lens, cu_q, max_q=None, causal: bool = 
     if rc != FA_OK:
         _check("fa_fwd_paged4", rc)
     return out, lse
+
+
+def _pools(pools, num_pages, dev):
+    """The caches of a call on pages, as host arrays of addresses and of a page's
+    bytes, and their number.  pools: a tensor (caches, num_pages, ...) or a
+    sequence of tensors (num_pages, ...)."""
+    if isinstance(pools, torch.Tensor):
+        if (not pools.is_cuda or pools.get_device() != dev or not pools.is_contiguous()
+                or pools.dim() < 3 or pools.shape[1] != num_pages):
+            raise ValueError("pools must be a contiguous tensor (caches, %d, ...) on cuda:%d, got "
+                             "%s on %s" % (num_pages, dev, tuple(pools.shape), pools.device))
+        n, base = pools.shape[0], pools.data_ptr()
+        size = pools.stride(1) * pools.element_size()
+        step = size * num_pages
+        return (struct.pack("%dQ" % n, *range(base, base + n * step, step)) if step else b"",
+                struct.pack("Q", size) * n, n)
+    at, sizes = [], []
+    for t in pools:
+        if (not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev
+                or not t.is_contiguous() or t.dim() < 2 or t.shape[0] != num_pages):
+            raise ValueError("every pool must be a contiguous tensor (%d, ...) on cuda:%d"
+                             % (num_pages, dev))
+        at.append(t.data_ptr())
+        sizes.append(t.stride(0) * t.element_size())
+    n = len(at)
+    return struct.pack("%dQ" % n, *at), struct.pack("%dQ" % n, *sizes), n
+
+
+def _book(page_table, seq_lens, refs, lists):
+    """Checks the tables of a call on pages; returns their device and sizes."""
+    ok = False
+    try:
+        dev, (rows, width), (num_pages,) = page_table.get_device(), page_table.shape, refs.shape
+        ok = (dev >= 0 and seq_lens.shape == (rows,) and page_table.dtype is _I32
+              and seq_lens.dtype is _I32 and refs.dtype is _I32
+              and seq_lens.get_device() == dev and refs.get_device() == dev
+              and page_table.is_contiguous() and seq_lens.is_contiguous() and refs.is_contiguous())
+        for name, t in lists:
+            ok = (ok and t.dtype is _I32 and t.get_device() == dev and t.dim() == 1
+                  and t.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        ok = False
+    if not ok:
+        if not isinstance(page_table, torch.Tensor) or not page_table.is_cuda or page_table.dim() != 2:
+            raise ValueError("page_table must be a CUDA tensor of shape (rows, max_pages)")
+        dev, rows = page_table.get_device(), page_table.shape[0]
+        for n, t, s in (("page_table", page_table, tuple(page_table.shape)),
+                        ("seq_lens", seq_lens, (rows,)),
+                        ("refs", refs, getattr(refs, "shape", ())[:1]),
+                        *((n, t, getattr(t, "shape", ())[:1]) for n, t in lists)):
+            _check_one(n, t, s, _I32, dev)
+        raise ValueError("arguments of other types, shapes or devices than the call takes")
+    return dev, rows, width, num_pages
+
+
+def _with_workspace(workspace, need, dev, stream, call):
+    """call(address, bytes) with the caller's workspace, or one from torch's allocator
+    (as in _fwd_paged)."""
+    if workspace is not None:
+        if (not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev
+                or not workspace.is_contiguous()):
+            _refuse("workspace", workspace, getattr(workspace, "shape", ()),
+                    getattr(workspace, "dtype", None), dev)
+        return call(workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(max(need, 1), stream)
+    try:
+        return call(ws, need)
+    finally:
+        torch._C._cuda_cudaCachingAllocator_raw_delete(ws)
+
+
+def pages_copy(src, dst, pools):
+    """Copy page src[k] to page dst[k] (int32 tensors) in every cache.  ``pools``: a
+    tensor (caches, num_pages, ...), or a sequence of tensors (num_pages, ...)
+    such as the k_pages and v_pages of every layer."""
+    if (not isinstance(src, torch.Tensor) or not src.is_cuda or src.dim() != 1):
+        raise ValueError("src must be a CUDA tensor of shape (n,)")
+    dev, n = src.get_device(), src.shape[0]
+    for name, t in (("src", src), ("dst", dst)):
+        _check_one(name, t, (n,), _I32, dev)
+    num_pages = pools.shape[1] if isinstance(pools, torch.Tensor) else pools[0].shape[0]
+    at, sizes, count = _pools(pools, num_pages, dev)
+    with torch.cuda.device(dev):
+        rc = (_lib or load()).fa_pages_copy(at, sizes, count, src.data_ptr(), dst.data_ptr(), n,
+                                            num_pages, _current_stream(dev))
+    _check("fa_pages_copy", rc)
+
+
+@functools.lru_cache(maxsize=256)
+def pages_fork_workspace_size(num_pages, n) -> int:
+    return int(load().fa_pages_fork_workspace_size(num_pages, n))
+
+
+def pages_fork(parents, children, page_table, seq_lens, refs, pools, page_size: int,
+               workspace=None):
+    """Make row children[i] of the tables a copy of row parents[i] (int32 tensors):
+    whole pages are shared, a last page that is not full is copied to the lowest
+    free one, in every cache of ``pools`` (see pages_copy).  page_table (rows,
+    max_pages), seq_lens (rows,) and refs (num_pages,), how many sequences hold
+    each page, are updated in place.  Children have to be empty rows."""
+    dev, rows, width, num_pages = _book(page_table, seq_lens, refs,
+                                        (("parents", parents), ("children", children)))
+    n = parents.shape[0]
+    if children.shape[0] != n:
+        raise ValueError("children has shape %s, expected (%d,)" % (tuple(children.shape), n))
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return pages_fork(parents, children, page_table, seq_lens, refs, pools, page_size,
+                              workspace)
+    at, sizes, count = _pools(pools, num_pages, dev)
+    lib, stream = _lib or load(), _current_stream(dev)
+    rc = _with_workspace(
+        workspace, pages_fork_workspace_size(num_pages, n), dev, stream,
+        lambda ws, size: lib.fa_pages_fork(
+            parents.data_ptr(), children.data_ptr(), n, page_table.data_ptr(), seq_lens.data_ptr(),
+            refs.data_ptr(), rows, width, num_pages, page_size, at, sizes, count, ws, size, stream))
+    if rc != FA_OK:
+        _check("fa_pages_fork", rc)
+
+
+def pages_free(rows, page_table, seq_lens, refs, page_size: int):
+    """Empty the rows listed (int32 tensor): every page of theirs counts one less in
+    refs, their lengths become 0."""
+    dev, n_rows, width, num_pages = _book(page_table, seq_lens, refs, (("rows", rows),))
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return pages_free(rows, page_table, seq_lens, refs, page_size)
+    rc = (_lib or load()).fa_pages_free(
+        rows.data_ptr(), rows.shape[0], page_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(),
+        n_rows, width, num_pages, page_size, _current_stream(dev))
+    if rc != FA_OK:
+        _check("fa_pages_free", rc)
+
+
+@functools.lru_cache(maxsize=256)
+def pages_compact_workspace_size(num_pages) -> int:
+    return int(load().fa_pages_compact_workspace_size(num_pages))
+
+
+def pages_compact(page_table, seq_lens, refs, pools, page_size: int, live=None, workspace=None):
+    """Move the pages in use to the lowest numbers, in every cache of ``pools`` (see
+    pages_copy), in refs and in the rows of page_table, so that the pool can be
+    cut behind them.  ``live`` (int32 tensor of one, allocated if not given)
+    receives how many are in use, and is returned."""
+    dev, rows, width, num_pages = _book(page_table, seq_lens, refs, ())
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return pages_compact(page_table, seq_lens, refs, pools, page_size, live, workspace)
+    if live is None:
+        live = torch.empty(1, dtype=_I32, device=page_table.device)
+    else:
+        _check_one("live", live, (1,), _I32, dev)
+    at, sizes, count = _pools(pools, num_pages, dev)
+    lib, stream = _lib or load(), _current_stream(dev)
+    rc = _with_workspace(
+        workspace, pages_compact_workspace_size(num_pages), dev, stream,
+        lambda ws, size: lib.fa_pages_compact(
+            page_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), rows, width, num_pages,
+            page_size, at, sizes, count, live.data_ptr(), ws, size, stream))
+    if rc != FA_OK:
+        _check("fa_pages_compact", rc)
+    return live
 
 
 def device_status(stream=None):
