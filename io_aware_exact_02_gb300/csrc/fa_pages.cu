@@ -192,15 +192,15 @@ __global__ void __launch_bounds__(kThreads) fa_pages_plan_kernel(const PagesPara
   }
 }
 
-// Copies pages from[k] to to[k], k < n, in all pools: chunks of kChunk bytes, dealt to
-// the CTAs in turn.
+// Copies pages from[k] to to[k], k < n, in all pools: chunks of up to kChunk bytes,
+// dealt to the CTAs in turn.
 template <int N>
 __device__ __forceinline__ void copy_pages(const PagesParams& p, const PagesPools<N>& pools,
                                            const int* from, const int* to, int n) {
   const long long total = (long long)n * pools.chunks;
   for (long long w = blockIdx.x; w < total; w += gridDim.x) {
     const int k = (int)(w / pools.chunks);
-    int chunk = (int)(w - (long long)k * pools.chunks), pool = 0;
+    int chunk = (int)(w - (long long)k * pools.chunks), pool = 0, each;
     char* base = reinterpret_cast<char*>(pools.base[0]);
     unsigned bytes = pools.bytes[0];
     if constexpr (N > 1) {
@@ -213,14 +213,18 @@ __device__ __forceinline__ void copy_pages(const PagesParams& p, const PagesPool
           hi = mid;
       }
       chunk -= pools.first[pool];
+      each = (pool + 1 < pools.n ? pools.first[pool + 1] : pools.chunks) - pools.first[pool];
       base = reinterpret_cast<char*>(pools.base[pool]);
       bytes = pools.bytes[pool];
     } else {
-      const int each = pools.chunks / pools.n;
+      each = pools.chunks / pools.n;
       pool = chunk / each;
       chunk -= pool * each;
       base += pool * pools.stride;
     }
+    // A page's chunks are of one size: [lo, hi) is this one's.
+    const unsigned part = ((bytes >> 4) + each - 1) / each << 4;
+    const unsigned lo = chunk * part, hi = min(lo + part, bytes);
     const int src = from[k], dst = to[k];
     if (src < 0 || src >= p.num_pages || dst < 0 || dst >= p.num_pages) {
       if (threadIdx.x == 0) report(p.status, kSitePagedPage);
@@ -231,13 +235,13 @@ __device__ __forceinline__ void copy_pages(const PagesParams& p, const PagesPool
     uint4 x[kCopyEach];
 #pragma unroll
     for (int i = 0; i < kCopyEach; ++i) {
-      const unsigned at = (unsigned)chunk * kChunk + (i * kCopyThreads + threadIdx.x) * 16;
-      if (at < bytes) x[i] = *reinterpret_cast<const uint4*>(s + at);
+      const unsigned at = lo + (i * kCopyThreads + threadIdx.x) * 16;
+      if (at < hi) x[i] = *reinterpret_cast<const uint4*>(s + at);
     }
 #pragma unroll
     for (int i = 0; i < kCopyEach; ++i) {
-      const unsigned at = (unsigned)chunk * kChunk + (i * kCopyThreads + threadIdx.x) * 16;
-      if (at < bytes) *reinterpret_cast<uint4*>(d + at) = x[i];
+      const unsigned at = lo + (i * kCopyThreads + threadIdx.x) * 16;
+      if (at < hi) *reinterpret_cast<uint4*>(d + at) = x[i];
     }
   }
 }
