@@ -7,6 +7,12 @@
 // product and difference of the rotation rounded by itself, so that a code does
 // not depend on how the compiler joins them.
 //
+// Bound by memory, but for the quantisation: 16,384 rows of 32 query and 8 key/value
+// heads, d = 128: append 70 us (5.0 TB/s of the 6.8 that a copy reaches; keys and
+// values alone 35 us, of 1.5 TB/s: some 20 instructions a number), reading back 20 us
+// (4.4 TB/s).  Twice as many registers a thread, two rows to find a place for at a
+// time, made the append 106 us.
+//
 // A byte of V holds a pair of neighbouring keys.  The row of the even slot
 // writes both where the odd slot's row is new too; an odd slot whose neighbour
 // was there before keeps that one's half.
@@ -47,38 +53,92 @@ __device__ __forceinline__ float top8(const float* y) {
   return m;
 }
 
-// A value row's 16 channels of one group, divided by the tensor's scale.
-__device__ __forceinline__ void quantize_group(const __nv_bfloat16* src, float inv, uint32_t (&code)[2],
-                                               uint32_t& scale) {
-  float y[16], s;
-  widen8(reinterpret_cast<const uint4*>(src)[0], y);
-  widen8(reinterpret_cast<const uint4*>(src)[1], y + 8);
+// Infinities (of a group whose largest magnitude is one) to numbers beyond every
+// code's, for kv4_quotient.
+template <int N>
+__device__ __forceinline__ void bound(float (&y)[N], float top) {
+  if (top != __int_as_float(0x7f800000)) return;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) y[i] = __fmul_rn(y[i], inv);
-  scale = kv4_scale(max_nan(top8(y), top8(y + 8)), s);
-  code[0] = kv4_codes(y, s);
-  code[1] = kv4_codes(y + 8, s);
+  for (int i = 0; i < N; ++i) y[i] = fminf(fmaxf(y[i], -65536.f), 65536.f);
 }
 
-// Eight codes of the even key and eight of the odd one to eight bytes.
-__device__ __forceinline__ uint2 join_codes(uint32_t even, uint32_t odd) {
-  uint32_t r[2];
+// Half of a value row's group, divided by the tensor's scale.
+__device__ __forceinline__ void scaled8(const uint4& x, float inv, float (&y)[8]) {
+  widen8(x, y);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    r[h] = 0;
+  for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(y[i], inv);
+}
+// The largest magnitude of a group.
+__device__ __forceinline__ float top16(const uint4 (&x)[2], float inv) {
+  float y[8];
+  scaled8(x[0], inv, y);
+  const float t = top8(y);
+  scaled8(x[1], inv, y);
+  return max_nan(t, top8(y));
+}
+// Half of a group's quotients.
+__device__ __forceinline__ void quotients8(const uint4& x, float inv, float top, float s, float r,
+                                           float (&y)[8]) {
+  scaled8(x, inv, y);
+  bound(y, top);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = (even >> (16 * h + 4 * i)) & 15u, hi = (odd >> (16 * h + 4 * i)) & 15u;
-      r[h] |= (lo | hi << 4) << (8 * i);
-    }
+  for (int i = 0; i < 8; ++i) y[i] = kv4_quotient(y[i], s, r);
+}
+
+// Where a row goes: its sequence, position, and page (b -1: nowhere).
+struct RowPlace {
+  int b, pos, t0, t1, page;  // t0, t1: the sequence's rows
+};
+
+// The place of row t.  `last`: that of row t - 1, if the CTA has had it (b -1: not):
+// the next row of the same sequence needs no search, and mostly the same page.
+template <class Params>
+__device__ __forceinline__ RowPlace place_row(const Params& p, int t, const RowPlace& last,
+                                              int rope_len) {
+  RowPlace r = last;
+  int abort_flag = 0;
+  if (last.b >= 0 && t < last.t1) {
+    ++r.pos;
+  } else {
+    const PagedRow at = paged_row(p.cu_q, p.seq_lens, p.B, p.T, t, p.status);
+    r.b = at.b;
+    r.pos = at.pos;
+    r.page = -1;
+    if (at.b < 0) return r;
+    r.t0 = p.cu_q[at.b];
+    r.t1 = p.cu_q[at.b + 1];
   }
-  return make_uint2(r[0], r[1]);
+  if (r.pos < 0 || r.pos >= (long long)p.max_pages << p.page_shift ||
+      (rope_len >= 0 && r.pos >= rope_len)) {
+    if (threadIdx.x == 0) report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPosition);
+    r.b = -1;
+    return r;
+  }
+  if (r.page < 0 || (r.pos & (p.page_size - 1)) == 0)
+    r.page = p.page_table[(long long)r.b * p.max_pages + (r.pos >> p.page_shift)];
+  if (r.page < 0 || r.page >= p.num_pages) {
+    if (threadIdx.x == 0) report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
+    r.b = -1;
+  }
+  return r;
 }
 
-// One CTA per row, threads as in fa_kv.cu: a thread owns two 8-channel chunks of
-// every kRows-th head.
+// The ranges of all sequences, those without a row among them, by the threads of
+// all CTAs in turn.
+template <class Params>
+__device__ __forceinline__ void check_ranges(const Params& p) {
+  for (long long b = (long long)blockIdx.x * kThreads + threadIdx.x; b < p.B;
+       b += (long long)gridDim.x * kThreads) {
+    int abort_flag = 0;
+    if (!paged_range_ok(p.cu_q[b], p.cu_q[b + 1], p.T))
+      report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedRows);
+  }
+}
+
+// Row t, threads as in fa_kv.cu: a thread owns two 8-channel chunks of every kRows-th
+// head.
 template <int D>
-__device__ __forceinline__ void append_row(const Kv4AppendParams& p, int t) {
+__device__ __forceinline__ void append_row(const Kv4AppendParams& p, int t, const RowPlace& at) {
   using Block = Kv4Block<D>;
   constexpr int kPairs = D / 16;             // chunk pairs (and groups) of a head
   constexpr int kRows = kThreads / kPairs;   // heads in one sweep of the CTA
@@ -93,29 +153,14 @@ __device__ __forceinline__ void append_row(const Kv4AppendParams& p, int t) {
     cb = pr + half;
     turn = true;
   }
-  const PagedRow at = paged_row(p.cu_q, p.seq_lens, p.B, p.T, t, p.status);
-  if (at.b < 0) return;
-  const long long cap = (long long)p.max_pages << p.page_shift;
-  int abort_flag = 0;
-  if (at.pos < 0 || at.pos >= cap || (rd > 0 && at.pos >= p.rope_len)) {
-    if (threadIdx.x == 0) report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPosition);
-    return;
-  }
-  const int page = p.page_table[(long long)at.b * p.max_pages + (at.pos >> p.page_shift)];
-  if (page < 0 || page >= p.num_pages) {
-    if (threadIdx.x == 0) report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
-    return;
-  }
-  float cs[8], sn[8];
-  if (turn) {
-    const float* tab = p.rope + (long long)at.pos * rd;
-    load8(tab + pr * 8, cs);
-    load8(tab + rd / 2 + pr * 8, sn);
-  }
+  const int page = at.page;
+  // (Read where it is used, from L1 but for the first time: to keep the 16 numbers
+  // through the values' quantisation takes registers that it has not.)
+  const float* const tab = p.rope + (long long)at.pos * rd + pr * 8;
   const int slot = at.pos & (p.page_size - 1), r = slot & 15;
   const int Hq = p.q ? p.Hq : 0;
   const bool odd = (r & 1) != 0;
-  const bool before = odd && t > p.cu_q[at.b], after = !odd && t + 1 < p.cu_q[at.b + 1];
+  const bool before = odd && t > at.t0, after = !odd && t + 1 < at.t1;
   const unsigned group = (kPairs == 8 ? 0xffu : 0xfu) << ((threadIdx.x & 31) & ~(kPairs - 1));
   for (int h = row; h < Hq + 2 * p.Hkv; h += kRows) {
     if (h < Hq) {
@@ -124,6 +169,9 @@ __device__ __forceinline__ void append_row(const Kv4AppendParams& p, int t) {
       uint4 a = *reinterpret_cast<const uint4*>(src + ca * 8);
       uint4 b = *reinterpret_cast<const uint4*>(src + cb * 8);
       if (turn) {
+        float cs[8], sn[8];
+        load8(tab, cs);
+        load8(tab + rd / 2, sn);
         if (p.interleaved) {
           rotate_neighbours(a, cs, sn);
           rotate_neighbours(b, cs + 4, sn + 4);
@@ -144,6 +192,9 @@ __device__ __forceinline__ void append_row(const Kv4AppendParams& p, int t) {
       widen8(*reinterpret_cast<const uint4*>(src + ca * 8), a);
       widen8(*reinterpret_cast<const uint4*>(src + cb * 8), b);
       if (turn) {
+        float cs[8], sn[8];
+        load8(tab, cs);
+        load8(tab + rd / 2, sn);
         if (p.interleaved) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -175,30 +226,44 @@ __device__ __forceinline__ void append_row(const Kv4AppendParams& p, int t) {
         return second ? y : x;
       };
       float sa, sb;
-      const uint32_t ba = kv4_scale(max_nan(ta, other(ca ^ 1)), sa);
-      const uint32_t bb = kv4_scale(max_nan(tb, other(cb ^ 1)), sb);
-      *reinterpret_cast<uint32_t*>(blk + Block::k_code(r) + ca * 4) = kv4_codes(a, sa);
-      *reinterpret_cast<uint32_t*>(blk + Block::k_code(r) + cb * 4) = kv4_codes(b, sb);
+      const float ga = max_nan(ta, other(ca ^ 1)), gb = max_nan(tb, other(cb ^ 1));
+      const uint32_t ba = kv4_scale(ga, sa), bb = kv4_scale(gb, sb);
+      auto codes = [&](float (&y)[8], float top, float s) -> uint32_t {
+        bound(y, top);
+        const float inv = kv4_inverse(s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = kv4_quotient(y[i], s, inv);
+        return kv4_codes({y[0], y[2], y[4], y[6]}, {y[1], y[3], y[5], y[7]});
+      };
+      *reinterpret_cast<uint32_t*>(blk + Block::k_code(r) + ca * 4) = codes(a, ga, sa);
+      *reinterpret_cast<uint32_t*>(blk + Block::k_code(r) + cb * 4) = codes(b, gb, sb);
       if ((ca & 1) == 0) blk[Block::k_scale(r) + (ca >> 1)] = (uint8_t)ba;
       if ((cb & 1) == 0) blk[Block::k_scale(r) + (cb >> 1)] = (uint8_t)bb;
     } else if (!before) {
       const __nv_bfloat16* src = p.v + t * p.v_stride + (long long)hk * D + pr * 16;
-      uint32_t mine[2], next[2] = {0u, 0u}, s_mine, s_next = 0;
-      quantize_group(src, p.v_inv, mine, s_mine);
-      if (after) quantize_group(src + p.v_stride, p.v_inv, next, s_next);
+      // This row's group, and the next row's (else its own once more), divided by the
+      // tensor's scale twice over, to spare registers.
+      const uint4* const other_src = reinterpret_cast<const uint4*>(src + (after ? p.v_stride : 0));
+      const uint4 mine[2] = {reinterpret_cast<const uint4*>(src)[0], reinterpret_cast<const uint4*>(src)[1]};
+      const uint4 next[2] = {other_src[0], other_src[1]};
+      const float tm = top16(mine, p.v_inv), tn = top16(next, p.v_inv);
+      float sm, sn2;
+      const uint32_t s_mine = kv4_scale(tm, sm), s_next = kv4_scale(tn, sn2);
+      const float rm = kv4_inverse(sm), rn = kv4_inverse(sn2);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         // Eight channels: an eighth of d = 64, half of one of d = 128.
         uint2* const dst = reinterpret_cast<uint2*>(
             blk + (D == 128 ? Block::v_code(r, pr) + 8 * i : Block::v_code(r, 2 * pr + i)));
-        uint2 x;
-        if (odd) {
+        float e[8], o[8];
+        quotients8(mine[i], p.v_inv, tm, sm, rm, e);
+        quotients8(next[i], p.v_inv, tn, sn2, rn, o);
+        uint2 x = make_uint2(kv4_codes({e[0], e[1], e[2], e[3]}, {o[0], o[1], o[2], o[3]}),
+                             kv4_codes({e[4], e[5], e[6], e[7]}, {o[4], o[5], o[6], o[7]}));
+        if (odd) {  // the even key's half stays
           const uint2 old = *dst;
-          x = join_codes(0u, mine[i]);
-          x.x |= old.x & 0x0f0f0f0fu;
-          x.y |= old.y & 0x0f0f0f0fu;
-        } else {
-          x = join_codes(mine[i], next[i]);
+          x.x = x.x & 0xf0f0f0f0u | old.x & 0x0f0f0f0fu;
+          x.y = x.y & 0xf0f0f0f0u | old.y & 0x0f0f0f0fu;
         }
         *dst = x;
       }
@@ -211,45 +276,27 @@ __device__ __forceinline__ void append_row(const Kv4AppendParams& p, int t) {
   }
 }
 
+// A CTA takes `run` rows one after another: to find a row's place takes four rounds of
+// loads of which each waits for the one before, to find the next one's none.
 template <int D>
-__global__ void __launch_bounds__(kThreads) fa_kv4_append_kernel(const Kv4AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 8) fa_kv4_append_kernel(const Kv4AppendParams p, int run) {
   launch_dependents();
   wait_prior_grid();
-  append_row<D>(p, (int)blockIdx.x);
-  // The ranges of all sequences, those without a row among them.
-  for (long long b = (long long)blockIdx.x * kThreads + threadIdx.x; b < p.B;
-       b += (long long)p.T * kThreads) {
-    int abort_flag = 0;
-    if (!paged_range_ok(p.cu_q[b], p.cu_q[b + 1], p.T))
-      report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedRows);
+  RowPlace at = {-1, 0, 0, 0, -1};
+  const int t0 = (int)blockIdx.x * run, t1 = min(t0 + run, p.T);
+  for (int t = t0; t < t1; ++t) {
+    at = place_row(p, t, at, p.rope_dim > 0 ? p.rope_len : -1);
+    if (at.b >= 0) append_row<D>(p, t, at);
   }
+  check_ranges(p);
 }
 
-// One CTA per row; a thread takes 16 channels of a key or value head.
+// A thread takes 16 channels of a key or value head.
 template <int D>
-__global__ void __launch_bounds__(kThreads) fa_kv4_read_kernel(const Kv4ReadParams p) {
+__device__ __forceinline__ void read_row(const Kv4ReadParams& p, int t, const RowPlace& at) {
   using Block = Kv4Block<D>;
   constexpr int kGroups = D / 16;
-  launch_dependents();
-  wait_prior_grid();
-  const int t = (int)blockIdx.x;
-  for (long long b = (long long)t * kThreads + threadIdx.x; b < p.B; b += (long long)p.T * kThreads) {
-    int abort_flag = 0;
-    if (!paged_range_ok(p.cu_q[b], p.cu_q[b + 1], p.T))
-      report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedRows);
-  }
-  const PagedRow at = paged_row(p.cu_q, p.seq_lens, p.B, p.T, t, p.status);
-  if (at.b < 0) return;
-  int abort_flag = 0;
-  if (at.pos < 0 || at.pos >= (long long)p.max_pages << p.page_shift) {
-    if (threadIdx.x == 0) report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPosition);
-    return;
-  }
-  const int page = p.page_table[(long long)at.b * p.max_pages + (at.pos >> p.page_shift)];
-  if (page < 0 || page >= p.num_pages) {
-    if (threadIdx.x == 0) report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
-    return;
-  }
+  const int page = at.page;
   const int slot = at.pos & (p.page_size - 1), r = slot & 15;
   for (int i = threadIdx.x; i < 2 * p.Hkv * kGroups; i += kThreads) {
     const int g = i % kGroups, hh = i / kGroups;
@@ -301,18 +348,33 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_read_kernel(const Kv4ReadPara
   }
 }
 
+template <int D>
+__global__ void __launch_bounds__(kThreads, 8) fa_kv4_read_kernel(const Kv4ReadParams p, int run) {
+  launch_dependents();
+  wait_prior_grid();
+  RowPlace at = {-1, 0, 0, 0, -1};
+  const int t0 = (int)blockIdx.x * run, t1 = min(t0 + run, p.T);
+  for (int t = t0; t < t1; ++t) {
+    at = place_row(p, t, at, -1);
+    if (at.b >= 0) read_row<D>(p, t, at);
+  }
+  check_ranges(p);
+}
+
+// Rows of a CTA: one as long as all CTAs run at once (8 an SM), then `most`.
 template <class Params>
-int launch_rows(void (*kernel)(Params), const Params& p, cudaStream_t stream) {
+int launch_rows(void (*kernel)(Params, int), const Params& p, int most, cudaStream_t stream) {
+  const int run = p.T <= 1216 ? 1 : most;
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((unsigned)p.T, 1, 1);
+  c.gridDim = dim3((unsigned)(((long long)p.T + run - 1) / run), 1, 1);
   c.blockDim = dim3(kThreads, 1, 1);
   c.stream = stream;
   c.attrs = pdl;
   c.numAttrs = 1;
-  if (cudaLaunchKernelEx(&c, kernel, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&c, kernel, p, run) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
   }
@@ -322,10 +384,10 @@ int launch_rows(void (*kernel)(Params), const Params& p, cudaStream_t stream) {
 }  // namespace
 
 int launch_kv4_append(const Kv4AppendParams& p, int d, cudaStream_t stream) {
-  return launch_rows(d == 128 ? fa_kv4_append_kernel<128> : fa_kv4_append_kernel<64>, p, stream);
+  return launch_rows(d == 128 ? fa_kv4_append_kernel<128> : fa_kv4_append_kernel<64>, p, 2, stream);
 }
 int launch_kv4_read(const Kv4ReadParams& p, int d, cudaStream_t stream) {
-  return launch_rows(d == 128 ? fa_kv4_read_kernel<128> : fa_kv4_read_kernel<64>, p, stream);
+  return launch_rows(d == 128 ? fa_kv4_read_kernel<128> : fa_kv4_read_kernel<64>, p, 4, stream);
 }
 
 }  // namespace fa

@@ -85,23 +85,29 @@ __device__ __forceinline__ uint32_t kv4_scale(float top, float& s) {
   s = __half2float(__ushort_as_half((unsigned short)(e4m3_to_half(two) & 0xffffu)));
   return two & 0xffu;
 }
-// The codes of y / s for eight numbers, number i in bits 4 i .. 4 i + 3; halfway
-// cases to the even code, beyond the range to 6, 0 for a scale of 0.
-__device__ __forceinline__ uint32_t kv4_codes(const float* y, float s) {
-  uint32_t r = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = s == 0.f ? 0.f : __fdiv_rn(y[2 * i], s);
-    const float b = s == 0.f ? 0.f : __fdiv_rn(y[2 * i + 1], s);
-    uint32_t two;
-    asm("{\n\t.reg .b8 c, z;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\t"
-        "mov.b16 {z, _}, 0;\n\t"
-        "mov.b32 %0, {c, z, z, z};\n\t}"
-        : "=r"(two)
-        : "f"(b), "f"(a));
-    r |= two << (8 * i);
-  }
+// The inverse of a scale, for kv4_quotient: 0 for a scale of 0, whose codes are 0.
+__device__ __forceinline__ float kv4_inverse(float s) { return s == 0.f ? 0.f : __frcp_rn(s); }
+// y / s rounded to nearest, of a y that is finite: a product with the rounded inverse
+// r, and what that leaves over once more (Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990: so corrected, a quotient
+// within one unit of the last place is the rounded one).  A true quotient halfway
+// between two codes is then met exactly.
+__device__ __forceinline__ float kv4_quotient(float y, float s, float r) {
+  const float q = __fmul_rn(y, r);
+  return __fmaf_rn(__fmaf_rn(-q, s, y), r, q);
+}
+// Eight quotients to codes, number 2i in the lower half of byte i and 2i + 1 in the
+// upper one; halfway cases to the even code, beyond the range to 6.
+__device__ __forceinline__ uint32_t kv4_codes(const float (&lo)[4], const float (&hi)[4]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %5, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %6, %2;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %7, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %4;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(lo[0]), "f"(lo[1]), "f"(lo[2]), "f"(lo[3]), "f"(hi[0]), "f"(hi[1]), "f"(hi[2]), "f"(hi[3]));
   return r;
 }
 
