@@ -62,35 +62,28 @@ __device__ __forceinline__ void paged4_produce_items(const PagedParams& p, const
   __syncwarp();
 }
 
-// What a lane has read of two blocks: its codes of K or V, and scales with the masks
-// that leave a slot without a key 0 (its codes may be anything, and are finite).
+// What a lane has read of two blocks: its codes of K or V, and scales; of V how many
+// keys the blocks hold (the scales of slots past them become 0: their codes may be
+// anything, and are finite).
 template <int D>
 struct Raw4 {
   uint32_t code[2][2][D / 32];
-  uint32_t scale[2][2], mask[2];  // (the second eight keys' mask in the upper half)
+  uint32_t scale[2][2];
+  int keys;
 };
 
-// Reads blocks 2 part, 2 part + 1 of the tile whose first key is `key` (keys end at
-// k_hi); `page`: lane b holds the page of the tile's block b.  Straight-line code
-// that looks at nothing it loads: a block past the keys, or without a page, reads
-// page 0.  (With branches around the loads it took the warp 1,200 cycles.)
+// Reads two blocks (at blk[0] and blk[1]), keys in their slots until `keys` and `keys`
+// - 16 of them.  Straight-line code that looks at nothing it loads.
 template <int D, bool kV>
-__device__ __forceinline__ void read_raw4(const Paged4Params& p, int h, int key, int k_hi, int page,
-                                          int part, Raw4<D>& r) {
+__device__ __forceinline__ void read_raw4(const uint8_t* const (&blk)[2], int keys, Raw4<D>& r) {
   using Block = Kv4Block<D>;
   const int lane = (int)lane_id(), g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
-    const int block = 2 * part + b, at = key + 16 * block;
-    int id = __shfl_sync(0xffffffffu, page, block);
-    const bool there = at < k_hi && (unsigned)id < (unsigned)p.num_pages;
-    id = there ? id : 0;
-    const uint8_t* const blk =
-        p.pages + kv4_block_at(id, p.Hkv, h, p.page_shift, at & (p.page_size - 1), Block::kBytes);
-    const uint8_t* const codes = blk + (kV ? Block::v_code(0, 0) : Block::k_code(0)) + lane * (D / 8);
+    const uint8_t* const codes = blk[b] + (kV ? Block::v_code(0, 0) : Block::k_code(0)) + lane * (D / 8);
     const uint8_t* const scales =
-        blk + (kV ? Block::v_scale(D == 128 ? g : g / 2) + 2 * t
-                  : Block::k_scale(0) + lane * (D == 128 ? 2 : 1));
+        blk[b] + (kV ? Block::v_scale(D == 128 ? g : g / 2) + 2 * t
+                     : Block::k_scale(0) + lane * (D == 128 ? 2 : 1));
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if constexpr (D == 128) {
@@ -108,16 +101,8 @@ __device__ __forceinline__ void read_raw4(const Paged4Params& p, int h, int key,
       else
         r.scale[b][u] = __ldg(scales + u * 32);
     }
-    if constexpr (kV) {
-      // Keys of this lane's pairs 2t, 2t + 1 and 8 further on: a byte of mask each.
-      const int n = k_hi - (at + 2 * t);
-      const uint32_t m = (n > 0 ? 0xffu : 0u) | (n > 1 ? 0xff00u : 0u) | (n > 8 ? 0xff0000u : 0u) |
-                         (n > 9 ? 0xff000000u : 0u);
-      r.mask[b] = there ? m : 0u;
-    } else {
-      r.mask[b] = there ? 0xffffffffu : 0u;
-    }
   }
+  if constexpr (kV) r.keys = keys;
 }
 
 // Turns them into rows 32 part .. 32 part + 31 of a tile.
@@ -128,7 +113,12 @@ __device__ __forceinline__ void store_raw4(const Raw4<D>& r, int part, uint8_t* 
   for (int b = 0; b < 2; ++b) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const uint32_t s = e4m3_to_half(r.scale[b][u] & r.mask[b] >> (16 * u));
+      uint32_t bytes = r.scale[b][u];
+      if (kV && r.keys < 32) {  // (the end of a unit's keys)
+        const int n = r.keys - (16 * b + 8 * u + 2 * t);
+        bytes &= n > 1 ? 0xffffu : n > 0 ? 0xffu : 0u;
+      }
+      const uint32_t s = e4m3_to_half(bytes);
       if constexpr (!kV) {
         // Key g of these eight, channels t d/4 ..: a word is a chunk of eight.
         const int row = 32 * part + 16 * b + 8 * u + g;
@@ -181,23 +171,37 @@ __device__ __forceinline__ void paged4_produce_tiles(const Paged4Params& p, Smem
   volatile int* abortf = &sm.abort_flag;
   const int lane = (int)lane_id();
   bool ok = true;
-  // The tile that is read next: its segment's place, and its blocks' pages in lanes
-  // 0 .. 7, with those of the tile behind it.
-  int m = -1, j = 0, nj = 0, h = 0, key0 = 0, k_hi = 0, page = 0, next = 0;
-  const int* list = nullptr;
+  // The tile that is read next: its segment's place, its two blocks, and the pages of
+  // the next tile's blocks (even lanes the first, odd lanes the second).  A block
+  // past the keys, or without a page, reads page 0.
+  int m = -1, left = 0, h = 0, key = 0, k_hi = 0, next = 0;
   bool end = false;
-  auto pages = [&](int j) -> int {
-    const int key = key0 + j * kTile + 16 * (lane & 7);
-    return j < nj && key < k_hi ? list[key >> p.page_shift] : 0;
+  const int* list = nullptr;
+  const uint8_t* blk[2] = {p.pages, p.pages};
+  auto pages = [&](int first) -> int {
+    const int at = first + 16 * (2 * part + (lane & 1));
+    return at < k_hi ? list[at >> p.page_shift] : 0;
   };
-  auto step = [&] {
-    if ((unsigned)page >= (unsigned)p.num_pages) {  // of the tile just read
+  auto locate = [&](int page) {
+    const bool valid = (unsigned)page < (unsigned)p.num_pages;
+    const int at = key + 16 * (2 * part + (lane & 1));
+    if (!valid) {
       int abort_flag = 0;
       report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
     }
-    if (++j < nj) {
-      page = next;
-      next = pages(j + 1);
+    const unsigned long long mine = reinterpret_cast<unsigned long long>(
+        p.pages + kv4_block_at(valid ? page : 0, p.Hkv, h, p.page_shift, at & (p.page_size - 1),
+                               Kv4Block<D>::kBytes));
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      blk[b] = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, mine, b));
+  };
+  auto step = [&] {
+    if (--left > 0) {
+      key += kTile;
+      const int page = next;
+      next = left > 1 ? pages(key + kTile) : 0;
+      locate(page);
       return;
     }
     do {  // the next segment with keys
@@ -207,15 +211,15 @@ __device__ __forceinline__ void paged4_produce_tiles(const Paged4Params& p, Smem
       if (!ok) return;
       const PagedItem& it = sm.item[is];
       end = it.end != 0;
-      nj = it.nj, h = it.h, key0 = it.key, k_hi = it.k_hi;
+      left = it.nj, h = it.h, key = it.key, k_hi = it.k_hi;
       list = p.page_table + (long long)it.b * p.max_pages;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[is]);
-    } while (!end && nj == 0);
-    j = 0;
+    } while (!end && left == 0);
     if (end) return;
-    page = pages(0);
-    next = pages(1);
+    const int page = pages(key);
+    next = left > 1 ? pages(key + kTile) : 0;
+    locate(page);
   };
   auto ready = [&](int c) -> bool {
     if (c >= S)
@@ -229,11 +233,10 @@ __device__ __forceinline__ void paged4_produce_tiles(const Paged4Params& p, Smem
     if (lane == 0) mbar_arrive(&sm.kv_full[c % S]);
   };
   Raw4<D> k, v;
-  j = -1;
   step();
   if (ok && !end) {
-    read_raw4<D, false>(p, h, key0, k_hi, page, part, k);
-    read_raw4<D, true>(p, h, key0, k_hi, page, part, v);
+    read_raw4<D, false>(blk, 0, k);
+    read_raw4<D, true>(blk, k_hi - (key + 32 * part), v);
   }
   for (int c = 0; ok && !end; c += 2) {
     if (!ready(c)) break;
@@ -241,11 +244,11 @@ __device__ __forceinline__ void paged4_produce_tiles(const Paged4Params& p, Smem
     hand_on(c);
     step();
     if (!ok) break;
-    if (!end) read_raw4<D, false>(p, h, key0 + j * kTile, k_hi, page, part, k);
+    if (!end) read_raw4<D, false>(blk, 0, k);
     if (!ready(c + 1)) break;
     store_raw4<D, true>(v, part, sm.kv[(c + 1) % S]);
     hand_on(c + 1);
-    if (!end) read_raw4<D, true>(p, h, key0 + j * kTile, k_hi, page, part, v);
+    if (!end) read_raw4<D, true>(blk, k_hi - (key + 32 * part), v);
   }
   __syncwarp();
 }
