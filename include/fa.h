@@ -366,9 +366,9 @@ int fa_fwd_paged_prefix(const void* q, const void* k_pages, const void* v_pages,
  *     V scales [d / 16][16 keys]
  *
  * fa_kv4_append is fa_kv_append into it: keys are quantised after their
- * rotation, from fp32.  A byte of V holds a pair of keys: appending to an odd
- * slot reads the byte and writes the even slot's half back as it was, so no
- * other call may write that slot meanwhile.
+ * rotation, from fp32.  A byte of V holds a pair of keys: appending one of the
+ * two reads the byte and writes the other's half back as it was, so no other
+ * call may write that slot meanwhile.
  *
  * fa_kv4_read reads rows back: row t of sequence b is position
  * seq_lens[b] - (cu_q[b+1] - t), as in the append, and k_out, v_out

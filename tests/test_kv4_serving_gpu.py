@@ -274,6 +274,21 @@ def test_rope_rows_are_checked():
     assert torch.equal(s.pool, before)
 
 
+def test_a_row_past_the_rotations_table_leaves_its_slot_alone():
+    s = Server(1, 8, 16, 8, 2, 1, 64, seed=16)
+    s.step([0], [20])
+    k = torch.full((2, 1, 64), 6.0, dtype=torch.bfloat16, device="cuda")
+    tables = s.table, ints([22]), ints([0, 2])
+    s.pool.fill_(0x22)  # codes 1, scales 5/32
+    fa.kv4_append(k, k, s.pool, *tables, rope=s.rope[:21].contiguous())
+    assert fa.device_status() == (fa.FA_ERR_PAGE, 303)
+    k_out, v_out = torch.zeros_like(k), torch.zeros_like(k)
+    fa.kv4_read(s.pool, *tables, k_out, v_out)
+    fa.check_device_status()
+    assert (k_out[1] == 0.15625).all() and (v_out[1] == 0.15625).all()
+    assert (v_out[0] == 6.0).all()
+
+
 def test_pages_behind_four_gigabytes():
     """Block offsets that pass 32 bits, appended, read and attended."""
     Hkv, page, d = 8, 256, 128
