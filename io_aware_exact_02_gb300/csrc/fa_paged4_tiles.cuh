@@ -10,6 +10,14 @@
 // would leave: [d / 64][128 keys][128 bytes], the 16-byte chunk c of row r at
 // c ^ (r % 8).  Which lane stores which of its pieces first is chosen so that
 // eight lanes meet eight chunks.
+//
+// Measured: 4 chunks of 1,024 rows over 4K keys, H_q 32, H_kv 8, d = 128: 242 us (992
+// TFLOP/s, tensor pipe active 46%); with the tile warps handing on what the slots
+// hold 188, over the bf16 cache 173.  Bound by those warps beside the softmax: their
+// instructions share its schedulers, and any use of a loaded value right behind the
+// load waits for it.  Hence the reads a step ahead, looked at only when stored
+// (295 -> 256 us with registers enough for that), and a block's place found once for
+// K and V (256 -> 242).
 #pragma once
 
 #include "fa_internal.h"

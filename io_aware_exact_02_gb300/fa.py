@@ -1059,7 +1059,7 @@ def pages_compact(page_table, seq_lens, refs, pools, page_size: int, live=None, 
         with torch.cuda.device(dev):
             return pages_compact(page_table, seq_lens, refs, pools, page_size, live, workspace)
     if live is None:
-        live = torch.empty(1, dtype=_I32, device=page_table.device)
+        live = refs.new_empty(1)
     else:
         _check_one("live", live, (1,), _I32, dev)
     at, sizes, count = _pools(pools, num_pages, dev)
