@@ -378,7 +378,10 @@ int fa_fwd_paged_prefix(const void* q, const void* k_pages, const void* v_pages,
  *
  * fa_fwd_paged4 is fa_fwd_paged over it, of those values unrounded.  A query
  * row is scaled by a power of two to fit fp16, in which the products run:
- * channels below 2^-38 of the row's largest lose bits.  Numbers in slots past a
+ * channels below 2^-38 of the row's largest lose bits.  workspace: at least
+ * fa_fwd_paged4_workspace_size bytes; with more, up to
+ * fa_fwd_paged4_best_workspace_size (512 MB more at most), long prompts run faster
+ * on a copy of their keys and values in fp16, with the same results.  Numbers in slots past a
  * sequence's length are never used; value rows that the causal mask hides have
  * to be finite, as in the other forward calls.
  * Errors of all three: as the call each is a form of, and FA_ERR_ARG for a
@@ -395,6 +398,8 @@ int fa_kv4_read(void* k_out, void* v_out, const void* pages, const int* page_tab
                 long long k_out_stride, long long v_out_stride, int num_pages, int page_size,
                 int max_pages, float k_scale, float v_scale, void* stream);
 size_t fa_fwd_paged4_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_q);
+size_t fa_fwd_paged4_best_workspace_size(int T, int B, int Hq, int Hkv, int d, int page_size,
+                                         int max_pages, int max_q);
 int fa_fwd_paged4(const void* q, const void* pages, void* o, float* lse, const int* page_table,
                   const int* seq_lens, const int* cu_q, int T, int B, int Hq, int Hkv, int d,
                   long long q_stride, int num_pages, int page_size, int max_pages, int max_q,

@@ -723,6 +723,17 @@ int fwd_paged4_impl(const void* q, const void* pages, void* o, float* lse, const
   p.status = ds->status;
   p.ctas = ds->sm_count < kPagedMaxCtas ? ds->sm_count : kPagedMaxCtas;
   p.workspace = static_cast<char*>(workspace);
+  // What is left of the workspace, for tiles in fp16.
+  const size_t least = fa_fwd_paged4_workspace_size(T, B, Hq, Hkv, d, max_q);
+  const size_t tile = (size_t)kTile * d * 4 * Hkv, bases = paged4_bases_bytes(B);
+  p.expand = 0;
+  if (workspace_bytes >= least + bases + tile) {
+    const size_t room = (workspace_bytes - least - bases) / tile;
+    const int want = paged4_expand_tiles(T, B, Hq / Hkv, Hkv, d, page_size, max_pages, max_q);
+    p.expand = room < (size_t)want ? (int)room : want;
+    p.tile_base = reinterpret_cast<int*>(p.workspace + least);
+    p.tiles = reinterpret_cast<uint8_t*>(p.workspace + least + bases);
+  }
   return launch_fwd_paged4(p, d, static_cast<cudaStream_t>(stream));
 }
 
@@ -1032,6 +1043,17 @@ size_t fa_fwd_paged4_workspace_size(int T, int B, int Hq, int Hkv, int d, int ma
   if (paged_shape(T, B, Hq, Hkv, d, 1, 16, 1, &shift) != FA_OK) return 0;
   if (Hq % Hkv != 0 || Hq / Hkv > 128 || max_q < 1) return 0;
   return paged4_workspace_layout(d, paged4_form(T, B, Hq / Hkv, max_q)).total;
+}
+
+size_t fa_fwd_paged4_best_workspace_size(int T, int B, int Hq, int Hkv, int d, int page_size,
+                                         int max_pages, int max_q) {
+  int shift;
+  if (paged_shape(T, B, Hq, Hkv, d, 1, page_size, max_pages, &shift) != FA_OK) return 0;
+  const size_t least = fa_fwd_paged4_workspace_size(T, B, Hq, Hkv, d, max_q);
+  if (least == 0) return 0;
+  const int tiles = paged4_expand_tiles(T, B, Hq / Hkv, Hkv, d, page_size, max_pages, max_q);
+  return tiles == 0 ? least
+                    : least + paged4_bases_bytes(B) + (size_t)tiles * kTile * d * 4 * Hkv;
 }
 
 int fa_fwd_paged4(const void* q, const void* pages, void* o, float* lse, const int* page_table,

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/fa.h"
 
 namespace fa {
@@ -373,6 +375,12 @@ int launch_fwd_paged(const PagedParams& p, int d, cudaStream_t stream);
 struct Paged4Params : PagedParams {
   const uint8_t* pages;
   float k_scale, v_scale;  // the tensors' scales
+  // Room for the tiles of `expand` x 128 keys in fp16, K and V of each head, as the
+  // prompt kernel has them in shared memory; and where each sequence's are (-1: not
+  // there).  expand 0: none.
+  uint8_t* tiles;
+  int* tile_base;
+  int expand;
 };
 int launch_fwd_paged4(const Paged4Params& p, int d, cudaStream_t stream);
 
@@ -404,6 +412,21 @@ inline Paged4Form paged4_form(int T, int B, int G, int max_q) {
   if (f.rows == 0) f.small_tokens = 0;
   return f;
 }
+// Query rows of a sequence and key/value head above which its keys and values are
+// turned into fp16 once for all units, if the workspace has room; and that room at
+// most.
+constexpr int kPaged4ExpandRows = 768;
+constexpr size_t kPaged4ExpandBytes = (size_t)512 << 20;
+// The tiles of 128 keys that a call may have to turn.
+inline int paged4_expand_tiles(int T, int B, int G, int Hkv, int d, int page_size, int max_pages,
+                               int max_q) {
+  const long long most = max_q < T ? max_q : T;
+  if (most * G <= kPaged4ExpandRows) return 0;
+  const long long seqs = std::min<long long>(B, (long long)T * G / (kPaged4ExpandRows + 1));
+  const long long each = ((long long)max_pages * page_size + kTile - 1) / kTile;
+  return (int)std::min<long long>(seqs * each, kPaged4ExpandBytes / ((size_t)kTile * d * 4 * Hkv));
+}
+inline size_t paged4_bases_bytes(int B) { return ((size_t)B * sizeof(int) + 255) & ~(size_t)255; }
 // Its workspace: the two phases' split records and slots.
 struct Paged4Workspace {
   size_t rec[2], slot_o[2], slot_lse[2], total;

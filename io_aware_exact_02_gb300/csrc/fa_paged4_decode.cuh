@@ -46,15 +46,6 @@
 
 namespace fa {
 
-// 16-byte aligned bytes (a multiple of 16) to shared memory, completing `bar`'s
-// transaction count.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
 // D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16).
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1) {

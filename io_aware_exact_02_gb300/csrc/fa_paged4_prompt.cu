@@ -16,6 +16,13 @@ __global__ void __launch_bounds__(kPaged4Threads, 1)
                                    smem_raw);
 }
 
+template <int D>
+__global__ void __launch_bounds__(256, 3) fa_paged4_expand_kernel(const Paged4Params p, int n_min) {
+  launch_dependents();
+  wait_prior_grid();
+  paged4_expand<D>(p, n_min, (int)(blockIdx.x * 8 + (threadIdx.x >> 5)), (int)gridDim.x * 8);
+}
+
 template <int D, bool kNeg>
 int launch(const PagedMaps& t, const Paged4Params& p, const PagedPhase& ph,
            const cudaLaunchConfig_t& base) {
@@ -44,6 +51,17 @@ int launch_paged4_prompt(const Paged4Params& p, PagedPhase& ph, int d,
   if (rc != FA_OK) return rc;
   rc = make_tmap_rows(p.q, p.Hq, p.T, p.q_stride, d, p.G, ph.tile_tokens, &t.q);
   if (rc != FA_OK) return rc;
+  if (p.expand > 0) {
+    cudaLaunchConfig_t c = base;
+    c.gridDim = dim3((unsigned)p.ctas * 3, 1, 1);
+    c.blockDim = dim3(256, 1, 1);
+    const int n_min = kPaged4ExpandRows / p.G + 1;
+    if (cudaLaunchKernelEx(&c, d == 128 ? fa_paged4_expand_kernel<128> : fa_paged4_expand_kernel<64>,
+                           (const Paged4Params&)p, n_min) != cudaSuccess) {
+      cudaGetLastError();
+      return FA_ERR_LAUNCH;
+    }
+  }
   if (p.scale_log2 < 0.f) return d == 128 ? launch<128, true>(t, p, ph, base) : launch<64, true>(t, p, ph, base);
   return d == 128 ? launch<128, false>(t, p, ph, base) : launch<64, false>(t, p, ph, base);
 }

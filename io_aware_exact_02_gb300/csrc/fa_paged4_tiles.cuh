@@ -173,6 +173,67 @@ __device__ __forceinline__ void store_raw4(const Raw4<D>& r, int part, uint8_t* 
   }
 }
 
+// The tiles of long prompts' sequences in fp16, once for all units: a warp makes a
+// quarter of a tile, K and V, as the prompt kernel's warps do; in the order of the
+// sequences, as far as the room goes.  n_min: the fewest rows of those sequences.
+template <int D>
+__device__ __forceinline__ void paged4_expand(const Paged4Params& p, int n_min, int w, int warps) {
+  constexpr int kBytes = kTile * D * 2;
+  const int lane = (int)lane_id();
+  const long long cap = (long long)p.max_pages << p.page_shift;
+  long long before = 0;  // tiles of the sequences that were looked at
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    int len = 0, tiles = 0;
+    if (b < p.B) {
+      const int t0 = p.cu_q[b], t1 = p.cu_q[b + 1];
+      len = p.seq_lens[b];
+      if (paged_range_ok(t0, t1, p.T) && t1 - t0 >= n_min && len > 0 && len <= cap)
+        tiles = (int)(((long long)len + kTile - 1) / kTile);
+    }
+    int upto = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const long long start = before + upto - tiles;
+    const bool fits = tiles > 0 && start + tiles <= p.expand;
+    if (w == 0 && b < p.B) p.tile_base[b] = fits ? (int)start : -1;
+    for (unsigned left = __ballot_sync(0xffffffffu, fits); left != 0; left &= left - 1) {
+      const int src = __ffs(left) - 1, base = __shfl_sync(0xffffffffu, (int)start, src);
+      const int n = __shfl_sync(0xffffffffu, tiles, src) * p.Hkv * 4;
+      const int keys = __shfl_sync(0xffffffffu, len, src);
+      const int* const list = p.page_table + (long long)(b0 + src) * p.max_pages;
+      const int at = (int)((long long)base * p.Hkv * 4 % warps);
+      for (int x = w >= at ? w - at : w - at + warps; x < n; x += warps) {
+        const int part = x & 3, tile = (x >> 2) / p.Hkv, h = (x >> 2) - tile * p.Hkv;
+        const int first = tile * kTile + 32 * part, key = first + 16 * (lane & 1);
+        const int page = key < keys ? list[key >> p.page_shift] : 0;
+        const bool valid = (unsigned)page < (unsigned)p.num_pages;
+        if (!valid) {
+          int abort_flag = 0;
+          report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
+        }
+        const unsigned long long mine = reinterpret_cast<unsigned long long>(
+            p.pages + kv4_block_at(valid ? page : 0, p.Hkv, h, p.page_shift,
+                                   key & (p.page_size - 1), Kv4Block<D>::kBytes));
+        const uint8_t* blk[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          blk[i] = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, mine, i));
+        Raw4<D> k, v;
+        read_raw4<D, false>(blk, 0, k);
+        read_raw4<D, true>(blk, keys - first, v);
+        uint8_t* const dst = p.tiles + ((long long)(base + tile) * p.Hkv + h) * (2 * kBytes);
+        store_raw4<D, false>(k, part, dst);
+        store_raw4<D, true>(v, part, dst + kBytes);
+      }
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+}
+
 // One of the warps that make the tiles of the CTA's segments: part `part` of each.
 template <int D, int S, int kRing, class Smem>
 __device__ __forceinline__ void paged4_produce_tiles(const Paged4Params& p, Smem& sm, int part) {
@@ -182,8 +243,11 @@ __device__ __forceinline__ void paged4_produce_tiles(const Paged4Params& p, Smem
   // The tile that is read next: its segment's place, its two blocks, and the pages of
   // the next tile's blocks (even lanes the first, odd lanes the second).  A block
   // past the keys, or without a page, reads page 0.
+  // (Or, where the sequence's tiles are in fp16 already, blk[0]: this one's K, with V
+  // behind it.)
+  constexpr int kBytes = kTile * D * 2;
   int m = -1, left = 0, h = 0, key = 0, k_hi = 0, next = 0;
-  bool end = false;
+  bool end = false, whole = false;
   const int* list = nullptr;
   const uint8_t* blk[2] = {p.pages, p.pages};
   auto pages = [&](int first) -> int {
@@ -207,6 +271,10 @@ __device__ __forceinline__ void paged4_produce_tiles(const Paged4Params& p, Smem
   auto step = [&] {
     if (--left > 0) {
       key += kTile;
+      if (whole) {
+        blk[0] += 2ll * kBytes * p.Hkv;
+        return;
+      }
       const int page = next;
       next = left > 1 ? pages(key + kTile) : 0;
       locate(page);
@@ -221,10 +289,13 @@ __device__ __forceinline__ void paged4_produce_tiles(const Paged4Params& p, Smem
       end = it.end != 0;
       left = it.nj, h = it.h, key = it.key, k_hi = it.k_hi;
       list = p.page_table + (long long)it.b * p.max_pages;
+      const int base = p.expand > 0 && !end ? p.tile_base[it.b] : -1;
+      whole = base >= 0;
+      if (whole) blk[0] = p.tiles + ((long long)(base + key / kTile) * p.Hkv + h) * (2 * kBytes);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.item_empty[is]);
     } while (!end && left == 0);
-    if (end) return;
+    if (end || whole) return;
     const int page = pages(key);
     next = left > 1 ? pages(key + kTile) : 0;
     locate(page);
@@ -240,24 +311,51 @@ __device__ __forceinline__ void paged4_produce_tiles(const Paged4Params& p, Smem
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.kv_full[c % S]);
   };
+  // Slot c from a tile in fp16: one warp copies it, the others only hand it on.
+  int copied = 0;  // tiles up to the last one copied
+  auto copy = [&](int c, const uint8_t* src) {
+    if (lane == 0) {
+      if (part == 0) {
+        mbar_arrive_expect_tx(&sm.kv_full[c % S], kBytes);
+        bulk_load(sm.kv[c % S], src, kBytes, &sm.kv_full[c % S]);
+      } else {
+        mbar_arrive(&sm.kv_full[c % S]);
+      }
+    }
+    __syncwarp();
+    copied = c + 1;
+  };
   Raw4<D> k, v;
   step();
-  if (ok && !end) {
+  if (ok && !end && !whole) {
     read_raw4<D, false>(blk, 0, k);
     read_raw4<D, true>(blk, k_hi - (key + 32 * part), v);
   }
   for (int c = 0; ok && !end; c += 2) {
+    const uint8_t* const src = whole ? blk[0] : nullptr;
     if (!ready(c)) break;
-    store_raw4<D, false>(k, part, sm.kv[c % S]);
-    hand_on(c);
+    if (src != nullptr) {
+      copy(c, src);
+    } else {
+      store_raw4<D, false>(k, part, sm.kv[c % S]);
+      hand_on(c);
+    }
     step();
     if (!ok) break;
-    if (!end) read_raw4<D, false>(blk, 0, k);
+    const bool raw = !end && !whole;
+    if (raw) read_raw4<D, false>(blk, 0, k);
     if (!ready(c + 1)) break;
-    store_raw4<D, true>(v, part, sm.kv[(c + 1) % S]);
-    hand_on(c + 1);
-    if (!end) read_raw4<D, true>(blk, k_hi - (key + 32 * part), v);
+    if (src != nullptr) {
+      copy(c + 1, src + kBytes);
+    } else {
+      store_raw4<D, true>(v, part, sm.kv[(c + 1) % S]);
+      hand_on(c + 1);
+    }
+    if (raw) read_raw4<D, true>(blk, k_hi - (key + 32 * part), v);
   }
+  // After a failure: the copies on their way have to land before the CTA exits.
+  if (*abortf && part == 0 && lane == 0)
+    for (int c = max(0, copied - S); c < copied; ++c) drain_wait(&sm.kv_full[c % S], (c / S) & 1);
   __syncwarp();
 }
 

@@ -74,6 +74,7 @@ SIGNATURES = {
     "fa_kv4_append": (_i, [_vp] * 9 + [_i] * 5 + [_ll] * 4 + [_i] * 6 + [_f] * 2 + [_vp]),
     "fa_kv4_read": (_i, [_vp] * 6 + [_i] * 4 + [_ll] * 2 + [_i] * 3 + [_f] * 2 + [_vp]),
     "fa_fwd_paged4_workspace_size": (_sz, [_i] * 6),
+    "fa_fwd_paged4_best_workspace_size": (_sz, [_i] * 8),
     "fa_fwd_paged4": (_i, [_vp] * 7 + [_i] * 5 + [_ll] + [_i] * 5 + [_f] * 3 + [_vp, _sz, _vp]),
     "fa_pages_copy": (_i, [_cp, _cp, _i, _vp, _vp, _i, _i, _vp]),
     "fa_pages_fork_workspace_size": (_sz, [_i, _i]),
@@ -854,6 +855,13 @@ def fwd_paged4_workspace_size(T, B, Hq, Hkv, d, max_q) -> int:
     return int(load().fa_fwd_paged4_workspace_size(T, B, Hq, Hkv, d, max_q))
 
 
+@functools.lru_cache(maxsize=256)
+def fwd_paged4_best_workspace_size(T, B, Hq, Hkv, d, page_size, max_pages, max_q) -> int:
+    """Bytes of workspace with which long prompts run fastest."""
+    return int(load().fa_fwd_paged4_best_workspace_size(T, B, Hq, Hkv, d, page_size, max_pages,
+                                                        max_q))
+
+
 def fwd_paged4(q, pages, page_table, seq_lens, cu_q, max_q=None, causal: bool = True,
                scale: float | None = None, k_scale: float = 1.0, v_scale: float = 1.0, out=None,
                lse=None, workspace=None):
@@ -894,7 +902,7 @@ def fwd_paged4(q, pages, page_table, seq_lens, cu_q, max_q=None, causal: bool = 
                               v_scale, out, lse, workspace)
     lib, stream = _lib or load(), _current_stream(dev)
     if workspace is None:  # (as in _fwd_paged)
-        ws_bytes = fwd_paged4_workspace_size(T, B, Hq, Hkv, d, max_q)
+        ws_bytes = fwd_paged4_best_workspace_size(T, B, Hq, Hkv, d, size // (9 * d) * 8, width, max_q)
         ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(max(ws_bytes, 1), stream)
     else:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()

@@ -134,6 +134,18 @@ def test_paged_other_errors(lib):
     expect_device(lambda: paged(lib, wsb=need))
     assert lib.fa_fwd_paged4_workspace_size(0, 2, 4, 2, 64, 2) == 0
     assert lib.fa_fwd_paged4_workspace_size(3, 2, 4, 2, 72, 2) == 0
+    # Room for tiles: only where a sequence may have more than 768 rows of a head.
+    best = lib.fa_fwd_paged4_best_workspace_size
+    assert best(3, 2, 4, 2, 64, 16, 4, 2) == need
+    assert best(3, 2, 4, 2, 72, 16, 4, 2) == best(3, 2, 4, 2, 64, 24, 4, 2) == 0
+    assert best(384, 2, 4, 2, 64, 16, 40, 384) == lib.fa_fwd_paged4_workspace_size(384, 2, 4, 2, 64, 384)
+    least = lib.fa_fwd_paged4_workspace_size(385, 2, 4, 2, 64, 385)
+    assert best(385, 2, 4, 2, 64, 16, 40, 385) == least + 256 + 5 * 65536
+    assert best(770, 2, 4, 2, 64, 16, 40, 385) == (
+        lib.fa_fwd_paged4_workspace_size(770, 2, 4, 2, 64, 385) + 256 + 10 * 65536)
+    most = best(770, 2, 4, 2, 64, 16, 1 << 26, 385) - lib.fa_fwd_paged4_workspace_size(
+        770, 2, 4, 2, 64, 385)
+    assert most == 256 + (512 << 20)
 
 
 def words(fmt, *args):

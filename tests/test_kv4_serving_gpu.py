@@ -144,6 +144,35 @@ def test_results_do_not_change_from_call_to_call():
             assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,page,lens,nq", [
+    (8, 1, 128, 16, [1000, 100, 333, 129], [97, 1, 300, 120]),
+    (6, 2, 64, 32, [2000, 300, 77, 512], [257, 290, 5, 400]),
+    (2, 2, 128, 128, [800] + [5] * 70 + [900], [800] + [1] * 70 + [769]),
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_room_for_tiles_changes_no_result(Hq, Hkv, d, page, lens, nq, causal):
+    x = c4.Batch4(Hq, Hkv, d, page, lens, nq, seed=17)
+    sizes = x.T, len(lens), Hq, Hkv, d
+    width = x.args()[2].shape[1]
+    least = fa.fwd_paged4_workspace_size(*sizes, max(nq))
+    best = fa.fwd_paged4_best_workspace_size(*sizes, page, width, max(nq))
+    tile, bases = 128 * d * 4 * Hkv, -(-4 * len(lens) // 256) * 256
+    assert best > least + bases and (best - least - bases) % tile == 0
+    got = []
+    for size in (least, best, least + bases + 8 * tile, least + bases - 1, best + 1000):
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")  # (NaN, whatever it is read as)
+        o, lse = fa.fwd_paged4(*x.args(), max_q=max(nq), causal=causal, out=x.out, lse=x.lse,
+                               workspace=ws)
+        fa.check_device_status()
+        got.append((o.clone(), lse.clone()))
+        if size == least:
+            x.check(o, lse, causal, d ** -0.5)
+        if size == best:  # they were used
+            assert not (ws[least + bases:least + bases + tile] == 255).all()
+    for o, lse in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1])
+
+
 def test_captured_with_other_lengths_and_pages():
     """One graph of an append and an attention, replayed as the sequences grow."""
     s = Server(3, 30, 16, 8, 4, 2, 64, seed=7)
