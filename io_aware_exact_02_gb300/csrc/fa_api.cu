@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <cstddef>
@@ -725,15 +726,16 @@ int fwd_paged4_impl(const void* q, const void* pages, void* o, float* lse, const
   p.workspace = static_cast<char*>(workspace);
   // What is left of the workspace, for tiles in fp16.
   const size_t least = fa_fwd_paged4_workspace_size(T, B, Hq, Hkv, d, max_q);
-  const size_t tile = (size_t)kTile * d * 4 * Hkv, bases = paged4_bases_bytes(B);
-  p.expand = 0;
-  if (workspace_bytes >= least + bases + tile) {
-    const size_t room = (workspace_bytes - least - bases) / tile;
-    const int want = paged4_expand_tiles(T, B, Hq / Hkv, Hkv, d, page_size, max_pages, max_q);
-    p.expand = room < (size_t)want ? (int)room : want;
-    p.tile_base = reinterpret_cast<int*>(p.workspace + least);
-    p.tiles = reinterpret_cast<uint8_t*>(p.workspace + least + bases);
-  }
+  const size_t bases = paged4_bases_bytes(B), tile = paged4_expand_tile_bytes(Hkv, d);
+  const size_t room = workspace_bytes < least + bases ? 0 : (workspace_bytes - least - bases) / tile;
+  const Paged4Expand x =
+      paged4_expand_form(paged4_form(T, B, Hq / Hkv, max_q), T, B, Hq / Hkv, page_size, max_pages,
+                         max_q, std::min(room, kPaged4ExpandBytes / tile));
+  p.expand = x.tiles;
+  p.expand_n_min = x.n_min;
+  p.whole = x.whole;
+  p.tile_base = reinterpret_cast<int*>(p.workspace + least);
+  p.tiles = reinterpret_cast<uint8_t*>(p.workspace + least + bases);
   return launch_fwd_paged4(p, d, static_cast<cudaStream_t>(stream));
 }
 
@@ -1051,9 +1053,11 @@ size_t fa_fwd_paged4_best_workspace_size(int T, int B, int Hq, int Hkv, int d, i
   if (paged_shape(T, B, Hq, Hkv, d, 1, page_size, max_pages, &shift) != FA_OK) return 0;
   const size_t least = fa_fwd_paged4_workspace_size(T, B, Hq, Hkv, d, max_q);
   if (least == 0) return 0;
-  const int tiles = paged4_expand_tiles(T, B, Hq / Hkv, Hkv, d, page_size, max_pages, max_q);
-  return tiles == 0 ? least
-                    : least + paged4_bases_bytes(B) + (size_t)tiles * kTile * d * 4 * Hkv;
+  const size_t tile = paged4_expand_tile_bytes(Hkv, d);
+  const Paged4Expand x =
+      paged4_expand_form(paged4_form(T, B, Hq / Hkv, max_q), T, B, Hq / Hkv, page_size, max_pages,
+                         max_q, kPaged4ExpandBytes / tile);
+  return x.tiles == 0 ? least : least + paged4_bases_bytes(B) + x.tiles * tile;
 }
 
 int fa_fwd_paged4(const void* q, const void* pages, void* o, float* lse, const int* page_table,

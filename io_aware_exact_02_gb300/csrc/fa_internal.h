@@ -375,12 +375,13 @@ int launch_fwd_paged(const PagedParams& p, int d, cudaStream_t stream);
 struct Paged4Params : PagedParams {
   const uint8_t* pages;
   float k_scale, v_scale;  // the tensors' scales
-  // Room for the tiles of `expand` x 128 keys in fp16, K and V of each head, as the
-  // prompt kernel has them in shared memory; and where each sequence's are (-1: not
-  // there).  expand 0: none.
+  // Room for `expand` tiles (x 128 keys) in fp16, K and V of each head, as the prompt
+  // kernel has them in shared memory, and where each sequence's begin (-1: not
+  // there); n_min and whole as below.  expand 0: none.
   uint8_t* tiles;
   int* tile_base;
-  int expand;
+  int expand, expand_n_min;
+  bool whole;
 };
 int launch_fwd_paged4(const Paged4Params& p, int d, cudaStream_t stream);
 
@@ -412,20 +413,33 @@ inline Paged4Form paged4_form(int T, int B, int G, int max_q) {
   if (f.rows == 0) f.small_tokens = 0;
   return f;
 }
-// Query rows of a sequence and key/value head above which its keys and values are
-// turned into fp16 once for all units, if the workspace has room; and that room at
-// most.
-constexpr int kPaged4ExpandRows = 768;
+// Where a sequence may have more than kPaged4ExpandRows query rows of a key/value head,
+// keys and values are turned into tiles in fp16 once for all units: those of every
+// sequence of the prompt kernel, if kPaged4ExpandBytes hold them (`whole`: it has no
+// warps then that make tiles), else those of the sequences with so many rows, as far
+// as the room goes.  (4 sequences of 4K keys, H_kv 8, d = 128, without and with: 1,024
+// rows 90 and 95 us, 2,048 rows 155 and 144, 4,096 rows 242 and 214; 8 of 16K: 500 and
+// 508, 962 and 858, 1,858 and 1,551.)
+constexpr int kPaged4ExpandRows = 1024;
 constexpr size_t kPaged4ExpandBytes = (size_t)512 << 20;
-// The tiles of 128 keys that a call may have to turn.
-inline int paged4_expand_tiles(int T, int B, int G, int Hkv, int d, int page_size, int max_pages,
-                               int max_q) {
+struct Paged4Expand {
+  int tiles;  // of 128 keys
+  int n_min;  // the fewest rows of a sequence whose keys are turned
+  bool whole;
+};
+// As much of it as `room` tiles hold.
+inline Paged4Expand paged4_expand_form(const Paged4Form& f, int T, int B, int G, int page_size,
+                                       int max_pages, int max_q, size_t room) {
   const long long most = max_q < T ? max_q : T;
-  if (most * G <= kPaged4ExpandRows) return 0;
-  const long long seqs = std::min<long long>(B, (long long)T * G / (kPaged4ExpandRows + 1));
+  if (most * G <= kPaged4ExpandRows || room == 0) return {0, 0, false};
   const long long each = ((long long)max_pages * page_size + kTile - 1) / kTile;
-  return (int)std::min<long long>(seqs * each, kPaged4ExpandBytes / ((size_t)kTile * d * 4 * Hkv));
+  const long long all = std::min<long long>(B, T / (f.small_tokens + 1)) * each;
+  if ((unsigned long long)all <= room) return {(int)all, f.small_tokens + 1, true};
+  const int n_min = kPaged4ExpandRows / G + 1;
+  const long long big = std::min<long long>(B, T / n_min) * each;
+  return {(int)std::min<unsigned long long>(big, room), n_min, false};
 }
+inline size_t paged4_expand_tile_bytes(int Hkv, int d) { return (size_t)kTile * d * 4 * Hkv; }
 inline size_t paged4_bases_bytes(int B) { return ((size_t)B * sizeof(int) + 255) & ~(size_t)255; }
 // Its workspace: the two phases' split records and slots.
 struct Paged4Workspace {

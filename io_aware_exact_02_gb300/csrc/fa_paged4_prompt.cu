@@ -6,36 +6,76 @@
 namespace fa {
 namespace {
 
-template <int D, bool kNeg>
-__global__ void __launch_bounds__(kPaged4Threads, 1)
+constexpr int kExpandWarps = 4;
+
+template <bool kWhole>
+constexpr int kPromptThreads = kWhole ? kPagedThreads : kPaged4Threads;
+
+template <int D, bool kNeg, bool kWhole>
+__global__ void __launch_bounds__(kPromptThreads<kWhole>, 1)
     fa_paged4_prompt_kernel(const __grid_constant__ CUtensorMap tq,
                             const __grid_constant__ CUtensorMap to, const Paged4Params p,
                             const PagedPhase ph) {
   extern __shared__ uint8_t smem_raw[];
-  prompt_cta<D, kNeg, false, true>(&tq, nullptr, nullptr, &to, p, ph, blockIdx.x, gridDim.x,
-                                   smem_raw);
+  prompt_cta<D, kNeg, false, true, kWhole>(&tq, nullptr, nullptr, &to, p, ph, blockIdx.x, gridDim.x,
+                                           smem_raw);
 }
 
 template <int D>
-__global__ void __launch_bounds__(256, 3) fa_paged4_expand_kernel(const Paged4Params p, int n_min) {
+struct alignas(128) ExpandSmem {
+  uint8_t stage[kExpandWarps][2][32 * D * 2];
+};
+
+template <int D>
+__global__ void __launch_bounds__(32 * kExpandWarps)
+    fa_paged4_expand_kernel(const Paged4Params p, int n_min) {
+  extern __shared__ uint8_t smem_raw[];
+  ExpandSmem<D>& sm = *reinterpret_cast<ExpandSmem<D>*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
   launch_dependents();
   wait_prior_grid();
-  paged4_expand<D>(p, n_min, (int)(blockIdx.x * 8 + (threadIdx.x >> 5)), (int)gridDim.x * 8);
+  const int warp = threadIdx.x >> 5;
+  paged4_expand<D>(p, n_min, (int)blockIdx.x * kExpandWarps + warp, (int)gridDim.x * kExpandWarps,
+                   sm.stage[warp]);
 }
 
-template <int D, bool kNeg>
-int launch(const PagedMaps& t, const Paged4Params& p, const PagedPhase& ph,
-           const cudaLaunchConfig_t& base) {
+template <int D>
+int launch_expand(const Paged4Params& p, const cudaLaunchConfig_t& base) {
   cudaLaunchConfig_t c = base;
-  c.blockDim = dim3(kPaged4Threads, 1, 1);
-  c.dynamicSmemBytes = sizeof(PromptSmem<D>) + 1024;
-  if (paged_kernel_ready<fa_paged4_prompt_kernel<D, kNeg>, kPaged4Regs>(c.dynamicSmemBytes) != FA_OK)
+  c.gridDim = dim3((unsigned)p.ctas * (233472 / (sizeof(ExpandSmem<D>) + 128 + 1024)), 1, 1);
+  c.blockDim = dim3(32 * kExpandWarps, 1, 1);
+  c.dynamicSmemBytes = sizeof(ExpandSmem<D>) + 128;
+  if (paged_kernel_ready<fa_paged4_expand_kernel<D>, 0>(c.dynamicSmemBytes) != FA_OK)
     return FA_ERR_LAUNCH;
-  if (cudaLaunchKernelEx(&c, fa_paged4_prompt_kernel<D, kNeg>, t.q, t.o, p, ph) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&c, fa_paged4_expand_kernel<D>, p, p.expand_n_min) != cudaSuccess) {
     cudaGetLastError();
     return FA_ERR_LAUNCH;
   }
   return FA_OK;
+}
+
+template <int D, bool kNeg, bool kWhole>
+int launch(const PagedMaps& t, const Paged4Params& p, const PagedPhase& ph,
+           const cudaLaunchConfig_t& base) {
+  cudaLaunchConfig_t c = base;
+  c.blockDim = dim3(kPromptThreads<kWhole>, 1, 1);
+  c.dynamicSmemBytes = sizeof(PromptSmem<D>) + 1024;
+  constexpr int kRegs = kWhole ? kPagedRegs : kPaged4Regs;
+  if (paged_kernel_ready<fa_paged4_prompt_kernel<D, kNeg, kWhole>, kRegs>(c.dynamicSmemBytes) != FA_OK)
+    return FA_ERR_LAUNCH;
+  if (cudaLaunchKernelEx(&c, fa_paged4_prompt_kernel<D, kNeg, kWhole>, t.q, t.o, p, ph) != cudaSuccess) {
+    cudaGetLastError();
+    return FA_ERR_LAUNCH;
+  }
+  return FA_OK;
+}
+
+template <bool kWhole>
+int launch_whole(const PagedMaps& t, const Paged4Params& p, const PagedPhase& ph, int d,
+                 const cudaLaunchConfig_t& base) {
+  if (p.scale_log2 < 0.f)
+    return d == 128 ? launch<128, true, kWhole>(t, p, ph, base) : launch<64, true, kWhole>(t, p, ph, base);
+  return d == 128 ? launch<128, false, kWhole>(t, p, ph, base) : launch<64, false, kWhole>(t, p, ph, base);
 }
 
 }  // namespace
@@ -52,18 +92,11 @@ int launch_paged4_prompt(const Paged4Params& p, PagedPhase& ph, int d,
   rc = make_tmap_rows(p.q, p.Hq, p.T, p.q_stride, d, p.G, ph.tile_tokens, &t.q);
   if (rc != FA_OK) return rc;
   if (p.expand > 0) {
-    cudaLaunchConfig_t c = base;
-    c.gridDim = dim3((unsigned)p.ctas * 3, 1, 1);
-    c.blockDim = dim3(256, 1, 1);
-    const int n_min = kPaged4ExpandRows / p.G + 1;
-    if (cudaLaunchKernelEx(&c, d == 128 ? fa_paged4_expand_kernel<128> : fa_paged4_expand_kernel<64>,
-                           (const Paged4Params&)p, n_min) != cudaSuccess) {
-      cudaGetLastError();
-      return FA_ERR_LAUNCH;
-    }
+    rc = d == 128 ? launch_expand<128>(p, base) : launch_expand<64>(p, base);
+    if (rc != FA_OK) return rc;
   }
-  if (p.scale_log2 < 0.f) return d == 128 ? launch<128, true>(t, p, ph, base) : launch<64, true>(t, p, ph, base);
-  return d == 128 ? launch<128, false>(t, p, ph, base) : launch<64, false>(t, p, ph, base);
+  if (p.whole) return launch_whole<true>(t, p, ph, d, base);
+  return launch_whole<false>(t, p, ph, d, base);
 }
 
 }  // namespace fa

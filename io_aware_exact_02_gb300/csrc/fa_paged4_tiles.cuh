@@ -113,8 +113,8 @@ __device__ __forceinline__ void read_raw4(const uint8_t* const (&blk)[2], int ke
   if constexpr (kV) r.keys = keys;
 }
 
-// Turns them into rows 32 part .. 32 part + 31 of a tile.
-template <int D, bool kV>
+// Turns them into rows 32 part .. 32 part + 31 of a tile (of kRows rows).
+template <int D, bool kV, int kRows = kTile>
 __device__ __forceinline__ void store_raw4(const Raw4<D>& r, int part, uint8_t* tile) {
   const int lane = (int)lane_id(), g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -143,7 +143,7 @@ __device__ __forceinline__ void store_raw4(const Raw4<D>& r, int part, uint8_t* 
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] = half2_mul(x[e], i >= 2 ? s1 : s0);
           const int ch = D == 128 ? (t & 1) * 4 + w : 2 * t + w;
-          *reinterpret_cast<uint4*>(tile + (D == 128 ? (t >> 1) * (kTile * 128) : 0) + row * 128 +
+          *reinterpret_cast<uint4*>(tile + (D == 128 ? (t >> 1) * (kRows * 128) : 0) + row * 128 +
                                     ((ch ^ (row & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
         }
       } else {
@@ -162,7 +162,7 @@ __device__ __forceinline__ void store_raw4(const Raw4<D>& r, int part, uint8_t* 
             // (Lanes of odd g store the odd key first.)
             const int key = k ^ (g & 1), row = 32 * part + 16 * b + 8 * u + 2 * t + key;
             const uint32_t sel = key ? 0x7632u : 0x5410u;
-            *reinterpret_cast<uint4*>(tile + (ch >> 3) * (kTile * 128) + row * 128 +
+            *reinterpret_cast<uint4*>(tile + (ch >> 3) * (kRows * 128) + row * 128 +
                                       (((ch & 7) ^ (row & 7)) << 4)) =
                 make_uint4(__byte_perm(x[0], x[1], sel), __byte_perm(x[2], x[3], sel),
                            __byte_perm(x[4], x[5], sel), __byte_perm(x[6], x[7], sel));
@@ -174,10 +174,12 @@ __device__ __forceinline__ void store_raw4(const Raw4<D>& r, int part, uint8_t* 
 }
 
 // The tiles of long prompts' sequences in fp16, once for all units: a warp makes a
-// quarter of a tile, K and V, as the prompt kernel's warps do; in the order of the
+// quarter of a tile, K and V, as the prompt kernel's warps do, in the warp's part
+// of shared memory, `stage`, from where it leaves in whole lines; in the order of the
 // sequences, as far as the room goes.  n_min: the fewest rows of those sequences.
 template <int D>
-__device__ __forceinline__ void paged4_expand(const Paged4Params& p, int n_min, int w, int warps) {
+__device__ __forceinline__ void paged4_expand(const Paged4Params& p, int n_min, int w, int warps,
+                                              uint8_t (&stage)[2][32 * D * 2]) {
   constexpr int kBytes = kTile * D * 2;
   const int lane = (int)lane_id();
   const long long cap = (long long)p.max_pages << p.page_shift;
@@ -226,12 +228,69 @@ __device__ __forceinline__ void paged4_expand(const Paged4Params& p, int n_min, 
         read_raw4<D, false>(blk, 0, k);
         read_raw4<D, true>(blk, keys - first, v);
         uint8_t* const dst = p.tiles + ((long long)(base + tile) * p.Hkv + h) * (2 * kBytes);
-        store_raw4<D, false>(k, part, dst);
-        store_raw4<D, true>(v, part, dst + kBytes);
+        if (lane == 0) bulk_wait_group_read0();  // (the last quarter has left)
+        __syncwarp();
+        store_raw4<D, false, 32>(k, 0, stage[0]);
+        store_raw4<D, true, 32>(v, 0, stage[1]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i)  // 64 channels of K, then V
+            bulk_store(dst + (i * kTile + 32 * part) * 128, stage[0] + i * 4096, 4096);
+          bulk_commit_group();
+        }
+        __syncwarp();
       }
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
   }
+  if (lane == 0) bulk_wait_group0();
+  __syncwarp();
+}
+
+// The warp that loads the tiles of the CTA's segments where all of them are in fp16.
+// (A sequence that was left out, for its table's sake, takes what is there.)
+template <int D, int S, int kRing, class Smem>
+__device__ __forceinline__ void paged4_load_tiles(const Paged4Params& p, Smem& sm) {
+  constexpr int kBytes = kTile * D * 2;
+  volatile int* abortf = &sm.abort_flag;
+  const int lane = (int)lane_id();
+  bool ok = true;
+  int c = 0;
+  for (int m = 0; ok; ++m) {
+    const int is = m % kRing;
+    ok = mbar_wait(&sm.item_full[is], (m / kRing) & 1, p.status, abortf, kSitePgItemFull);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    const PagedItem& it = sm.item[is];
+    const int nj = it.nj, h = it.h, at = it.key / kTile;
+    const bool end = it.end != 0;
+    const int base = end ? 0 : p.tile_base[it.b];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.item_empty[is]);
+    if (end) break;
+    for (int j = 0; ok && j < nj; ++j) {
+      const int tile = base + at + j;
+      const uint8_t* const src =
+          p.tiles + ((long long)(base >= 0 && tile < p.expand ? tile : 0) * p.Hkv + h) * (2 * kBytes);
+      for (int v = 0; ok && v < 2; ++v, ++c) {
+        if (c >= S)
+          ok = mbar_wait(&sm.kv_empty[c % S], (c / S - 1) & 1, p.status, abortf, kSitePgKvEmpty);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm.kv_full[c % S], kBytes);
+          bulk_load(sm.kv[c % S], src + v * kBytes, kBytes, &sm.kv_full[c % S]);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  // After a failure: the copies on their way have to land before the CTA exits.
+  if (*abortf && lane == 0)
+    for (int x = max(0, c - S); x < c; ++x) drain_wait(&sm.kv_full[x % S], (x / S) & 1);
+  __syncwarp();
 }
 
 // One of the warps that make the tiles of the CTA's segments: part `part` of each.

@@ -242,8 +242,8 @@ __device__ __noinline__ void store_box(uint32_t colO, float own, uint8_t* out,
 // kFour: over the cache in 4 bits (fa_kv4.cuh).  Four more warps, 12-15, turn its
 // codes into fp16 tiles, warp 8 has the list and Q only, 10 is idle too; the
 // products run in fp16, and the softmax warps scale each row of Q to its range
-// first.
-template <int D, bool kNeg, bool kStarted, bool kFour = false>
+// first.  kWhole: the tiles are in fp16 already, and warp 10 loads them.
+template <int D, bool kNeg, bool kStarted, bool kFour = false, bool kWhole = false>
 __device__ __forceinline__ void prompt_cta(
     const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const CUtensorMap* to,
     const std::conditional_t<kFour, Paged4Params, PagedParams>& p, const PagedPhase& ph, int cta,
@@ -255,16 +255,17 @@ __device__ __forceinline__ void prompt_cta(
   volatile int* abortf = &sm.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5;
   constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpLoadV = 10, kWarpTiles = 12;
-  constexpr int kThreads = kFour ? kPaged4Threads : kPagedThreads;
-  constexpr int kRegsCompute = kFour ? kPaged4RegsCompute : kPagedRegsCompute;
-  constexpr int kRegsLoad = kFour ? kPaged4RegsList : kPagedRegsLoad;
+  constexpr bool kMakes = kFour && !kWhole;  // (has warps that make tiles)
+  constexpr int kThreads = kMakes ? kPaged4Threads : kPagedThreads;
+  constexpr int kRegsCompute = kMakes ? kPaged4RegsCompute : kPagedRegsCompute;
+  constexpr int kRegsLoad = kMakes ? kPaged4RegsList : kPagedRegsLoad;
 
   if (tid == 0) {
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
     if constexpr (kFour) mbar_init(&sm.q_half, 256);
     for (int s = 0; s < S; ++s) {
-      mbar_init(&sm.kv_full[s], kFour ? 4 : 1);
+      mbar_init(&sm.kv_full[s], kMakes ? 4 : 1);
       mbar_init(&sm.kv_empty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -276,9 +277,9 @@ __device__ __forceinline__ void prompt_cta(
     }
     for (int i = 0; i < kPromptRing; ++i) {
       mbar_init(&sm.item_full[i], 1);
-      // Read by the issuing thread, the V warp (kFour: the four that make tiles)
+      // Read by the issuing thread, the V warp (kMakes: the four that make tiles)
       // and the eight softmax warps.
-      mbar_init(&sm.item_empty[i], (kFour ? 5 : 2) + 8);
+      mbar_init(&sm.item_empty[i], (kMakes ? 5 : 2) + 8);
     }
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
@@ -349,7 +350,10 @@ __device__ __forceinline__ void prompt_cta(
   } else if (warp == kWarpLoadV) {
     // ------------------------------------------------------------ V
     setmaxnreg_dec<kRegsLoad>();
-    if constexpr (!kFour) paged_produce_v<D, S, kPromptRing>(p, sm, tv, nullptr);
+    if constexpr (kWhole)
+      paged4_load_tiles<D, S, kPromptRing>(p, sm);
+    else if constexpr (!kFour)
+      paged_produce_v<D, S, kPromptRing>(p, sm, tv, nullptr);
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------ products
     setmaxnreg_dec<kRegsLoad>();
@@ -583,9 +587,9 @@ __device__ __forceinline__ void prompt_cta(
     }
     if (lane_id() == 0) bulk_wait_group0();
     __syncwarp();
-  } else if (kFour && warp >= kWarpTiles) {
+  } else if (kMakes && warp >= kWarpTiles) {
     // ------------------------------------------------------------ tiles
-    if constexpr (kFour) {
+    if constexpr (kMakes) {
       setmaxnreg_dec<kPaged4RegsTiles>();
       paged4_produce_tiles<D, S, kPromptRing>(p, sm, warp - kWarpTiles);
     }

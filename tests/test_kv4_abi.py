@@ -134,18 +134,22 @@ def test_paged_other_errors(lib):
     expect_device(lambda: paged(lib, wsb=need))
     assert lib.fa_fwd_paged4_workspace_size(0, 2, 4, 2, 64, 2) == 0
     assert lib.fa_fwd_paged4_workspace_size(3, 2, 4, 2, 72, 2) == 0
-    # Room for tiles: only where a sequence may have more than 768 rows of a head.
+    # Room for tiles: only where a sequence may have more than 1,024 rows of a head.
     best = lib.fa_fwd_paged4_best_workspace_size
     assert best(3, 2, 4, 2, 64, 16, 4, 2) == need
     assert best(3, 2, 4, 2, 72, 16, 4, 2) == best(3, 2, 4, 2, 64, 24, 4, 2) == 0
-    assert best(384, 2, 4, 2, 64, 16, 40, 384) == lib.fa_fwd_paged4_workspace_size(384, 2, 4, 2, 64, 384)
-    least = lib.fa_fwd_paged4_workspace_size(385, 2, 4, 2, 64, 385)
-    assert best(385, 2, 4, 2, 64, 16, 40, 385) == least + 256 + 5 * 65536
-    assert best(770, 2, 4, 2, 64, 16, 40, 385) == (
-        lib.fa_fwd_paged4_workspace_size(770, 2, 4, 2, 64, 385) + 256 + 10 * 65536)
-    most = best(770, 2, 4, 2, 64, 16, 1 << 26, 385) - lib.fa_fwd_paged4_workspace_size(
-        770, 2, 4, 2, 64, 385)
-    assert most == 256 + (512 << 20)
+    def room(T, B, max_pages, max_q):
+        return best(T, B, 4, 2, 64, 16, max_pages, max_q) - lib.fa_fwd_paged4_workspace_size(
+            T, B, 4, 2, 64, max_q)
+    assert room(512, 2, 40, 512) == 0
+    # All sequences of more than 24 rows,
+    assert room(513, 2, 40, 513) == 256 + 10 * 65536
+    assert room(49, 9, 40, 49) == 0
+    assert room(600, 100, 40, 513) == 512 + 24 * 5 * 65536
+    # those of more than 512 where that is beyond the bound, as far as the bound goes.
+    assert room(1538, 100, 16 * 256, 513) == 512 + 2 * 512 * 65536
+    assert room(1539, 100, 16 * 256, 513) == 512 + 3 * 512 * 65536
+    assert room(1539, 100, 1 << 26, 513) == 512 + (512 << 20)
 
 
 def words(fmt, *args):

@@ -145,9 +145,9 @@ def test_results_do_not_change_from_call_to_call():
 
 
 @pytest.mark.parametrize("Hq,Hkv,d,page,lens,nq", [
-    (8, 1, 128, 16, [1000, 100, 333, 129], [97, 1, 300, 120]),
-    (6, 2, 64, 32, [2000, 300, 77, 512], [257, 290, 5, 400]),
-    (2, 2, 128, 128, [800] + [5] * 70 + [900], [800] + [1] * 70 + [769]),
+    (8, 1, 128, 16, [1000, 100, 333, 129], [129, 1, 300, 140]),
+    (6, 2, 64, 32, [2000, 300, 77, 512], [360, 290, 5, 400]),
+    (2, 2, 128, 128, [1100] + [5] * 70 + [1200], [1100] + [1] * 70 + [1025]),
 ])
 @pytest.mark.parametrize("causal", [True, False])
 def test_room_for_tiles_changes_no_result(Hq, Hkv, d, page, lens, nq, causal):
