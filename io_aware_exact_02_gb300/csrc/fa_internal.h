@@ -417,9 +417,11 @@ inline Paged4Form paged4_form(int T, int B, int G, int max_q) {
 // keys and values are turned into tiles in fp16 once for all units: those of every
 // sequence of the prompt kernel, if kPaged4ExpandBytes hold them (`whole`: it has no
 // warps then that make tiles), else those of the sequences with so many rows, as far
-// as the room goes.  (4 sequences of 4K keys, H_kv 8, d = 128, without and with: 1,024
-// rows 90 and 95 us, 2,048 rows 155 and 144, 4,096 rows 242 and 214; 8 of 16K: 500 and
-// 508, 962 and 858, 1,858 and 1,551.)
+// as the room goes.  (Rows of each sequence, H_kv 8, d = 128, without and with, `whole`:
+// 4 sequences of 4K keys: 800 rows 97 and 89 us, 1,024 90 and 89, 2,048 155 and 133,
+// 4,096 242 and 190; 8 of 4K: 512 rows 94 and 106; 8 of 8K: 768 rows 215 and 228, 1,024
+// 274 and 270; 8 of 16K: 2,048 rows 964 and 829, 4,096 1,859 and 1,496.  Not whole,
+// 4 of 4K: 2,048 rows 155 and 144, 4,096 242 and 214.)
 constexpr int kPaged4ExpandRows = 1024;
 constexpr size_t kPaged4ExpandBytes = (size_t)512 << 20;
 struct Paged4Expand {

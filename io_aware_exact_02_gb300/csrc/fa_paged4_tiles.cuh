@@ -184,66 +184,82 @@ __device__ __forceinline__ void paged4_expand(const Paged4Params& p, int n_min, 
   const int lane = (int)lane_id();
   const long long cap = (long long)p.max_pages << p.page_shift;
   long long before = 0;  // tiles of the sequences that were looked at
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + lane;
-    int len = 0, tiles = 0;
-    if (b < p.B) {
-      const int t0 = p.cu_q[b], t1 = p.cu_q[b + 1];
-      len = p.seq_lens[b];
-      if (paged_range_ok(t0, t1, p.T) && t1 - t0 >= n_min && len > 0 && len <= cap)
-        tiles = (int)(((long long)len + kTile - 1) / kTile);
+  for (int b0 = 0; b0 < p.B; b0 += 128) {  // four neighbours to a lane: their loads together
+    int t0[4], t1[4], len[4], tiles[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = b0 + 4 * lane + i;
+      t0[i] = t1[i] = len[i] = 0;
+      if (b < p.B) t0[i] = p.cu_q[b], t1[i] = p.cu_q[b + 1], len[i] = p.seq_lens[b];
     }
-    int upto = tiles;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool on = paged_range_ok(t0[i], t1[i], p.T) && t1[i] - t0[i] >= n_min && len[i] > 0 &&
+                      len[i] <= cap;
+      tiles[i] = on ? min((len[i] - 1) / kTile + 1, p.expand + 1) : 0;  // (more have no room)
+      sum += tiles[i];
+    }
+    int upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += y;
     }
-    const long long start = before + upto - tiles;
-    const bool fits = tiles > 0 && start + tiles <= p.expand;
-    if (w == 0 && b < p.B) p.tile_base[b] = fits ? (int)start : -1;
-    for (unsigned left = __ballot_sync(0xffffffffu, fits); left != 0; left &= left - 1) {
-      const int src = __ffs(left) - 1, base = __shfl_sync(0xffffffffu, (int)start, src);
-      const int n = __shfl_sync(0xffffffffu, tiles, src) * p.Hkv * 4;
-      const int keys = __shfl_sync(0xffffffffu, len, src);
-      const int* const list = p.page_table + (long long)(b0 + src) * p.max_pages;
-      const int at = (int)((long long)base * p.Hkv * 4 % warps);
-      for (int x = w >= at ? w - at : w - at + warps; x < n; x += warps) {
-        const int part = x & 3, tile = (x >> 2) / p.Hkv, h = (x >> 2) - tile * p.Hkv;
-        const int first = tile * kTile + 32 * part, key = first + 16 * (lane & 1);
-        const int page = key < keys ? list[key >> p.page_shift] : 0;
-        const bool valid = (unsigned)page < (unsigned)p.num_pages;
-        if (!valid) {
-          int abort_flag = 0;
-          report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
-        }
-        const unsigned long long mine = reinterpret_cast<unsigned long long>(
-            p.pages + kv4_block_at(valid ? page : 0, p.Hkv, h, p.page_shift,
-                                   key & (p.page_size - 1), Kv4Block<D>::kBytes));
-        const uint8_t* blk[2];
+    long long at0 = before + upto - sum;
+    int start[4];  // (-1: no room)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          blk[i] = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, mine, i));
-        Raw4<D> k, v;
-        read_raw4<D, false>(blk, 0, k);
-        read_raw4<D, true>(blk, keys - first, v);
-        uint8_t* const dst = p.tiles + ((long long)(base + tile) * p.Hkv + h) * (2 * kBytes);
-        if (lane == 0) bulk_wait_group_read0();  // (the last quarter has left)
-        __syncwarp();
-        store_raw4<D, false, 32>(k, 0, stage[0]);
-        store_raw4<D, true, 32>(v, 0, stage[1]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i)  // 64 channels of K, then V
-            bulk_store(dst + (i * kTile + 32 * part) * 128, stage[0] + i * 4096, 4096);
-          bulk_commit_group();
-        }
-        __syncwarp();
-      }
+    for (int i = 0; i < 4; ++i) {
+      start[i] = tiles[i] > 0 && at0 + tiles[i] <= p.expand ? (int)at0 : -1;
+      at0 += tiles[i];
+      if (w == 0 && b0 + 4 * lane + i < p.B) p.tile_base[b0 + 4 * lane + i] = start[i];
     }
     before += __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      auto pick = [&](const int (&x)[4]) { return i == 0 ? x[0] : i == 1 ? x[1] : i == 2 ? x[2] : x[3]; };
+      const int my_start = pick(start), my_tiles = pick(tiles), my_len = pick(len);
+      for (unsigned left = __ballot_sync(0xffffffffu, my_start >= 0); left != 0; left &= left - 1) {
+        const int src = __ffs(left) - 1, base = __shfl_sync(0xffffffffu, my_start, src);
+        const int n = __shfl_sync(0xffffffffu, my_tiles, src) * p.Hkv * 4;
+        const int keys = __shfl_sync(0xffffffffu, my_len, src);
+        const int* const list = p.page_table + (long long)(b0 + 4 * src + i) * p.max_pages;
+        const int at = (int)((long long)base * p.Hkv * 4 % warps);
+        for (int x = w >= at ? w - at : w - at + warps; x < n; x += warps) {
+          const int part = x & 3, tile = (x >> 2) / p.Hkv, h = (x >> 2) - tile * p.Hkv;
+          const int first = tile * kTile + 32 * part, key = first + 16 * (lane & 1);
+          const int page = key < keys ? list[key >> p.page_shift] : 0;
+          const bool valid = (unsigned)page < (unsigned)p.num_pages;
+          if (!valid) {
+            int abort_flag = 0;
+            report_status(p.status, &abort_flag, FA_ERR_PAGE, kSitePagedPage);
+          }
+          const unsigned long long mine = reinterpret_cast<unsigned long long>(
+              p.pages + kv4_block_at(valid ? page : 0, p.Hkv, h, p.page_shift,
+                                     key & (p.page_size - 1), Kv4Block<D>::kBytes));
+          const uint8_t* blk[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            blk[e] = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, mine, e));
+          Raw4<D> k, v;
+          read_raw4<D, false>(blk, 0, k);
+          read_raw4<D, true>(blk, keys - first, v);
+          uint8_t* const dst = p.tiles + ((long long)(base + tile) * p.Hkv + h) * (2 * kBytes);
+          if (lane == 0) bulk_wait_group_read0();  // (the last quarter has left)
+          __syncwarp();
+          store_raw4<D, false, 32>(k, 0, stage[0]);
+          store_raw4<D, true, 32>(v, 0, stage[1]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e)  // 64 channels of K, then V
+              bulk_store(dst + (e * kTile + 32 * part) * 128, stage[0] + e * 4096, 4096);
+            bulk_commit_group();
+          }
+          __syncwarp();
+        }
+      }
+    }
   }
   if (lane == 0) bulk_wait_group0();
   __syncwarp();

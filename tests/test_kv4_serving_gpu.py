@@ -173,6 +173,17 @@ def test_room_for_tiles_changes_no_result(Hq, Hkv, d, page, lens, nq, causal):
         assert torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1])
 
 
+def test_long_prompts_among_many_sequences():
+    # (More sequences than a warp looks at together, the long ones anywhere among them.)
+    lens, nq = [9] * 300, [1] * 300
+    for b in (0, 3, 127, 128, 200, 299):
+        lens[b], nq[b] = 150 + b, 130
+    x = c4.Batch4(8, 1, 64, 16, lens, nq, seed=18)
+    o, lse = fa.fwd_paged4(*x.args(), max_q=130, out=x.out, lse=x.lse)
+    fa.check_device_status()
+    x.check(o, lse, True, 0.125)
+
+
 def test_captured_with_other_lengths_and_pages():
     """One graph of an append and an attention, replayed as the sequences grow."""
     s = Server(3, 30, 16, 8, 4, 2, 64, seed=7)
@@ -248,9 +259,9 @@ def test_on_a_stream_of_its_own():
     x.check(o, lse, True, 0.125)
 
 
-@pytest.mark.parametrize("nq", [[1, 1, 1], [100, 1, 80]])
-def test_tables_out_of_bounds_are_recorded(nq):
-    lens = [200, 64, 150]
+@pytest.mark.parametrize("nq,lens", [([1, 1, 1], [200, 64, 150]), ([100, 1, 80], [200, 64, 150]),
+                                     ([600, 550, 5], [700, 600, 150])])
+def test_tables_out_of_bounds_are_recorded(nq, lens):
 
     def call(change, site):
         x = c4.Batch4(4, 2, 64, 16, lens, nq, seed=11)
