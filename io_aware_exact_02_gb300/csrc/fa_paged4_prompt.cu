@@ -23,11 +23,11 @@ __global__ void __launch_bounds__(kPromptThreads<kWhole>, 1)
 
 template <int D>
 struct alignas(128) ExpandSmem {
-  uint8_t stage[kExpandWarps][2][32 * D * 2];
+  uint8_t stage[kExpandWarps][32 * D * 2];
 };
 
 template <int D>
-__global__ void __launch_bounds__(32 * kExpandWarps)
+__global__ void __launch_bounds__(32 * kExpandWarps, 6)
     fa_paged4_expand_kernel(const Paged4Params p, int n_min) {
   extern __shared__ uint8_t smem_raw[];
   ExpandSmem<D>& sm = *reinterpret_cast<ExpandSmem<D>*>(
@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(32 * kExpandWarps)
 template <int D>
 int launch_expand(const Paged4Params& p, const cudaLaunchConfig_t& base) {
   cudaLaunchConfig_t c = base;
-  c.gridDim = dim3((unsigned)p.ctas * (233472 / (sizeof(ExpandSmem<D>) + 128 + 1024)), 1, 1);
+  c.gridDim = dim3((unsigned)p.ctas * 6, 1, 1);
   c.blockDim = dim3(32 * kExpandWarps, 1, 1);
   c.dynamicSmemBytes = sizeof(ExpandSmem<D>) + 128;
   if (paged_kernel_ready<fa_paged4_expand_kernel<D>, 0>(c.dynamicSmemBytes) != FA_OK)

@@ -20,6 +20,8 @@
 // K and V (256 -> 242).
 #pragma once
 
+#include <type_traits>
+
 #include "fa_internal.h"
 #include "fa_kv4.cuh"
 #include "fa_paged.cuh"
@@ -174,12 +176,12 @@ __device__ __forceinline__ void store_raw4(const Raw4<D>& r, int part, uint8_t* 
 }
 
 // The tiles of long prompts' sequences in fp16, once for all units: a warp makes a
-// quarter of a tile, K and V, as the prompt kernel's warps do, in the warp's part
+// quarter of a tile of K or V, as the prompt kernel's warps do, in the warp's part
 // of shared memory, `stage`, from where it leaves in whole lines; in the order of the
 // sequences, as far as the room goes.  n_min: the fewest rows of those sequences.
 template <int D>
 __device__ __forceinline__ void paged4_expand(const Paged4Params& p, int n_min, int w, int warps,
-                                              uint8_t (&stage)[2][32 * D * 2]) {
+                                              uint8_t (&stage)[32 * D * 2]) {
   constexpr int kBytes = kTile * D * 2;
   const int lane = (int)lane_id();
   const long long cap = (long long)p.max_pages << p.page_shift;
@@ -220,12 +222,13 @@ __device__ __forceinline__ void paged4_expand(const Paged4Params& p, int n_min, 
       const int my_start = pick(start), my_tiles = pick(tiles), my_len = pick(len);
       for (unsigned left = __ballot_sync(0xffffffffu, my_start >= 0); left != 0; left &= left - 1) {
         const int src = __ffs(left) - 1, base = __shfl_sync(0xffffffffu, my_start, src);
-        const int n = __shfl_sync(0xffffffffu, my_tiles, src) * p.Hkv * 4;
+        const int n = __shfl_sync(0xffffffffu, my_tiles, src) * p.Hkv * 8;
         const int keys = __shfl_sync(0xffffffffu, my_len, src);
         const int* const list = p.page_table + (long long)(b0 + 4 * src + i) * p.max_pages;
-        const int at = (int)((long long)base * p.Hkv * 4 % warps);
+        const int at = (int)((long long)base * p.Hkv * 8 % warps);
         for (int x = w >= at ? w - at : w - at + warps; x < n; x += warps) {
-          const int part = x & 3, tile = (x >> 2) / p.Hkv, h = (x >> 2) - tile * p.Hkv;
+          const int part = x & 3, tile = (x >> 3) / p.Hkv, h = (x >> 3) - tile * p.Hkv;
+          const bool is_v = (x & 4) != 0;
           const int first = tile * kTile + 32 * part, key = first + 16 * (lane & 1);
           const int page = key < keys ? list[key >> p.page_shift] : 0;
           const bool valid = (unsigned)page < (unsigned)p.num_pages;
@@ -240,20 +243,25 @@ __device__ __forceinline__ void paged4_expand(const Paged4Params& p, int n_min, 
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             blk[e] = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, mine, e));
-          Raw4<D> k, v;
-          read_raw4<D, false>(blk, 0, k);
-          read_raw4<D, true>(blk, keys - first, v);
-          uint8_t* const dst = p.tiles + ((long long)(base + tile) * p.Hkv + h) * (2 * kBytes);
-          if (lane == 0) bulk_wait_group_read0();  // (the last quarter has left)
-          __syncwarp();
-          store_raw4<D, false, 32>(k, 0, stage[0]);
-          store_raw4<D, true, 32>(v, 0, stage[1]);
+          uint8_t* const dst = p.tiles + ((long long)(base + tile) * p.Hkv + h) * (2 * kBytes) +
+                               (is_v ? kBytes : 0);
+          Raw4<D> raw;
+          auto make = [&](auto v) {
+            read_raw4<D, decltype(v)::value>(blk, keys - first, raw);
+            if (lane == 0) bulk_wait_group_read0();  // (the last quarter has left)
+            __syncwarp();
+            store_raw4<D, decltype(v)::value, 32>(raw, 0, stage);
+          };
+          if (is_v)
+            make(std::true_type{});
+          else
+            make(std::false_type{});
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e)  // 64 channels of K, then V
-              bulk_store(dst + (e * kTile + 32 * part) * 128, stage[0] + e * 4096, 4096);
+            for (int e = 0; e < D / 64; ++e)  // 64 channels
+              bulk_store(dst + (e * kTile + 32 * part) * 128, stage + e * 4096, 4096);
             bulk_commit_group();
           }
           __syncwarp();
