@@ -11,13 +11,19 @@
 // c ^ (r % 8).  Which lane stores which of its pieces first is chosen so that
 // eight lanes meet eight chunks.
 //
-// Measured: 4 chunks of 1,024 rows over 4K keys, H_q 32, H_kv 8, d = 128: 242 us (992
-// TFLOP/s, tensor pipe active 46%); with the tile warps handing on what the slots
-// hold 188, over the bf16 cache 173.  Bound by those warps beside the softmax: their
-// instructions share its schedulers, and any use of a loaded value right behind the
-// load waits for it.  Hence the reads a step ahead, looked at only when stored
+// Measured: 4 chunks of 1,024 rows over 4K keys, H_q 32, H_kv 8, d = 128: 242 us with the
+// tile warps (992 TFLOP/s, tensor pipe active 46%), bound by them beside the softmax:
+// their instructions share its schedulers, and any use of a loaded value right behind
+// the load waits for it.  Hence the reads a step ahead, looked at only when stored
 // (295 -> 256 us with registers enough for that), and a block's place found once for
 // K and V (256 -> 242).
+//
+// There every tile is made 16 times, once for each unit of 256 rows.  Where a sequence
+// has more than 1,024 rows of a head, paged4_expand makes each once, by the same
+// functions, into the workspace, in the image that shared memory takes, so that one
+// copy of 32 KB is a tile.  Where that holds for all of the kernel's sequences, it runs
+// without tile warps: 187 us (1,284 TFLOP/s, tensor pipe active 64% of its 168 us; over
+// the bf16 cache 170), of which the making takes 15 (67 MB written) and the merge 12.
 #pragma once
 
 #include <type_traits>
