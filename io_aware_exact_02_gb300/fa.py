@@ -932,7 +932,9 @@ def _pools(pools, num_pages, dev):
         n, base = pools.shape[0], pools.data_ptr()
         size = pools.stride(1) * pools.element_size()
         step = size * num_pages
-        return (struct.pack("%dQ" % n, *range(base, base + n * step, step)) if step else b"",
+        if step == 0:
+            raise ValueError("pools of shape %s hold nothing" % (tuple(pools.shape),))
+        return (struct.pack("%dQ" % n, *range(base, base + n * step, step)),
                 struct.pack("Q", size) * n, n)
     at, sizes = [], []
     for t in pools:
@@ -998,6 +1000,8 @@ def pages_copy(src, dst, pools):
     dev, n = src.get_device(), src.shape[0]
     for name, t in (("src", src), ("dst", dst)):
         _check_one(name, t, (n,), _I32, dev)
+    if not len(pools):
+        raise ValueError("pools names no cache")
     num_pages = pools.shape[1] if isinstance(pools, torch.Tensor) else pools[0].shape[0]
     at, sizes, count = _pools(pools, num_pages, dev)
     with torch.cuda.device(dev):

@@ -96,6 +96,20 @@ def test_prompts_tokens_forks_and_compaction(Hq, Hkv, d, page):
     s.step([5, 3], [40, 1])
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,page,lens,nq", [
+    (17, 1, 64, 16, [300, 40], [90, 3]),       # whole tokens leave rows of a tile empty
+    (128, 1, 128, 32, [140, 33, 7], [40, 1, 7]),
+    (100, 1, 64, 16, [90], [60]),
+    (14, 2, 128, 64, [1, 200, 130], [1, 150, 130]),
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompts_of_many_heads_to_a_group(Hq, Hkv, d, page, lens, nq, causal):
+    x = c4.Batch4(Hq, Hkv, d, page, lens, nq, seed=19)
+    o, lse = fa.fwd_paged4(*x.args(), max_q=max(nq), causal=causal, out=x.out, lse=x.lse)
+    fa.check_device_status()
+    x.check(o, lse, causal, d ** -0.5)
+
+
 def test_any_max_q_gives_the_results():
     for max_q in (1, 2, 5, 13, 90, 1000):
         x = c4.Batch4(4, 1, 64, 16, [100, 40, 95], [90, 10, 3], seed=3)
@@ -365,6 +379,11 @@ def test_binding_refuses_what_does_not_fit():
         fa.kv4_append(q[:, :1], q[:, :1], pages, table, lens, cu)
     with pytest.raises(fa.FaError):
         fa.fwd_paged4(*x.args(), k_scale=0.0)
+    for pools in ([], pages.new_zeros(2, 0, 4), [pages.cpu()], [pages.transpose(0, 2)]):
+        with pytest.raises(ValueError):
+            fa.pages_copy(lens, lens, pools)
+    with pytest.raises(fa.FaError):
+        fa.pages_copy(lens, lens, pages.new_zeros(2, 4, 0))
     with pytest.raises(ValueError):
         fa.pages_fork(lens, lens[:0], table, lens, lens, [pages], 16)
     with pytest.raises(ValueError):
