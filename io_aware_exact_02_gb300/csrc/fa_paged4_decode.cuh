@@ -21,8 +21,8 @@
 // the layout of a block makes each one 16-byte load (d = 64: 8-byte) of
 // consecutive addresses.  P goes from the first product's layout to the
 // second's by a transposition of 8 x 8 matrices among the warp's registers.
-// The running maximum of a row is a warp's own, and moves only when a block's
-// scores exceed it by kRescaleSlack.  At a unit's end the warps' parts are
+// The reference of a row's exponents is a warp's own, kHalfHeadroom below the first
+// step's maximum, and moves only when scores exceed that by kRescaleSlack.  At a unit's end the warps' parts are
 // joined through shared memory.
 //
 // Measured, H_q 32, H_kv 8, d = 128, one row each: 8 sequences of 32K keys 65.9 us (302
@@ -436,20 +436,21 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; e += 2) over = fmax3(over, s[b][nt][e], s[b][nt][e + 1]);
-        if (j == 0 || __any_sync(0xffffffffu, over > kRescaleSlack)) {
+        if (j == 0 || __any_sync(0xffffffffu, over > kRescaleSlack + kHalfHeadroom)) {
           // The first scores, or some that outgrew the reference: every row's
-          // moves to its maximum.  (A row that the first step's keys, the lowest,
+          // moves to kHalfHeadroom below its maximum.  (A row that the first step's keys, the lowest,
           // are hidden from sees none of the later ones.)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float up = j == 0 ? ninf : 0.f;
+              float up = ninf;
 #pragma unroll
               for (int b = 0; b < U; ++b) up = fmax3(up, s[b][nt][e], s[b][nt][e + 2]);
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, x));
-              if (up == ninf) up = 0.f;
+              up -= kHalfHeadroom;
+              if (up == ninf || (j > 0 && up < 0.f)) up = 0.f;
               const float alpha = j == 0 ? 1.f : ex2_approx(-up);
               ref[nt][e] += up;
               l[nt][e] *= alpha;

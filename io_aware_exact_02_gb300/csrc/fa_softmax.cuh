@@ -19,6 +19,10 @@
 namespace fa {
 
 constexpr float kRescaleSlack = 8.0f;  // log2 units
+// Where P is fp16 the reference lies so far below the maximum that P ends at 2^15:
+// its smallest step, 2^-24, is then 2^-31 of the greatest weight.  (Without, a key of
+// weight 1 would make all those below 2^-25 vanish, however many.)
+constexpr float kHalfHeadroom = 7.0f;
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
@@ -78,7 +82,7 @@ __device__ __forceinline__ void softmax_tile_w(uint32_t colS, uint32_t colO, flo
 #pragma unroll
     for (int u = 0; u < w; ++u)
       mx8[u] = kNeg ? fminf(mx8[u], mx8[u + w]) : fmaxf(mx8[u], mx8[u + w]);
-  const float m_tile = mx8[0] * c2;
+  const float m_tile = mx8[0] * c2 - (kHalf ? kHalfHeadroom : 0.f);
   float alpha = 1.f;
   if (m_tile > m_ref + kRescaleSlack) {
     alpha = ex2_approx(m_ref - m_tile);  // 0 on the first tile (m_ref = -inf)

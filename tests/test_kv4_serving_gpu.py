@@ -149,6 +149,27 @@ def test_a_bad_query_spoils_its_own_row(nq):
     assert torch.equal(lse.cpu()[~bad], lse_good.cpu()[~bad])
 
 
+@pytest.mark.parametrize("rows", [1, 4, 64])
+@pytest.mark.parametrize("d", [64, 128])
+def test_weak_keys_beside_a_loud_one(rows, d):
+    # 127 keys of weight 2^-27 of the first one's, whose value is 0.  They are the
+    # result: fp16's step of 2^-24, 7 binary orders lower, is 2^-4 of such a weight.
+    k = torch.zeros((128, 1, d), dtype=torch.bfloat16, device="cuda")
+    k[0, 0, 0] = 6.0
+    v = torch.full_like(k, 6.0)
+    v[0] = 0.0
+    pool, table = fa.kv4_pages(8, 1, 16, d), torch.arange(8, dtype=torch.int32, device="cuda")[None]
+    fa.kv4_append(k, v, pool, table, ints([128]), ints([0, 128]))
+    q = torch.zeros((rows, 1, d), dtype=torch.bfloat16, device="cuda")
+    q[:, 0, 0] = 1.0
+    o, lse = fa.fwd_paged4(q, pool, table, ints([128]), ints([0, rows]), causal=False,
+                           scale=27 * math.log(2) / 6)
+    fa.check_device_status()
+    want = 6 * 127 * 2.0 ** -27 / (1 + 127 * 2.0 ** -27)
+    assert ((o.double() - want).abs() <= want * (2.0 ** -5 + 2.0 ** -8)).all(), (o.min(), o.max(), want)
+    assert ((lse - 27 * math.log(2)).abs() < 1e-4).all()
+
+
 def test_results_do_not_change_from_call_to_call():
     for nq in ([1] * 9, [50, 1, 1, 1, 1, 1, 1, 1, 1]):
         x = c4.Batch4(8, 2, 128, 16, [900, 300, 5, 128, 129, 700, 64, 33, 1000], nq, seed=6)
