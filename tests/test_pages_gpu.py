@@ -228,3 +228,44 @@ def test_what_is_left_out():
     assert t[2].tolist() == [0] * 4 and t[1].tolist() == [0, 0]
     fa.pages_copy(put([0, 9]), put([1, 2]), torch.zeros(1, 4, 16, dtype=torch.uint8, device="cuda"))
     assert status() == (fa.FA_ERR_PAGE, 304)
+
+
+@pytest.mark.parametrize("pages,given", [(60, True), (60, False), (9000, True)])
+def test_captured_and_replayed(pages, given):
+    # A fork, a release and a compaction in one graph, replayed on other tables.
+    width, rows, page = 12, 8, 16
+    gpu_pools = torch.zeros((2, pages, 2, 144), dtype=torch.uint8, device="cuda")
+    book = Book([33, 16, 100], rows, pages, page, width, 3)
+    table, lens, refs = book.tensors()
+    parents, children = (torch.tensor(x, dtype=torch.int32, device="cuda")
+                         for x in ([0, 2, 0], [3, 4, 5]))
+    gone = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    live = torch.zeros(1, dtype=torch.int32, device="cuda")
+    need = (fa.pages_fork_workspace_size(pages, 3), fa.pages_compact_workspace_size(pages))
+    ws = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") if given else None for n in need]
+    graph = torch.cuda.CUDAGraph()
+    stream = torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=stream):
+        fa.pages_fork(parents, children, table, lens, refs, gpu_pools, page, workspace=ws[0])
+        fa.pages_free(gone, table, lens, refs, page)
+        fa.pages_compact(table, lens, refs, gpu_pools, page, live=live, workspace=ws[1])
+    for seed, start in enumerate(([33, 16, 100], [7, 64, 150], [0, 1, 32], [190, 191, 192])):
+        book = Book(start, rows, pages, page, width, seed)
+        host = torch.randint(0, 256, gpu_pools.shape, dtype=torch.uint8,
+                             generator=torch.Generator().manual_seed(seed))
+        gpu_pools.copy_(host)
+        for a, b in zip((table, lens, refs), book.tensors()):
+            a.copy_(b)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            graph.replay()
+        stream.synchronize()
+        fa.check_device_status()
+        pools = list(host.unbind(0))
+        book.fork([0, 2, 0], [3, 4, 5], pools)
+        book.free([0, 1])
+        assert live.item() == book.compact(pools)
+        book.check(table, lens, refs)
+        for t, p in zip(gpu_pools.cpu(), pools):
+            held = torch.tensor(book.refs) > 0
+            assert torch.equal(t[held], p[held])
