@@ -866,7 +866,9 @@ def fwd_paged4(q, pages, page_table, seq_lens, cu_q, max_q=None, causal: bool = 
                scale: float | None = None, k_scale: float = 1.0, v_scale: float = 1.0, out=None,
                lse=None, workspace=None):
     """fwd_paged over a cache held in 4 bits (``pages``, see kv4_pages), with the
-    tensors' scales of the appends.  Returns (o, lse)."""
+    tensors' scales of the appends.  ``workspace``: fwd_paged4_workspace_size bytes
+    at least; allocated if not given, for long prompts with up to 512 MB in which
+    their keys and values are held in fp16 meanwhile.  Returns (o, lse)."""
     try:
         dev, (T, Hq, d) = q.get_device(), q.shape
         num_pages, Hkv, size = pages.shape
