@@ -450,8 +450,10 @@ __device__ __forceinline__ void paged4_produce_tiles(const Paged4Params& p, Smem
 
 // Row r of a Q tile from bf16 to fp16, in place, times the power of two that takes
 // it to fp16's range; returns the factor from products to exponents (c2 that of
-// the row as it was), which is never 0: a zero scale is a tiny one.
-template <int D>
+// the row as it was), which is never 0: what vanishes is a tiny one, negative where
+// the kernel's form is that of negative scales (c2 may be a 0 of either sign, its
+// product with the keys' scale being too small to hold).
+template <int D, bool kNeg>
 __device__ __forceinline__ float q_row_to_half(uint8_t* tile, int r, float c2) {
   uint8_t* const row = tile + r * 128;
   uint32_t top = 0u;
@@ -477,7 +479,7 @@ __device__ __forceinline__ float q_row_to_half(uint8_t* tile, int r, float c2) {
     *at = make_uint4(turn(x.x), turn(x.y), turn(x.z), turn(x.w));
   }
   const float x = c2 * kv4_pow2(-e), tiny = 1.17549435e-38f;
-  return fabsf(x) >= tiny ? x : (c2 < 0.f ? -tiny : tiny);
+  return fabsf(x) >= tiny ? x : (kNeg ? -tiny : tiny);
 }
 
 }  // namespace fa

@@ -501,7 +501,7 @@ __device__ __forceinline__ void prompt_cta(
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           ++n_q;
-          c2 = q_row_to_half<D>(sm.q[t], r, p.scale_log2 * p.k_scale);
+          c2 = q_row_to_half<D, kNeg>(sm.q[t], r, p.scale_log2 * p.k_scale);
           fence_proxy_async_smem();
           mbar_arrive(&sm.q_half);
         }

@@ -252,3 +252,14 @@ def test_attention_many_sequences():
     attend(c4.Batch4(4, 2, 64, 16, lens, [1] * 70, seed=8), max_q=1)
     nq = [min(n, 1 + (i % 9 == 0) * 40) for i, n in enumerate(lens)]
     attend(c4.Batch4(4, 1, 128, 16, lens, nq, seed=9), max_q=max(nq))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale,k_scale", [(-1e-10, 1e-37), (1e-10, 1e-37), (-1e-30, 1e-38),
+                                           (-0.0, 1.0), (-1e-20, 1.0)])
+def test_attention_of_a_scale_that_vanishes(scale, k_scale, d):
+    # (The product with the keys' scale is 0 with a sign, or next to it: every key
+    # that is seen counts the same, none that is hidden.)
+    for nq in ([1, 1, 1], [90, 3, 40], [600, 2, 300]):
+        lens = [max(n, 90 + i) for i, n in enumerate(nq)]
+        attend(c4.Batch4(4, 2, d, 16, lens, nq, seed=4, k_scale=k_scale), True, scale, max_q=max(nq))
