@@ -435,8 +435,8 @@ int fa_fwd_paged4(const void* q, const void* pages, void* o, float* lse, const i
  * 256-byte aligned.
  *
  * fa_pages_free empties the rows rows_list[i], i < n: refs - 1 for every page,
- * length 0.  A row listed twice is freed once.  A page whose count is 0 already
- * records FA_ERR_PAGE and keeps it.
+ * length 0.  A row listed twice is freed once, one whose length is out of bounds is
+ * left as it is.  A page whose count is 0 already records FA_ERR_PAGE and keeps it.
  *
  * fa_pages_compact moves the pages in use (`live` of them) to the numbers below
  * live: the highest page in use goes to the lowest free one and so on, in every

@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(kCopyThreads)
 }
 
 // One CTA a sequence: its pages count one less, its length is 0.  A row that is
-// listed twice is freed once.
+// listed twice is freed once: by the CTA that takes its length.  One of a length out
+// of bounds is left as it is.
 __global__ void __launch_bounds__(128) fa_pages_free_kernel(const PagesParams p) {
   launch_dependents();
   wait_prior_grid();
@@ -310,13 +311,18 @@ __global__ void __launch_bounds__(128) fa_pages_free_kernel(const PagesParams p)
     if (threadIdx.x == 0) report(p.status, kSitePagesRow);
     return;
   }
-  if (threadIdx.x == 0) s_len = atomicExch(p.seq_lens + row, 0);
+  if (threadIdx.x == 0) {
+    int len = *static_cast<volatile const int*>(p.seq_lens + row);
+    if (len < 0 || len > (long long)p.max_pages << p.page_shift) {
+      report(p.status, kSitePagedLength);
+      len = 0;
+    } else if (len > 0 && atomicCAS(p.seq_lens + row, len, 0) != len) {
+      len = 0;
+    }
+    s_len = len;
+  }
   __syncthreads();
   const int len = s_len;
-  if (len < 0 || len > (long long)p.max_pages << p.page_shift) {
-    if (threadIdx.x == 0) report(p.status, kSitePagedLength);
-    return;
-  }
   const int pages = (len + p.page_size - 1) >> p.page_shift;
   const int* const list = p.page_table + (long long)row * p.max_pages;
   for (int j = threadIdx.x; j < pages; j += blockDim.x) {

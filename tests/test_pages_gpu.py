@@ -269,3 +269,16 @@ def test_captured_and_replayed(pages, given):
         for t, p in zip(gpu_pools.cpu(), pools):
             held = torch.tensor(book.refs) > 0
             assert torch.equal(t[held], p[held])
+
+
+@pytest.mark.parametrize("bad", [-1, -(1 << 31), 4 * 16 + 1, (1 << 31) - 1])
+def test_a_row_of_bad_length_is_left_as_it_is(bad):
+    put = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    b = Book([20, 40, 64, 1], 5, 12, 16, 4, seed=8, share=False)
+    t = b.tensors()
+    t[1][1] = bad
+    fa.pages_free(put([1, 2, 1, 2, 4]), *t, 16)  # (2 twice, 4 empty)
+    assert status() == (fa.FA_ERR_PAGE, 302)
+    b.free([2])
+    b.lens[1] = bad
+    b.check(*t)
