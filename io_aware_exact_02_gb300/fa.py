@@ -867,8 +867,11 @@ def fwd_paged4(q, pages, page_table, seq_lens, cu_q, max_q=None, causal: bool = 
                lse=None, workspace=None):
     """fwd_paged over a cache held in 4 bits (``pages``, see kv4_pages), with the
     tensors' scales of the appends.  ``workspace``: fwd_paged4_workspace_size bytes
-    at least; allocated if not given, for long prompts with up to 512 MB in which
-    their keys and values are held in fp16 meanwhile.  Returns (o, lse)."""
+    at least.  If not given it is allocated: fwd_paged4_best_workspace_size bytes, or
+    the least where torch cannot have so many.  The best is up to 512 MB more where
+    a sequence may have more than 1,024 query rows of a key/value head, by max_q (all
+    T rows if not given: give it for batches of single tokens), for the keys and values
+    in fp16 of sequences as long as page_table is wide.  Returns (o, lse)."""
     try:
         dev, (T, Hq, d) = q.get_device(), q.shape
         num_pages, Hkv, size = pages.shape
@@ -905,7 +908,14 @@ def fwd_paged4(q, pages, page_table, seq_lens, cu_q, max_q=None, causal: bool = 
     lib, stream = _lib or load(), _current_stream(dev)
     if workspace is None:  # (as in _fwd_paged)
         ws_bytes = fwd_paged4_best_workspace_size(T, B, Hq, Hkv, d, size // (9 * d) * 8, width, max_q)
-        ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(max(ws_bytes, 1), stream)
+        try:
+            ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(max(ws_bytes, 1), stream)
+        except torch.OutOfMemoryError:
+            least = fwd_paged4_workspace_size(T, B, Hq, Hkv, d, max_q)
+            if least >= ws_bytes:
+                raise
+            ws_bytes = least
+            ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(ws_bytes, stream)
     else:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     try:

@@ -410,3 +410,58 @@ def test_binding_refuses_what_does_not_fit():
     with pytest.raises(ValueError):
         fa.pages_fork(lens, lens, table, lens, torch.zeros(99, dtype=torch.int32, device="cuda"),
                       [pages], 16)
+
+
+class Refuses:
+    """An allocator that has no more than `most` bytes."""
+
+    def __init__(self, alloc, most):
+        self.alloc, self.most, self.asked = alloc, most, []
+
+    def __call__(self, size, stream):
+        self.asked.append(size)
+        if size > self.most:
+            raise torch.OutOfMemoryError("no room")
+        return self.alloc(size, stream)
+
+
+def test_without_room_for_tiles_a_call_takes_the_least_workspace(monkeypatch):
+    x = c4.Batch4(8, 1, 64, 16, [1000, 70], [300, 1], seed=20)
+    sizes = x.T, 2, 8, 1, 64
+    least = fa.fwd_paged4_workspace_size(*sizes, 300)
+    best = fa.fwd_paged4_best_workspace_size(*sizes, 16, x.table.shape[1], 300)
+    assert best > least
+    want = [t.clone() for t in fa.fwd_paged4(*x.args(), max_q=300)]
+    alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
+    for most in (best - 1, least):
+        refuses = Refuses(alloc, most)
+        monkeypatch.setattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", refuses)
+        got = fa.fwd_paged4(*x.args(), max_q=300)
+        fa.check_device_status()
+        assert refuses.asked == [best, least]
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    monkeypatch.setattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", Refuses(alloc, least - 1))
+    with pytest.raises(torch.OutOfMemoryError):
+        fa.fwd_paged4(*x.args(), max_q=300)
+
+
+def test_a_full_allocator_still_serves_long_prompts():
+    # (Torch's own limit on what a process may hold, in place of a full GPU.)
+    x = c4.Batch4(32, 8, 128, 16, [300], [300], seed=21, width=8192)
+    sizes = x.T, 1, 32, 8, 128
+    least = fa.fwd_paged4_workspace_size(*sizes, 300)
+    best = fa.fwd_paged4_best_workspace_size(*sizes, 16, 8192, 300)
+    assert best - least > 500 << 20
+    want = [t.clone() for t in fa.fwd_paged4(*x.args(), max_q=300, out=x.out, lse=x.lse)]
+    x.check(*want, True, 128 ** -0.5)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    limit = torch.cuda.memory_reserved() + least + (128 << 20)
+    torch.cuda.set_per_process_memory_fraction(limit / total)
+    try:
+        got = fa.fwd_paged4(*x.args(), max_q=300, out=x.out, lse=x.lse)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    fa.check_device_status()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
