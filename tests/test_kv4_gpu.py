@@ -263,3 +263,80 @@ def test_attention_of_a_scale_that_vanishes(scale, k_scale, d):
     for nq in ([1, 1, 1], [90, 3, 40], [600, 2, 300]):
         lens = [max(n, 90 + i) for i, n in enumerate(nq)]
         attend(c4.Batch4(4, 2, d, 16, lens, nq, seed=4, k_scale=k_scale), True, scale, max_q=max(nq))
+
+
+# More rows than the append's and the read's CTAs have one each of: a CTA's next row
+# takes over from its last one.
+LONG = [
+    dict(Hq=4, Hkv=1, d=128, page=16, lens=[701, 40, 9, 399, 5, 517], nq=[701, 1, 0, 334, 5, 402], rope=64,
+         pad=3),
+    dict(Hq=2, Hkv=2, d=64, page=64, lens=[3, 1000, 778, 2], nq=[1, 999, 477, 2], rope=64, interleaved=True,
+         fused=True),
+    dict(Hq=1, Hkv=1, d=64, page=32, lens=[5] * 300 + [77], nq=[5, 4, 3, 5, 5] * 60 + [76], pad=1),
+]
+
+
+def check_rows(a, refused=()):
+    """The whole pool, bit for bit, and every row read back; `refused`: (first, end) of
+    packed rows that were not to be written or read."""
+    skip = torch.zeros(a.T, dtype=torch.bool)
+    for lo, hi in refused:
+        skip[lo:hi] = True
+    assert torch.equal(a.pages.cpu(), a.want), (a.pages.cpu() != a.want).nonzero()[:5]
+    k_out = torch.full((a.T, a.Hkv, a.d), 7.0, dtype=torch.bfloat16, device="cuda")
+    v_out = torch.full_like(k_out, 7.0)
+    fa.kv4_read(a.pages, a.table, a.seq_lens, a.cu_q, k_out, v_out, **a.scales)
+    status = fa.device_status()
+    want_k = torch.full((a.T, a.Hkv, a.d), 7.0, dtype=torch.float64)
+    want_v = want_k.clone()
+    for rows, k, v in a.rows:
+        want_k[rows], want_v[rows] = k, v
+    want_k[skip] = want_v[skip] = 7.0
+    assert torch.equal(k_out.cpu().double(), want_k) and torch.equal(v_out.cpu().double(), want_v)
+    return status
+
+
+@pytest.mark.parametrize("case", LONG)
+def test_append_and_read_many_rows(case):
+    a = Append(seed=13, **case)
+    assert a.T > 1216
+    a.run()
+    fa.check_device_status()
+    assert check_rows(a) == (0, 0)
+
+
+@pytest.mark.parametrize("case", LONG[:2])
+@pytest.mark.parametrize("number", [-1, 10 ** 9])
+def test_append_and_read_around_a_refused_page(case, number):
+    a = Append(seed=14, **case)
+    before = a.pages.cpu().clone()
+    b = case["nq"].index(max(case["nq"]))
+    j = case["lens"][b] // case["page"] // 2
+    page = int(a.table[b, j])
+    a.table[b, j] = number
+    a.want[page] = before[page]
+    first = int(a.cu_q[b + 1]) - (case["lens"][b] - j * case["page"])
+    a.run()
+    assert fa.device_status() == (fa.FA_ERR_PAGE, 304)
+    assert check_rows(a, [(first, first + case["page"])]) == (fa.FA_ERR_PAGE, 304)
+
+
+def test_append_many_rows_past_the_rotations_table():
+    a = Append(seed=15, **LONG[0])
+    before, page, cut = a.pages.cpu().clone(), 16, 480
+    for b, L in enumerate(a.lens):
+        for j in range(cut // page, -(-L // page)):
+            a.want[a.table[b, j].item()] = before[a.table[b, j].item()]
+    a.rope = a.rope[:cut].contiguous()
+    a.run()
+    assert fa.device_status() == (fa.FA_ERR_PAGE, 303)
+    assert torch.equal(a.pages.cpu(), a.want)
+
+
+@pytest.mark.parametrize("case", APPENDS)
+def test_append_leaves_the_other_key_of_a_pair(case):
+    """The whole pool bit for bit, the half of a byte that no row owns among it."""
+    a = Append(seed=12, **case)
+    a.run()
+    fa.check_device_status()
+    assert torch.equal(a.pages.cpu(), a.want), (a.pages.cpu() != a.want).nonzero()[:5]
