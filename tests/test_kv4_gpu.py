@@ -340,3 +340,48 @@ def test_append_leaves_the_other_key_of_a_pair(case):
     a.run()
     fa.check_device_status()
     assert torch.equal(a.pages.cpu(), a.want), (a.pages.cpu() != a.want).nonzero()[:5]
+
+
+def long_batch(Hq, Hkv, d, page, B, length, nq, seed, spread, pool_pages):
+    """B sequences of some `length` keys on pages that they share, each in an order of
+    its own, some pages more than once: the attention's inputs, and a sequence's keys
+    and values in fp64."""
+    x = c4.Batch4(Hq, Hkv, d, page, [pool_pages * page], [B * nq], seed=seed, spread=spread)
+    g = torch.Generator().manual_seed(seed + 1)
+    lens = [length - 37 * b for b in range(B)]
+    order = [torch.randint(pool_pages, (-(-n // page),), generator=g) for n in lens]
+    table = torch.full((B, -(-length // page)), 1 << 30, dtype=torch.int32)
+    base = x.table[0].cpu()
+    for b, o in enumerate(order):
+        table[b, :len(o)] = base[o]
+    x.table, x.lens, x.nq, x.B = table.cuda(), lens, [nq] * B, B
+    x.cu = [b * nq for b in range(B + 1)]
+    x.seq_lens, x.cu_q = (torch.tensor(t, dtype=torch.int32, device="cuda") for t in (lens, x.cu))
+
+    def sequence(b):
+        return [t.unflatten(0, (pool_pages, page))[order[b]].flatten(0, 1)[:lens[b]]
+                for t in (x.keys[0], x.vals[0])]
+    return x, sequence
+
+
+# A CTA has a run of some 30 tiles: its warps go round their rings many times, take
+# the numbers of their pages again and again, and (spread 20) meet louder keys late.
+@pytest.mark.parametrize("spread", [1.0, 20.0])
+@pytest.mark.parametrize("Hq,Hkv,d,page,nq", [
+    (4, 4, 128, 16, 1),      # 1 row
+    (32, 4, 128, 64, 1),     # 8
+    (16, 4, 64, 16, 2),      # 8 of two tokens
+    (64, 4, 128, 16, 1),     # 16
+    (16, 4, 64, 128, 4),     # 16 of four tokens
+    (16, 4, 128, 16, 5),     # 16, and 4
+])
+def test_decode_of_long_segments(Hq, Hkv, d, page, nq, spread):
+    x, sequence = long_batch(Hq, Hkv, d, page, 28, 16000, nq, 23, spread, 8192 // page)
+    o, lse = fa.fwd_paged4(*x.args(), max_q=nq, out=x.out, lse=x.lse)
+    fa.check_device_status()
+    o, lse = o.cpu(), lse.cpu()
+    for b in range(x.B):
+        k, v = sequence(b)
+        rows = slice(b * nq, b * nq + nq)
+        ref = c4.reference(x.q_host[rows], k, v, True, d ** -0.5)
+        c4.compare(o[rows], lse[rows], ref, (b, x.lens[b]))
