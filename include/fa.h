@@ -378,8 +378,8 @@ int fa_fwd_paged_prefix(const void* q, const void* k_pages, const void* v_pages,
  *
  * fa_fwd_paged4 is fa_fwd_paged over it, of those values unrounded.  A query
  * row is scaled by a power of two to fit fp16, in which the products run:
- * channels below 2^-38 of the row's largest lose bits; so do weights below
- * 2^-21 of its greatest, which end at 2^-32.  workspace: at least
+ * channels below 2^-31 of the row's largest lose bits, and vanish below 2^-39; so
+ * do weights below 2^-21 of its greatest, which end at 2^-32.  workspace: at least
  * fa_fwd_paged4_workspace_size bytes; with more, up to
  * fa_fwd_paged4_best_workspace_size (512 MB more at most), long prompts run
  * faster on a copy of their keys and values in fp16, with the same results.

@@ -112,11 +112,13 @@ __device__ __forceinline__ uint32_t kv4_codes(const float (&lo)[4], const float 
 }
 
 // The power of two that takes a query row, whose largest magnitude has the bits
-// `top` of an fp32 number, to [2^14, 2^15), where fp16 holds every channel but
-// for what is below 2^-38 of that one; as an exponent.  Zeros, infinities and
-// NaN stay.
+// `top` of an fp32 number, to [2^14, 2^15), where fp16 holds every channel of at
+// least 2^-31 of that one, and the others to 2^-39 of it; as an exponent.  At most
+// 126, whose inverse is a normal number too: it makes every bf16 number a multiple of
+// 2^-7, so rows that it leaves below 2^14 are held whole.  Zeros, infinities and NaN
+// stay.
 __device__ __forceinline__ int kv4_row_exponent(uint32_t top) {
-  return top > 0u && top < 0x7f800000u ? min(14 - ((int)(top >> 23) - 127), 100) : 0;
+  return top > 0u && top < 0x7f800000u ? min(14 - ((int)(top >> 23) - 127), 126) : 0;
 }
 __device__ __forceinline__ float kv4_pow2(int e) { return __int_as_float((e + 127) << 23); }
 // The larger of `top` and the magnitudes of a pair of bf16 numbers, as bits of

@@ -385,3 +385,14 @@ def test_decode_of_long_segments(Hq, Hkv, d, page, nq, spread):
         rows = slice(b * nq, b * nq + nq)
         ref = c4.reference(x.q_host[rows], k, v, True, d ** -0.5)
         c4.compare(o[rows], lse[rows], ref, (b, x.lens[b]))
+
+
+@pytest.mark.parametrize("size", [1e-24, 1e-28, 1e-32, 1e-36, 1e-38, 3e-40])
+@pytest.mark.parametrize("nq", [[1, 2], [90, 3]])
+def test_attention_of_tiny_queries(nq, size):
+    """Down to the numbers of bf16 that are not normal, under scales that make as much
+    of them as of others."""
+    x = c4.Batch4(4, 2, 128, 16, [200, 64], nq, seed=24, spread=3.0)
+    x.q_host = (x.q_host.double() * size).to(torch.bfloat16)
+    x.q = x.q_host.cuda()
+    attend(x, True, 128 ** -0.5 * min(1 / size, 2e38), max_q=max(nq))
