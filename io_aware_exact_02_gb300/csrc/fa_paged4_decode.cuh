@@ -572,16 +572,18 @@ __device__ __forceinline__ void decode4_cta(const Paged4Params& p, const PagedPh
         const float f = __shfl_sync(0xffffffffu, weight, w);
         acc.x += f * y[w].x, acc.y += f * y[w].y;
       }
-      const float own = sum == 0.f ? 0.f : p.v_scale / sum;
+      // (The values' scale by itself: over the sum it may be too small to hold.)
+      const float own = sum == 0.f ? 0.f : 1.f / sum;
+      acc.x = acc.x * own * p.v_scale, acc.y = acc.y * own * p.v_scale;
       const float lse2 = sum == 0.f ? ninf : top + log2f(sum);
       const int tok = r / p.G;
       const long long at = (long long)(r_tok0 + tok) * p.Hq + r_head0 + (r - tok * p.G);
       if (r_slot >= 0) {
         const long long row = ((long long)cta * 2 + r_slot) * ph.slot_rows + r;
-        *reinterpret_cast<float2*>(ph.slot_o + row * D + ch) = make_float2(acc.x * own, acc.y * own);
+        *reinterpret_cast<float2*>(ph.slot_o + row * D + ch) = acc;
         if (ch == 0) ph.slot_lse[row] = lse2;
       } else {
-        *reinterpret_cast<uint32_t*>(p.o + at * D + ch) = pack_bf16x2(acc.x * own, acc.y * own);
+        *reinterpret_cast<uint32_t*>(p.o + at * D + ch) = pack_bf16x2(acc.x, acc.y);
         if (ch == 0) p.lse[at] = lse2 == ninf ? ninf : lse2 * kLn2;
       }
     }

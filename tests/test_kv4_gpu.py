@@ -396,3 +396,27 @@ def test_attention_of_tiny_queries(nq, size):
     x.q_host = (x.q_host.double() * size).to(torch.bfloat16)
     x.q = x.q_host.cuda()
     attend(x, True, 128 ** -0.5 * min(1 / size, 2e38), max_q=max(nq))
+
+
+@pytest.mark.parametrize("rows", [1, 12, 100, 300])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_of_tiny_values(d, rows):
+    """Values next to the smallest normal numbers, of keys that all weigh the same: the
+    mean of 30,000 equal ones is that one, however large the sum of their weights (many
+    sequences on the same pages, so that a CTA adds up most of one)."""
+    L, Hkv, v_scale, B = 30000, 4, 4e-39, max(40 * 8 // (rows + 7), 8)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    v = torch.full((L, Hkv, d), 2688 * v_scale, dtype=torch.bfloat16, device="cuda")
+    v[:, :, 1::2] *= -0.5
+    n = -(-L // 16)
+    pool, table = fa.kv4_pages(n, Hkv, 16, d), torch.arange(n, dtype=torch.int32, device="cuda")[None]
+    fa.kv4_append(torch.ones_like(v), v, pool, table, ints([L]), ints([0, L]), v_scale=v_scale)
+    q = torch.ones((B * rows, 4 * Hkv, d), dtype=torch.bfloat16, device="cuda")
+    o, _ = fa.fwd_paged4(q, pool, table.expand(B, n).contiguous(), ints([L] * B),
+                         ints([b * rows for b in range(B + 1)]), max_q=rows, causal=False, v_scale=v_scale)
+    fa.check_device_status()
+    held = torch.tensor([2688.0, -1344.0], dtype=torch.float64).repeat(d // 2) * v_scale
+    # one rounding to bf16, sums of L terms and a few more roundings in fp32, v_scale's
+    # own below fp32's normal range
+    off = (o.cpu().double() - held).abs() / held.abs()
+    assert (off <= c4.BF16 + (L + 64) * c4.FP32 + 2.0 ** -150 / v_scale).all(), off.max().item()
