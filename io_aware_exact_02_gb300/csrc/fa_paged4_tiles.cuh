@@ -89,7 +89,9 @@ struct Raw4 {
 };
 
 // Reads two blocks (at blk[0] and blk[1]), keys in their slots until `keys` and `keys`
-// - 16 of them.  Straight-line code that looks at nothing it loads.
+// - 16 of them.  Straight-line code that looks at nothing it loads.  (Ordinary loads: an
+// append may write the blocks after this kernel has begun, up to its wait_prior_grid,
+// which loads for data that stay the same while a kernel runs do not allow.)
 template <int D, bool kV>
 __device__ __forceinline__ void read_raw4(const uint8_t* const (&blk)[2], int keys, Raw4<D>& r) {
   using Block = Kv4Block<D>;
@@ -103,19 +105,19 @@ __device__ __forceinline__ void read_raw4(const uint8_t* const (&blk)[2], int ke
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if constexpr (D == 128) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(codes + u * 512));
+        const uint4 x = *reinterpret_cast<const uint4*>(codes + u * 512);
         r.code[b][u][0] = x.x, r.code[b][u][1] = x.y;
         r.code[b][u][D / 32 - 2] = x.z, r.code[b][u][D / 32 - 1] = x.w;
       } else {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(codes + u * 256));
+        const uint2 x = *reinterpret_cast<const uint2*>(codes + u * 256);
         r.code[b][u][0] = x.x, r.code[b][u][1] = x.y;
       }
       if constexpr (kV)
-        r.scale[b][u] = __ldg(reinterpret_cast<const uint16_t*>(scales + u * 8));
+        r.scale[b][u] = *reinterpret_cast<const uint16_t*>(scales + u * 8);
       else if constexpr (D == 128)
-        r.scale[b][u] = __ldg(reinterpret_cast<const uint16_t*>(scales + u * 64));
+        r.scale[b][u] = *reinterpret_cast<const uint16_t*>(scales + u * 64);
       else
-        r.scale[b][u] = __ldg(scales + u * 32);
+        r.scale[b][u] = scales[u * 32];
     }
   }
   if constexpr (kV) r.keys = keys;

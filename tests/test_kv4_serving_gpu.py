@@ -465,3 +465,37 @@ def test_a_full_allocator_still_serves_long_prompts():
         torch.cuda.set_per_process_memory_fraction(1.0)
     fa.check_device_status()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("nq", [60, 330])
+@pytest.mark.parametrize("best", [False, True])
+def test_appends_and_attentions_back_to_back(nq, best):
+    """The same slots written anew and attended, one call after another without a wait:
+    what each attention saw is what the append before it wrote."""
+    page, L, B, Hq, Hkv, d = 16, 700, 3, 8, 2, 64
+    s = Server(B, 150, page, 48, Hq, Hkv, d, seed=22)
+    s.grow([0, 1, 2], [L, L - 1, L - 13])
+    s.pool.fill_(0x22)
+    sizes = B * nq, B, Hq, Hkv, d
+    size = (fa.fwd_paged4_best_workspace_size(*sizes, page, 48, nq) if best
+            else fa.fwd_paged4_workspace_size(*sizes, nq))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    cu = ints([b * nq for b in range(B + 1)])
+    x = torch.randn((6, B * nq, Hq + 2 * Hkv, d), generator=s.g).to(torch.bfloat16).cuda()
+    o = torch.zeros((2, 6, B * nq, Hq, d), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((2, 6, B * nq, Hq), device="cuda")
+    q_out = torch.empty((B * nq, Hq, d), dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    for waits in (0, 1):
+        for i in range(6):
+            q, k, v = x[i].split([Hq, Hkv, Hkv], 1)
+            fa.kv4_append(k, v, s.pool, s.table, s.lens, cu, q=q, q_out=q_out, rope=s.rope)
+            if waits:
+                torch.cuda.synchronize()
+            fa.fwd_paged4(q_out, s.pool, s.table, s.lens, cu, max_q=nq, out=o[waits, i],
+                          lse=lse[waits, i], workspace=ws)
+            if waits:
+                torch.cuda.synchronize()
+    fa.check_device_status()
+    assert torch.equal(o[0], o[1]) and torch.equal(lse[0], lse[1])
+    assert not torch.equal(o[0, 0], o[0, 1])
