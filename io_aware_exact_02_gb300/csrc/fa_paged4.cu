@@ -43,7 +43,7 @@ int launch_paged4_d(const Paged4Params& p, cudaStream_t stream) {
   c.stream = stream;
   c.attrs = pdl;
   c.numAttrs = 1;
-  const Paged4Form f = paged4_form(p.T, p.B, p.G, p.max_q);
+  const Paged4Form f = paged4_form(p.T, p.B, p.G, p.max_q, p.v_scale);
   const Paged4Workspace w = paged4_workspace_layout(D, f);
   auto at = [&](size_t offset) { return reinterpret_cast<float*>(p.workspace + offset); };
   int rc;

@@ -71,24 +71,19 @@ __device__ __forceinline__ int tile_steps(const PagedParams& p, const PagedPhase
   return x <= 0 ? 0 : min((x + kTile - 1) / kTile, it.nj);
 }
 
-// x times a row's factor, and the values' scale where there is one: by itself, since
-// over the row's sum it may be too small to hold.
-__device__ __forceinline__ float times(float x, float own) { return x * own; }
-__device__ __forceinline__ float times(float x, float own, float v_scale) { return x * own * v_scale; }
-
 // A softmax warp's rows of O out of tensor memory (at colO; ~0: zeros), times
-// `own` (and v_scale, if given), plus `pre` times row `row` of pre_o (if given),
-// to row dst_row (none if negative) of `wide` (fp32) or of o (bf16); slot: the
-// warp's first row where wide is a slot.  A thread has a row, but rows
+// `own`, plus `pre` times row `row` of pre_o (if given), to row dst_row (none
+// if negative) of `wide` (fp32) or of o (bf16); slot: the warp's first row where
+// wide is a slot.  A thread has a row, but rows
 // are stored by lanes that share them: 128 bytes of the warp's 32 rows at a
 // time through `out`, 16-byte chunk c of row r at c ^ (r % 8).  (A thread
 // storing its own row wrote 16 of its 256 or 512 bytes at a time: 10,000
 // cycles a unit.)  Not inlined: the softmax loop around it needs every
 // register, and addresses computed here would be kept through it.
-template <int D, class... Scale>
+template <int D>
 __device__ __noinline__ void store_rows(uint32_t colO, float own, float pre, long long row,
                                         long long dst_row, uint8_t* out, float* wide, float* slot,
-                                        const float* pre_o, __nv_bfloat16* o, Scale... v_scale) {
+                                        const float* pre_o, __nv_bfloat16* o) {
   const int lane = (int)lane_id(), e = lane & 7;
   uint8_t* const mine = out + lane * 128;
   if (slot != nullptr && pre_o == nullptr) {
@@ -107,8 +102,7 @@ __device__ __noinline__ void store_rows(uint32_t colO, float own, float pre, lon
       for (int i = 0; i < 8; ++i) {
         float x[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          x[k] = own == 0.f ? 0.f : times(__uint_as_float(w[4 * i + k]), own, v_scale...);
+        for (int k = 0; k < 4; ++k) x[k] = own == 0.f ? 0.f : __uint_as_float(w[4 * i + k]) * own;
         *reinterpret_cast<float4*>(mine + ((i ^ (lane & 7)) << 4)) =
             make_float4(x[0], x[1], x[2], x[3]);
       }
@@ -135,7 +129,7 @@ __device__ __noinline__ void store_rows(uint32_t colO, float own, float pre, lon
       }
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        w[i] = own == 0.f ? 0u : __float_as_uint(times(__uint_as_float(w[i]), own, v_scale...));
+        w[i] = own == 0.f ? 0u : __float_as_uint(__uint_as_float(w[i]) * own);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         *reinterpret_cast<uint4*>(mine + ((i ^ (lane & 7)) << 4)) =
@@ -178,8 +172,8 @@ __device__ __noinline__ void store_rows(uint32_t colO, float own, float pre, lon
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         w[i] = own == 0.f ? 0u
-                          : pack_bf16x2(times(__uint_as_float(w[2 * i]), own, v_scale...),
-                                        times(__uint_as_float(w[2 * i + 1]), own, v_scale...));
+                          : pack_bf16x2(__uint_as_float(w[2 * i]) * own,
+                                        __uint_as_float(w[2 * i + 1]) * own);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<uint4*>(mine + (((4 * h + i) ^ (lane & 7)) << 4)) =
@@ -201,9 +195,9 @@ __device__ __noinline__ void store_rows(uint32_t colO, float own, float pre, lon
 // The same for 32 rows of o that are all valid and whole tokens: a box of 64
 // channels at a time, stored by TMA (row r's 16-byte chunk c at c ^ (r % 8), as
 // its swizzle wants it): 3,000 cycles a unit against 5,700 of store_rows.
-template <int D, class... Scale>
+template <int D>
 __device__ __noinline__ void store_box(uint32_t colO, float own, uint8_t* out,
-                                       const CUtensorMap* to, int head, int tok, Scale... v_scale) {
+                                       const CUtensorMap* to, int head, int tok) {
   const int lane = (int)lane_id();
   uint8_t* const mine = out + lane * 128;
 #pragma unroll 1
@@ -221,8 +215,8 @@ __device__ __noinline__ void store_box(uint32_t colO, float own, uint8_t* out,
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         w[h][i] = own == 0.f ? 0u
-                             : pack_bf16x2(times(__uint_as_float(x[2 * i]), own, v_scale...),
-                                           times(__uint_as_float(x[2 * i + 1]), own, v_scale...));
+                             : pack_bf16x2(__uint_as_float(x[2 * i]) * own,
+                                           __uint_as_float(x[2 * i + 1]) * own);
     }
     if (c > 0) {
       if (lane == 0) bulk_wait_group_read0();
@@ -545,6 +539,7 @@ __device__ __forceinline__ void prompt_cta(
       const bool any = l > 0.f || l != l;
       float lse2 = any ? m_ref + __log2f(l) : ninf;
       float own = any ? 1.f / l : 0.f, pre = 0.f;
+      if constexpr (kFour) own *= p.v_scale;
       if (it.first && ph.pre_o != nullptr && valid) {
         const float other = ph.pre_lse[row], top = fmaxf(lse2, other);
         if (top != ninf) {
@@ -566,21 +561,15 @@ __device__ __forceinline__ void prompt_cta(
       // A warp's 32 rows are whole tokens; all of them are the unit's.
       const bool box = ph.box_out && it.slot < 0 && !(it.first && ph.pre_o != nullptr) &&
                        __all_sync(0xffffffffu, valid);
-      auto store = [&](auto... v_scale) {
-        if (box)
-          store_box<D>(n_t > 0 ? colO : ~0u, own, sm.out[warp], to, it.h * p.G,
-                       it.tok0 + t * ph.tile_tokens + (warp & 3) * (32 / p.G), v_scale...);
-        else
-          store_rows<D>(n_t > 0 ? colO : ~0u, own, pre, row,
-                        valid ? (it.slot >= 0 ? slot_row : row) : -1, sm.out[warp],
-                        it.slot >= 0 ? ph.slot_o : ph.out_o,
-                        it.slot >= 0 ? ph.slot_o + (slot_row - lane_id()) * D : nullptr,
-                        it.first ? ph.pre_o : nullptr, p.o, v_scale...);
-      };
-      if constexpr (kFour)
-        store(p.v_scale);
+      if (box)
+        store_box<D>(n_t > 0 ? colO : ~0u, own, sm.out[warp], to, it.h * p.G,
+                     it.tok0 + t * ph.tile_tokens + (warp & 3) * (32 / p.G));
       else
-        store();
+        store_rows<D>(n_t > 0 ? colO : ~0u, own, pre, row,
+                      valid ? (it.slot >= 0 ? slot_row : row) : -1, sm.out[warp],
+                      it.slot >= 0 ? ph.slot_o : ph.out_o,
+                      it.slot >= 0 ? ph.slot_o + (slot_row - lane_id()) * D : nullptr,
+                      it.first ? ph.pre_o : nullptr, p.o);
       if (n_t > 0) {
         // O_t may now be overwritten by the next unit's first product.
         tc_fence_before();
