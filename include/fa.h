@@ -382,7 +382,9 @@ int fa_fwd_paged_prefix(const void* q, const void* k_pages, const void* v_pages,
  * do weights below 2^-21 of its greatest, which end at 2^-32.  workspace: at least
  * fa_fwd_paged4_workspace_size bytes; with more, up to
  * fa_fwd_paged4_best_workspace_size (512 MB more at most), long prompts run
- * faster on a copy of their keys and values in fp16, with the same results.
+ * faster on a copy of their keys and values in fp16, with the same results.  (The
+ * best follows from T, max_q and max_pages, not from the lengths, which the call does
+ * not know: as long as a sequence may be by its table.)
  * Numbers in slots past a sequence's length are never used; value rows that the
  * causal mask hides have to be finite, as in the other forward calls.
  * Errors of all three: as the call each is a form of, and FA_ERR_ARG for a
@@ -418,7 +420,8 @@ int fa_fwd_paged4(const void* q, const void* pages, void* o, float* lse, const i
  * read by the call only.  page_table: [rows][max_pages] int32, seq_lens: [rows]
  * int32, the keys of each row's sequence (0: the row is empty); entries past a
  * sequence's last page mean nothing.  refs: [num_pages] int32, the sequences that
- * hold a page; 0: it is free.  page_size as above.  The tables are device memory,
+ * hold a page; 0: it is free, and may be given to a child or moved onto: a row's page
+ * that refs does not count is lost.  page_size as above.  The tables are device memory,
  * read and written by the kernels only; entries outside their bounds record
  * FA_ERR_PAGE and are left out, and so are the cases named below.
  *
@@ -440,9 +443,12 @@ int fa_fwd_paged4(const void* q, const void* pages, void* o, float* lse, const i
  *
  * fa_pages_compact moves the pages in use (`live` of them) to the numbers below
  * live: the highest page in use goes to the lowest free one and so on, in every
- * pool, in refs and in the tables of all rows.  The pages from live on are free
- * then; their bytes are left as they were.  live, if not NULL, receives the
- * number (device memory).  workspace: fa_pages_compact_workspace_size bytes.
+ * pool, in refs and in the tables of all rows.  Page numbers that stand elsewhere are
+ * not renumbered: the prefix_pages of fa_fwd_paged_prefix, copies of a table; a row of
+ * page_table that holds a prefix's pages keeps them counted and up to date.  The pages
+ * from live on are free then; their bytes are left as they were.  live, if not NULL,
+ * receives the number (device memory).  workspace: fa_pages_compact_workspace_size
+ * bytes.  Two calls in flight at once need two workspaces.
  *
  * Errors: FA_ERR_ARG, FA_ERR_ALIGN (16 bytes for pools and page_bytes, 4 for the
  * tables), FA_ERR_WORKSPACE, FA_ERR_DEVICE, FA_ERR_LAUNCH.

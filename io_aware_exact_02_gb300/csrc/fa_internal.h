@@ -390,9 +390,10 @@ int launch_fwd_paged4(const Paged4Params& p, int d, cudaStream_t stream);
 // key/value head; where a token has more, its heads are dealt in `subs` equal
 // runs.  The others go to the prompt kernel.
 constexpr int kPaged4CtasPerSm = 3;    // of the decode kernel
-// (8 sequences of 8K keys, 8 key/value heads, d = 128: 16 rows 46 us, 32 70, 64 116 in
-// units of 16 on the decode kernel, 92 on the prompt kernel; 33 of 2K, 16 heads, d =
-// 64: 51, 88 and 156 against 149.)
+// (8 sequences of 8K keys, 8 key/value heads, d = 128: 16 rows 44 us, 32 68, 48 91, 64 116
+// in units of 16 on the decode kernel, 64 83 on the prompt kernel; 33 of 2K, 16 heads,
+// d = 64: 50, 84, 119 and 156 against 136.  The bf16 cache takes 51, 54, 59 and 59; 55,
+// 60, 84 and 85.)
 constexpr int kPaged4DecodeMost = 48;  // query rows of a sequence and key/value head
 struct Paged4Form {
   int heads, subs;   // query heads of a decode unit's token; runs of a token's heads

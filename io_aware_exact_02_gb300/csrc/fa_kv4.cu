@@ -7,11 +7,11 @@
 // product and difference of the rotation rounded by itself, so that a code does
 // not depend on how the compiler joins them.
 //
-// Bound by memory, but for the quantisation: 16,384 rows of 32 query and 8 key/value
-// heads, d = 128: append 70 us (5.0 TB/s of the 6.8 that a copy reaches; keys and
-// values alone 35 us, of 1.5 TB/s: some 20 instructions a number), reading back 20 us
-// (4.4 TB/s).  Twice as many registers a thread, two rows to find a place for at a
-// time, made the append 106 us.
+// 16,384 rows of 32 query and 8 key/value heads, d = 128: append 69 us (5.1 TB/s of the
+// 6.8 that a copy reaches; keys and values alone 34 us), reading back 19 us (4.5 TB/s).
+// Neither the issue slots (58% and 52%) nor memory are full: of the 12 cycles that a
+// warp takes for an instruction it waits 6 for loads from global memory.  Twice as many
+// registers a thread, two rows to find a place for at a time, made the append 106 us.
 //
 // A byte of V holds a pair of neighbouring keys.  The row of the even slot
 // writes both where the odd slot's row is new too; a row whose neighbour is not

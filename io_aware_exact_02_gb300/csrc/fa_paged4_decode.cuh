@@ -26,9 +26,11 @@
 // joined through shared memory.
 //
 // Measured, H_q 32, H_kv 8, d = 128, one row each: 8 sequences of 32K keys 65.9 us (302
-// MB: 4.6 TB/s; the steps alone 6.1), 64 of up to 4K 46.1, one of 1,000 10.3; 33 of 2K
-// with 1 to 4 rows, 16 heads, d = 64: 25.1.  What is left is around the steps: 4 us of
-// start, 2 to 4 of a unit's end, 4 to 6 of the merge.  Three CTAs an SM, because
+// MB: 4.6 TB/s), 64 of up to 4K 46.1, one of 1,000 10.3; 33 of 2K with 1 to 4 rows, 16
+// heads, d = 64: 25.1.  The steps alone, by what more keys cost (8 sequences of 128K and
+// 256K): 5.9 TB/s, 87% of the copy rate; d = 64 4.7 to 5; with 16 rows, d = 128, 3.5.
+// So 14 of the 65.9 us lie around the steps: start, units' ends, and the merge, a
+// kernel of 6 to 7 us.  Three CTAs an SM, because
 // one's unit end hides behind the others' steps (one CTA of 16 warps: 62.6 us
 // instead of 50 for the 64 sequences); steps of two blocks, whose chains of latencies
 // hide behind one another (79.6 us instead of 69.2 for the 8).

@@ -65,8 +65,8 @@ __device__ __forceinline__ int block_scan(int x, int& all) {
   return before + inc - x;
 }
 
-// The reference counts of a thread's kPer pages from page0 on (past the pool: used,
-// so that they are nobody's free page).
+// Which of a thread's kPer pages from page0 on are in use, and how many (past the pool:
+// not; the plan's loop over them ends before).
 __device__ __forceinline__ int load_used(const PagesParams& p, int page0, bool (&used)[kPer]) {
   int n = 0;
 #pragma unroll
@@ -96,8 +96,8 @@ __global__ void __launch_bounds__(kThreads) fa_pages_plan_kernel(const PagesPara
   const int tid = threadIdx.x;
   if (kFork && blockIdx.x == (unsigned)p.ranges) {
     // The children, in order.  All parents' lengths are read before the first child
-    // is claimed (length -1, until it has its parent's): a child that is listed
-    // twice, or holds keys, is nobody's.
+    // is claimed (length -1, until it has its parent's): one that holds keys is
+    // nobody's, one that is listed twice that listing's which claims it first.
     const long long cap = (long long)p.max_pages << p.page_shift;
     for (int i = tid; i < p.n; i += kThreads) {
       const int from = p.parents[i], to = p.children[i];

@@ -1076,7 +1076,8 @@ def pages_compact_workspace_size(num_pages) -> int:
 def pages_compact(page_table, seq_lens, refs, pools, page_size: int, live=None, workspace=None):
     """Move the pages in use to the lowest numbers, in every cache of ``pools`` (see
     pages_copy), in refs and in the rows of page_table, so that the pool can be
-    cut behind them.  ``live`` (int32 tensor of one, allocated if not given)
+    cut behind them.  Page numbers kept elsewhere (fwd_paged_prefix's prefix_pages)
+    are not renumbered.  ``live`` (int32 tensor of one, allocated if not given)
     receives how many are in use, and is returned."""
     dev, rows, width, num_pages = _book(page_table, seq_lens, refs, ())
     if _current_device() != dev:
